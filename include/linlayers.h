@@ -23,6 +23,9 @@
  *               loading holds back compute), so this entry point takes them
  *               once per request and computes their contribution once per
  *               request, not once per candidate.
+ *  - embed_*, layernorm_*: what stands in front of a model's linear layers: the
+ *               lookup of its tokens' (or items') rows and the norm of the
+ *               activations, each with its gradients.
  *
  * Conventions shared by every entry point:
  *
@@ -328,6 +331,109 @@ ll_status lincomp_ragged_run(const lincomp_ragged_desc* desc, const int64_t* off
 /* lincomp_ragged_run with the bias of an LL_EPI_BIAS epilogue (as lincomp_run_ex). */
 ll_status lincomp_ragged_run_ex(const lincomp_ragged_desc* desc, const int64_t* offsets, const void* user,
                                 const void* item, const void* W, const float* bias, void* Y, void* stream);
+
+/*
+ * Embedding lookup: out[t][d] = scale * table[ids[t]][d] (0 <= t < T, 0 <= d < D),
+ * formed in fp32 and rounded once to `type` (LL_BF16, LL_F16 or LL_F32; table
+ * and out alike).  Row r of the table starts at table + r*stride_table, row t
+ * of out at out + t*stride_out; the last dimension is contiguous; strides at
+ * least D.  ids: device array of T int64.  An id outside [0, V) gives a row
+ * of zeros (no access outside the table).  T == 0 or D == 0: nothing is written.
+ * Rows move 16 bytes at a time where both pointers are 16-byte aligned and D
+ * and the strides are multiples of 16 bytes, else element by element.
+ * One kernel on `stream`; no workspace; may be captured into a HIP graph.
+ * Errors: LL_ERR_INVALID_ARG (null desc/pointer, negative size, stride below
+ * D, a pointer not aligned to its element, out overlapping the table or ids),
+ * LL_ERR_UNSUPPORTED (type, sizes of 2^31 and more, device),
+ * LL_ERR_NO_DEVICE, LL_ERR_HIP.
+ */
+typedef struct {
+  int64_t V, T, D;
+  int64_t stride_table, stride_out;
+  int32_t type; /* ll_dtype of table and out */
+  float scale;
+} embed_desc;
+
+ll_status embed_run(const embed_desc* desc, const void* table, const int64_t* ids, void* out, void* stream);
+
+/*
+ * Gradient of the lookup with respect to the table, dense:
+ *   dtable[v][d] = scale * sum over t with ids[t] == v of dout[t][d]
+ * for every 0 <= v < V (rows no token refers to are written as zeros).
+ * Tokens whose id is padding_id or outside [0, V) contribute nothing
+ * (padding_id -1: no padding).  LL_EMBED_ACCUMULATE: the sums are added to
+ * dtable instead (a tied table, several batches); rows without a token are
+ * then not touched.  Tokens are sorted by id, stably; each row is summed in
+ * fp32, in an order that depends on the ids alone, and rounded once to
+ * `type`, so equal inputs give equal bits.
+ * Workspace (256-byte aligned): embed_grad_workspace_size; 0 for few tokens.
+ * Only kernels are launched, so the call may be captured into a HIP graph.
+ * Errors as for embed_run (dtable must not overlap dout, ids or the
+ * workspace), unknown flag bits (LL_ERR_INVALID_ARG), and LL_ERR_WORKSPACE.
+ */
+#define LL_EMBED_ACCUMULATE 0x1u
+
+typedef struct {
+  int64_t V, T, D;
+  int64_t stride_dout, stride_dtable;
+  int64_t padding_id;
+  int32_t type; /* ll_dtype of dout and dtable */
+  float scale;
+  uint32_t flags; /* LL_EMBED_ACCUMULATE or 0 */
+} embed_grad_desc;
+
+ll_status embed_grad_workspace_size(const embed_grad_desc* desc, size_t* bytes);
+ll_status embed_grad_run(const embed_grad_desc* desc, const int64_t* ids, const void* dout, void* dtable,
+                         void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Layer norm over the D columns of each of N rows:
+ *   y = (x - mean) * rstd * gamma + beta,  rstd = 1 / sqrt(var + eps)
+ * with mean and (biased) variance in fp32 from the row itself, the variance
+ * around that mean; y rounded once to `type`.  x, y: row strides stride_x,
+ * stride_y (elements, at least D), last dimension contiguous.  gamma, beta:
+ * D values of param_type (`type` or LL_F32), each may be NULL (ones, zeros).
+ * mean, rstd: N fp32 values each for the gradient, each may be NULL.
+ * y may be x itself (same pointer and stride).  N == 0 or D == 0: nothing is
+ * written.  One kernel on `stream`, no workspace, graph-capturable.
+ * Errors: LL_ERR_INVALID_ARG (null desc, x or y; negative size, stride below
+ * D, eps negative or not finite, misaligned pointer, y overlapping an input
+ * otherwise), LL_ERR_UNSUPPORTED (types, D of 2^31 and more, device),
+ * LL_ERR_NO_DEVICE, LL_ERR_HIP.
+ */
+typedef struct {
+  int64_t N, D;
+  int64_t stride_x, stride_y;
+  int32_t type, param_type; /* ll_dtype */
+  float eps;
+} layernorm_desc;
+
+ll_status layernorm_run(const layernorm_desc* desc, const void* x, const void* gamma, const void* beta, void* y,
+                        float* mean, float* rstd, void* stream);
+
+/*
+ * Gradients of layer norm, from its input and the mean and rstd it gave:
+ *   xhat = (x - mean) * rstd,  h = dy * gamma,
+ *   dx = rstd * (h - mean_D(h) - xhat * mean_D(h * xhat)),
+ *   dgamma = sum over rows of dy * xhat,  dbeta = sum over rows of dy
+ * in fp32, each result rounded once.  dgamma and dbeta: D values of
+ * param_type, both or neither NULL (neither wanted: dx alone).  Sums over
+ * rows are formed in an order that depends on the sizes alone.  N == 0: dgamma
+ * and dbeta are written as zeros.  Workspace (256-byte aligned):
+ * layernorm_grad_workspace_size.  Kernels only, graph-capturable.
+ * Errors as for layernorm_run (dx must not overlap any input), and
+ * LL_ERR_WORKSPACE.
+ */
+typedef struct {
+  int64_t N, D;
+  int64_t stride_dy, stride_x, stride_dx;
+  int32_t type, param_type; /* ll_dtype */
+} layernorm_grad_desc;
+
+ll_status layernorm_grad_workspace_size(const layernorm_grad_desc* desc, size_t* bytes);
+ll_status layernorm_grad_run(const layernorm_grad_desc* desc, const void* dy, const void* x, const void* gamma,
+                             const float* mean, const float* rstd, void* dx, void* dgamma, void* dbeta,
+                             void* workspace, size_t ws_bytes, void* stream);
 
 /* Static, human-readable name of a status code ("LL_OK", ...). */
 const char* ll_status_string(ll_status s);

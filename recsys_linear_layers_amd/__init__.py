@@ -33,6 +33,7 @@ LL_FLAG_PACK_B = 0x2
 LL_FLAG_PRODUCER_CONSUMER = 0x4
 LL_FLAG_COOPERATIVE = 0x8
 LL_LINCOMP_NO_DEDUP = 0x1
+LL_EMBED_ACCUMULATE = 0x1
 
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
@@ -64,6 +65,27 @@ class LincompRaggedDesc(ctypes.Structure):
                 ("y_type", ctypes.c_int32), ("flags", ctypes.c_uint32), ("epilogue", ctypes.c_uint32)]
 
 
+class EmbedDesc(ctypes.Structure):
+    _fields_ = [("V", _i64), ("T", _i64), ("D", _i64), ("stride_table", _i64), ("stride_out", _i64),
+                ("type", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class EmbedGradDesc(ctypes.Structure):
+    _fields_ = [("V", _i64), ("T", _i64), ("D", _i64), ("stride_dout", _i64), ("stride_dtable", _i64),
+                ("padding_id", _i64), ("type", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
+
+
+class LayernormDesc(ctypes.Structure):
+    _fields_ = [("N", _i64), ("D", _i64), ("stride_x", _i64), ("stride_y", _i64),
+                ("type", ctypes.c_int32), ("param_type", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class LayernormGradDesc(ctypes.Structure):
+    _fields_ = [("N", _i64), ("D", _i64), ("stride_dy", _i64), ("stride_x", _i64), ("stride_dx", _i64),
+                ("type", ctypes.c_int32), ("param_type", ctypes.c_int32)]
+
+
 _lib.ll_status_string.restype = ctypes.c_char_p
 _lib.ll_status_string.argtypes = [ctypes.c_int]
 _lib.ll_last_error.restype = ctypes.c_char_p
@@ -80,9 +102,16 @@ _lib.lincomp_run.argtypes = [ctypes.POINTER(LincompDesc), _vp, _vp, _vp, _vp, _v
 _lib.lincomp_ragged_run.argtypes = [ctypes.POINTER(LincompRaggedDesc), _vp, _vp, _vp, _vp, _vp, _vp]
 _lib.lincomp_run_ex.argtypes = [ctypes.POINTER(LincompDesc), _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
 _lib.lincomp_ragged_run_ex.argtypes = [ctypes.POINTER(LincompRaggedDesc), _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+_lib.embed_run.argtypes = [ctypes.POINTER(EmbedDesc), _vp, _vp, _vp, _vp]
+_lib.embed_grad_workspace_size.argtypes = [ctypes.POINTER(EmbedGradDesc), ctypes.POINTER(ctypes.c_size_t)]
+_lib.embed_grad_run.argtypes = [ctypes.POINTER(EmbedGradDesc), _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+_lib.layernorm_run.argtypes = [ctypes.POINTER(LayernormDesc), *[_vp] * 7]
+_lib.layernorm_grad_workspace_size.argtypes = [ctypes.POINTER(LayernormGradDesc), ctypes.POINTER(ctypes.c_size_t)]
+_lib.layernorm_grad_run.argtypes = [ctypes.POINTER(LayernormGradDesc), *[_vp] * 9, ctypes.c_size_t, _vp]
 for _f in ("gemm_plan_create", "gemm_plan_workspace_size", "gemm_plan_describe", "gemm_run", "gemm_run_ex",
            "gemm_run_noalloc", "gemm_plan_destroy", "lincomp_workspace_size", "lincomp_run", "lincomp_ragged_run",
-           "lincomp_run_ex", "lincomp_ragged_run_ex"):
+           "lincomp_run_ex", "lincomp_ragged_run_ex", "embed_run", "embed_grad_workspace_size", "embed_grad_run",
+           "layernorm_run", "layernorm_grad_workspace_size", "layernorm_grad_run"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 
@@ -173,6 +202,38 @@ def lincomp_ragged_run_ex(desc: LincompRaggedDesc, offsets: int, user: int, item
                           Y: int, stream: int = 0) -> None:
     _check(_lib.lincomp_ragged_run_ex(ctypes.byref(desc), offsets, user, item, W, bias, Y, stream),
            "lincomp_ragged_run_ex")
+
+
+def embed_run(desc: EmbedDesc, table: int, ids: int, out: int, stream: int = 0) -> None:
+    _check(_lib.embed_run(ctypes.byref(desc), table, ids, out, stream), "embed_run")
+
+
+def embed_grad_workspace_size(desc: EmbedGradDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.embed_grad_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "embed_grad_workspace_size")
+    return n.value
+
+
+def embed_grad_run(desc: EmbedGradDesc, ids: int, dout: int, dtable: int, workspace: int, ws_bytes: int,
+                   stream: int = 0) -> None:
+    _check(_lib.embed_grad_run(ctypes.byref(desc), ids, dout, dtable, workspace, ws_bytes, stream), "embed_grad_run")
+
+
+def layernorm_run(desc: LayernormDesc, x: int, gamma: int | None, beta: int | None, y: int, mean: int | None,
+                  rstd: int | None, stream: int = 0) -> None:
+    _check(_lib.layernorm_run(ctypes.byref(desc), x, gamma, beta, y, mean, rstd, stream), "layernorm_run")
+
+
+def layernorm_grad_workspace_size(desc: LayernormGradDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.layernorm_grad_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "layernorm_grad_workspace_size")
+    return n.value
+
+
+def layernorm_grad_run(desc: LayernormGradDesc, dy: int, x: int, gamma: int | None, mean: int, rstd: int, dx: int,
+                       dgamma: int | None, dbeta: int | None, workspace: int, ws_bytes: int, stream: int = 0) -> None:
+    _check(_lib.layernorm_grad_run(ctypes.byref(desc), dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace,
+                                   ws_bytes, stream), "layernorm_grad_run")
 
 
 # ---------------------------------------------------------------------------
@@ -375,3 +436,150 @@ def lincomp_ragged(user, item, W, offsets, out=None, out_dtype=None, flags: int 
     lincomp_ragged_run_ex(desc, offsets.data_ptr(), user.data_ptr(), item.data_ptr(), W.data_ptr(),
                           bias.data_ptr() if bias is not None else None, out.data_ptr(), stream)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Operators around the linear layers.  Workspaces: one buffer per device and
+# stream, grown to the largest call; calls on one stream run one after the
+# other, so they can share it.
+# ---------------------------------------------------------------------------
+
+_op_ws: dict = {}
+
+
+def _stream_of(t):
+    return _torch().cuda.current_stream(t.device).cuda_stream
+
+
+def _op_workspace(device, stream: int, need: int):
+    torch = _torch()
+    key = (device.index, stream)
+    ws = _op_ws.get(key)
+    if ws is None or ws.numel() < need:
+        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+        _op_ws[key] = ws
+    return ws
+
+
+def _rows(t, what: str):
+    """Row stride of a 2-D tensor whose last dimension is contiguous (one of a
+    single row or column may have any stride)."""
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be 2-D")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: last dimension must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _vector(t, n: int, what: str, dtypes):
+    if tuple(t.shape) != (n,) or t.dtype not in dtypes or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous tensor of {n} values ({', '.join(map(str, dtypes))})")
+
+
+def _same_device(*ts) -> None:
+    dev = ts[0].device
+    for t in ts[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors on different devices: {dev}, {t.device}")
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def embedding(table, ids, scale: float = 1.0, out=None):
+    """out[t] = scale * table[ids[t]] for table [V][D] (bf16, fp16 or fp32, any row
+    stride) and int64 ids [T]; an id outside [0, V) gives a row of zeros."""
+    torch = _torch()
+    _vector(ids, ids.numel(), "ids", (torch.int64,))
+    (V, D), T = table.shape, ids.shape[0]
+    if out is None:
+        out = torch.empty((T, D), dtype=table.dtype, device=table.device)
+    if tuple(out.shape) != (T, D) or out.dtype != table.dtype:
+        raise ValueError("out must be [T][D] of the table's type")
+    _same_device(table, ids, out)
+    desc = EmbedDesc(V, T, D, _rows(table, "table"), _rows(out, "out"), _dtype_code(table.dtype), scale)
+    embed_run(desc, table.data_ptr(), ids.data_ptr(), out.data_ptr(), _stream_of(table))
+    return out
+
+
+def embedding_grad(ids, dout, rows: int, scale: float = 1.0, padding_idx: int | None = None, out=None,
+                   accumulate: bool = False):
+    """Dense gradient of ``embedding`` with respect to a table of ``rows`` rows:
+    scale times the sum of dout's rows per id.  Tokens with padding_idx or an id
+    outside the table contribute nothing.  accumulate: add to ``out``."""
+    torch = _torch()
+    _vector(ids, ids.numel(), "ids", (torch.int64,))
+    T, D = dout.shape
+    if ids.shape[0] != T:
+        raise ValueError("ids and dout differ in length")
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate needs out")
+        out = torch.empty((rows, D), dtype=dout.dtype, device=dout.device)
+    if tuple(out.shape) != (rows, D) or out.dtype != dout.dtype:
+        raise ValueError("out must be [rows][D] of dout's type")
+    if padding_idx is not None and padding_idx < 0:
+        raise ValueError("padding_idx must not be negative")
+    _same_device(dout, ids, out)
+    desc = EmbedGradDesc(rows, T, D, _rows(dout, "dout"), _rows(out, "out"), -1 if padding_idx is None else padding_idx,
+                         _dtype_code(dout.dtype), scale, LL_EMBED_ACCUMULATE if accumulate else 0)
+    stream = _stream_of(dout)
+    ws = _op_workspace(dout.device, stream, embed_grad_workspace_size(desc))
+    embed_grad_run(desc, ids.data_ptr(), dout.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+    return out
+
+
+def _norm_params(x, *params):
+    """param_type of gamma and beta (None: ones, zeros)."""
+    given = [p for p in params if p is not None]
+    for p in given:
+        _vector(p, x.shape[1], "gamma and beta", (x.dtype, _torch().float32))
+        if p.dtype != given[0].dtype:
+            raise ValueError("gamma and beta must have one type")
+    return given[0].dtype if given else x.dtype
+
+
+def layernorm(x, gamma=None, beta=None, eps: float = 1e-5, out=None):
+    """y = (x - mean) * rstd * gamma + beta over the rows of x [N][D] (bf16, fp16 or
+    fp32, any row stride); gamma, beta [D] of x's type or fp32, or None.  Returns
+    (y, mean, rstd), the latter fp32 [N], which layernorm_grad takes."""
+    torch = _torch()
+    N, D = x.shape
+    if out is None:
+        out = torch.empty((N, D), dtype=x.dtype, device=x.device)
+    if tuple(out.shape) != (N, D) or out.dtype != x.dtype:
+        raise ValueError("out must be [N][D] of x's type")
+    ptype = _norm_params(x, gamma, beta)
+    _same_device(x, gamma, beta, out)
+    mean, rstd = torch.empty((2, N), dtype=torch.float32, device=x.device).unbind(0)
+    desc = LayernormDesc(N, D, _rows(x, "x"), _rows(out, "out"), _dtype_code(x.dtype), _dtype_code(ptype), eps)
+    layernorm_run(desc, x.data_ptr(), _ptr(gamma), _ptr(beta), out.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+                  _stream_of(x))
+    return out, mean, rstd
+
+
+def layernorm_grad(dy, x, mean, rstd, gamma=None, out=None, param_grads: bool = True):
+    """(dx, dgamma, dbeta) of ``layernorm`` from its input and the mean and rstd it
+    returned.  dgamma and dbeta have gamma's type (x's without gamma);
+    param_grads=False: dx alone, the others None."""
+    torch = _torch()
+    N, D = x.shape
+    if tuple(dy.shape) != (N, D) or dy.dtype != x.dtype:
+        raise ValueError("dy must have x's shape and type")
+    if out is None:
+        out = torch.empty((N, D), dtype=x.dtype, device=x.device)
+    if tuple(out.shape) != (N, D) or out.dtype != x.dtype:
+        raise ValueError("out must be [N][D] of x's type")
+    for t in (mean, rstd):
+        _vector(t, N, "mean and rstd", (torch.float32,))
+    ptype = _norm_params(x, gamma)
+    _same_device(x, dy, mean, rstd, gamma, out)
+    dgamma, dbeta = torch.empty((2, D), dtype=ptype, device=x.device).unbind(0) if param_grads else (None, None)
+    desc = LayernormGradDesc(N, D, _rows(dy, "dy"), _rows(x, "x"), _rows(out, "out"), _dtype_code(x.dtype),
+                             _dtype_code(ptype))
+    stream = _stream_of(x)
+    ws = _op_workspace(x.device, stream, layernorm_grad_workspace_size(desc) if param_grads else 0)
+    layernorm_grad_run(desc, dy.data_ptr(), x.data_ptr(), _ptr(gamma), mean.data_ptr(), rstd.data_ptr(),
+                       out.data_ptr(), _ptr(dgamma), _ptr(dbeta), ws.data_ptr(), ws.numel(), stream)
+    return out, dgamma, dbeta

@@ -43,8 +43,9 @@ def _run(cmd, verbose):
 # Units built with the compiler's default machine scheduler instead: the
 # linear-compression kernels are bound by HBM, not by their instruction
 # schedule, and iterative-ilp spilled their fused-epilogue instantiations
-# (bias + GELU 34 registers against 10).
-DEFAULT_SCHED = {"lincomp.hip"}
+# (bias + GELU 34 registers against 10).  The embedding, layer norm and
+# cross-entropy row kernels are bound by HBM too.
+DEFAULT_SCHED = {"lincomp.hip", "embed.hip", "layernorm.hip", "xent.hip"}
 
 
 def _flags(src):

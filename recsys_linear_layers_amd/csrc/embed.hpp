@@ -1,0 +1,48 @@
+// Embedding lookup and its gradient: arguments and launches (embed.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace ll {
+
+struct EmbedArgs {
+  const void* table;
+  const int64_t* ids;
+  void* out;
+  int64_t V, ldt, ldo;
+  int32_t T, D;
+  float scale;
+};
+
+// Sorted positions per chunk whose sum is formed once, ahead of the rows, when
+// the whole chunk belongs to one row.
+constexpr int kEmbedChunk = 64;
+// Tokens up to which the rows find their tokens by themselves, without a sort.
+constexpr int kEmbedDirect = 512;
+// Tokens per workgroup of the sort, and its most digit values per pass.
+constexpr int kSortItems = 2048;
+constexpr int kSortMaxBits = 10;
+
+struct EmbedGradArgs {
+  const int64_t* ids;
+  const void* dout;
+  void* dw;
+  int64_t V, ldg, ldw;
+  int64_t padding;  // id without a gradient, or -1
+  int32_t T, D;
+  int32_t accumulate;
+  float scale;
+  // workspace (null when T <= kEmbedDirect)
+  uint32_t* key[2];
+  uint32_t* pos[2];
+  uint32_t* hist;   // [sort workgroups][1 << bits]
+  int2* seg;        // [V] sorted positions first, last + 1 of each row's tokens
+  float* partial;   // [T / kEmbedChunk][D] sums of whole chunks
+  int32_t bits, passes;
+};
+
+hipError_t launch_embed(const EmbedArgs& a, int type, hipStream_t s);
+hipError_t launch_embed_grad(const EmbedGradArgs& a, int type, int cus, hipStream_t s);
+
+}  // namespace ll

@@ -1,0 +1,428 @@
+// Layer norm y = (x - mean) * rstd * gamma + beta over the D columns of each
+// row, rstd = 1 / sqrt(var + eps), and its gradients
+//   h = dy * gamma,  xhat = (x - mean) * rstd,
+//   dx = rstd * (h - mean_D(h) - xhat * mean_D(h * xhat)),
+//   dgamma = sum over rows of dy * xhat,  dbeta = sum over rows of dy.
+//
+// Both are HBM bound: a row is read once and held in registers, so the mean,
+// the variance around that mean (two passes over registers: no cancellation)
+// and the output need no second read.  The gradient keeps the column sums of
+// dgamma and dbeta in fp32 registers over all rows a workgroup visits; one
+// partial row per workgroup goes to the workspace and a second kernel adds
+// them in a fixed order, so the result does not depend on timing.
+#include "layernorm.hpp"
+
+#include <algorithm>
+
+#include "ops_common.hpp"
+
+namespace ll {
+
+// Parameter column chunk as fp32, stored as TY or (param_f32) as fp32.
+template <int TY, int VEC>
+__device__ __forceinline__ void load_param(const void* p, int param_f32, int c, float dflt, float (&v)[VEC]) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = dflt;
+  } else if (TY == LL_F32 || param_f32) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = ((const float*)p)[(int64_t)c * VEC + i];
+  } else {
+    const typename Elem<TY>::raw* q = (const typename Elem<TY>::raw*)p + (int64_t)c * VEC;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] = Elem<TY>::get(q[i]);
+  }
+}
+
+// Sum over the TPR lanes of one row (64: one wave; more: the row's waves,
+// through red, two floats per wave of the workgroup).
+template <int TPR, int WAVES>
+__device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
+  a = lanes_sum<64>(a);
+  b = lanes_sum<64>(b);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    const int wave = threadIdx.x >> 6;
+    __syncthreads();  // red may still be read for the sums before
+    if ((threadIdx.x & 63) == 0) {
+      red[2 * wave] = a;
+      red[2 * wave + 1] = b;
+    }
+    __syncthreads();
+    const int w0 = wave / W * W;
+    a = 0.f;
+    b = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      a += red[2 * (w0 + w)];
+      b += red[2 * (w0 + w) + 1];
+    }
+  }
+}
+
+// TPR lanes hold a row in NCH chunks of VEC columns each; THREADS / TPR rows
+// per workgroup and step.
+template <int TY, int VEC, int TPR, int NCH, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
+  typedef Chunk<TY, VEC> C;
+  typedef typename Elem<TY>::raw raw;
+  __shared__ float red[THREADS / 64 * 2];
+  constexpr int ROWS = THREADS / TPR;
+  const int x = threadIdx.x % TPR, y = threadIdx.x / TPR;
+  const int chunks = a.D / VEC;
+  const float cols = (float)a.D;
+  // every row group takes part in each step's barriers, rows past N as zeros
+  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += (int64_t)gridDim.x * ROWS) {
+    const int64_t r = r0 + y;
+    const bool live = r < a.N;
+    C v[NCH];
+    const C* src = (const C*)((const raw*)a.x + r * a.ldx);
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int c = x + k * TPR;
+      if (live && c < chunks) v[k] = src[c];
+      else
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) v[k].e[i] = 0;
+    }
+    float s = 0.f, q = 0.f;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k)
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) s += v[k].get(i);
+    row_sum2<TPR, THREADS / 64>(s, q, red);
+    const float mean = s / cols;
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k)
+      if (x + k * TPR < chunks) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          const float d = v[k].get(i) - mean;
+          s = fmaf(d, d, s);
+        }
+      }
+    row_sum2<TPR, THREADS / 64>(s, q, red);
+    const float rstd = 1.f / sqrtf(s / cols + a.eps);
+    if (!live) continue;
+    C* dst = (C*)((raw*)a.y + r * a.ldy);
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int c = x + k * TPR;
+      if (c >= chunks) continue;
+      float g[VEC], b[VEC];
+      load_param<TY, VEC>(a.gamma, a.param_f32, c, 1.f, g);
+      load_param<TY, VEC>(a.beta, a.param_f32, c, 0.f, b);
+      C o;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) o.put(i, fmaf((v[k].get(i) - mean) * rstd, g[i], b[i]));
+      dst[c] = o;
+    }
+    if (x == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+  }
+}
+
+template <int TY, int VEC, int TPR, int NCH, int THREADS>
+static hipError_t norm_go(const NormArgs& a, int cus, hipStream_t s) {
+  constexpr int ROWS = THREADS / TPR;
+  const int64_t blocks = std::min<int64_t>((a.N + ROWS - 1) / ROWS, (int64_t)cus * 64);
+  hipLaunchKernelGGL((norm_kernel<TY, VEC, TPR, NCH, THREADS>), dim3((unsigned)blocks), dim3(THREADS), 0, s, a);
+  return hipGetLastError();
+}
+
+// Rows too wide for registers: one workgroup per row, three passes over it
+// (the second and third mostly from L2).
+template <int TY>
+__global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
+  typedef Chunk<TY, 1> C;
+  typedef typename Elem<TY>::raw raw;
+  __shared__ float red[32];
+  const float cols = (float)a.D;
+  for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
+    const C* src = (const C*)((const raw*)a.x + r * a.ldx);
+    float s = 0.f, q = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += 1024) s += src[c].get(0);
+    row_sum2<1024, 16>(s, q, red);
+    const float mean = s / cols;
+    s = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += 1024) {
+      const float d = src[c].get(0) - mean;
+      s = fmaf(d, d, s);
+    }
+    row_sum2<1024, 16>(s, q, red);
+    const float rstd = 1.f / sqrtf(s / cols + a.eps);
+    C* dst = (C*)((raw*)a.y + r * a.ldy);
+    for (int c = threadIdx.x; c < a.D; c += 1024) {
+      float g[1], b[1];
+      load_param<TY, 1>(a.gamma, a.param_f32, c, 1.f, g);
+      load_param<TY, 1>(a.beta, a.param_f32, c, 0.f, b);
+      C o;
+      o.put(0, fmaf((src[c].get(0) - mean) * rstd, g[0], b[0]));
+      dst[c] = o;
+    }
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+  }
+}
+
+// Columns a lane holds grow with the row, up to 32 where they move 16 bytes at
+// a time and 16 where they move one by one, before more lanes take part.
+template <int TY, int VEC>
+static hipError_t launch_norm_t(const NormArgs& a, int cus, hipStream_t s) {
+  const int chunks = a.D / VEC;
+  constexpr int K = (VEC > 1 ? 32 : 16) / VEC;
+  if (chunks <= 64) return norm_go<TY, VEC, 64, 1, 256>(a, cus, s);
+  if (chunks <= 64 * (K / 2)) return norm_go<TY, VEC, 64, K / 2, 256>(a, cus, s);
+  if (chunks <= 256 * (K / 2)) return norm_go<TY, VEC, 256, K / 2, 256>(a, cus, s);
+  if (chunks <= 256 * K) return norm_go<TY, VEC, 256, K, 256>(a, cus, s);
+  if (a.D <= 16384) return norm_go<TY, VEC, 1024, 16 / VEC, 1024>(a, cus, s);
+  const int64_t blocks = std::min<int64_t>(a.N, (int64_t)cus * 64);
+  hipLaunchKernelGGL((norm_long_kernel<TY>), dim3((unsigned)blocks), dim3(1024), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm(const NormArgs& a, int type, int cus, hipStream_t s) {
+  const bool wide = wide_rows(a.x, a.ldx, a.D, type) && wide_rows(a.y, a.ldy, a.D, type);
+  switch (type) {
+    case LL_BF16: return wide ? launch_norm_t<LL_BF16, 8>(a, cus, s) : launch_norm_t<LL_BF16, 1>(a, cus, s);
+    case LL_F16: return wide ? launch_norm_t<LL_F16, 8>(a, cus, s) : launch_norm_t<LL_F16, 1>(a, cus, s);
+    case LL_F32: return wide ? launch_norm_t<LL_F32, 4>(a, cus, s) : launch_norm_t<LL_F32, 1>(a, cus, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients
+// ---------------------------------------------------------------------------
+
+// Row r of step k of workgroup b: consecutive rows over the workgroups.  A
+// lane's column sums stay in registers over all its rows; the row groups of a
+// workgroup (THREADS / TPR) add theirs up at the end, in order, through LDS.
+template <int TY, int VEC, int TPR, int NCH, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradArgs a) {
+  typedef Chunk<TY, VEC> C;
+  typedef typename Elem<TY>::raw raw;
+  constexpr int ROWS = THREADS / TPR;
+  __shared__ float red[THREADS / 64 * 2];
+  __shared__ float col[ROWS > 1 ? THREADS * VEC : 1];
+  const int x = threadIdx.x % TPR, y = threadIdx.x / TPR;
+  const int chunks = a.D / VEC;
+  const float cols = (float)a.D;
+  float dg[NCH][VEC], db[NCH][VEC];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) dg[k][i] = db[k][i] = 0.f;
+  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += (int64_t)gridDim.x * ROWS) {
+    const int64_t r = r0 + y;
+    const bool live = r < a.N;
+    C vx[NCH], vd[NCH];
+    const C* sx = (const C*)((const raw*)a.x + r * a.ldx);
+    const C* sd = (const C*)((const raw*)a.dy + r * a.lddy);
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int c = x + k * TPR;
+      if (live && c < chunks) {
+        vx[k] = sx[c];
+        vd[k] = sd[c];
+      } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) vx[k].e[i] = vd[k].e[i] = 0;
+      }
+    }
+    const float mean = live ? a.mean[r] : 0.f, rstd = live ? a.rstd[r] : 0.f;
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int c = x + k * TPR;
+      if (c >= chunks) continue;
+      float g[VEC];
+      load_param<TY, VEC>(a.gamma, a.param_f32, c, 1.f, g);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float d = vd[k].get(i), n = (vx[k].get(i) - mean) * rstd;
+        const float h = d * g[i];
+        s1 += h;
+        s2 = fmaf(h, n, s2);
+        dg[k][i] = fmaf(d, n, dg[k][i]);
+        db[k][i] += d;
+      }
+    }
+    row_sum2<TPR, THREADS / 64>(s1, s2, red);
+    if (!live) continue;
+    const float m1 = s1 / cols, m2 = s2 / cols;
+    C* dst = (C*)((raw*)a.dx + r * a.lddx);
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int c = x + k * TPR;
+      if (c >= chunks) continue;
+      float g[VEC];
+      load_param<TY, VEC>(a.gamma, a.param_f32, c, 1.f, g);
+      C o;
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) {
+        const float h = vd[k].get(i) * g[i], n = (vx[k].get(i) - mean) * rstd;
+        o.put(i, (h - m1 - n * m2) * rstd);
+      }
+      dst[c] = o;
+    }
+  }
+  if (!a.partial) return;
+  float* out = a.partial + (int64_t)blockIdx.x * 2 * a.D;
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) {
+    const int c = x + k * TPR;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      float v[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = which ? db[k][i] : dg[k][i];
+      if constexpr (ROWS > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) col[i * THREADS + threadIdx.x] = v[i];
+        __syncthreads();
+        if (y == 0) {
+#pragma unroll
+          for (int w = 1; w < ROWS; ++w)
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] += col[i * THREADS + w * TPR + x];
+        }
+      }
+      if (y == 0 && c < chunks) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) out[(int64_t)which * a.D + (int64_t)c * VEC + i] = v[i];
+      }
+    }
+  }
+}
+
+// Adds the partial rows: 64 columns per workgroup, four waves taking a
+// quarter of the rows each, joined in order.
+template <int TY>
+__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* partial, int nblk, int D, void* dgamma,
+                                                          void* dbeta, int param_f32) {
+  __shared__ float red[4][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t col = (int64_t)blockIdx.x * 64 + lane;  // over both sums
+  float s = 0.f;
+  const int lo = nblk * w / 4, hi = nblk * (w + 1) / 4;
+  if (col < 2ll * D) {
+#pragma unroll 8
+    for (int k = lo; k < hi; ++k) s += partial[(int64_t)k * 2 * D + col];
+  }
+  red[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && col < 2ll * D) {
+    s = red[0][lane] + red[1][lane] + red[2][lane] + red[3][lane];
+    void* out = col < D ? dgamma : dbeta;
+    const int64_t c = col < D ? col : col - D;
+    if (TY == LL_F32 || param_f32) ((float*)out)[c] = s;
+    else ((typename Elem<TY>::raw*)out)[c] = Elem<TY>::put(s);
+  }
+}
+
+// Rows too wide for registers: dx one workgroup per row in two passes, and
+// the column sums in a kernel of their own, thread per column, workgroup y
+// taking every gridDim.y-th row.
+template <int TY>
+__global__ void __launch_bounds__(1024) norm_grad_long_kernel(const NormGradArgs a) {
+  typedef Chunk<TY, 1> C;
+  typedef typename Elem<TY>::raw raw;
+  __shared__ float red[32];
+  const float cols = (float)a.D;
+  for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x) {
+    const C* sx = (const C*)((const raw*)a.x + r * a.ldx);
+    const C* sd = (const C*)((const raw*)a.dy + r * a.lddy);
+    const float mean = a.mean[r], rstd = a.rstd[r];
+    float s1 = 0.f, s2 = 0.f;
+    for (int c = threadIdx.x; c < a.D; c += 1024) {
+      float g[1];
+      load_param<TY, 1>(a.gamma, a.param_f32, c, 1.f, g);
+      const float h = sd[c].get(0) * g[0];
+      s1 += h;
+      s2 = fmaf(h, (sx[c].get(0) - mean) * rstd, s2);
+    }
+    row_sum2<1024, 16>(s1, s2, red);
+    const float m1 = s1 / cols, m2 = s2 / cols;
+    C* dst = (C*)((raw*)a.dx + r * a.lddx);
+    for (int c = threadIdx.x; c < a.D; c += 1024) {
+      float g[1];
+      load_param<TY, 1>(a.gamma, a.param_f32, c, 1.f, g);
+      C o;
+      o.put(0, (sd[c].get(0) * g[0] - m1 - (sx[c].get(0) - mean) * rstd * m2) * rstd);
+      dst[c] = o;
+    }
+  }
+}
+
+template <int TY>
+__global__ void __launch_bounds__(256) norm_grad_columns_kernel(const NormGradArgs a) {
+  typedef typename Elem<TY>::raw raw;
+  const int c = blockIdx.x * 256 + threadIdx.x;
+  if (c >= a.D) return;
+  float dg = 0.f, db = 0.f;
+  for (int64_t r = blockIdx.y; r < a.N; r += gridDim.y) {
+    const float d = Elem<TY>::get(((const raw*)a.dy)[r * a.lddy + c]);
+    const float n = (Elem<TY>::get(((const raw*)a.x)[r * a.ldx + c]) - a.mean[r]) * a.rstd[r];
+    dg = fmaf(d, n, dg);
+    db += d;
+  }
+  float* out = a.partial + (int64_t)blockIdx.y * 2 * a.D;
+  out[c] = dg;
+  out[a.D + c] = db;
+}
+
+int norm_grad_blocks(int64_t N, int cus) { return (int)std::max<int64_t>(1, std::min<int64_t>(N, 2ll * cus)); }
+
+template <int TY, int VEC, int TPR, int NCH, int THREADS>
+static int norm_grad_go(const NormGradArgs& a, int cus, hipStream_t s) {
+  constexpr int ROWS = THREADS / TPR;
+  const int blocks = norm_grad_blocks((a.N + ROWS - 1) / ROWS, cus);
+  hipLaunchKernelGGL((norm_grad_kernel<TY, VEC, TPR, NCH, THREADS>), dim3(blocks), dim3(THREADS), 0, s, a);
+  return blocks;
+}
+
+template <int TY, int VEC>
+static hipError_t launch_norm_grad_t(const NormGradArgs& a, int cus, hipStream_t s) {
+  const int chunks = a.D / VEC;
+  constexpr int K = (VEC > 1 ? 32 : 16) / VEC;
+  int blocks;
+  if (chunks <= 64) blocks = norm_grad_go<TY, VEC, 64, 1, 256>(a, cus, s);
+  else if (chunks <= 64 * (K / 2)) blocks = norm_grad_go<TY, VEC, 64, K / 2, 256>(a, cus, s);
+  else if (chunks <= 64 * K) blocks = norm_grad_go<TY, VEC, 64, K, 256>(a, cus, s);
+  else if (chunks <= 256 * (K / 2)) blocks = norm_grad_go<TY, VEC, 256, K / 2, 256>(a, cus, s);
+  else if (chunks <= 256 * K) blocks = norm_grad_go<TY, VEC, 256, K, 256>(a, cus, s);
+  else if (a.D <= 16384) blocks = norm_grad_go<TY, VEC, 1024, 16 / VEC, 1024>(a, cus, s);
+  else {
+    const int64_t rows = std::min<int64_t>(a.N, (int64_t)cus * 64);
+    if (rows > 0)
+      hipLaunchKernelGGL((norm_grad_long_kernel<TY>), dim3((unsigned)rows), dim3(1024), 0, s, a);
+    blocks = norm_grad_blocks(a.N, cus);
+    if (a.partial)
+      hipLaunchKernelGGL((norm_grad_columns_kernel<TY>), dim3((a.D + 255) / 256, blocks), dim3(256), 0, s, a);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !a.partial) return e;
+  hipLaunchKernelGGL((norm_reduce_kernel<TY>), dim3((unsigned)((2ll * a.D + 63) / 64)), dim3(256), 0, s, a.partial,
+                     blocks, a.D, a.dgamma, a.dbeta, a.param_f32);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_grad(const NormGradArgs& a, int type, int cus, hipStream_t s) {
+  const bool wide = wide_rows(a.x, a.ldx, a.D, type) && wide_rows(a.dy, a.lddy, a.D, type) &&
+                    wide_rows(a.dx, a.lddx, a.D, type);
+  switch (type) {
+    case LL_BF16: return wide ? launch_norm_grad_t<LL_BF16, 8>(a, cus, s) : launch_norm_grad_t<LL_BF16, 1>(a, cus, s);
+    case LL_F16: return wide ? launch_norm_grad_t<LL_F16, 8>(a, cus, s) : launch_norm_grad_t<LL_F16, 1>(a, cus, s);
+    case LL_F32: return wide ? launch_norm_grad_t<LL_F32, 4>(a, cus, s) : launch_norm_grad_t<LL_F32, 1>(a, cus, s);
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace ll

@@ -11,16 +11,16 @@
 #include <string>
 
 #include "../../include/linlayers.h"
+#include "api.hpp"
 #include "kernels.hpp"
 #include "lincomp_kernel.hpp"
 
 using namespace ll;
 
-namespace {
+namespace ll {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
-ll_status fail(ll_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 ll_status fail(ll_status s, const char* fmt, ...) {
   char buf[512];
   va_list ap;
@@ -40,17 +40,9 @@ ll_status hip_fail(hipError_t e, const char* what) {
   return fail(LL_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
-struct DeviceInfo {
-  bool probed = false;
-  bool gfx950 = false;
-  int cus = 0;
-  char arch[64] = {0};
-};
+static std::mutex g_dev_mu;
+static DeviceInfo g_dev[64];
 
-std::mutex g_dev_mu;
-DeviceInfo g_dev[64];
-
-// Current device, its CU count, and whether it is gfx950.
 ll_status current_device(int* dev, const DeviceInfo** info) {
   int count = 0;
   hipError_t e = hipGetDeviceCount(&count);
@@ -74,8 +66,9 @@ ll_status current_device(int* dev, const DeviceInfo** info) {
   return LL_OK;
 }
 
-inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-inline size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+}  // namespace ll
+
+namespace {
 
 // The hand-ordered kind's tail split: at most this many K splits per tile of
 // a last round that is at most half full, each of at least this many slices.
@@ -125,51 +118,7 @@ constexpr int kRoundSyncMinSlices = 128;
 constexpr int64_t kPrefetchBMinStride = 16384;
 constexpr int kPrefetchBMinSlices = 128;
 
-// Byte extent [lo, hi) touched by a 2-D strided view of `rows` x `cols` elements.
-struct Span {
-  uintptr_t lo, hi;
-};
-Span span_of(const void* p, int64_t rows, int64_t cols, int64_t sr, int64_t sc, int64_t esize) {
-  const uintptr_t b = (uintptr_t)p;
-  const int64_t last = (rows - 1) * sr + (cols - 1) * sc;
-  return {b, b + (uintptr_t)((last + 1) * esize)};
-}
-bool overlaps(Span a, Span b) { return a.lo < b.hi && b.lo < a.hi; }
-
-// One operand as the kernel sees it.
-struct OperandPlan {
-  bool kmajor;      // K-contiguous as the kernel reads it (the original layout, or the packed copy's)
-  bool pack;        // copied into the workspace (layout below)
-  bool pack_mn;     // the packed copy is [K][ldp] (rows contiguous), else [rows][ldp] (K contiguous)
-  int64_t ldp;      // row stride of the packed copy: its row length rounded up to 64 elements, so
-                    // that every packed row starts on a 128-byte line
-  int64_t ld;       // leading dimension of the direct view
-  int64_t s_r, s_k; // original strides (rows = M or N)
-  size_t ws_off;    // workspace offset of the packed copy
-};
-
 }  // namespace
-
-struct gemm_plan {
-  gemm_desc d;
-  int device;
-  int cus;
-  int kind;
-  int layout;
-  OperandPlan a, b;
-  int64_t Kp;       // K rounded up to a multiple of 8
-  int splits;
-  int epi;          // fused-epilogue instantiation (0: none, or the split-K reduce applies it)
-  int kiters, kps;
-  int tiles_m, tiles_n, total, grid, group_m;
-  int round_sync;   // hand-ordered kind: round barrier per XCD (counters in the workspace)
-  int b_prefetch;   // hand-ordered kind: L2 prefetch of B's slice after the next
-  int tail_tiles, tail_splits, tail_kps, tail_first;  // hand-ordered kind: K-split last round
-  size_t ws_partial_off;
-  size_t ws_sync_off;
-  size_t ws_tail_off;
-  size_t ws_bytes;
-};
 
 namespace {
 
@@ -180,7 +129,7 @@ namespace {
 // load an N-contiguous B faster (64 k-rows of whole lines per slice instead
 // of 256 rows) and the 256x128 tile is indifferent to it.
 ll_status plan_operand(const char* name, int64_t rows, int64_t K, int64_t s_r, int64_t s_k, bool force_pack,
-                       bool prefer_mn, OperandPlan* op) {
+                       bool prefer_mn, bool padded, OperandPlan* op) {
   op->s_r = s_r;
   op->s_k = s_k;
   if (s_k == 1) {
@@ -200,10 +149,11 @@ ll_status plan_operand(const char* name, int64_t rows, int64_t K, int64_t s_r, i
   // is never read as out of range.
   bool direct = !force_pack && op->ld % 8 == 0;
   if (op->kmajor)
-    direct = direct && K % 8 == 0 && op->ld * 2 * 256 < (1ll << 30);
+    direct = direct && (padded || K % 8 == 0) && op->ld * 2 * 256 < (1ll << 30);
   else
-    direct = direct && rows % 8 == 0 && op->ld * 2 * kBK < (1ll << 30);
+    direct = direct && (padded || rows % 8 == 0) && op->ld * 2 * kBK < (1ll << 30);
   op->pack = !direct;
+  op->padded = direct && padded;
   op->pack_mn = op->pack && prefer_mn && round_up(rows, 64) * 2 * kBK < (1ll << 30);
   op->ldp = round_up(op->pack_mn ? rows : K, 64);
   if (op->pack) op->kmajor = !op->pack_mn;
@@ -231,6 +181,11 @@ void fill_operand_args(OperandArgs* oa, const void* ptr, const OperandPlan& op, 
     oa->ld = op.ldp;
     oa->kvalid = (int32_t)Kp;
     oa->extent = rows * op.ldp;
+  } else if (op.padded) {
+    oa->ptr = (const uint16_t*)ptr;
+    oa->ld = op.ld;
+    oa->kvalid = (int32_t)(op.kmajor ? Kp : K);
+    oa->extent = op.kmajor ? (rows - 1) * op.ld + round_up(K, 64) : (K - 1) * op.ld + round_up(rows, 64);
   } else {
     oa->ptr = (const uint16_t*)ptr;
     oa->ld = op.ld;
@@ -261,6 +216,18 @@ const char* ll_last_error(void) { return g_last_error.c_str(); }
 ll_status gemm_plan_create(gemm_plan** out, const gemm_desc* d) {
   if (!out || !d) return fail(LL_ERR_INVALID_ARG, "gemm_plan_create: null argument");
   *out = nullptr;
+  gemm_plan p;
+  const ll_status s = gemm_plan_build(d, 0, &p);
+  if (s != LL_OK) return s;
+  gemm_plan* h = new (std::nothrow) gemm_plan(p);
+  if (!h) return fail(LL_ERR_INVALID_ARG, "out of host memory");
+  *out = h;
+  return ok();
+}
+
+}  // extern "C"
+
+ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t padded, gemm_plan* out) {
   if (d->M < 0 || d->N < 0 || d->K < 0) return fail(LL_ERR_INVALID_ARG, "negative size");
   if (d->stride_am < 1 || d->stride_ak < 1 || d->stride_bk < 1 || d->stride_bn < 1 || d->stride_cm < 1 ||
       d->stride_cn < 1)
@@ -282,14 +249,16 @@ ll_status gemm_plan_create(gemm_plan** out, const gemm_desc* d) {
   gemm_plan p;
   memset(&p, 0, sizeof p);
   p.d = *d;
-  ll_status s = plan_operand("A", d->M, d->K, d->stride_am, d->stride_ak, d->flags & LL_FLAG_PACK_A, false, &p.a);
+  ll_status s = plan_operand("A", d->M, d->K, d->stride_am, d->stride_ak, d->flags & LL_FLAG_PACK_A, false,
+                             padded & kPaddedA, &p.a);
   if (s != LL_OK) return s;
   // A packed B is N-contiguous (above), except a B given K-contiguous beside a
   // K-contiguous A: its copy stays K-contiguous (a plain copy, not a
   // transpose) for the hand-ordered kind's variant for such a B (8191 x 5003
   // x 4099, column-major B with rows 4099 elements apart: 336 -> 329 us).
   const bool b_prefer_mn = !(d->stride_bk == 1 && p.a.kmajor);
-  s = plan_operand("B", d->N, d->K, d->stride_bn, d->stride_bk, d->flags & LL_FLAG_PACK_B, b_prefer_mn, &p.b);
+  s = plan_operand("B", d->N, d->K, d->stride_bn, d->stride_bk, d->flags & LL_FLAG_PACK_B, b_prefer_mn,
+                   padded & kPaddedB, &p.b);
   if (s != LL_OK) return s;
   // Any K-contiguous operand needs K padded to a multiple of 8; packed copies carry zeros there.
   p.Kp = round_up(d->K, 8);
@@ -331,15 +300,17 @@ ll_status gemm_plan_create(gemm_plan** out, const gemm_desc* d) {
   // the kernel reads it, spans less than 2 GB from its base.
   auto span_bytes = [&](const OperandPlan& op, int64_t rows) -> int64_t {
     if (op.pack) return (op.pack_mn ? d->K : rows) * op.ldp * 2;
+    if (op.padded) return (op.kmajor ? rows : d->K) * op.ld * 2;
     return (op.kmajor ? (rows - 1) * op.ld + d->K : (d->K - 1) * op.ld + rows) * 2;
   };
   // The hand-ordered kind loads whole 64-deep slices with no k mask.  With K
   // not a multiple of 64 that is still exact when every operand reads zeros
-  // past K: a packed copy (zero columns up to ldp, K rounded up to 64), or an
-  // M/N-contiguous operand, whose k-rows past K lie beyond its descriptor
-  // range.  A K-contiguous operand read in place would give its next row's
+  // past K: a packed copy or padded operand (zero columns up to K rounded up
+  // to 64), or an M/N-contiguous operand, whose k-rows past K lie beyond its
+  // descriptor range.  A K-contiguous operand read in place would give its next row's
   // values there, and an Inf or NaN among them would reach C.
-  const bool sq4_k_ok = d->K % 64 == 0 || ((!p.a.kmajor || p.a.pack) && (!p.b.kmajor || p.b.pack));
+  auto zeros_past_k = [](const OperandPlan& op) { return !op.kmajor || op.pack || op.padded; };
+  const bool sq4_k_ok = d->K % 64 == 0 || (zeros_past_k(p.a) && zeros_past_k(p.b));
   const bool sq4_fits = sq4_k_ok && span_bytes(p.a, M) < 0x7FFFFFF0ll && span_bytes(p.b, N) < 0x7FFFFFF0ll;
   if (free_choice && p.a.kmajor && (kind == KIND_WIDE_PC || kind == KIND_TALL_PC)) {
     const int64_t pb = passes(kind), pt = passes(KIND_T192_PC);
@@ -528,11 +499,11 @@ ll_status gemm_plan_create(gemm_plan** out, const gemm_desc* d) {
   if (p.tail_tiles > 0) off = align256(off + (size_t)p.tail_tiles * p.tail_splits * 256 * 256 * 4);
   p.ws_bytes = off;
 
-  gemm_plan* h = new (std::nothrow) gemm_plan(p);
-  if (!h) return fail(LL_ERR_INVALID_ARG, "out of host memory");
-  *out = h;
+  *out = p;
   return ok();
 }
+
+extern "C" {
 
 ll_status gemm_plan_workspace_size(const gemm_plan* p, size_t* bytes) {
   if (!p || !bytes) return fail(LL_ERR_INVALID_ARG, "null argument");
@@ -559,23 +530,20 @@ ll_status gemm_plan_destroy(gemm_plan* p) {
   return ok();
 }
 
-static ll_status gemm_run_impl(const gemm_plan* p, const void* A, const void* B, void* C, const float* bias,
-                               void* ws, size_t ws_bytes, void* stream);
-
 ll_status gemm_run_ex(const gemm_plan* p, const void* A, const void* B, void* C, const float* bias, void* ws,
                       size_t ws_bytes, void* stream) {
   if (!p) return fail(LL_ERR_INVALID_ARG, "null plan");
   const bool has_bias = p->d.epilogue & LL_EPI_BIAS;
   if (has_bias && !bias) return fail(LL_ERR_INVALID_ARG, "the plan's epilogue adds a bias: bias is null");
   if (has_bias && ((uintptr_t)bias & 3)) return fail(LL_ERR_INVALID_ARG, "bias must be 4-byte aligned");
-  return gemm_run_impl(p, A, B, C, has_bias ? bias : nullptr, ws, ws_bytes, stream);
+  return gemm_run_plan(p, A, B, C, has_bias ? bias : nullptr, ws, ws_bytes, stream);
 }
 
 ll_status gemm_run(const gemm_plan* p, const void* A, const void* B, void* C, void* ws, size_t ws_bytes,
                    void* stream) {
   if (p && (p->d.epilogue & LL_EPI_BIAS))
     return fail(LL_ERR_INVALID_ARG, "the plan's epilogue adds a bias: use gemm_run_ex");
-  return gemm_run_impl(p, A, B, C, nullptr, ws, ws_bytes, stream);
+  return gemm_run_plan(p, A, B, C, nullptr, ws, ws_bytes, stream);
 }
 
 // ---------------------------------------------------------------------------
@@ -629,12 +597,14 @@ ll_status gemm_run_noalloc(const gemm_plan* p, const void* A, const void* B, voi
     const ll_status s = scratch_on_device(dev, &ws);
     if (s != LL_OK) return s;
   }
-  return gemm_run_impl(p, A, B, C, has_bias ? bias : nullptr, ws, ws ? (size_t)LL_NOALLOC_SCRATCH_BYTES : 0,
+  return gemm_run_plan(p, A, B, C, has_bias ? bias : nullptr, ws, ws ? (size_t)LL_NOALLOC_SCRATCH_BYTES : 0,
                        stream);
 }
 
-static ll_status gemm_run_impl(const gemm_plan* p, const void* A, const void* B, void* C, const float* bias,
-                               void* ws, size_t ws_bytes, void* stream) {
+}  // extern "C"
+
+ll_status ll::gemm_run_plan(const gemm_plan* p, const void* A, const void* B, void* C, const float* bias, void* ws,
+                            size_t ws_bytes, void* stream) {
   if (!p) return fail(LL_ERR_INVALID_ARG, "null plan");
   const gemm_desc& d = p->d;
   if (d.M == 0 || d.N == 0) return ok();
@@ -733,6 +703,8 @@ static ll_status gemm_run_impl(const gemm_plan* p, const void* A, const void* B,
 // ---------------------------------------------------------------------------
 // Linear compression
 // ---------------------------------------------------------------------------
+
+extern "C" {
 
 static ll_status lincomp_check(const lincomp_desc* d, bool ragged = false) {
   if (!d) return fail(LL_ERR_INVALID_ARG, "null desc");

@@ -1,0 +1,62 @@
+// Element types and small device helpers shared by the memory-bound operators
+// (embedding, layer norm) and the cross entropy's row kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/linlayers.h"
+#include "gemm_kernel.hpp"
+
+namespace ll {
+
+// One element type (an ll_dtype code) as stored; every computation is in fp32.
+template <int TY>
+struct Elem;
+template <>
+struct Elem<LL_BF16> {
+  typedef uint16_t raw;
+  static __device__ __forceinline__ float get(uint16_t b) { return __builtin_bit_cast(float, (uint32_t)b << 16); }
+  static __device__ __forceinline__ uint16_t put(float v) { return f32_to_bf16_bits(v); }
+};
+template <>
+struct Elem<LL_F16> {
+  typedef uint16_t raw;
+  static __device__ __forceinline__ float get(uint16_t b) { return (float)__builtin_bit_cast(_Float16, b); }
+  static __device__ __forceinline__ uint16_t put(float v) { return f32_to_f16_bits(v); }
+};
+template <>
+struct Elem<LL_F32> {
+  typedef uint32_t raw;
+  static __device__ __forceinline__ float get(uint32_t b) { return __builtin_bit_cast(float, b); }
+  static __device__ __forceinline__ uint32_t put(float v) { return __builtin_bit_cast(uint32_t, v); }
+};
+
+// VEC consecutive elements moved by one load or store (aligned to their size).
+template <int TY, int VEC>
+struct alignas(sizeof(typename Elem<TY>::raw) * VEC) Chunk {
+  typename Elem<TY>::raw e[VEC];
+  __device__ __forceinline__ float get(int i) const { return Elem<TY>::get(e[i]); }
+  __device__ __forceinline__ void put(int i, float v) { e[i] = Elem<TY>::put(v); }
+};
+
+template <int TY>
+constexpr int kWide = 16 / (int)sizeof(typename Elem<TY>::raw);  // elements of a 16-byte access
+
+inline int dtype_size(int ty) { return ty == LL_F32 ? 4 : 2; }
+
+// Whether rows of D elements at `ld` apart starting at `p` can be moved 16 bytes at a time.
+inline bool wide_rows(const void* p, int64_t ld, int64_t D, int ty) {
+  const int64_t v = 16 / dtype_size(ty);
+  return ((uintptr_t)p & 15) == 0 && ld % v == 0 && D % v == 0;
+}
+
+// Sum over aligned groups of W lanes (a power of two up to 64); every lane gets it.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int m = 1; m < W; m <<= 1) v += __shfl_xor(v, m, 64);
+  return v;
+}
+
+}  // namespace ll

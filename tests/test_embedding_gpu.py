@@ -1,0 +1,245 @@
+"""Embedding lookup and its gradient against their definitions in 64 bits.
+
+Tolerances, with u = 2^-24 and h = eps(type) / 2 (half a step of the stored
+type): the lookup rounds the fp32 product once (u, none for fp32 storage) and
+the stored value once (h).  The gradient's n terms are added in fp32 in some
+order (at most n - 1 roundings of partial sums no larger than S = sum |terms|),
+scaled, added to the old value where it accumulates, and stored once.  fp16
+values below its normal range are off by up to 2^-25."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+TYPES = ["bfloat16", "float16", "float32"]
+
+
+def _ll():
+    import recsys_linear_layers_amd as ll
+    return ll
+
+
+def _half(dt):
+    import torch
+    return torch.finfo(dt).eps / 2
+
+
+def _tiny(dt):
+    import torch
+    return 2.0 ** -25 if dt == torch.float16 else 0.0
+
+
+def _within(got, ref, tol, what):
+    import torch
+    err = (got.double() - ref).abs()
+    assert bool(torch.isfinite(got).all()), what
+    worst = (err / tol.clamp_min(1e-300)).max().item() if err.numel() else 0.0
+    assert bool((err <= tol).all()), f"{what}: err/tol {worst:.3g}"
+
+
+def _strided(rows, cols, pad, dt, g):
+    import torch
+    return torch.randn((rows, cols + pad), generator=g, device="cuda", dtype=torch.float32).to(dt)[:, :cols]
+
+
+def _gen(seed):
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V,D,pad", [(1, 1, 1, 0), (1, 7, 64, 0), (3, 100, 8, 8), (65, 1000, 1001, 0),
+                                       (257, 50, 4096, 0), (1000, 3001, 130, 3), (70000, 33, 16, 0), (5, 9, 20000, 0)])
+def test_lookup(dtype, T, V, D, pad):
+    import torch
+    ll = _ll()
+    dt, g = getattr(torch, dtype), _gen(T + D)
+    table = _strided(V, D, pad, dt, g)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    for scale in (1.0, 11.3):
+        out = ll.embedding(table, ids, scale=scale)
+        s32 = torch.tensor(scale, dtype=torch.float32).double().item()
+        ref = table[ids].double() * s32
+        assert out.shape == (T, D) and out.dtype == dt
+        _within(out, ref, ref.abs() * ((_half(dt) + U) * 1.01) + _tiny(dt), f"{dtype} {T}x{V}x{D}")
+        if scale == 1.0:
+            assert torch.equal(out, table[ids])
+
+
+def test_lookup_of_ids_outside_the_table_gives_zeros_and_reads_nothing_else():
+    import torch
+    ll = _ll()
+    table = torch.full((10, 24), float("nan"), device="cuda")
+    table[3] = 1.5
+    ids = torch.tensor([3, -1, 10, -(2 ** 62), 2 ** 62, 3], device="cuda")
+    out = ll.embedding(table, ids, scale=2.0)
+    want = torch.zeros((6, 24), device="cuda")
+    want[0] = want[5] = 3.0
+    assert torch.equal(out, want)
+    assert ll.embedding(table, ids[:0]).shape == (0, 24)
+
+
+def test_lookup_keeps_infinities_and_nan():
+    import torch
+    ll = _ll()
+    table = torch.tensor([[float("inf"), float("-inf"), float("nan"), 0.0]], device="cuda")
+    out = ll.embedding(table, torch.zeros(2, dtype=torch.int64, device="cuda"))
+    assert torch.equal(out.nan_to_num(7.0, 8.0, 9.0), table[[0, 0]].nan_to_num(7.0, 8.0, 9.0))
+
+
+def _grad_case(dtype, T, V, D, pad, ids, scale, padding, accumulate, g):
+    import torch
+    ll = _ll()
+    dt = getattr(torch, dtype)
+    dout = _strided(T, D, pad, dt, g)
+    old = _strided(V, D, pad, dt, g)
+    out = torch.full((V, D + pad), float("nan"), dtype=dt, device="cuda")[:, :D]
+    if accumulate:
+        out.copy_(old)
+    got = ll.embedding_grad(ids, dout, V, scale=scale, padding_idx=padding, out=out, accumulate=accumulate)
+    live = (ids >= 0) & (ids < V)
+    if padding is not None:
+        live &= ids != padding
+    s = torch.tensor(scale, dtype=torch.float32).double().item()
+    sums = torch.zeros((V, D), dtype=torch.float64, device="cuda").index_add_(0, ids[live], dout[live].double())
+    mags = torch.zeros((V, D), dtype=torch.float64, device="cuda").index_add_(0, ids[live], dout[live].double().abs())
+    n = torch.zeros(V, dtype=torch.float64, device="cuda").index_add_(
+        0, ids[live], torch.ones(int(live.sum()), dtype=torch.float64, device="cuda"))
+    ref, S = sums * s, mags * abs(s)
+    if accumulate:
+        ref, S = ref + old.double(), S + old.double().abs()
+    tol = ref.abs() * _half(dt) + (n[:, None] + 3) * U * S * (1 + 2 * _half(dt)) + _tiny(dt)
+    _within(got, ref, tol, f"grad {dtype} {T}x{V}x{D}")
+    untouched = n == 0
+    assert torch.equal(got[untouched], old[untouched] if accumulate else torch.zeros_like(old[untouched]))
+    again = ll.embedding_grad(ids, dout, V, scale=scale, padding_idx=padding,
+                              out=old.clone() if accumulate else None, accumulate=accumulate)
+    assert torch.equal(again, got), "equal inputs, other bits"
+
+
+# 512 tokens are summed without a sort, 513 with one; 2048 and 2049 fill and
+# overfill one workgroup of the sort
+SIZES = [(0, 5, 8, 0), (1, 1, 1, 0), (1, 300, 64, 0), (300, 77, 101, 0), (512, 33, 256, 8), (513, 33, 256, 0),
+         (2048, 1024, 40, 0), (2049, 1023, 40, 3), (9000, 2000, 136, 0), (9000, 3, 1040, 0), (5000, 70000, 8, 0),
+         (4000, 1100000, 4, 0), (1500, 10, 5003, 0)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,V,D,pad", SIZES)
+def test_gradient(dtype, T, V, D, pad):
+    import torch
+    g = _gen(T * 7 + D)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    _grad_case(dtype, T, V, D, pad, ids, 1.0, None, False, g)
+
+
+@pytest.mark.parametrize("T", [100, 512, 513, 6000, 20001])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_gradient_of_frequent_ids_padding_and_ids_outside(T, accumulate):
+    """Rows with hundreds to thousands of tokens (whole chunks of the sorted
+    order and loose ends on both sides), a padding id in between, ids outside."""
+    import torch
+    g = _gen(T)
+    V, D = 500, 72
+    u = torch.rand(T, generator=g, device="cuda")
+    ids = (u ** 4 * V).long()
+    ids[torch.rand(T, generator=g, device="cuda") < 0.2] = 7
+    ids[torch.rand(T, generator=g, device="cuda") < 0.1] = -3
+    ids[torch.rand(T, generator=g, device="cuda") < 0.1] = V
+    ids[torch.rand(T, generator=g, device="cuda") < 0.1] = 2 ** 40
+    for dtype in ("bfloat16", "float32"):
+        _grad_case(dtype, T, V, D, 0, ids, 0.37, 7, accumulate, g)
+
+
+@pytest.mark.parametrize("T", [500, 700, 64 * 33, 5000])
+def test_gradient_of_one_id(T):
+    import torch
+    g = _gen(T)
+    for v in (0, 4):
+        ids = torch.full((T,), v, dtype=torch.int64, device="cuda")
+        _grad_case("float16", T, 5, 520, 0, ids, 0.01, None, False, g)
+
+
+def test_padded_rows_may_hold_anything():
+    import torch
+    ll = _ll()
+    for T in (200, 3000):
+        ids = torch.arange(T, device="cuda") % 9
+        dout = torch.ones((T, 12), device="cuda")
+        dout[ids == 2] = float("nan")
+        dout[ids == 3] = float("inf")
+        ids[ids == 3] = 99
+        got = ll.embedding_grad(ids, dout, 9, padding_idx=2)
+        assert bool(torch.isfinite(got).all())
+        assert got[2].abs().max() == 0 and got[3].abs().max() == 0 and got[1, 0] == float((ids == 1).sum())
+
+
+def test_gradient_agrees_with_differences():
+    """d/dtable of sum(out * R) by central differences in 64 bits of the definition."""
+    import torch
+    ll = _ll()
+    g = _gen(5)
+    V, D, T, scale = 6, 5, 40, 1.75
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    table = torch.randn((V, D), generator=g, device="cuda", dtype=torch.float64)
+    R = torch.randn((T, D), generator=g, device="cuda")
+    f = lambda w: float((w[ids] * scale * R.double()).sum())  # noqa: E731
+    got = ll.embedding_grad(ids, R, V, scale=scale)
+    for v in range(V):
+        for d in range(D):
+            step = torch.zeros_like(table)
+            step[v, d] = 0.5  # the function is linear: differences are exact up to rounding
+            num = f(table + step) - f(table - step)
+            S = float(R[ids == v, d].abs().sum()) * scale
+            assert abs(num - float(got[v, d])) <= 45 * U * S + 1e-10
+
+
+def test_streams_and_graph():
+    """On another stream than the tensors', and captured: every replay the same."""
+    import torch
+    ll = _ll()
+    g = _gen(9)
+    for T in (300, 5000):
+        ids = torch.randint(0, 1000, (T,), generator=g, device="cuda")
+        dout = torch.randn((T, 96), generator=g, device="cuda")
+        table = torch.randn((1000, 96), generator=g, device="cuda")
+        want = ll.embedding_grad(ids, dout, 1000)
+        look = ll.embedding(table, ids, scale=3.0)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            out = torch.empty_like(want)
+            out2 = torch.empty_like(look)
+            ll.embedding_grad(ids, dout, 1000, out=out)
+            ll.embedding(table, ids, scale=3.0, out=out2)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(out2, look)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            ll.embedding_grad(ids, dout, 1000, out=out)
+            ll.embedding(table, ids, scale=3.0, out=out2)
+        for _ in range(3):
+            out.fill_(float("nan"))
+            out2.fill_(float("nan"))
+            torch.cuda.synchronize()
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(out2, look)
+            torch.randn(64, 64, device="cuda").sum().item()
+
+
+def test_table_beyond_2_to_31_elements():
+    """Row offsets pass 32 bits: the last rows of a table of 2.2e9 elements."""
+    import torch
+    ll = _ll()
+    V, D = 2 ** 20 + 3, 2112
+    table = torch.zeros((V, D), dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, V // 2, V - 2, V - 1], device="cuda")
+    table[rows] = torch.arange(1, 5, device="cuda", dtype=torch.bfloat16)[:, None].expand(4, D)
+    assert torch.equal(ll.embedding(table, rows), table[rows])
+    dout = torch.ones((4, D), dtype=torch.bfloat16, device="cuda")
+    got = ll.embedding_grad(rows, dout, V, scale=2.0)
+    assert torch.equal(got[rows], dout * 2) and float(got[V - 3].abs().max()) == 0
+    assert got.sum(dtype=torch.float32).item() == 8.0 * D
