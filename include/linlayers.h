@@ -26,6 +26,8 @@
  *  - embed_*, layernorm_*: what stands in front of a model's linear layers: the
  *               lookup of its tokens' (or items') rows and the norm of the
  *               activations, each with its gradients.
+ *  - xent_*   : what stands behind them: the softmax cross entropy over a
+ *               vocabulary, in pieces of the vocabulary, with its gradients.
  *
  * Conventions shared by every entry point:
  *
@@ -434,6 +436,71 @@ ll_status layernorm_grad_workspace_size(const layernorm_grad_desc* desc, size_t*
 ll_status layernorm_grad_run(const layernorm_grad_desc* desc, const void* dy, const void* x, const void* gamma,
                              const float* mean, const float* rstd, void* dx, void* dgamma, void* dbeta,
                              void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Softmax cross entropy of N rows against a vocabulary of V entries, in pieces
+ * of the vocabulary, without the [N][V] logits:
+ *   z = x w^T,  lse[i] = log sum_v exp(z[i][v]),  loss[i] = lse[i] - z[i][target[i]],
+ * and, for the gradient of sum_i dloss[i] * loss[i],
+ *   dz = (exp(z - lse) - onehot(target)) * dloss,  dx = dz w,  dw = dz^T x.
+ * x [N][D] and w [V][D] of `type` (LL_BF16 or LL_F16), rows stride_x and
+ * stride_w elements apart, last dimension contiguous (w stored as a linear
+ * layer's weight).  dx [N][D] and dw [V][D] of dx_type and dw_type (`type` or
+ * LL_F32), rows stride_dx and stride_dw apart; LL_XENT_DX and LL_XENT_DW say
+ * which are wanted (neither: the loss alone).
+ * A row whose target is ignore_index or outside [0, V) has no loss: loss, lse
+ * and its row of dx are zeros, and it adds nothing to dw, whatever it holds.
+ * Products are accumulated in fp32, row sums carried in fp32 with their
+ * maximum; dz is rounded to `type` (with fp16 after multiplication by a power
+ * of two, taken out again in fp32, so that small probabilities keep their
+ * bits), dx and dw once each.
+ * piece_bytes bounds the buffers that hold logits and dz (0: 2 GiB); when
+ * the whole vocabulary does not fit, it is cut into pieces of a multiple of
+ * 256 entries (at least one such), the logits of all but the last are formed
+ * again for the gradients.  w must be 16-byte aligned unless it is copied into
+ * the workspace: LL_XENT_PACK_W, or a D or stride_w not a multiple of 8, or
+ * D not a multiple of 64 with 512 rows or more.
+ */
+#define LL_XENT_DX 0x1u
+#define LL_XENT_DW 0x2u
+#define LL_XENT_PACK_W 0x4u
+
+typedef struct {
+  int64_t N, V, D;
+  int64_t stride_x, stride_w, stride_dx, stride_dw;
+  int64_t ignore_index;
+  int64_t piece_bytes;
+  int32_t type, dx_type, dw_type; /* ll_dtype */
+  uint32_t flags;                 /* LL_XENT_* */
+} xent_desc;
+
+typedef struct xent_plan xent_plan; /* opaque, host-side, immutable */
+
+/*
+ * Validate `desc` and choose pieces and products for the CURRENT HIP device.
+ * Errors: LL_ERR_INVALID_ARG (null argument, negative size, V or D of zero,
+ * stride below D, unknown flags), LL_ERR_UNSUPPORTED (types, N or V of 2^30 and
+ * more, D of 2^20 and more, device), LL_ERR_NO_DEVICE, LL_ERR_HIP.
+ * Argument checks run before any device query.
+ */
+ll_status xent_plan_create(xent_plan** out, const xent_desc* desc);
+ll_status xent_plan_workspace_size(const xent_plan* plan, size_t* bytes);
+/* One line: pieces, columns per piece, the kernels of the products. */
+ll_status xent_plan_describe(const xent_plan* plan, char* buf, size_t len);
+
+/*
+ * Loss (and gradients, if the plan has them) on `stream`.  target: N int64;
+ * dloss: N fp32, needed with gradients, ignored otherwise; loss: N fp32; lse:
+ * N fp32 or NULL; dx, dw as the plan's flags say.  N == 0: dw, if wanted, is
+ * written as zeros.  Kernels only: may be captured into a HIP graph.
+ * Errors: LL_ERR_INVALID_ARG (null or misaligned pointer, an output overlapping
+ * an input, the workspace or another output, current device differs from the
+ * plan's), LL_ERR_WORKSPACE, LL_ERR_HIP.
+ */
+ll_status xent_run(const xent_plan* plan, const void* x, const void* w, const int64_t* target, const float* dloss,
+                   float* loss, float* lse, void* dx, void* dw, void* workspace, size_t ws_bytes, void* stream);
+
+ll_status xent_plan_destroy(xent_plan* plan);
 
 /* Static, human-readable name of a status code ("LL_OK", ...). */
 const char* ll_status_string(ll_status s);

@@ -34,6 +34,7 @@ LL_FLAG_PRODUCER_CONSUMER = 0x4
 LL_FLAG_COOPERATIVE = 0x8
 LL_LINCOMP_NO_DEDUP = 0x1
 LL_EMBED_ACCUMULATE = 0x1
+LL_XENT_DX, LL_XENT_DW, LL_XENT_PACK_W = 0x1, 0x2, 0x4
 
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
@@ -86,6 +87,14 @@ class LayernormGradDesc(ctypes.Structure):
                 ("type", ctypes.c_int32), ("param_type", ctypes.c_int32)]
 
 
+class XentDesc(ctypes.Structure):
+    _fields_ = [("N", _i64), ("V", _i64), ("D", _i64),
+                ("stride_x", _i64), ("stride_w", _i64), ("stride_dx", _i64), ("stride_dw", _i64),
+                ("ignore_index", _i64), ("piece_bytes", _i64),
+                ("type", ctypes.c_int32), ("dx_type", ctypes.c_int32), ("dw_type", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
 _lib.ll_status_string.restype = ctypes.c_char_p
 _lib.ll_status_string.argtypes = [ctypes.c_int]
 _lib.ll_last_error.restype = ctypes.c_char_p
@@ -108,10 +117,16 @@ _lib.embed_grad_run.argtypes = [ctypes.POINTER(EmbedGradDesc), _vp, _vp, _vp, _v
 _lib.layernorm_run.argtypes = [ctypes.POINTER(LayernormDesc), *[_vp] * 7]
 _lib.layernorm_grad_workspace_size.argtypes = [ctypes.POINTER(LayernormGradDesc), ctypes.POINTER(ctypes.c_size_t)]
 _lib.layernorm_grad_run.argtypes = [ctypes.POINTER(LayernormGradDesc), *[_vp] * 9, ctypes.c_size_t, _vp]
+_lib.xent_plan_create.argtypes = [ctypes.POINTER(_vp), ctypes.POINTER(XentDesc)]
+_lib.xent_plan_workspace_size.argtypes = [_vp, ctypes.POINTER(ctypes.c_size_t)]
+_lib.xent_plan_describe.argtypes = [_vp, ctypes.c_char_p, ctypes.c_size_t]
+_lib.xent_run.argtypes = [*[_vp] * 10, ctypes.c_size_t, _vp]
+_lib.xent_plan_destroy.argtypes = [_vp]
 for _f in ("gemm_plan_create", "gemm_plan_workspace_size", "gemm_plan_describe", "gemm_run", "gemm_run_ex",
            "gemm_run_noalloc", "gemm_plan_destroy", "lincomp_workspace_size", "lincomp_run", "lincomp_ragged_run",
            "lincomp_run_ex", "lincomp_ragged_run_ex", "embed_run", "embed_grad_workspace_size", "embed_grad_run",
-           "layernorm_run", "layernorm_grad_workspace_size", "layernorm_grad_run"):
+           "layernorm_run", "layernorm_grad_workspace_size", "layernorm_grad_run", "xent_plan_create",
+           "xent_plan_workspace_size", "xent_plan_describe", "xent_run", "xent_plan_destroy"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 
@@ -234,6 +249,33 @@ def layernorm_grad_run(desc: LayernormGradDesc, dy: int, x: int, gamma: int | No
                        dgamma: int | None, dbeta: int | None, workspace: int, ws_bytes: int, stream: int = 0) -> None:
     _check(_lib.layernorm_grad_run(ctypes.byref(desc), dy, x, gamma, mean, rstd, dx, dgamma, dbeta, workspace,
                                    ws_bytes, stream), "layernorm_grad_run")
+
+
+def xent_plan_create(desc: XentDesc) -> int:
+    h = _vp()
+    _check(_lib.xent_plan_create(ctypes.byref(h), ctypes.byref(desc)), "xent_plan_create")
+    return h.value
+
+
+def xent_plan_workspace_size(plan: int) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.xent_plan_workspace_size(plan, ctypes.byref(n)), "xent_plan_workspace_size")
+    return n.value
+
+
+def xent_plan_describe(plan: int) -> str:
+    buf = ctypes.create_string_buffer(512)
+    _check(_lib.xent_plan_describe(plan, buf, 512), "xent_plan_describe")
+    return buf.value.decode()
+
+
+def xent_run(plan: int, x: int, w: int, target: int, dloss: int | None, loss: int, lse: int | None, dx: int | None,
+             dw: int | None, workspace: int, ws_bytes: int, stream: int = 0) -> None:
+    _check(_lib.xent_run(plan, x, w, target, dloss, loss, lse, dx, dw, workspace, ws_bytes, stream), "xent_run")
+
+
+def xent_plan_destroy(plan: int) -> None:
+    _check(_lib.xent_plan_destroy(plan), "xent_plan_destroy")
 
 
 # ---------------------------------------------------------------------------
@@ -583,3 +625,85 @@ def layernorm_grad(dy, x, mean, rstd, gamma=None, out=None, param_grads: bool = 
     layernorm_grad_run(desc, dy.data_ptr(), x.data_ptr(), _ptr(gamma), mean.data_ptr(), rstd.data_ptr(),
                        out.data_ptr(), _ptr(dgamma), _ptr(dbeta), ws.data_ptr(), ws.numel(), stream)
     return out, dgamma, dbeta
+
+
+class XentPlan:
+    """Owns one xent_plan."""
+
+    def __init__(self, desc: XentDesc):
+        self.desc = desc
+        self.handle = xent_plan_create(desc)
+        self.ws_bytes = xent_plan_workspace_size(self.handle)
+
+    def describe(self) -> str:
+        return xent_plan_describe(self.handle)
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h and _lib is not None:  # _lib is None once the interpreter tears the module down
+            _lib.xent_plan_destroy(h)
+            self.handle = None
+
+
+_xent_plans: dict = {}
+
+
+def xent_plan_for(x, w, dx=None, dw=None, ignore_index: int = -100, piece_bytes: int = 0) -> XentPlan:
+    """The (kept) plan for these tensors' sizes, strides and types."""
+    N, D = x.shape
+    V = w.shape[0]
+    if w.shape[1] != D or w.dtype != x.dtype:
+        raise ValueError("w must be [V][D] of x's type")
+    code = _dtype_code(x.dtype)
+    flags = (LL_XENT_DX if dx is not None else 0) | (LL_XENT_DW if dw is not None else 0)
+    if w.data_ptr() % 16:
+        flags |= LL_XENT_PACK_W
+    key = (x.device.index, N, V, D, _rows(x, "x"), _rows(w, "w"), _rows(dx, "dx") if dx is not None else 0,
+           _rows(dw, "dw") if dw is not None else 0, ignore_index, piece_bytes, code,
+           _dtype_code(dx.dtype) if dx is not None else code, _dtype_code(dw.dtype) if dw is not None else code, flags)
+    plan = _xent_plans.get(key)
+    if plan is None:
+        plan = _xent_plans[key] = XentPlan(XentDesc(*key[1:]))
+    return plan
+
+
+def _xent(x, w, target, dloss, dx, dw, ignore_index, piece_bytes):
+    torch = _torch()
+    N = x.shape[0]
+    plan = xent_plan_for(x, w, dx, dw, ignore_index, piece_bytes)
+    _vector(target, N, "target", (torch.int64,))
+    _same_device(x, w, target, dloss, dx, dw)
+    loss, lse = torch.empty((2, N), dtype=torch.float32, device=x.device).unbind(0)
+    stream = _stream_of(x)
+    ws = _op_workspace(x.device, stream, plan.ws_bytes)
+    xent_run(plan.handle, x.data_ptr(), w.data_ptr(), target.data_ptr(), _ptr(dloss), loss.data_ptr(), lse.data_ptr(),
+             _ptr(dx), _ptr(dw), ws.data_ptr(), ws.numel(), stream)
+    return loss, lse
+
+
+def vocab_xent(x, w, target, ignore_index: int = -100, piece_bytes: int = 0):
+    """Softmax cross entropy of rows x [N][D] against the vocabulary w [V][D] (both
+    bf16 or fp16, any row stride): (loss, lse), fp32 [N] each, without the
+    [N][V] logits.  target: int64 [N]; ignore_index, or one outside [0, V):
+    loss and lse are 0.  piece_bytes: bound of the buffers that hold a piece of
+    the logits (0: 2 GiB)."""
+    return _xent(x, w, target, None, None, None, ignore_index, piece_bytes)
+
+
+def vocab_xent_grad(x, w, target, dloss, ignore_index: int = -100, piece_bytes: int = 0, dx=None, dw=None,
+                    want_dx: bool = True, want_dw: bool = True):
+    """(loss, lse, dx, dw): ``vocab_xent`` with the gradients of sum(dloss * loss)
+    for fp32 dloss [N].  dx [N][D] and dw [V][D] may be given (of x's type or
+    fp32); want_dx / want_dw=False: that gradient is not formed (None)."""
+    torch = _torch()
+    _vector(dloss, x.shape[0], "dloss", (torch.float32,))
+    if want_dx and dx is None:
+        dx = torch.empty(tuple(x.shape), dtype=x.dtype, device=x.device)
+    if want_dw and dw is None:
+        dw = torch.empty(tuple(w.shape), dtype=w.dtype, device=w.device)
+    dx, dw = dx if want_dx else None, dw if want_dw else None
+    for t, like, what in ((dx, x, "dx"), (dw, w, "dw")):
+        if t is not None and (t.shape != like.shape or t.dtype not in (like.dtype, torch.float32)):
+            raise ValueError(f"{what} must have its operand's shape, and its type or fp32")
+    loss, lse = _xent(x, w, target, dloss, dx, dw, ignore_index, piece_bytes)
+    return loss, lse, dx, dw

@@ -1,0 +1,278 @@
+// Row kernels of the vocabulary cross entropy: everything around its three
+// matrix products.
+//
+//   z = x w^T,  lse = log sum_v exp(z_v),  loss = lse - z_target,
+//   dz = (exp(z - lse) - onehot(target)) * dloss,  dx = dz w,  dw = dz^T x
+//
+// The row sums are carried as pairs (m, s) with sum = s * exp(m), so any
+// number of pieces of a row can be joined in any grouping without overflow.
+#include "xent.hpp"
+
+#include <algorithm>
+
+#include "ops_common.hpp"
+
+namespace ll {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// (m, s) joined with (m2, s2).  An empty or all -inf piece is (-inf, 0).
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+  const float M = fmaxf(m, m2);
+  s = (m == M ? s : s * __expf(m - M)) + (m2 == M ? s2 : s2 * __expf(m2 - M));
+  m = M;
+}
+
+// Over the 256 threads of a workgroup; every thread gets it.
+__device__ __forceinline__ void block_join(float& m, float& s, float* red) {
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) join(m, s, __shfl_xor(m, k, 64), __shfl_xor(s, k, 64));
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) {
+    red[2 * wave] = m;
+    red[2 * wave + 1] = s;
+  }
+  __syncthreads();
+  m = red[0];
+  s = red[1];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) join(m, s, red[2 * w], red[2 * w + 1]);
+}
+
+__device__ __forceinline__ bool has_target(const XentRows& r, int64_t t) { return t >= 0 && t < r.V && t != r.ignore; }
+
+// Eight elements from p, of which the first n exist.
+template <bool WIDE>
+__device__ __forceinline__ void load8(const uint16_t* p, int n, uint16_t (&v)[8]) {
+  if (WIDE && n >= 8) {
+    const uint4 q = *(const uint4*)p;
+    __builtin_memcpy(v, &q, 16);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : (uint16_t)0;
+  }
+}
+
+// One workgroup per row: the aligned copy of x (a row without a target becomes
+// zeros, so that whatever it holds cannot reach dw through 0 * inf), and the
+// target's logit as a dot product of its own.
+template <int TY, bool WX, bool WW>
+__global__ void __launch_bounds__(256) xent_prep_kernel(const XentRows r) {
+  __shared__ float red[4];
+  for (int64_t i = blockIdx.x; i < r.N; i += gridDim.x) {
+    const int64_t t = r.target[i];
+    const bool live = has_target(r, t);
+    const uint16_t* x = (const uint16_t*)r.x + i * r.ldx;
+    const uint16_t* w = (const uint16_t*)r.w + (live ? t : 0) * r.ldw;
+    uint4* dst = (uint4*)((uint16_t*)r.xp + i * r.ldp);
+    float acc = 0.f;
+    for (int c = threadIdx.x; c < r.ldp / 8; c += 256) {
+      uint16_t v[8] = {};
+      if (live) {
+        uint16_t u[8];
+        const int n = r.D - 8 * c;
+        load8<WX>(x + 8 * c, n, v);
+        load8<WW>(w + 8 * c, n, u);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc = fmaf(Elem<TY>::get(v[k]), Elem<TY>::get(u[k]), acc);
+      }
+      uint4 q;
+      __builtin_memcpy(&q, v, 16);
+      dst[c] = q;
+    }
+    acc = lanes_sum<64>(acc);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
+    __syncthreads();
+    if (threadIdx.x == 0) r.zt[i] = red[0] + red[1] + red[2] + red[3];
+  }
+}
+
+hipError_t launch_xent_prep(const XentRows& r, int type, hipStream_t s) {
+  const bool wx = ((uintptr_t)r.x & 15) == 0 && r.ldx % 8 == 0, ww = ((uintptr_t)r.w & 15) == 0 && r.ldw % 8 == 0;
+  const dim3 grid((unsigned)std::min<int64_t>(r.N, 1 << 16));
+#define LL_PREP(TY)                                                                                            \
+  if (wx && ww) hipLaunchKernelGGL((xent_prep_kernel<TY, true, true>), grid, dim3(256), 0, s, r);             \
+  else if (wx) hipLaunchKernelGGL((xent_prep_kernel<TY, true, false>), grid, dim3(256), 0, s, r);             \
+  else if (ww) hipLaunchKernelGGL((xent_prep_kernel<TY, false, true>), grid, dim3(256), 0, s, r);             \
+  else hipLaunchKernelGGL((xent_prep_kernel<TY, false, false>), grid, dim3(256), 0, s, r);
+  if (type == LL_BF16) {
+    LL_PREP(LL_BF16)
+  } else {
+    LL_PREP(LL_F16)
+  }
+#undef LL_PREP
+  return hipGetLastError();
+}
+
+__global__ void __launch_bounds__(1024) xent_scale_kernel(const XentRows r) {
+  __shared__ float red[16];
+  float m = 0.f;
+  for (int64_t i = threadIdx.x; i < r.N; i += 1024) {
+    const float g = fabsf(r.dloss[i]);
+    if (has_target(r, r.target[i]) && g < __builtin_huge_valf()) m = fmaxf(m, g);
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 16; ++w) m = fmaxf(m, red[w]);
+    // largest |dloss| in [2^13, 2^14); the inverse stays a normal number
+    int e = 0;
+    if (m > 0.f) frexpf(m, &e);
+    e = max(-100, min(100, 14 - e));
+    r.scale[0] = ldexpf(1.f, e);
+    r.scale[1] = ldexpf(1.f, -e);
+  }
+}
+
+hipError_t launch_xent_scale(const XentRows& r, hipStream_t s) {
+  hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, r);
+  return hipGetLastError();
+}
+
+// Columns [lo, hi) of a split, in whole groups of four.
+__device__ __forceinline__ void split_range(int cols, int splits, int k, int& lo, int& hi) {
+  const int quads = (cols + 3) / 4;
+  lo = (int)((int64_t)quads * k / splits) * 4;
+  hi = min((int)((int64_t)quads * (k + 1) / splits) * 4, cols);
+}
+
+__global__ void __launch_bounds__(256) xent_stats_kernel(const XentRows r, const float* z, int64_t ldz, int cols,
+                                                         int p0, int splits) {
+  __shared__ float red[8];
+  const int64_t items = r.N * splits;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t i = it / splits;
+    const int k = (int)(it % splits);
+    int lo, hi;
+    split_range(cols, splits, k, lo, hi);
+    const float* row = z + i * ldz;
+    float m = kNegInf, s = 0.f;
+    for (int c = lo + 4 * threadIdx.x; c < hi; c += 1024) {
+      float v[4];
+      const float4 q = *(const float4*)(row + c);  // ldz covers whole groups of four
+      v[0] = q.x;
+      v[1] = c + 1 < hi ? q.y : kNegInf;
+      v[2] = c + 2 < hi ? q.z : kNegInf;
+      v[3] = c + 3 < hi ? q.w : kNegInf;
+      const float m4 = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+      float s4 = 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s4 += v[e] == kNegInf ? 0.f : __expf(v[e] - m4);
+      join(m, s, m4, s4);
+    }
+    __syncthreads();
+    block_join(m, s, red);
+    if (threadIdx.x == 0) r.parts[i * r.np + p0 + k] = XentPart{m, s};
+  }
+}
+
+hipError_t launch_xent_stats(const XentRows& r, const float* z, int64_t ldz, int cols, int p0, int splits,
+                             hipStream_t s) {
+  const int64_t items = r.N * splits;
+  hipLaunchKernelGGL(xent_stats_kernel, dim3((unsigned)std::min<int64_t>(items, 1 << 20)), dim3(256), 0, s, r, z, ldz,
+                     cols, p0, splits);
+  return hipGetLastError();
+}
+
+// One wave per row: joins its parts.
+__global__ void __launch_bounds__(256) xent_lse_kernel(const XentRows r) {
+  const int lane = threadIdx.x & 63;
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (i >= r.N) return;
+  float m = kNegInf, s = 0.f;
+  for (int p = lane; p < r.np; p += 64) {
+    const XentPart q = r.parts[i * r.np + p];
+    join(m, s, q.m, q.s);
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) join(m, s, __shfl_xor(m, k, 64), __shfl_xor(s, k, 64));
+  if (lane == 0) {
+    const bool live = has_target(r, r.target[i]);
+    const float lse = live ? m + logf(s) : 0.f;
+    r.lse[i] = lse;
+    r.loss[i] = live ? lse - r.zt[i] : 0.f;
+    if (r.lse_out) r.lse_out[i] = lse;
+    if (r.dloss) r.coef[i] = live ? r.dloss[i] * (r.scale ? r.scale[0] : 1.f) : 0.f;
+  }
+}
+
+hipError_t launch_xent_lse(const XentRows& r, hipStream_t s) {
+  const int64_t blocks = (r.N + 3) / 4;
+  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)blocks), dim3(256), 0, s, r);
+  return hipGetLastError();
+}
+
+// Four columns per thread.  dz is rounded to the 16-bit type of the products
+// that follow (the matrix instruction takes no wider operand): relative to
+// each element, half a step of the type, as any 16-bit gradient is.
+template <int TY>
+__global__ void __launch_bounds__(256) xent_dz_kernel(const XentRows r, const float* z, int64_t ldz, int64_t v0,
+                                                      int cols, uint16_t* dz, int64_t ldd, int splits) {
+  const int64_t items = r.N * splits;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int64_t i = it / splits;
+    int lo, hi;
+    split_range((int)ldd, splits, (int)(it % splits), lo, hi);
+    const float coef = r.coef[i], lse = r.lse[i];
+    const bool live = has_target(r, r.target[i]);
+    const int64_t t = live ? r.target[i] - v0 : -1;
+    for (int c = lo + 4 * threadIdx.x; c < hi; c += 1024) {
+      uint16_t o[4] = {};
+      if (live && c < cols) {
+        const float4 q = *(const float4*)(z + i * ldz + c);
+        const float v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (c + e < cols) o[e] = Elem<TY>::put((__expf(v[e] - lse) - (c + e == t ? 1.f : 0.f)) * coef);
+      }
+      uint2 w;
+      __builtin_memcpy(&w, o, 8);
+      *(uint2*)(dz + i * ldd + c) = w;
+    }
+  }
+}
+
+hipError_t launch_xent_dz(const XentRows& r, const float* z, int64_t ldz, int64_t v0, int cols, void* dz, int64_t ldd,
+                          int type, int cus, hipStream_t s) {
+  const int splits = (int)std::max<int64_t>(1, std::min<int64_t>((ldd + 1023) / 1024, 8ll * cus / r.N));
+  const dim3 grid((unsigned)std::min<int64_t>(r.N * splits, 1 << 20));
+  if (type == LL_BF16)
+    hipLaunchKernelGGL((xent_dz_kernel<LL_BF16>), grid, dim3(256), 0, s, r, z, ldz, v0, cols, (uint16_t*)dz, ldd,
+                       splits);
+  else
+    hipLaunchKernelGGL((xent_dz_kernel<LL_F16>), grid, dim3(256), 0, s, r, z, ldz, v0, cols, (uint16_t*)dz, ldd,
+                       splits);
+  return hipGetLastError();
+}
+
+template <int TY>
+__global__ void __launch_bounds__(256) xent_finish_kernel(const float* a, const float* b, const float* scale,
+                                                          int64_t rows, int64_t cols, int64_t lda, void* out,
+                                                          int64_t ldo) {
+  const float f = scale ? *scale : 1.f;
+  for (int64_t i = blockIdx.x; i < rows; i += gridDim.x)
+    for (int64_t c = threadIdx.x; c < cols; c += 256) {
+      float v = a[i * lda + c];
+      if (b) v += b[i * lda + c];
+      ((typename Elem<TY>::raw*)out)[i * ldo + c] = Elem<TY>::put(v * f);
+    }
+}
+
+hipError_t launch_xent_finish(const float* a, const float* b, const float* scale, int64_t rows, int64_t cols,
+                              int64_t lda, void* out, int64_t ldo, int type, int cus, hipStream_t s) {
+  if (rows == 0 || cols == 0) return hipSuccess;
+  const dim3 grid((unsigned)std::min<int64_t>(rows, 64ll * cus));
+#define LL_FINISH(TY) \
+  hipLaunchKernelGGL((xent_finish_kernel<TY>), grid, dim3(256), 0, s, a, b, scale, rows, cols, lda, out, ldo)
+  if (type == LL_BF16) LL_FINISH(LL_BF16);
+  else if (type == LL_F16) LL_FINISH(LL_F16);
+  else LL_FINISH(LL_F32);
+#undef LL_FINISH
+  return hipGetLastError();
+}
+
+}  // namespace ll

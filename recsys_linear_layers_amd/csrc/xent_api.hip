@@ -1,0 +1,338 @@
+// C ABI of the vocabulary cross entropy: argument checks, the pieces of the
+// vocabulary, workspace layout and the sequence of launches.  The declarations
+// and their contracts are in include/linlayers.h.
+#include <stdio.h>
+#include <string.h>
+
+#include <algorithm>
+#include <new>
+
+#include "api.hpp"
+#include "kernels.hpp"
+#include "ops_common.hpp"
+#include "xent.hpp"
+
+using namespace ll;
+
+struct xent_plan {
+  xent_desc d;
+  int device, cus;
+  bool dx, dw;
+  int64_t ldp;        // row stride of the copy of x (and of a packed w): D rounded up to 64
+  int64_t ldw;        // row stride of w as the products read it
+  bool pack_w;
+  int64_t cols;       // vocabulary entries per piece (the last may have fewer)
+  int pieces, splits; // splits: parts per row and piece
+  int64_t ldz, ldd;   // row strides of the fp32 logits and of the 16-bit dz of a piece
+  bool dx_direct;     // dx leaves its product in its final form
+  bool dw_direct;
+  gemm_plan logits[2], dxp[2], dwp[2];  // [1]: the last piece
+  size_t off_xp, off_wp, off_zt, off_lse, off_coef, off_scale, off_parts, off_z, off_dz, off_dxa, off_dxb, off_dwt,
+      off_gemm, gemm_bytes, ws_bytes;
+};
+
+namespace {
+
+// Bytes the logits and their gradient may take when the description does not
+// say: 2 GiB, under 1% of the card's memory.
+constexpr int64_t kDefaultPieceBytes = 2ll << 30;
+// Rows from which a weight whose rows are not whole 64-element blocks is copied
+// first: the copy costs 4 V D bytes of traffic, and lets the products run on
+// the hand-ordered kind.
+constexpr int64_t kPackRows = 512;
+
+ll_status xent_check(const xent_desc* d) {
+  if (d->N < 0 || d->V < 0 || d->D < 0) return fail(LL_ERR_INVALID_ARG, "negative size");
+  if (d->V == 0 || d->D == 0) return fail(LL_ERR_INVALID_ARG, "V and D must be positive");
+  if (d->piece_bytes < 0) return fail(LL_ERR_INVALID_ARG, "negative piece_bytes");
+  if (d->flags & ~(uint32_t)(LL_XENT_DX | LL_XENT_DW | LL_XENT_PACK_W))
+    return fail(LL_ERR_INVALID_ARG, "unknown flag bits");
+  if (d->type != LL_BF16 && d->type != LL_F16) return fail(LL_ERR_UNSUPPORTED, "type must be LL_BF16 or LL_F16");
+  if ((d->flags & LL_XENT_DX) && d->dx_type != d->type && d->dx_type != LL_F32)
+    return fail(LL_ERR_UNSUPPORTED, "dx_type must be the type of x or LL_F32");
+  if ((d->flags & LL_XENT_DW) && d->dw_type != d->type && d->dw_type != LL_F32)
+    return fail(LL_ERR_UNSUPPORTED, "dw_type must be the type of w or LL_F32");
+  if (d->N >= (1ll << 30) || d->V >= (1ll << 30) || d->D >= (1ll << 20))
+    return fail(LL_ERR_UNSUPPORTED, "N and V must be below 2^30, D below 2^20");
+  if (d->stride_x < d->D || d->stride_w < d->D || ((d->flags & LL_XENT_DX) && d->stride_dx < d->D) ||
+      ((d->flags & LL_XENT_DW) && d->stride_dw < d->D))
+    return fail(LL_ERR_INVALID_ARG, "row strides shorter than the rows");
+  for (int64_t st : {d->stride_x, d->stride_w, (d->flags & LL_XENT_DX) ? d->stride_dx : 0,
+                     (d->flags & LL_XENT_DW) ? d->stride_dw : 0})
+    if (st >= (1ll << 28)) return fail(LL_ERR_UNSUPPORTED, "row strides must be below 2^28");
+  return LL_OK;
+}
+
+gemm_desc product(int64_t M, int64_t N, int64_t K, int64_t sam, int64_t sak, int64_t sbk, int64_t sbn, int64_t ldc,
+                  int type, int c_type) {
+  gemm_desc g;
+  memset(&g, 0, sizeof g);
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.stride_am = sam;
+  g.stride_ak = sak;
+  g.stride_bk = sbk;
+  g.stride_bn = sbn;
+  g.stride_cm = ldc;
+  g.stride_cn = 1;
+  g.a_type = g.b_type = type;
+  g.c_type = c_type;
+  return g;
+}
+
+}  // namespace
+
+extern "C" {
+
+ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
+  if (!out || !d) return fail(LL_ERR_INVALID_ARG, "xent_plan_create: null argument");
+  *out = nullptr;
+  ll_status s = xent_check(d);
+  if (s != LL_OK) return s;
+  xent_plan p;
+  memset(&p, 0, sizeof p);
+  p.d = *d;
+  p.dx = d->flags & LL_XENT_DX;
+  p.dw = d->flags & LL_XENT_DW;
+  const bool grads = p.dx || p.dw;
+  p.ldp = round_up(d->D, 64);
+  p.pack_w = (d->flags & LL_XENT_PACK_W) || d->stride_w % 8 || d->D % 8 || (d->D % 64 && d->N >= kPackRows);
+  p.ldw = p.pack_w ? p.ldp : d->stride_w;
+  const bool f16 = d->type == LL_F16;
+
+  const DeviceInfo* info = nullptr;
+  s = current_device(&p.device, &info);
+  if (s != LL_OK) return s;
+  p.cus = info->cus;
+
+  // Pieces of the vocabulary: as many columns as the bound holds, in whole
+  // tiles, all pieces alike but the last; a piece of w and of dz stays below
+  // 2 GB, which the hand-ordered kind's descriptors need.
+  const int64_t N = d->N, rows = std::max<int64_t>(N, 1);
+  const int64_t limit = d->piece_bytes ? d->piece_bytes : kDefaultPieceBytes;
+  const bool dw_tmp = p.dw && f16 && d->dw_type != LL_F32;
+  const int64_t per_col = rows * (grads ? 6 : 4) + (dw_tmp ? d->D * 4 : 0);
+  const int64_t two_gb = (1 << 30) / std::max(rows, p.ldw) - 256;
+  int64_t cols = std::min(limit / per_col, two_gb) / 256 * 256;
+  cols = std::max<int64_t>(cols, 256);
+  p.pieces = (int)((d->V + cols - 1) / cols);
+  p.cols = round_up((d->V + p.pieces - 1) / p.pieces, 256);
+  p.pieces = (int)((d->V + p.cols - 1) / p.cols);
+  const int64_t last = d->V - (p.pieces - 1) * p.cols;
+  const int64_t first = p.pieces > 1 ? p.cols : last;
+  p.ldz = round_up(first, 4);
+  p.ldd = round_up(first, 64);
+  // parts of at least 1024 columns, up to 8 workgroups per CU over all rows
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((first + 1023) / 1024, 8ll * p.cus / rows));
+  p.dx_direct = p.dx && p.pieces == 1 && !f16;
+  p.dw_direct = p.dw && !f16;
+
+  size_t off = 0;
+  auto take = [&](size_t n) {
+    const size_t at = off;
+    off = align256(off + n);
+    return at;
+  };
+  p.off_xp = take((size_t)N * p.ldp * 2);
+  p.off_wp = take(p.pack_w ? (size_t)d->V * p.ldp * 2 : 0);
+  p.off_zt = take((size_t)N * 4);
+  p.off_lse = take((size_t)N * 4);
+  p.off_coef = take((size_t)N * 4);
+  p.off_scale = take(8);
+  p.off_parts = take((size_t)N * p.pieces * p.splits * sizeof(XentPart));
+  p.off_z = take((size_t)N * p.ldz * 4);
+  if (grads) p.off_dz = take((size_t)N * p.ldd * 2);
+  if (p.dx && !p.dx_direct) p.off_dxa = take((size_t)N * d->D * 4);
+  if (p.dx && p.pieces > 1) p.off_dxb = take((size_t)N * d->D * 4);
+  if (dw_tmp) p.off_dwt = take((size_t)first * d->D * 4);
+  p.off_gemm = off;
+  const uint32_t padded_w = p.pack_w ? kPaddedB : 0;
+  for (int i = 0; i < 2; ++i) {
+    const int64_t n = i ? last : first;
+    gemm_desc g = product(N, n, d->D, p.ldp, 1, 1, p.ldw, p.ldz, d->type, LL_F32);
+    s = gemm_plan_build(&g, kPaddedA | padded_w, &p.logits[i]);
+    if (s != LL_OK) return s;
+    p.gemm_bytes = std::max(p.gemm_bytes, p.logits[i].ws_bytes);
+    if (p.dx) {
+      g = product(N, d->D, n, p.ldd, 1, p.ldw, 1, p.dx_direct ? d->stride_dx : d->D, d->type,
+                  p.dx_direct ? d->dx_type : LL_F32);
+      s = gemm_plan_build(&g, kPaddedA | padded_w, &p.dxp[i]);
+      if (s != LL_OK) return s;
+      p.gemm_bytes = std::max(p.gemm_bytes, p.dxp[i].ws_bytes);
+    }
+    if (p.dw) {
+      g = product(n, d->D, N, 1, p.ldd, p.ldp, 1, dw_tmp ? d->D : d->stride_dw, d->type,
+                  dw_tmp ? (int)LL_F32 : d->dw_type);
+      s = gemm_plan_build(&g, kPaddedA | kPaddedB, &p.dwp[i]);
+      if (s != LL_OK) return s;
+      p.gemm_bytes = std::max(p.gemm_bytes, p.dwp[i].ws_bytes);
+    }
+  }
+  p.ws_bytes = off + align256(p.gemm_bytes);
+  xent_plan* h = new (std::nothrow) xent_plan(p);
+  if (!h) return fail(LL_ERR_INVALID_ARG, "out of host memory");
+  *out = h;
+  return ok();
+}
+
+ll_status xent_plan_workspace_size(const xent_plan* p, size_t* bytes) {
+  if (!p || !bytes) return fail(LL_ERR_INVALID_ARG, "null argument");
+  *bytes = p->ws_bytes;
+  return ok();
+}
+
+ll_status xent_plan_describe(const xent_plan* p, char* buf, size_t len) {
+  if (!p || !buf || len == 0) return fail(LL_ERR_INVALID_ARG, "null argument");
+  snprintf(buf, len, "pieces=%d cols=%lld packW=%d logits=%s dx=%s dw=%s ws=%zu", p->pieces, (long long)p->cols,
+           (int)p->pack_w, kind_info(p->logits[0].kind).name, p->dx ? kind_info(p->dxp[0].kind).name : "-",
+           p->dw ? kind_info(p->dwp[0].kind).name : "-", p->ws_bytes);
+  return ok();
+}
+
+ll_status xent_plan_destroy(xent_plan* p) {
+  delete p;
+  return ok();
+}
+
+ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64_t* target, const float* dloss,
+                   float* loss, float* lse, void* dx, void* dw, void* ws, size_t ws_bytes, void* stream) {
+  if (!p) return fail(LL_ERR_INVALID_ARG, "null plan");
+  const xent_desc& d = p->d;
+  const int64_t N = d.N;
+  const bool grads = p->dx || p->dw;
+  if (!w || (N > 0 && (!x || !target || !loss || (grads && !dloss) || (p->dx && !dx))) || (p->dw && !dw))
+    return fail(LL_ERR_INVALID_ARG, "null pointer");
+  auto bad = [](const void* q, size_t a) { return ((uintptr_t)q & (a - 1)) != 0; };
+  if (bad(x, 2) || bad(w, 2) || bad(target, 8) || bad(dloss, 4) || bad(loss, 4) || bad(lse, 4) ||
+      (p->dx && bad(dx, dtype_size(d.dx_type))) || (p->dw && bad(dw, dtype_size(d.dw_type))))
+    return fail(LL_ERR_INVALID_ARG, "misaligned pointer");
+  if (!p->pack_w && bad(w, 16))
+    return fail(LL_ERR_INVALID_ARG, "w must be 16-byte aligned unless packed (LL_XENT_PACK_W)");
+  if (ws_bytes < p->ws_bytes || (p->ws_bytes > 0 && !ws))
+    return fail(LL_ERR_WORKSPACE, "workspace %zu bytes, plan needs %zu", ws_bytes, p->ws_bytes);
+  if (p->ws_bytes > 0 && bad(ws, 256)) return fail(LL_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  auto flat = [](const void* q, int64_t n, int64_t e) { return span_of(q, q && n > 0 ? 1 : 0, n, 0, 1, e); };
+  const Span in[5] = {span_of(x, N, d.D, d.stride_x, 1, 2), span_of(w, d.V, d.D, d.stride_w, 1, 2),
+                      flat(target, N, 8), flat(grads ? dloss : nullptr, N, 4), flat(ws, (int64_t)p->ws_bytes, 1)};
+  const Span outs[4] = {flat(loss, N, 4), flat(lse, N, 4),
+                        span_of(dx, p->dx ? N : 0, d.D, d.stride_dx, 1, p->dx ? dtype_size(d.dx_type) : 1),
+                        span_of(dw, p->dw ? d.V : 0, d.D, d.stride_dw, 1, p->dw ? dtype_size(d.dw_type) : 1)};
+  for (int i = 0; i < 4; ++i) {
+    for (const Span& t : in)
+      if (overlaps(outs[i], t)) return fail(LL_ERR_INVALID_ARG, "an output overlaps an input or the workspace");
+    for (int j = 0; j < i; ++j)
+      if (overlaps(outs[i], outs[j])) return fail(LL_ERR_INVALID_ARG, "outputs overlap");
+  }
+  int dev = -1;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+  if (dev != p->device) return fail(LL_ERR_INVALID_ARG, "plan made for device %d, current is %d", p->device, dev);
+  hipStream_t st = (hipStream_t)stream;
+  char* const base = (char*)ws;
+  void* const gws = base + p->off_gemm;
+  const bool f16 = d.type == LL_F16;
+
+  XentRows r;
+  memset(&r, 0, sizeof r);
+  r.x = x;
+  r.w = w;
+  r.target = target;
+  r.dloss = grads ? dloss : nullptr;
+  r.N = N;
+  r.V = d.V;
+  r.ldx = d.stride_x;
+  r.ldw = d.stride_w;
+  r.ignore = d.ignore_index;
+  r.D = (int32_t)d.D;
+  r.ldp = (int32_t)p->ldp;
+  r.xp = base + p->off_xp;
+  r.zt = (float*)(base + p->off_zt);
+  r.lse = (float*)(base + p->off_lse);
+  r.coef = (float*)(base + p->off_coef);
+  r.scale = f16 && grads ? (float*)(base + p->off_scale) : nullptr;
+  r.parts = (XentPart*)(base + p->off_parts);
+  r.np = p->pieces * p->splits;
+  r.loss = loss;
+  r.lse_out = lse;
+  float* const z = (float*)(base + p->off_z);
+  void* const dz = base + p->off_dz;
+  float* const dxa = (float*)(base + p->off_dxa);
+  float* const dxb = (float*)(base + p->off_dxb);
+  float* const dwt = (float*)(base + p->off_dwt);
+  const float* const unscale = r.scale ? r.scale + 1 : nullptr;
+
+  if (N > 0) {
+    e = launch_xent_prep(r, d.type, st);
+    if (e != hipSuccess) return hip_fail(e, "xent prep launch");
+    if (r.scale) {
+      e = launch_xent_scale(r, st);
+      if (e != hipSuccess) return hip_fail(e, "xent scale launch");
+    }
+    if (p->pack_w) {
+      e = launch_pack_kmajor((const uint16_t*)w, d.stride_w, 1, d.V, d.D, (uint16_t*)(base + p->off_wp), p->ldp, st);
+      if (e != hipSuccess) return hip_fail(e, "pack w launch");
+    }
+  }
+  const uint16_t* const wk = p->pack_w ? (const uint16_t*)(base + p->off_wp) : (const uint16_t*)w;
+  auto logits_of = [&](int k) {
+    return gemm_run_plan(&p->logits[k + 1 == p->pieces], r.xp, wk + (int64_t)k * p->cols * p->ldw, z, nullptr, gws,
+                         p->gemm_bytes, st);
+  };
+  auto cols_of = [&](int k) { return (int)std::min(p->cols, d.V - (int64_t)k * p->cols); };
+  ll_status s;
+  if (N > 0) {
+    for (int k = 0; k < p->pieces; ++k) {
+      s = logits_of(k);
+      if (s != LL_OK) return s;
+      e = launch_xent_stats(r, z, p->ldz, cols_of(k), k * p->splits, p->splits, st);
+      if (e != hipSuccess) return hip_fail(e, "xent stats launch");
+    }
+    e = launch_xent_lse(r, st);
+    if (e != hipSuccess) return hip_fail(e, "xent lse launch");
+  }
+  if (!grads) return ok();
+  // The last piece's logits are still there; the others are formed again.
+  for (int k = p->pieces - 1, n = 0; k >= 0; --k, ++n) {
+    const int li = k + 1 == p->pieces;
+    const int64_t v0 = (int64_t)k * p->cols;
+    const int cols = cols_of(k);
+    if (N > 0) {
+      if (n > 0) {
+        s = logits_of(k);
+        if (s != LL_OK) return s;
+      }
+      const int64_t ldd = p->ldd;
+      e = launch_xent_dz(r, z, p->ldz, v0, cols, dz, ldd, d.type, p->cus, st);
+      if (e != hipSuccess) return hip_fail(e, "xent dz launch");
+      if (p->dx) {
+        s = gemm_run_plan(&p->dxp[li], dz, wk + v0 * p->ldw, p->dx_direct ? dx : n == 0 ? dxa : dxb, nullptr, gws,
+                          p->gemm_bytes, st);
+        if (s != LL_OK) return s;
+        if (!p->dx_direct) {
+          if (k == 0)
+            e = launch_xent_finish(dxa, n > 0 ? dxb : nullptr, unscale, N, d.D, d.D, dx, d.stride_dx, d.dx_type,
+                                   p->cus, st);
+          else if (n > 0)
+            e = launch_xent_finish(dxa, dxb, nullptr, N, d.D, d.D, dxa, d.D, LL_F32, p->cus, st);
+          if (e != hipSuccess) return hip_fail(e, "xent dx sum launch");
+        }
+      }
+    }
+    if (p->dw) {
+      const int64_t esz = dtype_size(d.dw_type);
+      char* const dst = (char*)dw + v0 * d.stride_dw * esz;
+      const bool tmp = f16 && d.dw_type != LL_F32;
+      s = gemm_run_plan(&p->dwp[li], dz, r.xp, tmp ? (void*)dwt : (void*)dst, nullptr, gws, p->gemm_bytes, st);
+      if (s != LL_OK) return s;
+      if (f16) {
+        e = launch_xent_finish(tmp ? dwt : (const float*)dst, nullptr, N > 0 ? unscale : nullptr, cols, d.D,
+                               tmp ? d.D : d.stride_dw, dst, d.stride_dw, d.dw_type, p->cus, st);
+        if (e != hipSuccess) return hip_fail(e, "xent dw scale launch");
+      }
+    }
+  }
+  return ok();
+}
+
+}  // extern "C"

@@ -166,3 +166,72 @@ def test_python_checks():
                  lambda: ll.layernorm_grad(x, x, torch.ones(3), torch.ones(4))):
         with pytest.raises((ValueError, TypeError)):
             call()
+
+
+def _xent(**kw):
+    ll = _ll()
+    base = dict(N=4, V=100, D=16, stride_x=16, stride_w=16, stride_dx=16, stride_dw=16, ignore_index=-100,
+                piece_bytes=0, type=ll.LL_BF16, dx_type=ll.LL_BF16, dw_type=ll.LL_F32, flags=3)
+    base.update(kw)
+    return ll.XentDesc(**base)
+
+
+@pytest.mark.parametrize("kw,expect", [
+    (dict(N=-1), "LL_ERR_INVALID_ARG"), (dict(V=0), "LL_ERR_INVALID_ARG"), (dict(D=0), "LL_ERR_INVALID_ARG"),
+    (dict(stride_x=15), "LL_ERR_INVALID_ARG"), (dict(stride_w=15), "LL_ERR_INVALID_ARG"),
+    (dict(stride_dx=15), "LL_ERR_INVALID_ARG"), (dict(stride_dw=15), "LL_ERR_INVALID_ARG"),
+    (dict(piece_bytes=-1), "LL_ERR_INVALID_ARG"), (dict(flags=8), "LL_ERR_INVALID_ARG"),
+    (dict(type=1), "LL_ERR_UNSUPPORTED"), (dict(dx_type=2), "LL_ERR_UNSUPPORTED"),
+    (dict(dw_type=2), "LL_ERR_UNSUPPORTED"), (dict(V=1 << 30), "LL_ERR_UNSUPPORTED"),
+    (dict(D=1 << 20, stride_x=1 << 20, stride_w=1 << 20, stride_dx=1 << 20, stride_dw=1 << 20), "LL_ERR_UNSUPPORTED"),
+    (dict(stride_x=1 << 28), "LL_ERR_UNSUPPORTED"),
+])
+def test_xent_descriptions(kw, expect):
+    ll = _ll()
+    h = ctypes.c_void_p()
+    assert ll.ll_status_string(ll._lib.xent_plan_create(ctypes.byref(h), ctypes.byref(_xent(**kw)))) == expect
+    assert not h.value
+
+
+def test_xent_null_arguments():
+    ll = _ll()
+    h = ctypes.c_void_p()
+    n = ctypes.c_size_t()
+    assert ll._lib.xent_plan_create(None, ctypes.byref(_xent())) == ll.LL_ERR_INVALID_ARG
+    assert ll._lib.xent_plan_create(ctypes.byref(h), None) == ll.LL_ERR_INVALID_ARG
+    assert ll._lib.xent_plan_workspace_size(None, ctypes.byref(n)) == ll.LL_ERR_INVALID_ARG
+    assert ll._lib.xent_plan_describe(None, None, 0) == ll.LL_ERR_INVALID_ARG
+    assert ll._lib.xent_run(None, P, Q, R, None, P, None, None, None, None, 0, None) == ll.LL_ERR_INVALID_ARG
+    assert ll._lib.xent_plan_destroy(None) == ll.LL_OK
+
+
+@pytest.mark.gpu
+def test_xent_run_refusals():
+    """These need a plan, which needs a device; every call is refused on the host."""
+    import torch
+    ll = _ll()
+    h = ll.xent_plan_create(_xent())
+    try:
+        need = ll.xent_plan_workspace_size(h)
+        run = ll._lib.xent_run
+        X, W, T, G, L, E, DX, DW, WS = [(i + 1) << 32 for i in range(9)]
+        good = [X, W, T, G, L, E, DX, DW, WS]
+
+        def status(args, ws_bytes=need):
+            return ll.ll_status_string(run(h, *args, ws_bytes, None))
+
+        assert status(good, need - 1) == "LL_ERR_WORKSPACE"
+        for i, bad, want in ((0, None, "INVALID_ARG"), (1, None, "INVALID_ARG"), (2, None, "INVALID_ARG"),
+                             (3, None, "INVALID_ARG"), (4, None, "INVALID_ARG"), (6, None, "INVALID_ARG"),
+                             (7, None, "INVALID_ARG"), (8, None, "WORKSPACE"), (8, WS + 64, "WORKSPACE"),
+                             (0, X + 1, "INVALID_ARG"), (1, W + 2, "INVALID_ARG"), (2, T + 4, "INVALID_ARG"),
+                             (6, DX + 1, "INVALID_ARG"), (7, DW + 2, "INVALID_ARG"), (6, X, "INVALID_ARG"),
+                             (7, W, "INVALID_ARG"), (4, E, "INVALID_ARG"), (5, G, "INVALID_ARG"),
+                             (6, WS, "INVALID_ARG"), (7, DX, "INVALID_ARG")):
+            a = list(good)
+            a[i] = bad
+            assert status(a) == "LL_ERR_" + want, (i, bad)
+    finally:
+        ll.xent_plan_destroy(h)
+    with pytest.raises(ValueError):
+        ll.vocab_xent(torch.zeros(2, 8).half(), torch.zeros(5, 9).half(), torch.zeros(2, dtype=torch.int64))
