@@ -341,8 +341,6 @@ ll_status lincomp_ragged_run_ex(const lincomp_ragged_desc* desc, const int64_t* 
  * of out at out + t*stride_out; the last dimension is contiguous; strides at
  * least D.  ids: device array of T int64.  An id outside [0, V) gives a row
  * of zeros (no access outside the table).  T == 0 or D == 0: nothing is written.
- * Rows move 16 bytes at a time where both pointers are 16-byte aligned and D
- * and the strides are multiples of 16 bytes, else element by element.
  * One kernel on `stream`; no workspace; may be captured into a HIP graph.
  * Errors: LL_ERR_INVALID_ARG (null desc/pointer, negative size, stride below
  * D, a pointer not aligned to its element, out overlapping the table or ids),

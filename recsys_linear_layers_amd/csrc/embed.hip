@@ -3,15 +3,19 @@
 //
 // The lookup reads and writes each row once: HBM bound.
 //
-// The gradient sorts the tokens by id (a stable radix sort of (id, position)
-// pairs, so a row's tokens stay in their order) and then every row of dw is
-// written once, by the lanes that own it, as the sum of its tokens in that
-// order: no floating-point atomics, so the result does not depend on timing.
-// A few ids take a large share of the positions in real data.  A row's tokens
-// are consecutive after the sort, so sums over whole chunks of kEmbedChunk
-// sorted positions are formed ahead (in parallel over the chunks), and a long
-// row is then the sum of its chunks and the loose tokens at both ends, split
-// over the groups of a workgroup.
+// The gradient sorts the tokens by id, stably (a counting sort by digits of
+// the (id, position) pairs, so a row's tokens stay in their order), and then
+// every row of dw is written once, by the lanes that own it, as the sum of its
+// tokens in that order: no floating-point atomics, so the result does not
+// depend on timing.  A few ids take a large share of the positions in real
+// data.  A row's tokens are consecutive after the sort, so sums over whole
+// chunks of kEmbedChunk sorted positions are formed ahead, in parallel over
+// the chunks, and the rows that hold one are shared out over workgroups of
+// their own.
+//
+// Rows start at any element and have any width: a 16-byte access needs no
+// alignment here, so the lanes always move 16 bytes and only a row's last
+// lane takes single elements.
 #include "embed.hpp"
 
 #include <algorithm>
@@ -25,62 +29,59 @@ namespace ll {
 // ---------------------------------------------------------------------------
 
 // lx lanes move one row; 256 / lx rows per workgroup and step.
-template <int TY, int VEC>
+template <int TY, bool TAIL>
 __global__ void __launch_bounds__(256) embed_kernel(const EmbedArgs a, int lx_log2) {
+  constexpr int VEC = kWide<TY>;
   typedef Chunk<TY, VEC> C;
+  typedef typename C::raw raw;
   const int lx = 1 << lx_log2;
   const int x = threadIdx.x & (lx - 1), y = threadIdx.x >> lx_log2;
   const int rows = 256 >> lx_log2;
-  const int chunks = a.D / VEC;
   for (int64_t t = (int64_t)blockIdx.x * rows + y; t < a.T; t += (int64_t)gridDim.x * rows) {
     const int64_t id = a.ids[t];
-    C* dst = (C*)((typename Elem<TY>::raw*)a.out + t * a.ldo);
-    if (id < 0 || id >= a.V) {
-      C z;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) z.put(i, 0.f);
-      for (int c = x; c < chunks; c += lx) dst[c] = z;
-      continue;
-    }
-    const C* src = (const C*)((const typename Elem<TY>::raw*)a.table + id * a.ldt);
-    for (int c = x; c < chunks; c += lx) {
-      C v = src[c];
+    const bool inside = id >= 0 && id < a.V;
+    raw* dst = (raw*)a.out + t * a.ldo;
+    const raw* src = (const raw*)a.table + (inside ? id : 0) * a.ldt;
+    for (int d = x * VEC; d < a.D; d += lx * VEC) {
+      C v;
+      if (inside) v.template load<TAIL>(src + d, a.D - d);
+      else v.clear();
 #pragma unroll
       for (int i = 0; i < VEC; ++i) v.put(i, v.get(i) * a.scale);
-      dst[c] = v;
+      v.template store<TAIL>(dst + d, a.D - d);
     }
   }
 }
 
-// Smallest power of two >= n, at most `most`, as its logarithm.
+// Smallest power of two >= n, at most 2^most_log2, as its logarithm.
 static int log2_up(int64_t n, int most_log2) {
   int l = 0;
   while (l < most_log2 && (1ll << l) < n) ++l;
   return l;
 }
 
-template <int TY, int VEC>
+template <int TY, bool TAIL>
 static hipError_t launch_embed_t(const EmbedArgs& a, hipStream_t s) {
-  const int lx = log2_up(a.D / VEC, 8);
+  constexpr int VEC = kWide<TY>;
+  const int lx = log2_up((a.D + VEC - 1) / VEC, 8);
   const int rows = 256 >> lx;
   const int64_t blocks = std::min<int64_t>((a.T + rows - 1) / rows, 1 << 16);
-  hipLaunchKernelGGL((embed_kernel<TY, VEC>), dim3((unsigned)blocks), dim3(256), 0, s, a, lx);
+  hipLaunchKernelGGL((embed_kernel<TY, TAIL>), dim3((unsigned)blocks), dim3(256), 0, s, a, lx);
   return hipGetLastError();
 }
 
 hipError_t launch_embed(const EmbedArgs& a, int type, hipStream_t s) {
-  const bool wide = wide_rows(a.table, a.ldt, a.D, type) && wide_rows(a.out, a.ldo, a.D, type);
   switch (type) {
-    case LL_BF16: return wide ? launch_embed_t<LL_BF16, 8>(a, s) : launch_embed_t<LL_BF16, 1>(a, s);
-    case LL_F16: return wide ? launch_embed_t<LL_F16, 8>(a, s) : launch_embed_t<LL_F16, 1>(a, s);
-    case LL_F32: return wide ? launch_embed_t<LL_F32, 4>(a, s) : launch_embed_t<LL_F32, 1>(a, s);
+    case LL_BF16: return a.D % 8 ? launch_embed_t<LL_BF16, true>(a, s) : launch_embed_t<LL_BF16, false>(a, s);
+    case LL_F16: return a.D % 8 ? launch_embed_t<LL_F16, true>(a, s) : launch_embed_t<LL_F16, false>(a, s);
+    case LL_F32: return a.D % 4 ? launch_embed_t<LL_F32, true>(a, s) : launch_embed_t<LL_F32, false>(a, s);
     default: return hipErrorInvalidValue;
   }
 }
 
 // ---------------------------------------------------------------------------
-// Stable radix sort of (id, position).  Tokens without a gradient (padding or
-// an id outside the table) get the key V and end up behind all others.
+// Stable sort of (id, position).  Tokens without a gradient (padding or an id
+// outside the table) get the key V and end up behind all others.
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ uint32_t token_key(const EmbedGradArgs& a, int t) {
@@ -88,121 +89,233 @@ __device__ __forceinline__ uint32_t token_key(const EmbedGradArgs& a, int t) {
   return (id < 0 || id >= a.V || id == a.padding) ? (uint32_t)a.V : (uint32_t)id;
 }
 
-template <bool FIRST>
-__device__ __forceinline__ uint32_t sort_key(const EmbedGradArgs& a, int src, int t) {
-  return FIRST ? token_key(a, t) : a.key[src][t];
+// One wave-step of a stable counting sort: lanes with equal digits find each
+// other with one ballot per digit bit and take consecutive places after the
+// digit's count so far (cnt, of this wave), which then moves on.
+__device__ __forceinline__ uint32_t wave_place(uint32_t* cnt, uint32_t digit, int bits, bool live, uint64_t below) {
+  uint64_t peers = __ballot(live);
+  for (int k = 0; k < bits; ++k) {
+    const uint64_t set = __ballot((digit >> k) & 1);
+    peers &= ((digit >> k) & 1) ? set : ~set;
+  }
+  const uint32_t rank = (uint32_t)__popcll(peers & below);
+  const uint32_t at = live ? cnt[digit] + rank : 0;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  if (live && rank == 0) cnt[digit] += (uint32_t)__popcll(peers);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  return at;
 }
 
-// Digit counts of each sort workgroup's tokens; the workgroups beyond them
-// clear seg (first pass only).
-template <bool FIRST>
-__global__ void __launch_bounds__(256) embed_hist_kernel(const EmbedGradArgs a, int src, int shift, int nblk) {
+// Exclusive scan of v over the workgroup's threads; tmp holds one word per wave.
+template <int THREADS>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  uint32_t s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t t = __shfl_up(s, d, 64);
+    if (lane >= d) s += t;
+  }
+  if (lane == 63) tmp[wave] = s;
+  __syncthreads();
+  uint32_t base = 0;
+  for (int w = 0; w < wave; ++w) base += tmp[w];
+  __syncthreads();
+  return base + s - v;
+}
+
+// Clears seg and the long-row count (and hist, if given) with workgroups
+// first .. first + n of the launch.
+__device__ __forceinline__ void clear_for_rows(const EmbedGradArgs& a, int first, int threads, uint32_t* hist,
+                                               int64_t hist_n) {
+  const int64_t i0 = (int64_t)(blockIdx.x - first) * threads + threadIdx.x;
+  const int64_t step = (int64_t)(gridDim.x - first) * threads;
+  for (int64_t i = i0; i < a.V; i += step) a.seg[i] = int2{0, 0};
+  for (int64_t i = i0; i < hist_n; i += step) hist[i] = 0;
+  if (i0 == 0) *a.long_count = 0;
+}
+
+// Up to kEmbedSmall tokens: all passes in the first workgroup, tokens in
+// registers between them.  Wave w holds tokens [512 w, 512 w + 512).
+__global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradArgs a) {
+  constexpr int I = kEmbedSmall / 1024;
+  __shared__ uint32_t skey[kEmbedSmall], spos[kEmbedSmall];
+  __shared__ uint32_t cnt[16][256];
+  __shared__ uint32_t tmp[16];
+  if (blockIdx.x > 0) {
+    clear_for_rows(a, 1, 1024, nullptr, 0);
+    return;
+  }
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint64_t below = (1ull << lane) - 1;
+  const int t0 = wave * (I * 64) + lane;
+  uint32_t key[I], pos[I];
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int t = t0 + i * 64;
+    key[i] = t < a.T ? token_key(a, t) : 0;
+    pos[i] = t;
+  }
+  for (int p = 0; p < a.passes; ++p) {
+    const int shift = 8 * p;
+    for (int b = threadIdx.x; b < 16 * 256; b += 1024) cnt[b >> 8][b & 255] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < I; ++i)
+      if (t0 + i * 64 < a.T) atomicAdd(&cnt[wave][(key[i] >> shift) & 255], 1u);  // whole numbers: any order
+    __syncthreads();
+    uint32_t sum = 0;
+    if (threadIdx.x < 256)
+#pragma unroll
+      for (int w = 0; w < 16; ++w) sum += cnt[w][threadIdx.x];
+    uint32_t at = block_scan<1024>(sum, tmp);
+    if (threadIdx.x < 256)
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        const uint32_t n = cnt[w][threadIdx.x];
+        cnt[w][threadIdx.x] = at;
+        at += n;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const bool live = t0 + i * 64 < a.T;
+      const uint32_t q = wave_place(cnt[wave], (key[i] >> shift) & 255, 8, live, below);
+      if (live) {
+        skey[q] = key[i];
+        spos[q] = pos[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      const int t = t0 + i * 64;
+      if (t < a.T) {
+        key[i] = skey[t];
+        pos[i] = spos[t];
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int t = t0 + i * 64;
+    if (t < a.T) {
+      a.key[0][t] = key[i];
+      a.pos[0][t] = pos[i];
+    }
+  }
+}
+
+// More tokens: per pass the digit counts of each workgroup's tokens (the
+// first pass counts here, the later ones while the pass before moves the
+// tokens), their running sums over the workgroups, and the move.
+__global__ void __launch_bounds__(256) embed_hist_kernel(const EmbedGradArgs a, int nblk) {
   __shared__ uint32_t cnt[1 << kSortMaxBits];
   const int bins = 1 << a.bits;
-  if (FIRST && (int)blockIdx.x >= nblk) {
-    const int64_t n = a.V;
-    for (int64_t i = (int64_t)(blockIdx.x - nblk) * 256 + threadIdx.x; i < n; i += (int64_t)(gridDim.x - nblk) * 256)
-      a.seg[i] = int2{0, 0};
+  if ((int)blockIdx.x >= nblk) {
+    clear_for_rows(a, nblk, 256, a.passes > 1 ? a.hist[1] : nullptr, a.passes > 1 ? (int64_t)nblk * bins : 0);
     return;
   }
   for (int b = threadIdx.x; b < bins; b += 256) cnt[b] = 0;
   __syncthreads();
-  const int t0 = blockIdx.x * kSortItems;
 #pragma unroll
   for (int i = 0; i < kSortItems / 256; ++i) {
-    const int t = t0 + i * 256 + threadIdx.x;
-    if (t < a.T) atomicAdd(&cnt[(sort_key<FIRST>(a, src, t) >> shift) & (bins - 1)], 1u);  // whole numbers: any order
+    const int t = blockIdx.x * kSortItems + i * 256 + threadIdx.x;
+    if (t < a.T) atomicAdd(&cnt[token_key(a, t) & (bins - 1)], 1u);
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += 256) a.hist[(int64_t)blockIdx.x * bins + b] = cnt[b];
+  for (int b = threadIdx.x; b < bins; b += 256) a.hist[0][(int64_t)blockIdx.x * bins + b] = cnt[b];
 }
 
-// hist[k][b] becomes the first sorted position of workgroup k's tokens with
-// digit b.  One workgroup, thread b for digit b.
-__global__ void __launch_bounds__(1024) embed_scan_kernel(uint32_t* hist, int nblk, int bins) {
-  __shared__ uint32_t tot[1024];
-  const int b = threadIdx.x;
+// hist[k][b] becomes the tokens with digit b in workgroups before k; total[b]
+// all of them.  64 digits per workgroup, four waves with a quarter of the k each.
+__global__ void __launch_bounds__(256) embed_scan_kernel(uint32_t* hist, uint32_t* total, int nblk, int bins) {
+  __shared__ uint32_t part[4][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int b = blockIdx.x * 64 + lane;
+  const int lo = nblk * w / 4, hi = nblk * (w + 1) / 4;
   uint32_t sum = 0;
   if (b < bins) {
 #pragma unroll 8
-    for (int k = 0; k < nblk; ++k) sum += hist[(int64_t)k * bins + b];
+    for (int k = lo; k < hi; ++k) sum += hist[(int64_t)k * bins + b];
   }
-  tot[b] = sum;
+  part[w][lane] = sum;
   __syncthreads();
-  for (int d = 1; d < 1024; d <<= 1) {
-    const uint32_t v = b >= d ? tot[b - d] : 0;
-    __syncthreads();
-    tot[b] += v;
-    __syncthreads();
-  }
   if (b >= bins) return;
-  uint32_t at = tot[b] - sum;
-  for (int k0 = 0; k0 < nblk; k0 += 8) {
+  uint32_t at = 0;
+  for (int q = 0; q < w; ++q) at += part[q][lane];
+  if (w == 3) total[b] = at + sum;
+  for (int k0 = lo; k0 < hi; k0 += 8) {
     uint32_t v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = k0 + i < nblk ? hist[(int64_t)(k0 + i) * bins + b] : 0;
+    for (int i = 0; i < 8; ++i) v[i] = k0 + i < hi ? hist[(int64_t)(k0 + i) * bins + b] : 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (k0 + i < nblk) {
+      if (k0 + i < hi) {
         hist[(int64_t)(k0 + i) * bins + b] = at;
         at += v[i];
       }
   }
 }
 
-// Moves each token to its sorted position.  A wave owns 512 consecutive
-// tokens and takes them 64 at a time in order, so equal digits keep their
-// order: lanes with the same digit find each other with one ballot per digit
-// bit, and the count of that digit so far is kept per wave in LDS.
-template <bool FIRST>
-__global__ void __launch_bounds__(256) embed_scatter_kernel(const EmbedGradArgs a, int src, int shift) {
+// Moves each token to its place by the pass's digit; a wave owns consecutive
+// tokens and takes them 64 at a time in order, so equal digits keep theirs.
+template <bool FIRST, bool LAST>
+__global__ void __launch_bounds__(256) embed_scatter_kernel(const EmbedGradArgs a, int pass) {
+  constexpr int I = kSortItems / 256;
   __shared__ uint32_t cnt[4][1 << kSortMaxBits];
-  const int bins = 1 << a.bits;
+  __shared__ uint32_t tmp[4];
+  const int bins = 1 << a.bits, shift = pass * a.bits, src = pass & 1;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int t0 = blockIdx.x * kSortItems + wave * (kSortItems / 4);
+  const int t0 = blockIdx.x * kSortItems + wave * (I * 64) + lane;
   for (int b = threadIdx.x; b < 4 * bins; b += 256) cnt[b >> a.bits][b & (bins - 1)] = 0;
   __syncthreads();
-  uint32_t key[kSortItems / 256];
+  uint32_t key[I];
 #pragma unroll
-  for (int i = 0; i < kSortItems / 256; ++i) {
-    const int t = t0 + i * 64 + lane;
-    key[i] = t < a.T ? sort_key<FIRST>(a, src, t) : 0;
+  for (int i = 0; i < I; ++i) {
+    const int t = t0 + i * 64;
+    key[i] = t < a.T ? (FIRST ? token_key(a, t) : a.key[src][t]) : 0;
     if (t < a.T) atomicAdd(&cnt[wave][(key[i] >> shift) & (bins - 1)], 1u);
   }
-  __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += 256) {
-    uint32_t at = a.hist[(int64_t)blockIdx.x * bins + b];
+  // thread x: digits [x q, x q + q)
+  const int q = (bins + 255) / 256, b0 = threadIdx.x * q;
+  uint32_t tot[4], sum = 0;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t n = cnt[w][b];
-      cnt[w][b] = at;
-      at += n;
+  for (int i = 0; i < 4; ++i) {
+    tot[i] = i < q && b0 + i < bins ? a.total[b0 + i] : 0;
+    sum += tot[i];
+  }
+  uint32_t base = block_scan<256>(sum, tmp);  // its barriers also order the counts above
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = b0 + i;
+    if (i < q && b < bins) {
+      uint32_t at = base + a.hist[src][(int64_t)blockIdx.x * bins + b];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t n = cnt[w][b];
+        cnt[w][b] = at;
+        at += n;
+      }
     }
+    base += tot[i];
   }
   __syncthreads();
   const uint64_t below = (1ull << lane) - 1;
 #pragma unroll
-  for (int i = 0; i < kSortItems / 256; ++i) {
-    const int t = t0 + i * 64 + lane;
+  for (int i = 0; i < I; ++i) {
+    const int t = t0 + i * 64;
     const bool live = t < a.T;
-    const uint32_t d = (key[i] >> shift) & (bins - 1);
-    uint64_t peers = __ballot(live);
-    for (int k = 0; k < a.bits; ++k) {
-      const uint64_t set = __ballot((d >> k) & 1);
-      peers &= ((d >> k) & 1) ? set : ~set;
-    }
-    const uint32_t rank = (uint32_t)__popcll(peers & below);
-    uint32_t at = 0;
+    const uint32_t at = wave_place(cnt[wave], (key[i] >> shift) & (bins - 1), a.bits, live, below);
     if (live) {
-      at = cnt[wave][d] + rank;
       a.key[src ^ 1][at] = key[i];
       a.pos[src ^ 1][at] = FIRST ? (uint32_t)t : a.pos[src][t];
+      if (!LAST)  // whole numbers: any order
+        atomicAdd(&a.hist[src ^ 1][(int64_t)(at / kSortItems) * bins + ((key[i] >> (shift + a.bits)) & (bins - 1))], 1u);
     }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    if (live && rank == 0) cnt[wave][d] += (uint32_t)__popcll(peers);
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
   }
 }
 
@@ -217,40 +330,48 @@ __device__ __forceinline__ void add_chunk(float (&acc)[VEC], const Chunk<TY, VEC
   for (int i = 0; i < VEC; ++i) acc[i] += v.get(i);
 }
 
-// Adds tokens pos[lo .. hi) (dout rows) at column chunk c, in order, four loads at a time.
-template <int TY, int VEC, class Pos>
-__device__ __forceinline__ void add_tokens(const EmbedGradArgs& a, Pos pos, int lo, int hi, int c,
-                                           float (&acc)[VEC]) {
-  typedef Chunk<TY, VEC> C;
-  const typename Elem<TY>::raw* base = (const typename Elem<TY>::raw*)a.dout;
+// Adds tokens pos(lo) .. pos(hi - 1) (dout rows) at column d, in order, U loads at a time.
+template <int TY, bool TAIL, int U, class Pos>
+__device__ __forceinline__ void add_tokens(const EmbedGradArgs& a, Pos pos, int lo, int hi, int d,
+                                           float (&acc)[kWide<TY>]) {
+  typedef Chunk<TY, kWide<TY>> C;
+  const typename C::raw* base = (const typename C::raw*)a.dout + d;
   int p = lo;
-  for (; p + 4 <= hi; p += 4) {
-    C v[4];
+  for (; p + U <= hi; p += U) {
+    C v[U];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ((const C*)(base + (int64_t)pos[p + i] * a.ldg))[c];
+    for (int i = 0; i < U; ++i) v[i].template load<TAIL>(base + (int64_t)pos(p + i) * a.ldg, a.D - d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) add_chunk<TY, VEC>(acc, v[i]);
+    for (int i = 0; i < U; ++i) add_chunk(acc, v[i]);
   }
-  for (; p < hi; ++p) add_chunk<TY, VEC>(acc, ((const C*)(base + (int64_t)pos[p] * a.ldg))[c]);
+  for (; p < hi; ++p) {
+    C v;
+    v.template load<TAIL>(base + (int64_t)pos(p) * a.ldg, a.D - d);
+    add_chunk(acc, v);
+  }
 }
 
-// Adds the sums of whole chunks lo .. hi.
-template <int VEC>
-__device__ __forceinline__ void add_partials(const EmbedGradArgs& a, int lo, int hi, int c, float (&acc)[VEC]) {
+// Adds the sums of whole chunks lo .. hi - 1.
+template <int VEC, bool TAIL>
+__device__ __forceinline__ void add_partials(const EmbedGradArgs& a, int lo, int hi, int d, float (&acc)[VEC]) {
   typedef Chunk<LL_F32, VEC> F;
+  const uint32_t* base = (const uint32_t*)a.partial + d;
   int p = lo;
   for (; p + 4 <= hi; p += 4) {
     F v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = ((const F*)(a.partial + (int64_t)(p + i) * a.D))[c];
+    for (int i = 0; i < 4; ++i) v[i].template load<TAIL>(base + (int64_t)(p + i) * a.D, a.D - d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) add_chunk<LL_F32, VEC>(acc, v[i]);
+    for (int i = 0; i < 4; ++i) add_chunk(acc, v[i]);
   }
-  for (; p < hi; ++p) add_chunk<LL_F32, VEC>(acc, ((const F*)(a.partial + (int64_t)p * a.D))[c]);
+  for (; p < hi; ++p) {
+    F v;
+    v.template load<TAIL>(base + (int64_t)p * a.D, a.D - d);
+    add_chunk(acc, v);
+  }
 }
 
 // Sum over the workgroup's groups in group order; the first group gets it.
-// red holds 256 * VEC floats.
 template <int VEC>
 __device__ __forceinline__ void groups_sum(float* red, int lx_log2, int x, int g, float (&acc)[VEC]) {
   const int groups = 256 >> lx_log2;
@@ -265,12 +386,14 @@ __device__ __forceinline__ void groups_sum(float* red, int lx_log2, int x, int g
   }
 }
 
-// Row bounds in the sorted order, and the sums of the chunks of sorted
-// positions that belong to one row whole.
-template <int TY, int VEC>
+// Row bounds in the sorted order, the rows that hold a whole chunk of sorted
+// positions, and the sums of those chunks.
+template <int TY, bool TAIL>
 __global__ void __launch_bounds__(256) embed_chunk_kernel(const EmbedGradArgs a, int src, int lx_log2) {
+  constexpr int VEC = kWide<TY>;
   __shared__ float red[256 * VEC];
   const uint32_t* key = a.key[src];
+  const uint32_t* pos = a.pos[src];
   const int p0 = blockIdx.x * kEmbedChunk;
   if (blockIdx.y == 0 && threadIdx.x < kEmbedChunk) {
     const int p = p0 + threadIdx.x;
@@ -285,180 +408,241 @@ __global__ void __launch_bounds__(256) embed_chunk_kernel(const EmbedGradArgs a,
   if (p0 + kEmbedChunk > a.T) return;
   const uint32_t k0 = key[p0];
   if (key[p0 + kEmbedChunk - 1] != k0 || (int64_t)k0 >= a.V) return;  // uniform
+  // the first whole chunk of its row: sorted keys, so the one before is whole if it starts with the same key
+  if (blockIdx.y == 0 && threadIdx.x == 0 && (p0 == 0 || key[p0 - kEmbedChunk] != k0))
+    a.long_rows[atomicAdd(a.long_count, 1u)] = k0;
   const int lx = 1 << lx_log2;
   const int x = threadIdx.x & (lx - 1), g = threadIdx.x >> lx_log2;
   const int groups = 256 >> lx_log2;
-  const int chunks = a.D / VEC;
   const int per = (kEmbedChunk + groups - 1) / groups;
-  for (int c0 = blockIdx.y * lx; c0 < chunks; c0 += gridDim.y * lx) {
-    const int c = c0 + x;
+  const int lo = p0 + min(g * per, kEmbedChunk), hi = p0 + min((g + 1) * per, kEmbedChunk);
+  for (int d0 = blockIdx.y * lx * VEC; d0 < a.D; d0 += gridDim.y * lx * VEC) {
+    const int d = d0 + x * VEC;
     float acc[VEC] = {};
-    if (c < chunks)
-      add_tokens<TY, VEC>(a, a.pos[src], p0 + min(g * per, kEmbedChunk), p0 + min((g + 1) * per, kEmbedChunk), c, acc);
+    if (d < a.D) add_tokens<TY, TAIL, 4>(a, [&](int p) { return pos[p]; }, lo, hi, d, acc);
     groups_sum<VEC>(red, lx_log2, x, g, acc);
-    if (g == 0 && c < chunks) {
+    if (g == 0 && d < a.D) {
       Chunk<LL_F32, VEC> o;
 #pragma unroll
       for (int i = 0; i < VEC; ++i) o.put(i, acc[i]);
-      ((Chunk<LL_F32, VEC>*)(a.partial + (int64_t)blockIdx.x * a.D))[c] = o;
+      o.template store<TAIL>((uint32_t*)a.partial + (int64_t)blockIdx.x * a.D + d, a.D - d);
     }
   }
 }
 
-template <int TY, int VEC>
-__device__ __forceinline__ void write_row(const EmbedGradArgs& a, int64_t v, int c, const float (&acc)[VEC]) {
+template <int TY, bool TAIL>
+__device__ __forceinline__ void write_row(const EmbedGradArgs& a, int64_t v, int d, const float (&acc)[kWide<TY>]) {
+  constexpr int VEC = kWide<TY>;
   typedef Chunk<TY, VEC> C;
-  C* dst = (C*)((typename Elem<TY>::raw*)a.dw + v * a.ldw) + c;
+  typename C::raw* dst = (typename C::raw*)a.dw + v * a.ldw + d;
   C o;
   if (a.accumulate) {
-    const C old = *dst;
+    C old;
+    old.template load<TAIL>(dst, a.D - d);
 #pragma unroll
     for (int i = 0; i < VEC; ++i) o.put(i, old.get(i) + acc[i] * a.scale);
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) o.put(i, acc[i] * a.scale);
   }
-  *dst = o;
+  o.template store<TAIL>(dst, a.D - d);
 }
 
 // Rows a group handles one after the other.
 constexpr int kRowsPerGroup = 8;
 
-// The rows of dw: a group sums a row of up to kEmbedChunk tokens by itself;
-// the groups share the longer ones.  DIRECT (few tokens): the workgroup first
-// picks its rows' tokens from ids and orders them by (row, position) in LDS.
-template <int TY, int VEC, bool DIRECT>
-__global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedGradArgs a, int src, int lx_log2) {
+// The rows of dw after a sort.  The first `long_blocks` workgroups share out
+// the rows that hold a whole chunk, a block of columns at a time: loose tokens
+// in front, whole chunks, loose tokens behind, split over the groups and
+// joined in their order.  They come first because they take longest.  In the
+// other workgroups a group sums a row by itself.
+template <int TY, bool TAIL>
+__global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedGradArgs a, int src, int lx_log2,
+                                                         int long_blocks, int col_blocks) {
+  constexpr int VEC = kWide<TY>;
   __shared__ float red[256 * VEC];
-  __shared__ uint32_t list[DIRECT ? kEmbedDirect : 1], order[DIRECT ? kEmbedDirect : 1];
+  const uint32_t* order = a.pos[src];
+  auto pos = [&](int p) { return order[p]; };
+  const int lx = 1 << lx_log2;
+  const int x = threadIdx.x & (lx - 1), g = threadIdx.x >> lx_log2;
+  const int groups = 256 >> lx_log2;
+  if ((int)blockIdx.x < long_blocks) {
+    const int all_cols = (a.D + lx * VEC - 1) / (lx * VEC);
+    const int64_t items = (int64_t)*a.long_count * all_cols;
+    for (int64_t it = blockIdx.x; it < items; it += long_blocks) {
+      const int64_t v = a.long_rows[it / all_cols];
+      const int d = ((int)(it % all_cols) * lx + x) * VEC;
+      const int2 s = a.seg[v];
+      const int h0 = (s.x + kEmbedChunk - 1) / kEmbedChunk * kEmbedChunk, h1 = s.y / kEmbedChunk * kEmbedChunk;
+      const int nh = h0 - s.x, nc = (h1 - h0) / kEmbedChunk, n = nh + nc + (s.y - h1);
+      const int lo = (int)((int64_t)n * g / groups), hi = (int)((int64_t)n * (g + 1) / groups);
+      float acc[VEC] = {};
+      if (d < a.D) {
+        add_tokens<TY, TAIL, 4>(a, pos, s.x + lo, s.x + min(hi, nh), d, acc);
+        const int k0 = h0 / kEmbedChunk - nh;  // item i is chunk k0 + i
+        add_partials<VEC, TAIL>(a, k0 + max(lo, nh), k0 + min(hi, nh + nc), d, acc);
+        const int b0 = h1 - nh - nc;           // item i is sorted position b0 + i
+        add_tokens<TY, TAIL, 4>(a, pos, b0 + max(lo, nh + nc), b0 + hi, d, acc);
+      }
+      groups_sum<VEC>(red, lx_log2, x, g, acc);
+      if (g == 0 && d < a.D) write_row<TY, TAIL>(a, v, d, acc);
+    }
+    return;
+  }
+  const int item = blockIdx.x - long_blocks;
+  const int64_t v0 = (int64_t)(item / col_blocks) * groups * kRowsPerGroup;
+  const int cb = item % col_blocks;
+  for (int i = 0; i < kRowsPerGroup; ++i) {
+    const int64_t v = v0 + i * groups + g;
+    if (v >= a.V) break;
+    const int2 s = a.seg[v];
+    if ((s.x + kEmbedChunk - 1) / kEmbedChunk < s.y / kEmbedChunk) continue;  // holds a whole chunk
+    if (a.accumulate && s.x == s.y) continue;
+    for (int d = (cb * lx + x) * VEC; d < a.D; d += col_blocks * lx * VEC) {
+      float acc[VEC] = {};
+      add_tokens<TY, TAIL, 4>(a, pos, s.x, s.y, d, acc);
+      write_row<TY, TAIL>(a, v, d, acc);
+    }
+  }
+}
+
+// Few tokens: each workgroup picks its rows' tokens from ids itself, orders
+// them by (row, position) in LDS, and sums; rows of more than kEmbedChunk
+// tokens with all groups together.
+template <int TY, bool TAIL>
+__global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, int lx_log2, int col_blocks) {
+  constexpr int VEC = kWide<TY>;
+  __shared__ float red[256 * VEC];
+  __shared__ uint32_t list[kEmbedDirect], order[kEmbedDirect];
   __shared__ int wcnt[4];
   __shared__ int2 seg[256 * kRowsPerGroup];
   const int lx = 1 << lx_log2;
   const int x = threadIdx.x & (lx - 1), g = threadIdx.x >> lx_log2;
   const int groups = 256 >> lx_log2;
   const int nrows = groups * kRowsPerGroup;
-  const int64_t v0 = (int64_t)blockIdx.x * nrows;
-  const int chunks = a.D / VEC;
-  if constexpr (DIRECT) {
-    for (int r = threadIdx.x; r < nrows; r += 256) seg[r] = int2{0, 0};
-    int n = 0;  // matching tokens so far: local row << 16 | token
-    for (int t0 = 0; t0 < a.T; t0 += 256) {
-      const int t = t0 + threadIdx.x;
-      const uint32_t k = t < a.T ? token_key(a, t) : (uint32_t)a.V;
-      const bool hit = (int64_t)k < a.V && (int64_t)k >= v0 && (int64_t)k < v0 + nrows;
-      const uint64_t m = __ballot(hit);
-      const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-      if (lane == 0) wcnt[wave] = __popcll(m);
-      __syncthreads();
-      int at = n;
-      for (int w = 0; w < wave; ++w) at += wcnt[w];
-      if (hit) list[at + __popcll(m & ((1ull << lane) - 1))] = (uint32_t)((int64_t)k - v0) << 16 | (uint32_t)t;
-      n += wcnt[0] + wcnt[1] + wcnt[2] + wcnt[3];
-      __syncthreads();
+  const int64_t v0 = (int64_t)(blockIdx.x / col_blocks) * nrows;
+  const int cb = blockIdx.x % col_blocks;
+  for (int r = threadIdx.x; r < nrows; r += 256) seg[r] = int2{0, 0};
+  int n = 0;  // matching tokens so far: local row << 16 | token
+  for (int t0 = 0; t0 < a.T; t0 += 256) {
+    const int t = t0 + threadIdx.x;
+    const uint32_t k = t < a.T ? token_key(a, t) : (uint32_t)a.V;
+    const bool hit = (int64_t)k < a.V && (int64_t)k >= v0 && (int64_t)k < v0 + nrows;
+    const uint64_t m = __ballot(hit);
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    if (lane == 0) wcnt[wave] = __popcll(m);
+    __syncthreads();
+    int at = n;
+    for (int w = 0; w < wave; ++w) at += wcnt[w];
+    if (hit) list[at + __popcll(m & ((1ull << lane) - 1))] = (uint32_t)((int64_t)k - v0) << 16 | (uint32_t)t;
+    n += wcnt[0] + wcnt[1] + wcnt[2] + wcnt[3];
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < n; i += 256) {
+    const uint32_t e = list[i];
+    int rank = 0, first = 0, last = 0;
+    for (int j = 0; j < n; ++j) {
+      const uint32_t f = list[j];
+      rank += f < e;
+      first += (f >> 16) < (e >> 16);
+      last += (f >> 16) <= (e >> 16);
     }
-    for (int i = threadIdx.x; i < n; i += 256) {
-      const uint32_t e = list[i];
-      int rank = 0, first = 0, last = 0;
-      for (int j = 0; j < n; ++j) {
-        const uint32_t f = list[j];
-        rank += f < e;
-        first += (f >> 16) < (e >> 16);
-        last += (f >> 16) <= (e >> 16);
-      }
-      order[rank] = e & 0xFFFF;
-      if (rank == first) seg[e >> 16] = int2{first, last};
-    }
-  } else {
-    for (int r = threadIdx.x; r < nrows; r += 256) seg[r] = v0 + r < a.V ? a.seg[v0 + r] : int2{0, 0};
+    order[rank] = e & 0xFFFF;
+    if (rank == first) seg[e >> 16] = int2{first, last};
   }
   __syncthreads();
-  auto pos = [&](int p) { return DIRECT ? order[p] : a.pos[src][p]; };
-  struct PosOf {
-    decltype(pos)& f;
-    __device__ uint32_t operator[](int p) const { return f(p); }
-  } posof{pos};
-  for (int c0 = blockIdx.y * lx; c0 < chunks; c0 += gridDim.y * lx) {
-    const int c = c0 + x;
+  auto pos = [&](int p) { return order[p]; };
+  for (int d0 = cb * lx * VEC; d0 < a.D; d0 += col_blocks * lx * VEC) {
+    const int d = d0 + x * VEC;
     for (int i = 0; i < kRowsPerGroup; ++i) {
       const int r = i * groups + g;
-      const int64_t v = v0 + r;
       const int2 s = seg[r];
-      if (v >= a.V || c >= chunks || s.y - s.x > kEmbedChunk || (a.accumulate && s.y == s.x)) continue;
+      if (v0 + r >= a.V || d >= a.D || s.y - s.x > kEmbedChunk || (a.accumulate && s.y == s.x)) continue;
       float acc[VEC] = {};
-      add_tokens<TY, VEC>(a, posof, s.x, s.y, c, acc);
-      write_row<TY, VEC>(a, v, c, acc);
+      add_tokens<TY, TAIL, 4>(a, pos, s.x, s.y, d, acc);
+      write_row<TY, TAIL>(a, v0 + r, d, acc);
     }
-    for (int r = 0; r < nrows; ++r) {  // long rows, all groups together (uniform)
+    if (n <= kEmbedChunk) continue;
+    for (int r = 0; r < nrows; ++r) {  // uniform
       const int2 s = seg[r];
-      if (s.y - s.x <= kEmbedChunk) continue;
-      // loose tokens in front, whole chunks, loose tokens behind
-      int h0 = s.y, h1 = s.y;
-      if (!DIRECT) {
-        h0 = (s.x + kEmbedChunk - 1) / kEmbedChunk * kEmbedChunk;
-        h1 = s.y / kEmbedChunk * kEmbedChunk;
-        if (h0 >= h1) h0 = h1 = s.y;
-      }
-      const int nh = h0 - s.x, nc = (h1 - h0) / kEmbedChunk, n = nh + nc + (s.y - h1);
-      const int lo = (int)((int64_t)n * g / groups), hi = (int)((int64_t)n * (g + 1) / groups);
+      const int len = s.y - s.x;
+      if (len <= kEmbedChunk) continue;
       float acc[VEC] = {};
-      if (c < chunks) {
-        add_tokens<TY, VEC>(a, posof, s.x + lo, s.x + min(hi, nh), c, acc);
-        if (nc > 0) {
-          const int k0 = h0 / kEmbedChunk - nh;  // item i is chunk k0 + i
-          add_partials<VEC>(a, k0 + max(lo, nh), k0 + min(hi, nh + nc), c, acc);
-        }
-        const int b0 = h1 - nh - nc;             // item i is sorted position b0 + i
-        add_tokens<TY, VEC>(a, posof, b0 + max(lo, nh + nc), b0 + hi, c, acc);
-      }
+      if (d < a.D) add_tokens<TY, TAIL, 4>(a, pos, s.x + len * g / groups, s.x + len * (g + 1) / groups, d, acc);
       groups_sum<VEC>(red, lx_log2, x, g, acc);
-      if (g == 0 && c < chunks) write_row<TY, VEC>(a, v0 + r, c, acc);
+      if (g == 0 && d < a.D) write_row<TY, TAIL>(a, v0 + r, d, acc);
     }
   }
 }
 
-template <int TY, int VEC>
+__global__ void __launch_bounds__(256) embed_clear_kernel(uint32_t* p, int64_t n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
+}
+
+static hipError_t launch_clear(uint32_t* p, int64_t n, int cus, hipStream_t s) {
+  const int64_t blocks = std::min<int64_t>((n + 255) / 256, 4ll * cus);
+  hipLaunchKernelGGL(embed_clear_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p, n);
+  return hipGetLastError();
+}
+
+template <int TY, bool TAIL>
 static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream_t s) {
-  const int chunks = a.D / VEC;
+  constexpr int VEC = kWide<TY>;
+  const int chunks = (a.D + VEC - 1) / VEC;
   const int lx = log2_up(chunks, 6);
   const int nrows = (256 >> lx) * kRowsPerGroup;
   const int64_t rb = (a.V + nrows - 1) / nrows;
-  if (rb > 0x7FFFFFFF) return hipErrorInvalidValue;
   // workgroups along the columns only where the rows alone are few
-  const int cb_all = (chunks + (1 << lx) - 1) >> lx;
-  const int cb = (int)std::min<int64_t>(cb_all, std::max<int64_t>(1, 16 * (int64_t)cus / rb));
+  const int all_cols = (chunks + (1 << lx) - 1) >> lx;
+  const int cb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / rb));
+  if (rb * cb > 0x3FFFFFFF) return hipErrorInvalidValue;
+  if (a.T <= kEmbedDirect) {
+    hipLaunchKernelGGL((embed_few_kernel<TY, TAIL>), dim3((unsigned)(rb * cb)), dim3(256), 0, s, a, lx, cb);
+    return hipGetLastError();
+  }
   int src = 0;
-  if (a.T > kEmbedDirect) {
+  const int clear = (int)std::min<int64_t>((a.V + 1023) / 1024, 4 * cus);
+  if (a.T <= kEmbedSmall) {
+    hipLaunchKernelGGL(embed_small_sort_kernel, dim3(1 + clear), dim3(1024), 0, s, a);
+  } else {
     const int nblk = (a.T + kSortItems - 1) / kSortItems;
-    const int clear = (int)std::min<int64_t>((a.V + 1023) / 1024, 4 * cus);
+    hipLaunchKernelGGL(embed_hist_kernel, dim3(nblk + clear), dim3(256), 0, s, a, nblk);
     for (int p = 0; p < a.passes; ++p) {
-      const int shift = p * a.bits;
-      if (p == 0)
-        hipLaunchKernelGGL((embed_hist_kernel<true>), dim3(nblk + clear), dim3(256), 0, s, a, src, shift, nblk);
+      const bool first = p == 0, last = p == a.passes - 1;
+      hipLaunchKernelGGL(embed_scan_kernel, dim3(((1 << a.bits) + 63) / 64), dim3(256), 0, s, a.hist[p & 1], a.total,
+                         nblk, 1 << a.bits);
+      if (p > 0 && !last) {  // the next pass counts into what this one has read
+        const hipError_t e = launch_clear(a.hist[(p + 1) & 1], (int64_t)nblk << a.bits, cus, s);
+        if (e != hipSuccess) return e;
+      }
+      if (first && last)
+        hipLaunchKernelGGL((embed_scatter_kernel<true, true>), dim3(nblk), dim3(256), 0, s, a, p);
+      else if (first)
+        hipLaunchKernelGGL((embed_scatter_kernel<true, false>), dim3(nblk), dim3(256), 0, s, a, p);
+      else if (last)
+        hipLaunchKernelGGL((embed_scatter_kernel<false, true>), dim3(nblk), dim3(256), 0, s, a, p);
       else
-        hipLaunchKernelGGL((embed_hist_kernel<false>), dim3(nblk), dim3(256), 0, s, a, src, shift, nblk);
-      hipLaunchKernelGGL(embed_scan_kernel, dim3(1), dim3(1024), 0, s, a.hist, nblk, 1 << a.bits);
-      if (p == 0)
-        hipLaunchKernelGGL((embed_scatter_kernel<true>), dim3(nblk), dim3(256), 0, s, a, src, shift);
-      else
-        hipLaunchKernelGGL((embed_scatter_kernel<false>), dim3(nblk), dim3(256), 0, s, a, src, shift);
+        hipLaunchKernelGGL((embed_scatter_kernel<false, false>), dim3(nblk), dim3(256), 0, s, a, p);
       src ^= 1;
     }
-    const int nch = (a.T + kEmbedChunk - 1) / kEmbedChunk;
-    const int ccb = (int)std::min<int64_t>(cb_all, std::max<int64_t>(1, 16 * (int64_t)cus / nch));
-    hipLaunchKernelGGL((embed_chunk_kernel<TY, VEC>), dim3(nch, ccb), dim3(256), 0, s, a, src, lx);
-    hipLaunchKernelGGL((embed_rows_kernel<TY, VEC, false>), dim3((unsigned)rb, cb), dim3(256), 0, s, a, src, lx);
-  } else {
-    hipLaunchKernelGGL((embed_rows_kernel<TY, VEC, true>), dim3((unsigned)rb, cb), dim3(256), 0, s, a, 0, lx);
   }
+  const int nch = (a.T + kEmbedChunk - 1) / kEmbedChunk;
+  const int ccb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / nch));
+  const int lb = (int)std::min<int64_t>((int64_t)(a.T / kEmbedChunk) * all_cols, 4 * cus);
+  hipLaunchKernelGGL((embed_chunk_kernel<TY, TAIL>), dim3(nch, ccb), dim3(256), 0, s, a, src, lx);
+  hipLaunchKernelGGL((embed_rows_kernel<TY, TAIL>), dim3((unsigned)(lb + rb * cb)), dim3(256), 0, s, a, src, lx, lb,
+                     cb);
   return hipGetLastError();
 }
 
 hipError_t launch_embed_grad(const EmbedGradArgs& a, int type, int cus, hipStream_t s) {
-  const bool wide = wide_rows(a.dout, a.ldg, a.D, type) && wide_rows(a.dw, a.ldw, a.D, type);
   switch (type) {
-    case LL_BF16: return wide ? launch_embed_grad_t<LL_BF16, 8>(a, cus, s) : launch_embed_grad_t<LL_BF16, 1>(a, cus, s);
-    case LL_F16: return wide ? launch_embed_grad_t<LL_F16, 8>(a, cus, s) : launch_embed_grad_t<LL_F16, 1>(a, cus, s);
-    case LL_F32: return wide ? launch_embed_grad_t<LL_F32, 4>(a, cus, s) : launch_embed_grad_t<LL_F32, 1>(a, cus, s);
+    case LL_BF16:
+      return a.D % 8 ? launch_embed_grad_t<LL_BF16, true>(a, cus, s) : launch_embed_grad_t<LL_BF16, false>(a, cus, s);
+    case LL_F16:
+      return a.D % 8 ? launch_embed_grad_t<LL_F16, true>(a, cus, s) : launch_embed_grad_t<LL_F16, false>(a, cus, s);
+    case LL_F32:
+      return a.D % 4 ? launch_embed_grad_t<LL_F32, true>(a, cus, s) : launch_embed_grad_t<LL_F32, false>(a, cus, s);
     default: return hipErrorInvalidValue;
   }
 }

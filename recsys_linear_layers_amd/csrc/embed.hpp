@@ -15,13 +15,15 @@ struct EmbedArgs {
   float scale;
 };
 
-// Sorted positions per chunk whose sum is formed once, ahead of the rows, when
-// the whole chunk belongs to one row.
-constexpr int kEmbedChunk = 64;
-// Tokens up to which the rows find their tokens by themselves, without a sort.
+// Sorted positions per chunk; a chunk that belongs to one row whole is summed
+// once, ahead of the rows.
+constexpr int kEmbedChunk = 32;
+// Tokens up to which the rows find their tokens by themselves, without a sort,
 constexpr int kEmbedDirect = 512;
-// Tokens per workgroup of the sort, and its most digit values per pass.
-constexpr int kSortItems = 2048;
+// and up to which one workgroup sorts them in LDS.
+constexpr int kEmbedSmall = 8192;
+// Tokens per workgroup of the sort beyond that, and its most digit bits per pass.
+constexpr int kSortItems = 1024;
 constexpr int kSortMaxBits = 10;
 
 struct EmbedGradArgs {
@@ -36,10 +38,13 @@ struct EmbedGradArgs {
   // workspace (null when T <= kEmbedDirect)
   uint32_t* key[2];
   uint32_t* pos[2];
-  uint32_t* hist;   // [sort workgroups][1 << bits]
-  int2* seg;        // [V] sorted positions first, last + 1 of each row's tokens
-  float* partial;   // [T / kEmbedChunk][D] sums of whole chunks
-  int32_t bits, passes;
+  uint32_t* hist[2];    // by parity of the pass: [sort workgroups][1 << bits]
+  uint32_t* total;      // [1 << bits]
+  int2* seg;            // [V] sorted positions first, last + 1 of each row's tokens
+  float* partial;       // [T / kEmbedChunk][D] sums of whole chunks
+  uint32_t* long_count; // rows that hold a whole chunk,
+  uint32_t* long_rows;  // in any order
+  int32_t bits, passes; // digits; 8 bits where one workgroup sorts
 };
 
 hipError_t launch_embed(const EmbedArgs& a, int type, hipStream_t s);

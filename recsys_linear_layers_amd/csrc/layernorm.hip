@@ -18,21 +18,56 @@
 
 namespace ll {
 
-// Parameter column chunk as fp32, stored as TY or (param_f32) as fp32.
-template <int TY, int VEC>
-__device__ __forceinline__ void load_param(const void* p, int param_f32, int c, float dflt, float (&v)[VEC]) {
+// Parameter columns [d, d + VEC) as fp32, stored as TY or (param_f32) as fp32; n of them exist.
+template <int TY, int VEC, bool TAIL>
+__device__ __forceinline__ void load_param(const void* p, int param_f32, int d, int n, float dflt, float (&v)[VEC]) {
   if (!p) {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) v[i] = dflt;
   } else if (TY == LL_F32 || param_f32) {
+    Chunk<LL_F32, VEC> c;
+    c.template load<TAIL>((const uint32_t*)p + d, n);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = ((const float*)p)[(int64_t)c * VEC + i];
+    for (int i = 0; i < VEC; ++i) v[i] = c.get(i);
   } else {
-    const typename Elem<TY>::raw* q = (const typename Elem<TY>::raw*)p + (int64_t)c * VEC;
+    Chunk<TY, VEC> c;
+    c.template load<TAIL>((const typename Elem<TY>::raw*)p + d, n);
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) v[i] = Elem<TY>::get(q[i]);
+    for (int i = 0; i < VEC; ++i) v[i] = c.get(i);
   }
 }
+
+// The parameter columns of a lane, kept over its rows: as stored where that is
+// x's own type, else (REG false: fp32 beside 16-bit rows, twice the registers)
+// read again for each row, from L2.
+template <int TY, int VEC, int NCH, bool TAIL, bool REG>
+struct Params {
+  Chunk<TY, VEC> v[REG ? NCH : 1];
+  const void* p;
+  float dflt;
+  __device__ __forceinline__ void init(const void* p_, float dflt_, int d0, int step, int D) {
+    p = p_;
+    dflt = dflt_;
+    if constexpr (REG) {
+#pragma unroll
+      for (int k = 0; k < NCH; ++k) {
+        const int d = d0 + k * step;
+        if (p && d < D) v[k].template load<TAIL>((const typename Elem<TY>::raw*)p + d, D - d);
+        else
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) v[k].put(i, dflt);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(int k, int d, int n, float (&out)[VEC]) const {
+    if constexpr (REG) {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) out[i] = v[k].get(i);
+    } else {
+      load_param<TY, VEC, TAIL>(p, 1, d, n, dflt, out);
+    }
+  }
+};
 
 // Sum over the TPR lanes of one row (64: one wave; more: the row's waves,
 // through red, two floats per wave of the workgroup).
@@ -60,84 +95,117 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
   }
 }
 
-// TPR lanes hold a row in NCH chunks of VEC columns each; THREADS / TPR rows
-// per workgroup and step.
-template <int TY, int VEC, int TPR, int NCH, int THREADS>
+// One row of a lane's columns: NCH chunks of VEC, TPR chunks apart.  Lanes past
+// the row's end and rows past the last hold zeros.
+template <int TY, int VEC, int TPR, int NCH, bool TAIL>
+struct RowCols {
+  Chunk<TY, VEC> v[NCH];
+  __device__ __forceinline__ void load(const void* base, int64_t ld, int64_t r, bool live, int x, int D) {
+    const typename Elem<TY>::raw* row = (const typename Elem<TY>::raw*)base + (live ? r : 0) * ld;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k) {
+      const int d = (x + k * TPR) * VEC;
+      if (live && d < D) v[k].template load<TAIL>(row + d, D - d);
+      else v[k].clear();
+    }
+  }
+};
+
+// TPR lanes hold a row; THREADS / TPR rows per workgroup and step.  The next
+// row is loaded before this one's sums are joined, so that the loads run
+// behind the two barriers each of them takes.
+template <int TY, int VEC, int TPR, int NCH, int THREADS, bool TAIL, bool REG>
 __global__ void __launch_bounds__(THREADS) norm_kernel(const NormArgs a) {
   typedef Chunk<TY, VEC> C;
   typedef typename Elem<TY>::raw raw;
   __shared__ float red[THREADS / 64 * 2];
   constexpr int ROWS = THREADS / TPR;
   const int x = threadIdx.x % TPR, y = threadIdx.x / TPR;
-  const int chunks = a.D / VEC;
   const float cols = (float)a.D;
-  // every row group takes part in each step's barriers, rows past N as zeros
-  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += (int64_t)gridDim.x * ROWS) {
-    const int64_t r = r0 + y;
+  Params<TY, VEC, NCH, TAIL, REG> gamma, beta;
+  gamma.init(a.gamma, 1.f, x * VEC, TPR * VEC, a.D);
+  beta.init(a.beta, 0.f, x * VEC, TPR * VEC, a.D);
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t r = (int64_t)blockIdx.x * ROWS + y;
+  RowCols<TY, VEC, TPR, NCH, TAIL> cur, next;
+  cur.load(a.x, a.ldx, r, r < a.N, x, a.D);
+  // every row group takes part in each step's barriers
+  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += step, r += step) {
     const bool live = r < a.N;
-    C v[NCH];
-    const C* src = (const C*)((const raw*)a.x + r * a.ldx);
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int c = x + k * TPR;
-      if (live && c < chunks) v[k] = src[c];
-      else
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) v[k].e[i] = 0;
-    }
+    if (r0 + step < a.N) next.load(a.x, a.ldx, r + step, r + step < a.N, x, a.D);
     float s = 0.f, q = 0.f;
 #pragma unroll
     for (int k = 0; k < NCH; ++k)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) s += v[k].get(i);
+      for (int i = 0; i < VEC; ++i) s += cur.v[k].get(i);
     row_sum2<TPR, THREADS / 64>(s, q, red);
     const float mean = s / cols;
     s = 0.f;
 #pragma unroll
-    for (int k = 0; k < NCH; ++k)
-      if (x + k * TPR < chunks) {
+    for (int k = 0; k < NCH; ++k) {
+      const int n = a.D - (x + k * TPR) * VEC;  // columns of the row from this chunk on
+      if (n <= 0) continue;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          const float d = v[k].get(i) - mean;
-          s = fmaf(d, d, s);
-        }
+      for (int i = 0; i < VEC; ++i) {
+        const float d = TAIL && i >= n ? 0.f : cur.v[k].get(i) - mean;
+        s = fmaf(d, d, s);
       }
+    }
     row_sum2<TPR, THREADS / 64>(s, q, red);
     const float rstd = 1.f / sqrtf(s / cols + a.eps);
-    if (!live) continue;
-    C* dst = (C*)((raw*)a.y + r * a.ldy);
+    if (live) {
+      raw* dst = (raw*)a.y + r * a.ldy;
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int c = x + k * TPR;
-      if (c >= chunks) continue;
-      float g[VEC], b[VEC];
-      load_param<TY, VEC>(a.gamma, a.param_f32, c, 1.f, g);
-      load_param<TY, VEC>(a.beta, a.param_f32, c, 0.f, b);
-      C o;
+      for (int k = 0; k < NCH; ++k) {
+        const int d = (x + k * TPR) * VEC;
+        if (d >= a.D) continue;
+        float g[VEC], b[VEC];
+        gamma.get(k, d, a.D - d, g);
+        beta.get(k, d, a.D - d, b);
+        C o;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) o.put(i, fmaf((v[k].get(i) - mean) * rstd, g[i], b[i]));
-      dst[c] = o;
+        for (int i = 0; i < VEC; ++i) o.put(i, fmaf((cur.v[k].get(i) - mean) * rstd, g[i], b[i]));
+        o.template store<TAIL>(dst + d, a.D - d);
+      }
+      if (x == 0) {
+        if (a.mean) a.mean[r] = mean;
+        if (a.rstd) a.rstd[r] = rstd;
+      }
     }
-    if (x == 0) {
-      if (a.mean) a.mean[r] = mean;
-      if (a.rstd) a.rstd[r] = rstd;
-    }
+    cur = next;
   }
 }
 
-template <int TY, int VEC, int TPR, int NCH, int THREADS>
-static hipError_t norm_go(const NormArgs& a, int cus, hipStream_t s) {
+// Workgroups of `threads` of a kernel that a CU holds at once.
+static int per_cu(const void* kernel, int threads) {
+  int n = 0;
+  if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != hipSuccess || n < 1) n = 1;
+  return n;
+}
+
+template <int TY, int VEC, int TPR, int NCH, int THREADS, bool TAIL, bool REG>
+static hipError_t norm_launch(const NormArgs& a, int cus, hipStream_t s) {
   constexpr int ROWS = THREADS / TPR;
-  const int64_t blocks = std::min<int64_t>((a.N + ROWS - 1) / ROWS, (int64_t)cus * 64);
-  hipLaunchKernelGGL((norm_kernel<TY, VEC, TPR, NCH, THREADS>), dim3((unsigned)blocks), dim3(THREADS), 0, s, a);
+  const auto kernel = norm_kernel<TY, VEC, TPR, NCH, THREADS, TAIL, REG>;
+  static const int resident = per_cu((const void*)kernel, THREADS);
+  const int64_t blocks = std::min<int64_t>((a.N + ROWS - 1) / ROWS, (int64_t)cus * resident);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(THREADS), 0, s, a);
   return hipGetLastError();
+}
+
+template <int TY, int VEC, int TPR, int NCH, int THREADS, bool TAIL>
+static hipError_t norm_go(const NormArgs& a, int cus, hipStream_t s) {
+  if constexpr (TY != LL_F32) {
+    if (a.param_f32) return norm_launch<TY, VEC, TPR, NCH, THREADS, TAIL, false>(a, cus, s);
+  }
+  return norm_launch<TY, VEC, TPR, NCH, THREADS, TAIL, true>(a, cus, s);
 }
 
 // Rows too wide for registers: one workgroup per row, three passes over it
 // (the second and third mostly from L2).
 template <int TY>
 __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
-  typedef Chunk<TY, 1> C;
+  typedef Chunk<TY, 1> C;  // an element: get(0)
   typedef typename Elem<TY>::raw raw;
   __shared__ float red[32];
   const float cols = (float)a.D;
@@ -157,8 +225,8 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
     C* dst = (C*)((raw*)a.y + r * a.ldy);
     for (int c = threadIdx.x; c < a.D; c += 1024) {
       float g[1], b[1];
-      load_param<TY, 1>(a.gamma, a.param_f32, c, 1.f, g);
-      load_param<TY, 1>(a.beta, a.param_f32, c, 0.f, b);
+      load_param<TY, 1, false>(a.gamma, a.param_f32, c, 1, 1.f, g);
+      load_param<TY, 1, false>(a.beta, a.param_f32, c, 1, 0.f, b);
       C o;
       o.put(0, fmaf((src[c].get(0) - mean) * rstd, g[0], b[0]));
       dst[c] = o;
@@ -170,28 +238,26 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const NormArgs a) {
   }
 }
 
-// Columns a lane holds grow with the row, up to 32 where they move 16 bytes at
-// a time and 16 where they move one by one, before more lanes take part.
-template <int TY, int VEC>
+// A lane holds up to 32 columns before more lanes take part in a row.
+template <int TY, bool TAIL>
 static hipError_t launch_norm_t(const NormArgs& a, int cus, hipStream_t s) {
-  const int chunks = a.D / VEC;
-  constexpr int K = (VEC > 1 ? 32 : 16) / VEC;
-  if (chunks <= 64) return norm_go<TY, VEC, 64, 1, 256>(a, cus, s);
-  if (chunks <= 64 * (K / 2)) return norm_go<TY, VEC, 64, K / 2, 256>(a, cus, s);
-  if (chunks <= 256 * (K / 2)) return norm_go<TY, VEC, 256, K / 2, 256>(a, cus, s);
-  if (chunks <= 256 * K) return norm_go<TY, VEC, 256, K, 256>(a, cus, s);
-  if (a.D <= 16384) return norm_go<TY, VEC, 1024, 16 / VEC, 1024>(a, cus, s);
+  constexpr int VEC = kWide<TY>, K = 32 / VEC;
+  const int chunks = (a.D + VEC - 1) / VEC;
+  if (chunks <= 64) return norm_go<TY, VEC, 64, 1, 256, TAIL>(a, cus, s);
+  if (chunks <= 64 * (K / 2)) return norm_go<TY, VEC, 64, K / 2, 256, TAIL>(a, cus, s);
+  if (chunks <= 256 * (K / 2)) return norm_go<TY, VEC, 256, K / 2, 256, TAIL>(a, cus, s);
+  if (chunks <= 256 * K) return norm_go<TY, VEC, 256, K, 256, TAIL>(a, cus, s);
+  if (a.D <= 16384) return norm_go<TY, VEC, 1024, K / 2, 1024, TAIL>(a, cus, s);
   const int64_t blocks = std::min<int64_t>(a.N, (int64_t)cus * 64);
   hipLaunchKernelGGL((norm_long_kernel<TY>), dim3((unsigned)blocks), dim3(1024), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_norm(const NormArgs& a, int type, int cus, hipStream_t s) {
-  const bool wide = wide_rows(a.x, a.ldx, a.D, type) && wide_rows(a.y, a.ldy, a.D, type);
   switch (type) {
-    case LL_BF16: return wide ? launch_norm_t<LL_BF16, 8>(a, cus, s) : launch_norm_t<LL_BF16, 1>(a, cus, s);
-    case LL_F16: return wide ? launch_norm_t<LL_F16, 8>(a, cus, s) : launch_norm_t<LL_F16, 1>(a, cus, s);
-    case LL_F32: return wide ? launch_norm_t<LL_F32, 4>(a, cus, s) : launch_norm_t<LL_F32, 1>(a, cus, s);
+    case LL_BF16: return a.D % 8 ? launch_norm_t<LL_BF16, true>(a, cus, s) : launch_norm_t<LL_BF16, false>(a, cus, s);
+    case LL_F16: return a.D % 8 ? launch_norm_t<LL_F16, true>(a, cus, s) : launch_norm_t<LL_F16, false>(a, cus, s);
+    case LL_F32: return a.D % 4 ? launch_norm_t<LL_F32, true>(a, cus, s) : launch_norm_t<LL_F32, false>(a, cus, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -200,10 +266,10 @@ hipError_t launch_norm(const NormArgs& a, int type, int cus, hipStream_t s) {
 // Gradients
 // ---------------------------------------------------------------------------
 
-// Row r of step k of workgroup b: consecutive rows over the workgroups.  A
-// lane's column sums stay in registers over all its rows; the row groups of a
+// A lane's column sums stay in registers over all its rows; the row groups of a
 // workgroup (THREADS / TPR) add theirs up at the end, in order, through LDS.
-template <int TY, int VEC, int TPR, int NCH, int THREADS>
+// As above, the next row's loads run behind this one's barriers.
+template <int TY, int VEC, int TPR, int NCH, int THREADS, bool TAIL, bool REG>
 __global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradArgs a) {
   typedef Chunk<TY, VEC> C;
   typedef typename Elem<TY>::raw raw;
@@ -211,93 +277,87 @@ __global__ void __launch_bounds__(THREADS) norm_grad_kernel(const NormGradArgs a
   __shared__ float red[THREADS / 64 * 2];
   __shared__ float col[ROWS > 1 ? THREADS * VEC : 1];
   const int x = threadIdx.x % TPR, y = threadIdx.x / TPR;
-  const int chunks = a.D / VEC;
   const float cols = (float)a.D;
+  Params<TY, VEC, NCH, TAIL, REG> gamma;
+  gamma.init(a.gamma, 1.f, x * VEC, TPR * VEC, a.D);
   float dg[NCH][VEC], db[NCH][VEC];
 #pragma unroll
   for (int k = 0; k < NCH; ++k)
 #pragma unroll
     for (int i = 0; i < VEC; ++i) dg[k][i] = db[k][i] = 0.f;
-  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += (int64_t)gridDim.x * ROWS) {
-    const int64_t r = r0 + y;
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  int64_t r = (int64_t)blockIdx.x * ROWS + y;
+  RowCols<TY, VEC, TPR, NCH, TAIL> vx, vd, nx, nd;
+  vx.load(a.x, a.ldx, r, r < a.N, x, a.D);
+  vd.load(a.dy, a.lddy, r, r < a.N, x, a.D);
+  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += step, r += step) {
     const bool live = r < a.N;
-    C vx[NCH], vd[NCH];
-    const C* sx = (const C*)((const raw*)a.x + r * a.ldx);
-    const C* sd = (const C*)((const raw*)a.dy + r * a.lddy);
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int c = x + k * TPR;
-      if (live && c < chunks) {
-        vx[k] = sx[c];
-        vd[k] = sd[c];
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) vx[k].e[i] = vd[k].e[i] = 0;
-      }
+    if (r0 + step < a.N) {
+      nx.load(a.x, a.ldx, r + step, r + step < a.N, x, a.D);
+      nd.load(a.dy, a.lddy, r + step, r + step < a.N, x, a.D);
     }
     const float mean = live ? a.mean[r] : 0.f, rstd = live ? a.rstd[r] : 0.f;
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int c = x + k * TPR;
-      if (c >= chunks) continue;
+    for (int k = 0; k < NCH; ++k) {  // dy is 0 past the row's end, so nothing is added there
+      const int d = (x + k * TPR) * VEC;
       float g[VEC];
-      load_param<TY, VEC>(a.gamma, a.param_f32, c, 1.f, g);
+      if (REG || d < a.D) gamma.get(k, d, a.D - d, g);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) {
-        const float d = vd[k].get(i), n = (vx[k].get(i) - mean) * rstd;
-        const float h = d * g[i];
+        const float v = vd.v[k].get(i), n = (vx.v[k].get(i) - mean) * rstd;
+        const float h = REG || d < a.D ? v * g[i] : 0.f;
         s1 += h;
         s2 = fmaf(h, n, s2);
-        dg[k][i] = fmaf(d, n, dg[k][i]);
-        db[k][i] += d;
+        dg[k][i] = fmaf(v, n, dg[k][i]);
+        db[k][i] += v;
       }
     }
     row_sum2<TPR, THREADS / 64>(s1, s2, red);
-    if (!live) continue;
-    const float m1 = s1 / cols, m2 = s2 / cols;
-    C* dst = (C*)((raw*)a.dx + r * a.lddx);
+    if (live) {
+      const float m1 = s1 / cols, m2 = s2 / cols;
+      raw* dst = (raw*)a.dx + r * a.lddx;
 #pragma unroll
-    for (int k = 0; k < NCH; ++k) {
-      const int c = x + k * TPR;
-      if (c >= chunks) continue;
-      float g[VEC];
-      load_param<TY, VEC>(a.gamma, a.param_f32, c, 1.f, g);
-      C o;
+      for (int k = 0; k < NCH; ++k) {
+        const int d = (x + k * TPR) * VEC;
+        if (d >= a.D) continue;
+        float g[VEC];
+        gamma.get(k, d, a.D - d, g);
+        C o;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) {
-        const float h = vd[k].get(i) * g[i], n = (vx[k].get(i) - mean) * rstd;
-        o.put(i, (h - m1 - n * m2) * rstd);
+        for (int i = 0; i < VEC; ++i) {
+          const float h = vd.v[k].get(i) * g[i], n = (vx.v[k].get(i) - mean) * rstd;
+          o.put(i, (h - m1 - n * m2) * rstd);
+        }
+        o.template store<TAIL>(dst + d, a.D - d);
       }
-      dst[c] = o;
     }
+    vx = nx;
+    vd = nd;
   }
   if (!a.partial) return;
-  float* out = a.partial + (int64_t)blockIdx.x * 2 * a.D;
+  uint32_t* out = (uint32_t*)a.partial + (int64_t)blockIdx.x * 2 * a.D;
 #pragma unroll
   for (int k = 0; k < NCH; ++k) {
-    const int c = x + k * TPR;
+    const int d = (x + k * TPR) * VEC;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      float v[VEC];
+      Chunk<LL_F32, VEC> v;
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) v[i] = which ? db[k][i] : dg[k][i];
+      for (int i = 0; i < VEC; ++i) v.put(i, which ? db[k][i] : dg[k][i]);
       if constexpr (ROWS > 1) {
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) col[i * THREADS + threadIdx.x] = v[i];
+        for (int i = 0; i < VEC; ++i) col[i * THREADS + threadIdx.x] = v.get(i);
         __syncthreads();
         if (y == 0) {
 #pragma unroll
           for (int w = 1; w < ROWS; ++w)
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] += col[i * THREADS + w * TPR + x];
+            for (int i = 0; i < VEC; ++i) v.put(i, v.get(i) + col[i * THREADS + w * TPR + x]);
         }
       }
-      if (y == 0 && c < chunks) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) out[(int64_t)which * a.D + (int64_t)c * VEC + i] = v[i];
-      }
+      if (y == 0 && d < a.D) v.template store<TAIL>(out + (int64_t)which * a.D + d, a.D - d);
     }
   }
 }
@@ -332,7 +392,7 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* partial, 
 // taking every gridDim.y-th row.
 template <int TY>
 __global__ void __launch_bounds__(1024) norm_grad_long_kernel(const NormGradArgs a) {
-  typedef Chunk<TY, 1> C;
+  typedef Chunk<TY, 1> C;  // an element: get(0)
   typedef typename Elem<TY>::raw raw;
   __shared__ float red[32];
   const float cols = (float)a.D;
@@ -343,7 +403,7 @@ __global__ void __launch_bounds__(1024) norm_grad_long_kernel(const NormGradArgs
     float s1 = 0.f, s2 = 0.f;
     for (int c = threadIdx.x; c < a.D; c += 1024) {
       float g[1];
-      load_param<TY, 1>(a.gamma, a.param_f32, c, 1.f, g);
+      load_param<TY, 1, false>(a.gamma, a.param_f32, c, 1, 1.f, g);
       const float h = sd[c].get(0) * g[0];
       s1 += h;
       s2 = fmaf(h, (sx[c].get(0) - mean) * rstd, s2);
@@ -353,7 +413,7 @@ __global__ void __launch_bounds__(1024) norm_grad_long_kernel(const NormGradArgs
     C* dst = (C*)((raw*)a.dx + r * a.lddx);
     for (int c = threadIdx.x; c < a.D; c += 1024) {
       float g[1];
-      load_param<TY, 1>(a.gamma, a.param_f32, c, 1.f, g);
+      load_param<TY, 1, false>(a.gamma, a.param_f32, c, 1, 1.f, g);
       C o;
       o.put(0, (sd[c].get(0) * g[0] - m1 - (sx[c].get(0) - mean) * rstd * m2) * rstd);
       dst[c] = o;
@@ -380,25 +440,29 @@ __global__ void __launch_bounds__(256) norm_grad_columns_kernel(const NormGradAr
 
 int norm_grad_blocks(int64_t N, int cus) { return (int)std::max<int64_t>(1, std::min<int64_t>(N, 2ll * cus)); }
 
-template <int TY, int VEC, int TPR, int NCH, int THREADS>
+template <int TY, int VEC, int TPR, int NCH, int THREADS, bool TAIL>
 static int norm_grad_go(const NormGradArgs& a, int cus, hipStream_t s) {
   constexpr int ROWS = THREADS / TPR;
   const int blocks = norm_grad_blocks((a.N + ROWS - 1) / ROWS, cus);
-  hipLaunchKernelGGL((norm_grad_kernel<TY, VEC, TPR, NCH, THREADS>), dim3(blocks), dim3(THREADS), 0, s, a);
+  auto kernel = norm_grad_kernel<TY, VEC, TPR, NCH, THREADS, TAIL, true>;
+  if constexpr (TY != LL_F32) {
+    if (a.param_f32) kernel = norm_grad_kernel<TY, VEC, TPR, NCH, THREADS, TAIL, false>;
+  }
+  hipLaunchKernelGGL(kernel, dim3(blocks), dim3(THREADS), 0, s, a);
   return blocks;
 }
 
-template <int TY, int VEC>
+template <int TY, bool TAIL>
 static hipError_t launch_norm_grad_t(const NormGradArgs& a, int cus, hipStream_t s) {
-  const int chunks = a.D / VEC;
-  constexpr int K = (VEC > 1 ? 32 : 16) / VEC;
+  constexpr int VEC = kWide<TY>, K = 32 / VEC;
+  const int chunks = (a.D + VEC - 1) / VEC;
   int blocks;
-  if (chunks <= 64) blocks = norm_grad_go<TY, VEC, 64, 1, 256>(a, cus, s);
-  else if (chunks <= 64 * (K / 2)) blocks = norm_grad_go<TY, VEC, 64, K / 2, 256>(a, cus, s);
-  else if (chunks <= 64 * K) blocks = norm_grad_go<TY, VEC, 64, K, 256>(a, cus, s);
-  else if (chunks <= 256 * (K / 2)) blocks = norm_grad_go<TY, VEC, 256, K / 2, 256>(a, cus, s);
-  else if (chunks <= 256 * K) blocks = norm_grad_go<TY, VEC, 256, K, 256>(a, cus, s);
-  else if (a.D <= 16384) blocks = norm_grad_go<TY, VEC, 1024, 16 / VEC, 1024>(a, cus, s);
+  if (chunks <= 64) blocks = norm_grad_go<TY, VEC, 64, 1, 256, TAIL>(a, cus, s);
+  else if (chunks <= 64 * (K / 2)) blocks = norm_grad_go<TY, VEC, 64, K / 2, 256, TAIL>(a, cus, s);
+  else if (chunks <= 64 * K) blocks = norm_grad_go<TY, VEC, 64, K, 256, TAIL>(a, cus, s);
+  else if (chunks <= 256 * (K / 2)) blocks = norm_grad_go<TY, VEC, 256, K / 2, 256, TAIL>(a, cus, s);
+  else if (chunks <= 256 * K) blocks = norm_grad_go<TY, VEC, 256, K, 256, TAIL>(a, cus, s);
+  else if (a.D <= 16384) blocks = norm_grad_go<TY, VEC, 1024, K / 2, 1024, TAIL>(a, cus, s);
   else {
     const int64_t rows = std::min<int64_t>(a.N, (int64_t)cus * 64);
     if (rows > 0)
@@ -415,12 +479,13 @@ static hipError_t launch_norm_grad_t(const NormGradArgs& a, int cus, hipStream_t
 }
 
 hipError_t launch_norm_grad(const NormGradArgs& a, int type, int cus, hipStream_t s) {
-  const bool wide = wide_rows(a.x, a.ldx, a.D, type) && wide_rows(a.dy, a.lddy, a.D, type) &&
-                    wide_rows(a.dx, a.lddx, a.D, type);
   switch (type) {
-    case LL_BF16: return wide ? launch_norm_grad_t<LL_BF16, 8>(a, cus, s) : launch_norm_grad_t<LL_BF16, 1>(a, cus, s);
-    case LL_F16: return wide ? launch_norm_grad_t<LL_F16, 8>(a, cus, s) : launch_norm_grad_t<LL_F16, 1>(a, cus, s);
-    case LL_F32: return wide ? launch_norm_grad_t<LL_F32, 4>(a, cus, s) : launch_norm_grad_t<LL_F32, 1>(a, cus, s);
+    case LL_BF16:
+      return a.D % 8 ? launch_norm_grad_t<LL_BF16, true>(a, cus, s) : launch_norm_grad_t<LL_BF16, false>(a, cus, s);
+    case LL_F16:
+      return a.D % 8 ? launch_norm_grad_t<LL_F16, true>(a, cus, s) : launch_norm_grad_t<LL_F16, false>(a, cus, s);
+    case LL_F32:
+      return a.D % 4 ? launch_norm_grad_t<LL_F32, true>(a, cus, s) : launch_norm_grad_t<LL_F32, false>(a, cus, s);
     default: return hipErrorInvalidValue;
   }
 }

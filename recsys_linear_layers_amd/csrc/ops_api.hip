@@ -49,18 +49,22 @@ ll_status embed_sizes(int64_t V, int64_t T, int64_t D, int64_t s0, int64_t s1, i
 
 struct EmbedGradLayout {
   int bits = 0, passes = 0;
-  size_t key[2] = {0, 0}, pos[2] = {0, 0}, hist = 0, seg = 0, partial = 0, bytes = 0;
+  size_t key[2] = {0, 0}, pos[2] = {0, 0}, hist[2] = {0, 0}, total = 0, seg = 0, partial = 0, long_count = 0,
+         long_rows = 0, bytes = 0;
 };
 
-// Workspace of the sorted path: digits of at most kSortMaxBits bits, of equal
-// width over the passes that cover the keys 0 .. V.
+// Workspace of the sorted path.  One workgroup sorts in 8-bit digits; beyond
+// that, digits of at most kSortMaxBits bits, of equal width over the passes
+// that cover the keys 0 .. V.
 EmbedGradLayout embed_grad_layout(const embed_grad_desc* d) {
   EmbedGradLayout l;
   if (d->T <= kEmbedDirect || d->V == 0 || d->D == 0) return l;
+  const bool small = d->T <= kEmbedSmall;
   int kb = 1;
   while (kb < 31 && (1ll << kb) <= d->V) ++kb;  // V itself is a key
-  l.passes = (kb + kSortMaxBits - 1) / kSortMaxBits;
-  l.bits = (kb + l.passes - 1) / l.passes;
+  const int most = small ? 8 : kSortMaxBits;
+  l.passes = (kb + most - 1) / most;
+  l.bits = small ? 8 : (kb + l.passes - 1) / l.passes;
   const int64_t nblk = (d->T + kSortItems - 1) / kSortItems;
   size_t off = 0;
   auto take = [&](size_t n) {
@@ -68,13 +72,18 @@ EmbedGradLayout embed_grad_layout(const embed_grad_desc* d) {
     off = align256(off + n);
     return at;
   };
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < (small ? 1 : 2); ++i) {
     l.key[i] = take((size_t)d->T * 4);
     l.pos[i] = take((size_t)d->T * 4);
   }
-  l.hist = take(((size_t)nblk << l.bits) * 4);
+  if (!small) {
+    for (int i = 0; i < std::min(l.passes, 2); ++i) l.hist[i] = take(((size_t)nblk << l.bits) * 4);
+    l.total = take((size_t)4 << l.bits);
+  }
   l.seg = take((size_t)d->V * 8);
   l.partial = take((size_t)(d->T / kEmbedChunk) * (size_t)d->D * 4);
+  l.long_count = take(4);
+  l.long_rows = take((size_t)(d->T / kEmbedChunk) * 4);
   l.bytes = off;
   return l;
 }
@@ -160,10 +169,13 @@ ll_status embed_grad_run(const embed_grad_desc* d, const int64_t* ids, const voi
     for (int i = 0; i < 2; ++i) {
       a.key[i] = (uint32_t*)(w + l.key[i]);
       a.pos[i] = (uint32_t*)(w + l.pos[i]);
+      a.hist[i] = (uint32_t*)(w + l.hist[i]);
     }
-    a.hist = (uint32_t*)(w + l.hist);
+    a.total = (uint32_t*)(w + l.total);
     a.seg = (int2*)(w + l.seg);
     a.partial = (float*)(w + l.partial);
+    a.long_count = (uint32_t*)(w + l.long_count);
+    a.long_rows = (uint32_t*)(w + l.long_rows);
   }
   const hipError_t err = launch_embed_grad(a, d->type, info->cus, (hipStream_t)stream);
   return err == hipSuccess ? ok() : hip_fail(err, "embed gradient launch");

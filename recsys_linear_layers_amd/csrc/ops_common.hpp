@@ -32,24 +32,46 @@ struct Elem<LL_F32> {
   static __device__ __forceinline__ uint32_t put(float v) { return __builtin_bit_cast(uint32_t, v); }
 };
 
-// VEC consecutive elements moved by one load or store (aligned to their size).
+// VEC consecutive elements, moved by one load or store whatever their
+// alignment (a 16-byte access at any element is one instruction here).
 template <int TY, int VEC>
-struct alignas(sizeof(typename Elem<TY>::raw) * VEC) Chunk {
-  typename Elem<TY>::raw e[VEC];
+struct Chunk {
+  typedef typename Elem<TY>::raw raw;
+  raw e[VEC];
   __device__ __forceinline__ float get(int i) const { return Elem<TY>::get(e[i]); }
   __device__ __forceinline__ void put(int i, float v) { e[i] = Elem<TY>::put(v); }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) e[i] = 0;
+  }
+  // The n elements of a row from p on, as many as there are (the others 0).
+  // TAIL false: all VEC are there.
+  template <bool TAIL>
+  __device__ __forceinline__ void load(const raw* p, int n) {
+    if (!TAIL || n >= VEC) {
+      __builtin_memcpy(this, p, sizeof(*this));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) e[i] = i < n ? p[i] : (raw)0;
+    }
+  }
+  template <bool TAIL>
+  __device__ __forceinline__ void store(raw* p, int n) const {
+    if (!TAIL || n >= VEC) {
+      __builtin_memcpy(p, this, sizeof(*this));
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i)
+        if (i < n) p[i] = e[i];
+    }
+  }
 };
 
+// Elements of a 16-byte access.
 template <int TY>
-constexpr int kWide = 16 / (int)sizeof(typename Elem<TY>::raw);  // elements of a 16-byte access
+constexpr int kWide = 16 / (int)sizeof(typename Elem<TY>::raw);
 
 inline int dtype_size(int ty) { return ty == LL_F32 ? 4 : 2; }
-
-// Whether rows of D elements at `ld` apart starting at `p` can be moved 16 bytes at a time.
-inline bool wide_rows(const void* p, int64_t ld, int64_t D, int ty) {
-  const int64_t v = 16 / dtype_size(ty);
-  return ((uintptr_t)p & 15) == 0 && ld % v == 0 && D % v == 0;
-}
 
 // Sum over aligned groups of W lanes (a power of two up to 64); every lane gets it.
 template <int W>
