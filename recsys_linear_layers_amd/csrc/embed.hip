@@ -126,14 +126,11 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp) {
   return base + s - v;
 }
 
-// Clears seg and the long-row count (and hist, if given) with workgroups
-// first .. first + n of the launch.
-__device__ __forceinline__ void clear_for_rows(const EmbedGradArgs& a, int first, int threads, uint32_t* hist,
-                                               int64_t hist_n) {
+// Clears seg and the long-row count with the launch's workgroups from `first` on.
+__device__ __forceinline__ void clear_for_rows(const EmbedGradArgs& a, int first, int threads) {
   const int64_t i0 = (int64_t)(blockIdx.x - first) * threads + threadIdx.x;
   const int64_t step = (int64_t)(gridDim.x - first) * threads;
   for (int64_t i = i0; i < a.V; i += step) a.seg[i] = int2{0, 0};
-  for (int64_t i = i0; i < hist_n; i += step) hist[i] = 0;
   if (i0 == 0) *a.long_count = 0;
 }
 
@@ -145,7 +142,7 @@ __global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradA
   __shared__ uint32_t cnt[16][256];
   __shared__ uint32_t tmp[16];
   if (blockIdx.x > 0) {
-    clear_for_rows(a, 1, 1024, nullptr, 0);
+    clear_for_rows(a, 1, 1024);
     return;
   }
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -209,14 +206,16 @@ __global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradA
   }
 }
 
-// More tokens: per pass the digit counts of each workgroup's tokens (the
-// first pass counts here, the later ones while the pass before moves the
-// tokens), their running sums over the workgroups, and the move.
-__global__ void __launch_bounds__(256) embed_hist_kernel(const EmbedGradArgs a, int nblk) {
+// More tokens: per pass the digit counts of each workgroup's tokens, their
+// running sums over the workgroups, and the move.  (Counting the next pass's
+// digits with global atomics during the move is a launch less but slower: the
+// frequent ids meet on a few counters.  16 against 8.5 + 5 us at 32768 tokens.)
+template <bool FIRST>
+__global__ void __launch_bounds__(256) embed_hist_kernel(const EmbedGradArgs a, int pass, int nblk) {
   __shared__ uint32_t cnt[1 << kSortMaxBits];
-  const int bins = 1 << a.bits;
-  if ((int)blockIdx.x >= nblk) {
-    clear_for_rows(a, nblk, 256, a.passes > 1 ? a.hist[1] : nullptr, a.passes > 1 ? (int64_t)nblk * bins : 0);
+  const int bins = 1 << a.bits, shift = pass * a.bits, src = pass & 1;
+  if (FIRST && (int)blockIdx.x >= nblk) {
+    clear_for_rows(a, nblk, 256);
     return;
   }
   for (int b = threadIdx.x; b < bins; b += 256) cnt[b] = 0;
@@ -224,10 +223,10 @@ __global__ void __launch_bounds__(256) embed_hist_kernel(const EmbedGradArgs a, 
 #pragma unroll
   for (int i = 0; i < kSortItems / 256; ++i) {
     const int t = blockIdx.x * kSortItems + i * 256 + threadIdx.x;
-    if (t < a.T) atomicAdd(&cnt[token_key(a, t) & (bins - 1)], 1u);
+    if (t < a.T) atomicAdd(&cnt[((FIRST ? token_key(a, t) : a.key[src][t]) >> shift) & (bins - 1)], 1u);
   }
   __syncthreads();
-  for (int b = threadIdx.x; b < bins; b += 256) a.hist[0][(int64_t)blockIdx.x * bins + b] = cnt[b];
+  for (int b = threadIdx.x; b < bins; b += 256) a.hist[(int64_t)blockIdx.x * bins + b] = cnt[b];
 }
 
 // hist[k][b] becomes the tokens with digit b in workgroups before k; total[b]
@@ -263,7 +262,7 @@ __global__ void __launch_bounds__(256) embed_scan_kernel(uint32_t* hist, uint32_
 
 // Moves each token to its place by the pass's digit; a wave owns consecutive
 // tokens and takes them 64 at a time in order, so equal digits keep theirs.
-template <bool FIRST, bool LAST>
+template <bool FIRST>
 __global__ void __launch_bounds__(256) embed_scatter_kernel(const EmbedGradArgs a, int pass) {
   constexpr int I = kSortItems / 256;
   __shared__ uint32_t cnt[4][1 << kSortMaxBits];
@@ -293,7 +292,7 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(const EmbedGradArgs 
   for (int i = 0; i < 4; ++i) {
     const int b = b0 + i;
     if (i < q && b < bins) {
-      uint32_t at = base + a.hist[src][(int64_t)blockIdx.x * bins + b];
+      uint32_t at = base + a.hist[(int64_t)blockIdx.x * bins + b];
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const uint32_t n = cnt[w][b];
@@ -313,8 +312,6 @@ __global__ void __launch_bounds__(256) embed_scatter_kernel(const EmbedGradArgs 
     if (live) {
       a.key[src ^ 1][at] = key[i];
       a.pos[src ^ 1][at] = FIRST ? (uint32_t)t : a.pos[src][t];
-      if (!LAST)  // whole numbers: any order
-        atomicAdd(&a.hist[src ^ 1][(int64_t)(at / kSortItems) * bins + ((key[i] >> (shift + a.bits)) & (bins - 1))], 1u);
     }
   }
 }
@@ -489,12 +486,11 @@ __global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedGradArgs a, 
     }
     return;
   }
+  // rows far apart: neighbouring ids are often alike in frequency
   const int item = blockIdx.x - long_blocks;
-  const int64_t v0 = (int64_t)(item / col_blocks) * groups * kRowsPerGroup;
+  const int64_t step = (int64_t)((gridDim.x - long_blocks) / col_blocks) * groups;
   const int cb = item % col_blocks;
-  for (int i = 0; i < kRowsPerGroup; ++i) {
-    const int64_t v = v0 + i * groups + g;
-    if (v >= a.V) break;
+  for (int64_t v = (int64_t)(item / col_blocks) * groups + g; v < a.V; v += step) {
     const int2 s = a.seg[v];
     if ((s.x + kEmbedChunk - 1) / kEmbedChunk < s.y / kEmbedChunk) continue;  // holds a whole chunk
     if (a.accumulate && s.x == s.y) continue;
@@ -575,16 +571,6 @@ __global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, i
   }
 }
 
-__global__ void __launch_bounds__(256) embed_clear_kernel(uint32_t* p, int64_t n) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) p[i] = 0;
-}
-
-static hipError_t launch_clear(uint32_t* p, int64_t n, int cus, hipStream_t s) {
-  const int64_t blocks = std::min<int64_t>((n + 255) / 256, 4ll * cus);
-  hipLaunchKernelGGL(embed_clear_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p, n);
-  return hipGetLastError();
-}
-
 template <int TY, bool TAIL>
 static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream_t s) {
   constexpr int VEC = kWide<TY>;
@@ -592,9 +578,13 @@ static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream
   const int lx = log2_up(chunks, 6);
   const int nrows = (256 >> lx) * kRowsPerGroup;
   const int64_t rb = (a.V + nrows - 1) / nrows;
-  // workgroups along the columns only where the rows alone are few
+  // A block of columns per workgroup: a row of many tokens is then summed by
+  // several.  (The workgroups that pick their tokens from ids take all columns
+  // of a row unless the rows alone are few.)
   const int all_cols = (chunks + (1 << lx) - 1) >> lx;
-  const int cb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / rb));
+  const int cb = a.T > kEmbedDirect
+                     ? all_cols
+                     : (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / rb));
   if (rb * cb > 0x3FFFFFFF) return hipErrorInvalidValue;
   if (a.T <= kEmbedDirect) {
     hipLaunchKernelGGL((embed_few_kernel<TY, TAIL>), dim3((unsigned)(rb * cb)), dim3(256), 0, s, a, lx, cb);
@@ -606,23 +596,17 @@ static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream
     hipLaunchKernelGGL(embed_small_sort_kernel, dim3(1 + clear), dim3(1024), 0, s, a);
   } else {
     const int nblk = (a.T + kSortItems - 1) / kSortItems;
-    hipLaunchKernelGGL(embed_hist_kernel, dim3(nblk + clear), dim3(256), 0, s, a, nblk);
     for (int p = 0; p < a.passes; ++p) {
-      const bool first = p == 0, last = p == a.passes - 1;
-      hipLaunchKernelGGL(embed_scan_kernel, dim3(((1 << a.bits) + 63) / 64), dim3(256), 0, s, a.hist[p & 1], a.total,
-                         nblk, 1 << a.bits);
-      if (p > 0 && !last) {  // the next pass counts into what this one has read
-        const hipError_t e = launch_clear(a.hist[(p + 1) & 1], (int64_t)nblk << a.bits, cus, s);
-        if (e != hipSuccess) return e;
-      }
-      if (first && last)
-        hipLaunchKernelGGL((embed_scatter_kernel<true, true>), dim3(nblk), dim3(256), 0, s, a, p);
-      else if (first)
-        hipLaunchKernelGGL((embed_scatter_kernel<true, false>), dim3(nblk), dim3(256), 0, s, a, p);
-      else if (last)
-        hipLaunchKernelGGL((embed_scatter_kernel<false, true>), dim3(nblk), dim3(256), 0, s, a, p);
+      if (p == 0)
+        hipLaunchKernelGGL((embed_hist_kernel<true>), dim3(nblk + clear), dim3(256), 0, s, a, p, nblk);
       else
-        hipLaunchKernelGGL((embed_scatter_kernel<false, false>), dim3(nblk), dim3(256), 0, s, a, p);
+        hipLaunchKernelGGL((embed_hist_kernel<false>), dim3(nblk), dim3(256), 0, s, a, p, nblk);
+      hipLaunchKernelGGL(embed_scan_kernel, dim3(((1 << a.bits) + 63) / 64), dim3(256), 0, s, a.hist, a.total, nblk,
+                         1 << a.bits);
+      if (p == 0)
+        hipLaunchKernelGGL((embed_scatter_kernel<true>), dim3(nblk), dim3(256), 0, s, a, p);
+      else
+        hipLaunchKernelGGL((embed_scatter_kernel<false>), dim3(nblk), dim3(256), 0, s, a, p);
       src ^= 1;
     }
   }

@@ -38,7 +38,7 @@ struct EmbedGradArgs {
   // workspace (null when T <= kEmbedDirect)
   uint32_t* key[2];
   uint32_t* pos[2];
-  uint32_t* hist[2];    // by parity of the pass: [sort workgroups][1 << bits]
+  uint32_t* hist;       // [sort workgroups][1 << bits]
   uint32_t* total;      // [1 << bits]
   int2* seg;            // [V] sorted positions first, last + 1 of each row's tokens
   float* partial;       // [T / kEmbedChunk][D] sums of whole chunks

@@ -461,7 +461,7 @@ static hipError_t launch_norm_grad_t(const NormGradArgs& a, int cus, hipStream_t
   else if (chunks <= 64 * (K / 2)) blocks = norm_grad_go<TY, VEC, 64, K / 2, 256, TAIL>(a, cus, s);
   else if (chunks <= 64 * K) blocks = norm_grad_go<TY, VEC, 64, K, 256, TAIL>(a, cus, s);
   else if (chunks <= 256 * (K / 2)) blocks = norm_grad_go<TY, VEC, 256, K / 2, 256, TAIL>(a, cus, s);
-  else if (chunks <= 256 * K) blocks = norm_grad_go<TY, VEC, 256, K, 256, TAIL>(a, cus, s);
+  else if (chunks <= 512 * (K / 2)) blocks = norm_grad_go<TY, VEC, 512, K / 2, 512, TAIL>(a, cus, s);
   else if (a.D <= 16384) blocks = norm_grad_go<TY, VEC, 1024, K / 2, 1024, TAIL>(a, cus, s);
   else {
     const int64_t rows = std::min<int64_t>(a.N, (int64_t)cus * 64);

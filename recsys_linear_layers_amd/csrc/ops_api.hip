@@ -49,7 +49,7 @@ ll_status embed_sizes(int64_t V, int64_t T, int64_t D, int64_t s0, int64_t s1, i
 
 struct EmbedGradLayout {
   int bits = 0, passes = 0;
-  size_t key[2] = {0, 0}, pos[2] = {0, 0}, hist[2] = {0, 0}, total = 0, seg = 0, partial = 0, long_count = 0,
+  size_t key[2] = {0, 0}, pos[2] = {0, 0}, hist = 0, total = 0, seg = 0, partial = 0, long_count = 0,
          long_rows = 0, bytes = 0;
 };
 
@@ -77,7 +77,7 @@ EmbedGradLayout embed_grad_layout(const embed_grad_desc* d) {
     l.pos[i] = take((size_t)d->T * 4);
   }
   if (!small) {
-    for (int i = 0; i < std::min(l.passes, 2); ++i) l.hist[i] = take(((size_t)nblk << l.bits) * 4);
+    l.hist = take(((size_t)nblk << l.bits) * 4);
     l.total = take((size_t)4 << l.bits);
   }
   l.seg = take((size_t)d->V * 8);
@@ -169,8 +169,8 @@ ll_status embed_grad_run(const embed_grad_desc* d, const int64_t* ids, const voi
     for (int i = 0; i < 2; ++i) {
       a.key[i] = (uint32_t*)(w + l.key[i]);
       a.pos[i] = (uint32_t*)(w + l.pos[i]);
-      a.hist[i] = (uint32_t*)(w + l.hist[i]);
     }
+    a.hist = (uint32_t*)(w + l.hist);
     a.total = (uint32_t*)(w + l.total);
     a.seg = (int2*)(w + l.seg);
     a.partial = (float*)(w + l.partial);
