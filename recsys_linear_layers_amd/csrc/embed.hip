@@ -442,7 +442,8 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs& a, int64_t v, int
 #pragma unroll
     for (int i = 0; i < VEC; ++i) o.put(i, acc[i] * a.scale);
   }
-  o.template store<TAIL>(dst, a.D - d);
+  // the gradient is not read again soon (items case 149 -> 109 us, vocabulary case 236 -> 222 us)
+  o.template store<TAIL, true>(dst, a.D - d);
 }
 
 // Rows a group handles one after the other.

@@ -33,16 +33,42 @@ struct Elem<LL_F32> {
 };
 
 // VEC consecutive elements, moved by one load or store whatever their
-// alignment (a 16-byte access at any element is one instruction here).
+// alignment (a 16-byte access at any element is one instruction here).  Held
+// as whole words: as an array of 16-bit elements each would take a register
+// of its own once it lives across a loop step.
 template <int TY, int VEC>
 struct Chunk {
   typedef typename Elem<TY>::raw raw;
-  raw e[VEC];
-  __device__ __forceinline__ float get(int i) const { return Elem<TY>::get(e[i]); }
-  __device__ __forceinline__ void put(int i, float v) { e[i] = Elem<TY>::put(v); }
+  static constexpr int PER = 4 / (int)sizeof(raw);  // elements per word
+  static_assert(VEC % PER == 0, "whole words");
+  uint32_t w[VEC / PER];
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (TY == LL_F32) return Elem<TY>::get(w[i]);
+    else if constexpr (TY == LL_BF16)
+      return __builtin_bit_cast(float, i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
+    else return Elem<TY>::get((raw)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]));
+  }
+  __device__ __forceinline__ void put_raw(int i, raw v) {
+    if constexpr (PER == 1) w[i] = v;
+    else w[i >> 1] = i & 1 ? (w[i >> 1] & 0xFFFFu) | (uint32_t)v << 16 : (w[i >> 1] & 0xFFFF0000u) | v;
+  }
+  __device__ __forceinline__ raw get_raw(int i) const {
+    if constexpr (PER == 1) return w[i];
+    else return (raw)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
+  }
+  __device__ __forceinline__ void put(int i, float v) { put_raw(i, Elem<TY>::put(v)); }
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) e[i] = 0;
+    for (int i = 0; i < VEC / PER; ++i) w[i] = 0;
+  }
+  // Forgets what the compiler has derived from the stored elements: their fp32
+  // values are formed again where they are used next, instead of being held
+  // in twice the registers until then.
+  __device__ __forceinline__ void keep_packed() {
+    if constexpr (PER > 1) {
+#pragma unroll
+      for (int i = 0; i < VEC / PER; ++i) asm volatile("" : "+v"(w[i]));
+    }
   }
   // The n elements of a row from p on, as many as there are (the others 0).
   // TAIL false: all VEC are there.
@@ -51,18 +77,29 @@ struct Chunk {
     if (!TAIL || n >= VEC) {
       __builtin_memcpy(this, p, sizeof(*this));
     } else {
+      clear();
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) e[i] = i < n ? p[i] : (raw)0;
+      for (int i = 0; i < VEC; ++i)
+        if (i < n) put_raw(i, p[i]);
     }
   }
-  template <bool TAIL>
+  // NT: not read again soon (non-temporal).
+  template <bool TAIL, bool NT = false>
   __device__ __forceinline__ void store(raw* p, int n) const {
     if (!TAIL || n >= VEC) {
-      __builtin_memcpy(p, this, sizeof(*this));
+      if constexpr (NT) {
+        typedef uint32_t words __attribute__((ext_vector_type(VEC / PER)));
+        typedef words unaligned_words __attribute__((aligned(sizeof(raw))));
+        words v;
+        __builtin_memcpy(&v, this, sizeof v);
+        __builtin_nontemporal_store(v, (unaligned_words*)p);
+      } else {
+        __builtin_memcpy(p, this, sizeof(*this));
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < VEC; ++i)
-        if (i < n) p[i] = e[i];
+        if (i < n) p[i] = get_raw(i);
     }
   }
 };
