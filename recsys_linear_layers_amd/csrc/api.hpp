@@ -58,6 +58,9 @@ struct OperandPlan {
 // leading dimension at least that, a multiple of 8), 16-byte aligned.  Such an
 // operand is read in place whatever its logical size.
 constexpr uint32_t kPaddedA = 1u, kPaddedB = 2u;
+// The hand-ordered kind in whole tiles, K not split: what a softmax epilogue
+// needs (LL_ERR_UNSUPPORTED where that kind cannot take the operands).
+constexpr uint32_t kWholeTiles = 4u;
 
 }  // namespace ll
 
@@ -84,10 +87,14 @@ struct gemm_plan {
 
 namespace ll {
 
-// gemm_plan_create into a caller's plan, with kPadded* operands.
-ll_status gemm_plan_build(const gemm_desc* d, uint32_t padded, gemm_plan* out);
-// gemm_run on it.
+struct GemmKArgs;
+
+// gemm_plan_create into a caller's plan, with the options above.
+ll_status gemm_plan_build(const gemm_desc* d, uint32_t options, gemm_plan* out);
+// gemm_run on it.  softmax, with a kWholeTiles plan: launches epilogue `epi`
+// (SoftmaxEpilogue) with the softmax fields of *softmax; C may be null, and has
+// rows and columns up to whole tiles.
 ll_status gemm_run_plan(const gemm_plan* p, const void* A, const void* B, void* C, const float* bias, void* ws,
-                        size_t ws_bytes, void* stream);
+                        size_t ws_bytes, void* stream, int epi = 0, const GemmKArgs* softmax = nullptr);
 
 }  // namespace ll

@@ -87,6 +87,17 @@ struct GemmKArgs {
   // L2 (its loop always issues the prefetch; with 0 every lane's offset is
   // out of range and the load touches no memory).
   int32_t b_prefetch;
+  // Hand-ordered kind with a softmax epilogue only (gemm_sq4_xent.hip): C, if
+  // any, has rows and columns up to whole tiles.  Per 128 columns (part) and
+  // row: maximum and sum of exponentials, parts[part0 + part][row], rows
+  // part_ld apart; or the row's log-sum, gradient factor and target column.
+  float2* parts;
+  int64_t part_ld;
+  int32_t part0;
+  int32_t col0;          // vocabulary entry of column 0
+  const float* lse;
+  const float* coef;
+  const int32_t* column; // target of each row, -1 for none
 };
 
 template <int BM_, int BN_, int KT_, int WM_, int WN_, int NPROD_, int STAGES_, bool AK_, bool BK_,

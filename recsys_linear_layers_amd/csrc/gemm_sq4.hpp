@@ -317,6 +317,11 @@ __device__ __forceinline__ void sq4_issue(i32x4 ra, i32x4 rb, const uint32_t (&v
   }
 }
 
+// Softmax epilogues (EPI 5-7, kernels.hpp) of a wave's 128x128 block, defined
+// in gemm_sq4_xent.hip.
+template <bool F16, int EPI>
+__device__ void sq4_softmax(const GemmKArgs& p, const TileInfo& ti, int wm0, int wn0, int lane, char LL_LDS* img);
+
 template <bool F16, int EPI, bool BK, bool AM>
 __global__ void __launch_bounds__(Sq4::THREADS) __attribute__((amdgpu_waves_per_eu(1, 1)))
     gemm_sq4(const GemmKArgs p) {
@@ -520,6 +525,12 @@ __global__ void __launch_bounds__(Sq4::THREADS) __attribute__((amdgpu_waves_per_
 #undef LL_SQ4_OPERANDS
 
     lds_barrier();  // every wave is done reading the ring before it is reused
+    if constexpr (EPI >= 5) {
+      sq4_softmax<F16, EPI>(p, ti, wm0, wn0, lane, smem + wave * Sq4::IMG);
+      sq4_count_in(cnt, wave, lane);
+      if (EPI != 5 && t + stride < p.total) lds_barrier();  // as below
+      continue;
+    } else {
     if (slot >= 0) {  // a K split of a last-round tile: raw sums for the reduce
       sq4_tail_all(p, slot, wm0, wn0, lane);
       sq4_count_in(cnt, wave, lane);
@@ -547,6 +558,7 @@ __global__ void __launch_bounds__(Sq4::THREADS) __attribute__((amdgpu_waves_per_
     else
       sq4_store_all<EPI>(p, ti, wm0, wn0, lane);
     sq4_count_in(cnt, wave, lane);
+    }
   }
 }
 

@@ -66,6 +66,17 @@ hipError_t launch_gemm_sq4_bk(int f16, int epi, const GemmKArgs& args, int grid,
 hipError_t launch_gemm_sq4_am(int f16, int epi, const GemmKArgs& args, int grid, hipStream_t stream);
 hipError_t launch_gemm_sq4_am_bk(int f16, int epi, const GemmKArgs& args, int grid, hipStream_t stream);
 
+// The same kind, both operands K-contiguous, with the softmax epilogues of the
+// vocabulary cross entropy instead of C = A.B.
+enum SoftmaxEpilogue {
+  kSoftmaxStats = 5,       // parts alone
+  kSoftmaxNumerators = 6,  // parts, and exp(z - the part's maximum) * kNumeratorScale in C, as fp16
+  kSoftmaxGradient = 7     // (exp(z - lse) - onehot) * coef in C
+};
+// Numerators are at most 1; times 2^15 those down to 2^-29 are normal fp16 numbers.
+constexpr float kNumeratorScale = 32768.f;
+hipError_t launch_gemm_sq4_xent(int f16, int epi, const GemmKArgs& args, int grid, hipStream_t stream);
+
 // Fused linear-compression kernel (lincomp_kernel.hpp).
 struct LincompKArgs;
 struct LincompKind {

@@ -227,7 +227,7 @@ ll_status gemm_plan_create(gemm_plan** out, const gemm_desc* d) {
 
 }  // extern "C"
 
-ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t padded, gemm_plan* out) {
+ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t options, gemm_plan* out) {
   if (d->M < 0 || d->N < 0 || d->K < 0) return fail(LL_ERR_INVALID_ARG, "negative size");
   if (d->stride_am < 1 || d->stride_ak < 1 || d->stride_bk < 1 || d->stride_bn < 1 || d->stride_cm < 1 ||
       d->stride_cn < 1)
@@ -250,7 +250,7 @@ ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t padded, gemm_plan* ou
   memset(&p, 0, sizeof p);
   p.d = *d;
   ll_status s = plan_operand("A", d->M, d->K, d->stride_am, d->stride_ak, d->flags & LL_FLAG_PACK_A, false,
-                             padded & kPaddedA, &p.a);
+                             options & kPaddedA, &p.a);
   if (s != LL_OK) return s;
   // A packed B is N-contiguous (above), except a B given K-contiguous beside a
   // K-contiguous A: its copy stays K-contiguous (a plain copy, not a
@@ -258,7 +258,7 @@ ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t padded, gemm_plan* ou
   // x 4099, column-major B with rows 4099 elements apart: 336 -> 329 us).
   const bool b_prefer_mn = !(d->stride_bk == 1 && p.a.kmajor);
   s = plan_operand("B", d->N, d->K, d->stride_bn, d->stride_bk, d->flags & LL_FLAG_PACK_B, b_prefer_mn,
-                   padded & kPaddedB, &p.b);
+                   options & kPaddedB, &p.b);
   if (s != LL_OK) return s;
   // Any K-contiguous operand needs K padded to a multiple of 8; packed copies carry zeros there.
   p.Kp = round_up(d->K, 8);
@@ -388,6 +388,8 @@ ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t padded, gemm_plan* ou
       if (strcmp(env, kind_info(i).name) == 0) kind = i;
     if (env[0] >= '0' && env[0] <= '9' && atoi(env) < KIND_COUNT) kind = atoi(env);
   }
+  const bool whole_tiles = options & kWholeTiles;
+  if (whole_tiles) kind = KIND_SQ4_HO;
   // A fused epilogue runs in the kinds instantiated with it (the
   // producer/consumer tiles of the same orientation rule).
   if (d->epilogue && !kind_info(kind).epi) {
@@ -421,7 +423,7 @@ ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t padded, gemm_plan* ou
   const int64_t slots = (int64_t)p.cus * occ;
   // Split K when the tiles alone cannot fill the chip and K is long enough to share.
   int splits = 1;
-  if (tiles > 0 && tiles * 2 <= slots && p.Kp >= 1024) {
+  if (tiles > 0 && tiles * 2 <= slots && p.Kp >= 1024 && !whole_tiles) {
     int64_t want = slots / tiles;
     int64_t by_k = p.Kp / 512;
     splits = (int)(want < by_k ? want : by_k);
@@ -448,7 +450,7 @@ ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t padded, gemm_plan* ou
   p.tail_splits = 1;
   p.tail_kps = p.kiters;
   p.tail_first = p.total;
-  if (kind == KIND_SQ4_HO && splits == 1) {
+  if (kind == KIND_SQ4_HO && splits == 1 && !whole_tiles) {
     const int s = tail_splits_for(tiles, p.grid, p.kiters);
     if (s >= 2) {
       const int64_t last = tiles % p.grid;
@@ -604,11 +606,11 @@ ll_status gemm_run_noalloc(const gemm_plan* p, const void* A, const void* B, voi
 }  // extern "C"
 
 ll_status ll::gemm_run_plan(const gemm_plan* p, const void* A, const void* B, void* C, const float* bias, void* ws,
-                            size_t ws_bytes, void* stream) {
+                            size_t ws_bytes, void* stream, int epi, const GemmKArgs* softmax) {
   if (!p) return fail(LL_ERR_INVALID_ARG, "null plan");
   const gemm_desc& d = p->d;
   if (d.M == 0 || d.N == 0) return ok();
-  if (!C) return fail(LL_ERR_INVALID_ARG, "null C");
+  if (!C && !softmax) return fail(LL_ERR_INVALID_ARG, "null C");
   if (d.K > 0 && (!A || !B)) return fail(LL_ERR_INVALID_ARG, "null A or B");
   if (ws_bytes < p->ws_bytes || (p->ws_bytes > 0 && !ws))
     return fail(LL_ERR_WORKSPACE, "workspace %zu bytes, plan needs %zu", ws_bytes, p->ws_bytes);
@@ -619,7 +621,7 @@ ll_status ll::gemm_run_plan(const gemm_plan* p, const void* A, const void* B, vo
   if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
   if (dev != p->device) return fail(LL_ERR_INVALID_ARG, "plan made for device %d, current is %d", p->device, dev);
   const int64_t csz = d.c_type == LL_F32 ? 4 : 2;
-  const Span sc = span_of(C, d.M, d.N, d.stride_cm, d.stride_cn, csz);
+  const Span sc = span_of(C, C ? d.M : 0, d.N, d.stride_cm, d.stride_cn, csz);
   if (d.K > 0) {
     if (overlaps(sc, span_of(A, d.M, d.K, d.stride_am, d.stride_ak, 2)) ||
         overlaps(sc, span_of(B, d.K, d.N, d.stride_bk, d.stride_bn, 2)))
@@ -684,6 +686,17 @@ ll_status ll::gemm_run_plan(const gemm_plan* p, const void* A, const void* B, vo
     k.sync = (uint32_t*)((char*)ws + p->ws_sync_off);
     e = launch_clear_words(k.sync, kRoundSyncWords, st);
     if (e != hipSuccess) return hip_fail(e, "round counter clear launch");
+  }
+  if (softmax) {
+    k.parts = softmax->parts;
+    k.part_ld = softmax->part_ld;
+    k.part0 = softmax->part0;
+    k.col0 = softmax->col0;
+    k.lse = softmax->lse;
+    k.coef = softmax->coef;
+    k.column = softmax->column;
+    e = launch_gemm_sq4_xent(d.a_type == LL_F16, epi, k, p->grid, st);
+    return e == hipSuccess ? ok() : hip_fail(e, "gemm launch");
   }
   e = p->epi ? launch_gemm_epi(p->layout, p->kind, d.a_type == LL_F16, p->epi, k, p->grid, st)
              : launch_gemm(p->layout, p->kind, d.a_type == LL_F16, k, p->grid, st);

@@ -10,6 +10,7 @@
 
 #include <algorithm>
 
+#include "kernels.hpp"
 #include "ops_common.hpp"
 
 namespace ll {
@@ -165,7 +166,7 @@ __global__ void __launch_bounds__(256) xent_stats_kernel(const XentRows r, const
     }
     __syncthreads();
     block_join(m, s, red);
-    if (threadIdx.x == 0) r.parts[i * r.np + p0 + k] = XentPart{m, s};
+    if (threadIdx.x == 0) r.parts[(int64_t)(p0 + k) * r.part_ld + i] = float2{m, s};
   }
 }
 
@@ -177,32 +178,90 @@ hipError_t launch_xent_stats(const XentRows& r, const float* z, int64_t ldz, int
   return hipGetLastError();
 }
 
-// One wave per row: joins its parts.
-__global__ void __launch_bounds__(256) xent_lse_kernel(const XentRows r) {
-  const int lane = threadIdx.x & 63;
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (i >= r.N) return;
+// Joins each row's parts: 64 rows per workgroup, 16 waves taking every 16th
+// part of each, joined in wave order.
+__global__ void __launch_bounds__(1024) xent_lse_kernel(const XentRows r) {
+  __shared__ float red[16][2][64];
+  __shared__ float row_lse[64], row_coef[64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t i = (int64_t)blockIdx.x * 64 + lane;
   float m = kNegInf, s = 0.f;
-  for (int p = lane; p < r.np; p += 64) {
-    const XentPart q = r.parts[i * r.np + p];
-    join(m, s, q.m, q.s);
+  if (i < r.N) {
+#pragma unroll 4
+    for (int p = w; p < r.np; p += 16) {
+      const float2 q = r.parts[(int64_t)p * r.part_ld + i];
+      join(m, s, q.x, q.y);
+    }
   }
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) join(m, s, __shfl_xor(m, k, 64), __shfl_xor(s, k, 64));
-  if (lane == 0) {
-    const bool live = has_target(r, r.target[i]);
+  red[w][0][lane] = m;
+  red[w][1][lane] = s;
+  __syncthreads();
+  if (w == 0 && i < r.N) {
+    for (int k = 1; k < 16; ++k) join(m, s, red[k][0][lane], red[k][1][lane]);
+    const int64_t t = r.target[i];
+    const bool live = has_target(r, t);
     const float lse = live ? m + logf(s) : 0.f;
+    const float coef = live && r.dloss ? r.dloss[i] * (r.scale ? r.scale[0] : 1.f) : 0.f;
     r.lse[i] = lse;
+    r.coef[i] = coef;
+    r.column[i] = live ? (int32_t)t : -1;
     r.loss[i] = live ? lse - r.zt[i] : 0.f;
     if (r.lse_out) r.lse_out[i] = lse;
-    if (r.dloss) r.coef[i] = live ? r.dloss[i] * (r.scale ? r.scale[0] : 1.f) : 0.f;
+    row_lse[lane] = lse;
+    row_coef[lane] = coef * (1.f / kNumeratorScale);
+  }
+  if (r.factor0 >= r.np) return;  // uniform
+  __syncthreads();
+  if (i >= r.N) return;
+  for (int p = r.factor0 + w; p < r.np; p += 16) {
+    float2* const q = &r.parts[(int64_t)p * r.part_ld + i];
+    q->x = __expf(q->x - row_lse[lane]) * row_coef[lane];
   }
 }
 
 hipError_t launch_xent_lse(const XentRows& r, hipStream_t s) {
-  const int64_t blocks = (r.N + 3) / 4;
-  if (blocks > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)blocks), dim3(256), 0, s, r);
+  hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((r.N + 63) / 64)), dim3(1024), 0, s, r);
+  return hipGetLastError();
+}
+
+// 64 rows by 256 columns (two parts) per workgroup, 8 columns per thread and
+// step.  Rows without a target become zeros whatever their numerators are.
+template <int TY>
+__global__ void __launch_bounds__(256) xent_numerators_kernel(const XentRows r, uint16_t* dz, int64_t ldd, int64_t v0,
+                                                              int p0) {
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  const int c = blockIdx.x * 256 + 8 * x;
+  const float2* f = r.parts + (int64_t)(p0 + c / 128) * r.part_ld;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int64_t i = (int64_t)blockIdx.y * 64 + 8 * k + y;
+    if (i >= r.N) return;
+    Chunk<LL_F16, 8> e;
+    Chunk<TY, 8> o;
+    uint16_t* const p = dz + i * ldd + c;
+    e.template load<false>(p, 8);
+    const float g = f[i].x;
+    const int32_t t = r.column[i];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o.put(j, t < 0 ? 0.f : e.get(j) * g);
+    const int64_t at = t - v0 - c;  // the numerator's rounding would be lost against the 1
+    if (t >= 0 && at >= 0 && at < 8) {
+      const float own = (__expf(r.zt[i] - r.lse[i]) - 1.f) * r.coef[i];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (at == j) o.put(j, own);
+    }
+    o.template store<false>(p, 8);
+  }
+}
+
+hipError_t launch_xent_numerators(const XentRows& r, void* dz, int64_t ldd, int64_t v0, int cols, int p0, int type,
+                                  hipStream_t s) {
+  const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)((r.N + 63) / 64));
+  if (type == LL_BF16)
+    hipLaunchKernelGGL((xent_numerators_kernel<LL_BF16>), grid, dim3(256), 0, s, r, (uint16_t*)dz, ldd, v0, p0);
+  else
+    hipLaunchKernelGGL((xent_numerators_kernel<LL_F16>), grid, dim3(256), 0, s, r, (uint16_t*)dz, ldd, v0, p0);
   return hipGetLastError();
 }
 
@@ -218,8 +277,8 @@ __global__ void __launch_bounds__(256) xent_dz_kernel(const XentRows r, const fl
     int lo, hi;
     split_range((int)ldd, splits, (int)(it % splits), lo, hi);
     const float coef = r.coef[i], lse = r.lse[i];
-    const bool live = has_target(r, r.target[i]);
-    const int64_t t = live ? r.target[i] - v0 : -1;
+    const bool live = r.column[i] >= 0;
+    const int64_t t = r.column[i] - v0;
     for (int c = lo + 4 * threadIdx.x; c < hi; c += 1024) {
       uint16_t o[4] = {};
       if (live && c < cols) {

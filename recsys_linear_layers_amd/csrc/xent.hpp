@@ -6,11 +6,6 @@
 
 namespace ll {
 
-// Maximum and sum of exp(z - maximum) over some of a row's logits.
-struct XentPart {
-  float m, s;
-};
-
 struct XentRows {
   const void* x;           // [N][ldx]
   const void* w;           // [V][ldw], for the target's logit
@@ -21,11 +16,16 @@ struct XentRows {
   // workspace
   void* xp;                // [N][ldp] copy of x: zeros past D and in rows without a target
   float* zt;               // [N] the target's logit
-  float* lse;              // [N]
+  float* lse;              // [N], as coef and column up to whole tiles of rows
   float* coef;             // [N] upstream gradient times scale[0]; 0 without a target
+  int32_t* column;         // [N] the target, -1 for none
   float* scale;            // fp16: {S, 1/S}; null otherwise
-  XentPart* parts;         // [N][np]
-  int32_t np;
+  // Per part of a row's logits: maximum m and sum s of exp(z - m), [np][part_ld];
+  // parts from factor0 on then hold in place of m what turns their numerators
+  // exp(z - m) * kNumeratorScale into gradients.
+  float2* parts;
+  int64_t part_ld;
+  int32_t np, factor0;
   // outputs
   float* loss;
   float* lse_out;          // null: not wanted
@@ -34,13 +34,17 @@ struct XentRows {
 hipError_t launch_xent_prep(const XentRows& r, int type, hipStream_t s);
 // Power of two S that brings the largest |dloss| near 2^14 (fp16 gradients of the logits).
 hipError_t launch_xent_scale(const XentRows& r, hipStream_t s);
-// parts[row][p0 + split] of fp32 logits z [N][ldz], cols wide, in `splits` pieces per row.
+// parts[p0 + split][row] of fp32 logits z [N][ldz], cols wide, in `splits` pieces per row.
 hipError_t launch_xent_stats(const XentRows& r, const float* z, int64_t ldz, int cols, int p0, int splits,
                              hipStream_t s);
 hipError_t launch_xent_lse(const XentRows& r, hipStream_t s);
 // dz[row][c] = (exp(z - lse) - (v0 + c == target)) * coef for c < cols, 0 up to ldd.
 hipError_t launch_xent_dz(const XentRows& r, const float* z, int64_t ldz, int64_t v0, int cols, void* dz,
                           int64_t ldd, int type, int cus, hipStream_t s);
+// In place on the fp16 numerators of one piece, 128 columns per part from part
+// p0 on: dz = numerator * factor as `type`, and the target's own from its logit.
+hipError_t launch_xent_numerators(const XentRows& r, void* dz, int64_t ldd, int64_t v0, int cols, int p0, int type,
+                                  hipStream_t s);
 // out[i][j] = (a[i][j] + b[i][j]) * (*scale) as `type`; b and scale may be null.
 hipError_t launch_xent_finish(const float* a, const float* b, const float* scale, int64_t rows, int64_t cols,
                               int64_t lda, void* out, int64_t ldo, int type, int cus, hipStream_t s);

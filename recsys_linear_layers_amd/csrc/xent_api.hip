@@ -2,6 +2,7 @@
 // vocabulary, workspace layout and the sequence of launches.  The declarations
 // and their contracts are in include/linlayers.h.
 #include <stdio.h>
+#include <stdlib.h>
 #include <string.h>
 
 #include <algorithm>
@@ -22,19 +23,21 @@ struct xent_plan {
   int64_t ldw;        // row stride of w as the products read it
   bool pack_w;
   int64_t cols;       // vocabulary entries per piece (the last may have fewer)
-  int pieces, splits; // splits: parts per row and piece
+  bool fused;         // the softmax runs in the logits' product; else it reads fp32 logits
+  int pieces, kept;   // kept: the last pieces, whose numerators stay for the gradients
+  int parts, np;      // per row and piece, and over all pieces
+  int64_t rows;       // N, up to whole tiles where fused
   int64_t ldz, ldd;   // row strides of the fp32 logits and of the 16-bit dz of a piece
   bool dx_direct;     // dx leaves its product in its final form
-  bool dw_direct;
   gemm_plan logits[2], dxp[2], dwp[2];  // [1]: the last piece
-  size_t off_xp, off_wp, off_zt, off_lse, off_coef, off_scale, off_parts, off_z, off_dz, off_dxa, off_dxb, off_dwt,
+  size_t off_xp, off_wp, off_zt, off_lse, off_coef, off_column, off_scale, off_parts, off_z, off_dz, off_dxa, off_dxb, off_dwt,
       off_gemm, gemm_bytes, ws_bytes;
 };
 
 namespace {
 
-// Bytes the logits and their gradient may take when the description does not
-// say: 2 GiB, under 1% of the card's memory.
+// Bytes the logits or numerators and their gradient may take when the
+// description does not say: 2 GiB, under 1% of the card's memory.
 constexpr int64_t kDefaultPieceBytes = 2ll << 30;
 // Rows from which a weight whose rows are not whole 64-element blocks is copied
 // first: the copy costs 4 V D bytes of traffic, and lets the products run on
@@ -106,27 +109,49 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   if (s != LL_OK) return s;
   p.cus = info->cus;
 
+  // Whether the softmax runs in the logits' product (the hand-ordered kind's
+  // 256x256 tiles, whatever kind a plain product would take): from half a
+  // tile of rows on, when the tiles fill half of the CUs.  Both ways, us: loss
+  // and gradients 4096 x 131072 x 4096 10128 against 13096, 16384 x 8192 x 512
+  // 620 / 819, 1024 x 32768 x 2048 421 / 477, 256 x 32768 x 2048 214 / 206;
+  // loss alone 2000 x 9000 x 128 37 / 87, 256 x 32768 x 1024 40 / 44; with few
+  // rows the tiles' empty rows cost more: 64 x 131072 x 2048 451 / 421 and 1 x
+  // 131072 x 4096 718 / 669.  LL_XENT_FUSED=0 / 1 overrides (measurement).
+  const int64_t N = d->N, limit = d->piece_bytes ? d->piece_bytes : kDefaultPieceBytes;
+  const uint32_t padded_w = p.pack_w ? kPaddedB : 0;
+  const bool dw_tmp = p.dw && f16 && d->dw_type != LL_F32;
+  const int64_t tiles = (N + 255) / 256 * ((d->V + 255) / 256);
+  // x, and 256 rows of w, below 2 GB; whole 64-deep slices of w
+  const bool fits = N * p.ldp < (1 << 30) && p.ldw < (1 << 22) && (d->D % 64 == 0 || p.pack_w);
+  p.fused = fits && N > 128 && tiles * 2 > p.cus;
+  if (const char* env = getenv("LL_XENT_FUSED")) p.fused = fits && N > 0 && env[0] == '1';
+  p.rows = p.fused ? round_up(N, 256) : std::max<int64_t>(N, 1);
+
   // Pieces of the vocabulary: as many columns as the bound holds, in whole
   // tiles, all pieces alike but the last; a piece of w and of dz stays below
-  // 2 GB, which the hand-ordered kind's descriptors need.
-  const int64_t N = d->N, rows = std::max<int64_t>(N, 1);
-  const int64_t limit = d->piece_bytes ? d->piece_bytes : kDefaultPieceBytes;
-  const bool dw_tmp = p.dw && f16 && d->dw_type != LL_F32;
-  const int64_t per_col = rows * (grads ? 6 : 4) + (dw_tmp ? d->D * 4 : 0);
-  const int64_t two_gb = (1 << 30) / std::max(rows, p.ldw) - 256;
-  int64_t cols = std::min(limit / per_col, two_gb) / 256 * 256;
-  cols = std::max<int64_t>(cols, 256);
+  // 2 GB, which the hand-ordered kind's descriptors need.  Where numerators are
+  // kept but not all fit, a piece is a quarter of what fits, so that most of
+  // the bound is used.
+  const int64_t per_col = (p.fused ? (grads ? p.rows * 2 : 0) : p.rows * (grads ? 6 : 4)) + (dw_tmp ? d->D * 4 : 0);
+  const int64_t two_gb = (1 << 30) / std::max(grads ? p.rows : 1, p.ldw) - 256;
+  int64_t cols = std::min(per_col ? limit / per_col : two_gb, two_gb);
+  if (p.fused && grads && cols < d->V) cols = std::min(limit / 4 / per_col, two_gb);
+  cols = std::max<int64_t>(cols / 256 * 256, 256);
   p.pieces = (int)((d->V + cols - 1) / cols);
   p.cols = round_up((d->V + p.pieces - 1) / p.pieces, 256);
   p.pieces = (int)((d->V + p.cols - 1) / p.cols);
   const int64_t last = d->V - (p.pieces - 1) * p.cols;
   const int64_t first = p.pieces > 1 ? p.cols : last;
   p.ldz = round_up(first, 4);
-  p.ldd = round_up(first, 64);
-  // parts of at least 1024 columns, up to 8 workgroups per CU over all rows
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>((first + 1023) / 1024, 8ll * p.cus / rows));
+  p.ldd = round_up(first, 256);
+  const int64_t slot = p.rows * p.ldd * 2;
+  p.kept = !grads ? 0 : p.fused ? (int)std::max<int64_t>(1, std::min<int64_t>(p.pieces, limit / slot)) : 1;
+  // Fused: a part is 128 columns, two per tile.  Else parts of at least 1024
+  // columns, up to 8 workgroups per CU over all rows.
+  p.parts = p.fused ? (int)(p.ldd / 128)
+                    : (int)std::max<int64_t>(1, std::min<int64_t>((first + 1023) / 1024, 8ll * p.cus / p.rows));
+  p.np = (p.pieces - 1) * p.parts + (p.fused ? (int)(round_up(last, 256) / 128) : p.parts);
   p.dx_direct = p.dx && p.pieces == 1 && !f16;
-  p.dw_direct = p.dw && !f16;
 
   size_t off = 0;
   auto take = [&](size_t n) {
@@ -137,21 +162,22 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   p.off_xp = take((size_t)N * p.ldp * 2);
   p.off_wp = take(p.pack_w ? (size_t)d->V * p.ldp * 2 : 0);
   p.off_zt = take((size_t)N * 4);
-  p.off_lse = take((size_t)N * 4);
-  p.off_coef = take((size_t)N * 4);
+  p.off_lse = take((size_t)p.rows * 4);
+  p.off_coef = take((size_t)p.rows * 4);
+  p.off_column = take((size_t)p.rows * 4);
   p.off_scale = take(8);
-  p.off_parts = take((size_t)N * p.pieces * p.splits * sizeof(XentPart));
-  p.off_z = take((size_t)N * p.ldz * 4);
-  if (grads) p.off_dz = take((size_t)N * p.ldd * 2);
+  p.off_parts = take((size_t)p.rows * p.np * sizeof(float2));
+  if (!p.fused) p.off_z = take((size_t)N * p.ldz * 4);
+  if (grads) p.off_dz = take((size_t)slot * p.kept);
   if (p.dx && !p.dx_direct) p.off_dxa = take((size_t)N * d->D * 4);
   if (p.dx && p.pieces > 1) p.off_dxb = take((size_t)N * d->D * 4);
   if (dw_tmp) p.off_dwt = take((size_t)first * d->D * 4);
   p.off_gemm = off;
-  const uint32_t padded_w = p.pack_w ? kPaddedB : 0;
   for (int i = 0; i < 2; ++i) {
     const int64_t n = i ? last : first;
-    gemm_desc g = product(N, n, d->D, p.ldp, 1, 1, p.ldw, p.ldz, d->type, LL_F32);
-    s = gemm_plan_build(&g, kPaddedA | padded_w, &p.logits[i]);
+    gemm_desc g = p.fused ? product(N, n, d->D, p.ldp, 1, 1, p.ldw, p.ldd, d->type, d->type)
+                          : product(N, n, d->D, p.ldp, 1, 1, p.ldw, p.ldz, d->type, LL_F32);
+    s = gemm_plan_build(&g, kPaddedA | padded_w | (p.fused ? kWholeTiles : 0), &p.logits[i]);
     if (s != LL_OK) return s;
     p.gemm_bytes = std::max(p.gemm_bytes, p.logits[i].ws_bytes);
     if (p.dx) {
@@ -184,8 +210,8 @@ ll_status xent_plan_workspace_size(const xent_plan* p, size_t* bytes) {
 
 ll_status xent_plan_describe(const xent_plan* p, char* buf, size_t len) {
   if (!p || !buf || len == 0) return fail(LL_ERR_INVALID_ARG, "null argument");
-  snprintf(buf, len, "pieces=%d cols=%lld packW=%d logits=%s dx=%s dw=%s ws=%zu", p->pieces, (long long)p->cols,
-           (int)p->pack_w, kind_info(p->logits[0].kind).name, p->dx ? kind_info(p->dxp[0].kind).name : "-",
+  snprintf(buf, len, "pieces=%d cols=%lld kept=%d fused=%d packW=%d logits=%s dx=%s dw=%s ws=%zu", p->pieces,
+           (long long)p->cols, p->kept, (int)p->fused, (int)p->pack_w, kind_info(p->logits[0].kind).name, p->dx ? kind_info(p->dxp[0].kind).name : "-",
            p->dw ? kind_info(p->dwp[0].kind).name : "-", p->ws_bytes);
   return ok();
 }
@@ -251,16 +277,23 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
   r.lse = (float*)(base + p->off_lse);
   r.coef = (float*)(base + p->off_coef);
   r.scale = f16 && grads ? (float*)(base + p->off_scale) : nullptr;
-  r.parts = (XentPart*)(base + p->off_parts);
-  r.np = p->pieces * p->splits;
+  r.column = (int32_t*)(base + p->off_column);
+  r.parts = (float2*)(base + p->off_parts);
+  r.part_ld = p->rows;
+  r.np = p->np;
+  r.factor0 = p->fused && grads ? (p->pieces - p->kept) * p->parts : r.np;
   r.loss = loss;
   r.lse_out = lse;
   float* const z = (float*)(base + p->off_z);
-  void* const dz = base + p->off_dz;
   float* const dxa = (float*)(base + p->off_dxa);
   float* const dxb = (float*)(base + p->off_dxb);
   float* const dwt = (float*)(base + p->off_dwt);
   const float* const unscale = r.scale ? r.scale + 1 : nullptr;
+  auto is_kept = [&](int k) { return k >= p->pieces - p->kept; };
+  // kept pieces have their own place, the others the first one once its turn is over
+  auto dz_of = [&](int k) -> void* {
+    return base + p->off_dz + (is_kept(k) ? (size_t)(k - (p->pieces - p->kept)) * p->rows * p->ldd * 2 : 0);
+  };
 
   if (N > 0) {
     e = launch_xent_prep(r, d.type, st);
@@ -275,35 +308,53 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
     }
   }
   const uint16_t* const wk = p->pack_w ? (const uint16_t*)(base + p->off_wp) : (const uint16_t*)w;
-  auto logits_of = [&](int k) {
-    return gemm_run_plan(&p->logits[k + 1 == p->pieces], r.xp, wk + (int64_t)k * p->cols * p->ldw, z, nullptr, gws,
-                         p->gemm_bytes, st);
-  };
   auto cols_of = [&](int k) { return (int)std::min(p->cols, d.V - (int64_t)k * p->cols); };
+  // The logits' product of piece k, fused with softmax epilogue `epi` or into z.
+  auto logits_of = [&](int k, int epi) {
+    const uint16_t* const wp = wk + (int64_t)k * p->cols * p->ldw;
+    const gemm_plan* const g = &p->logits[k + 1 == p->pieces];
+    if (!p->fused) return gemm_run_plan(g, r.xp, wp, z, nullptr, gws, p->gemm_bytes, st);
+    GemmKArgs x;
+    memset(&x, 0, sizeof x);
+    x.parts = r.parts;
+    x.part_ld = r.part_ld;
+    x.part0 = k * p->parts;
+    x.col0 = (int32_t)(k * p->cols);
+    x.lse = r.lse;
+    x.coef = r.coef;
+    x.column = r.column;
+    return gemm_run_plan(g, r.xp, wp, epi == kSoftmaxStats ? nullptr : dz_of(k), nullptr, gws, p->gemm_bytes, st, epi,
+                         &x);
+  };
   ll_status s;
   if (N > 0) {
     for (int k = 0; k < p->pieces; ++k) {
-      s = logits_of(k);
+      s = logits_of(k, grads && is_kept(k) ? kSoftmaxNumerators : kSoftmaxStats);
       if (s != LL_OK) return s;
-      e = launch_xent_stats(r, z, p->ldz, cols_of(k), k * p->splits, p->splits, st);
-      if (e != hipSuccess) return hip_fail(e, "xent stats launch");
+      if (!p->fused) {
+        e = launch_xent_stats(r, z, p->ldz, cols_of(k), k * p->parts, p->parts, st);
+        if (e != hipSuccess) return hip_fail(e, "xent stats launch");
+      }
     }
     e = launch_xent_lse(r, st);
     if (e != hipSuccess) return hip_fail(e, "xent lse launch");
   }
   if (!grads) return ok();
-  // The last piece's logits are still there; the others are formed again.
+  // The kept pieces first; the logits of the others are formed again.
   for (int k = p->pieces - 1, n = 0; k >= 0; --k, ++n) {
     const int li = k + 1 == p->pieces;
     const int64_t v0 = (int64_t)k * p->cols;
     const int cols = cols_of(k);
+    void* const dz = dz_of(k);
     if (N > 0) {
-      if (n > 0) {
-        s = logits_of(k);
+      if (!is_kept(k)) {
+        s = logits_of(k, kSoftmaxGradient);
         if (s != LL_OK) return s;
       }
-      const int64_t ldd = p->ldd;
-      e = launch_xent_dz(r, z, p->ldz, v0, cols, dz, ldd, d.type, p->cus, st);
+      if (!p->fused)
+        e = launch_xent_dz(r, z, p->ldz, v0, cols, dz, p->ldd, d.type, p->cus, st);
+      else if (is_kept(k))
+        e = launch_xent_numerators(r, dz, p->ldd, v0, cols, k * p->parts, d.type, st);
       if (e != hipSuccess) return hip_fail(e, "xent dz launch");
       if (p->dx) {
         s = gemm_run_plan(&p->dxp[li], dz, wk + v0 * p->ldw, p->dx_direct ? dx : n == 0 ? dxa : dxb, nullptr, gws,

@@ -8,8 +8,10 @@ sum of V exponentials carries the largest of the logits' errors, the rounding
 of its argument differences and of the sum (V terms; 2 log2 V + 40 roundings
 each, in trees), and its own.  The exponentials are the hardware's: 2^-22
 relative plus the rounding of an argument r, |r| 2 u.  dz is then off by that
-error of z - lse relative to p, and once h of itself for its rounding; with
-fp16 it is scaled first, so that only values below 2^-14 / 2^13 of the largest
+error of z - lse relative to p, once h of itself for its rounding, and once
+2^-11 of p where its numerator was kept in fp16 (down to 2^-29 of the largest
+numerator of its part, which is at most 1; below, 2^-40 absolute); with fp16
+it is scaled first, so that only values below 2^-14 / 2^13 of the largest
 |dloss| lose bits: at most 2^-25 / 2^13 of it.  The products add (V + 2) u or
 (N + 2) u of the sum of magnitudes, and q of the result.  What is smaller than
 a normal fp32 or bf16 number, 2^-126, may be lost (the exponential, dz, an
@@ -87,7 +89,8 @@ def _check(x, w, target, dloss, out, ignore, what):
     dz = p.clone()
     dz.scatter_add_(1, at, -torch.ones_like(zt)[:, None])
     dz *= g
-    ed = (p * (elog + tol[:, None] + 2 * U * spread.abs() + 4 * U) * g.abs() + dz.abs() * (h + 4 * U)) * 1.01
+    kept = p * 2.0 ** -11 + 2.0 ** -40
+    ed = ((p * (elog + tol[:, None] + 2 * U * spread.abs() + 4 * U) + kept) * g.abs() + dz.abs() * (h + 4 * U)) * 1.01
     ed += 2.0 ** -126 * (1 + g.abs())
     if x.dtype == torch.float16:
         ed += 2.0 ** -38 * float(dloss.abs().max())
@@ -116,7 +119,8 @@ def _case(N, V, D, dtype, pad=0, seed=0, std=1.5, ignored=0.2):
 # tiles; enough rows and tiles for the large-tile products
 SIZES = [(1, 1, 8, 0), (1, 1000, 64, 0), (2, 300, 1, 0), (5, 257, 72, 8), (16, 4096, 128, 0), (65, 777, 100, 0),
          (130, 2001, 1000, 3), (300, 50, 33, 0), (257, 5003, 192, 0), (700, 1025, 96, 0), (1, 40000, 520, 0),
-         (1030, 4100, 320, 0), (2048, 8192, 64, 0), (4, 3, 5000, 0)]
+         (1030, 4100, 320, 0), (2048, 8192, 64, 0), (4, 3, 5000, 0), (4100, 2050, 72, 0), (300, 20000, 128, 8),
+         (1200, 9999, 200, 0), (513, 12801, 1088, 0)]
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
@@ -157,6 +161,23 @@ def test_pieces_of_the_vocabulary(N, V, D, pieces, dtype):
     _check(x, w, target, dloss, out, -100, f"{pieces} pieces {dtype}")
     loss, lse = ll.vocab_xent(x, w, target, piece_bytes=1)
     _check(x, w, target, None, (loss, lse, None, None), -100, f"256 columns {dtype}")
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_numerators_kept_for_some_pieces(dtype):
+    """Large enough for the softmax in the product: some pieces keep their
+    numerators, the logits of the others are formed again; the last is short."""
+    ll = _ll()
+    N, V, D = 2000, 9000, 128
+    x, w, target, dloss = _case(N, V, D, dtype, seed=6)
+    for cols, pieces, kept in ((1024, 9, 4), (1280, 8, 4), (256, 36, 4), (2048, 5, 4)):
+        # a column takes 2 bytes per padded row, and with fp16 4 per column of the dw that is scaled afterwards
+        bound = 4 * cols * (2 * 2048 + (4 * D if dtype == "float16" else 0))
+        plan = ll.xent_plan_for(x, w, x.clone(), w.clone(), piece_bytes=bound).describe()
+        assert "fused=1" in plan and f"pieces={pieces} " in plan, plan
+        assert f"kept={kept} " in plan or dtype == "float16", plan
+        out = ll.vocab_xent_grad(x, w, target, dloss, piece_bytes=bound)
+        _check(x, w, target, dloss, out, -100, f"{dtype} pieces of {cols}")
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
