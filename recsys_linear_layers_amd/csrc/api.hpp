@@ -61,6 +61,9 @@ constexpr uint32_t kPaddedA = 1u, kPaddedB = 2u;
 // The hand-ordered kind in whole tiles, K not split: what a softmax epilogue
 // needs (LL_ERR_UNSUPPORTED where that kind cannot take the operands).
 constexpr uint32_t kWholeTiles = 4u;
+// The hand-ordered kind, K split over the idle CUs, where its tiles alone would
+// leave more than half of the chip idle.
+constexpr uint32_t kDeepK = 8u;
 
 }  // namespace ll
 
@@ -93,7 +96,8 @@ struct GemmKArgs;
 ll_status gemm_plan_build(const gemm_desc* d, uint32_t options, gemm_plan* out);
 // gemm_run on it.  softmax, with a kWholeTiles plan: launches epilogue `epi`
 // (SoftmaxEpilogue) with the softmax fields of *softmax; C may be null, and has
-// rows and columns up to whole tiles.
+// rows and columns up to whole tiles.  epi kScaleEpilogue, with a kWholeTiles plan
+// of A^T B in fp16: C is multiplied by *bias.
 ll_status gemm_run_plan(const gemm_plan* p, const void* A, const void* B, void* C, const float* bias, void* ws,
                         size_t ws_bytes, void* stream, int epi = 0, const GemmKArgs* softmax = nullptr);
 

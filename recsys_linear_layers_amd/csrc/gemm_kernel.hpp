@@ -562,6 +562,10 @@ __device__ __forceinline__ float erf_as_scaled(float x) {
   return fmaf(-poly, g, 1.f);
 }
 
+// EPI of the hand-ordered kind whose epilogue multiplies by *bias (one factor
+// for all of C, e.g. the inverse of a loss scale).
+constexpr int kScaleEpilogue = 8;
+
 // Epilogue arithmetic on one fp32 sum z plus its column's bias b: the
 // activation ACT of z + b, in fp32.  GELU is the exact form z * Phi(z) =
 // z/2 (1 + erf(z / sqrt 2)), as the product of z/2 and 1 + erf (exact where
@@ -579,6 +583,8 @@ __device__ __forceinline__ float epi(float z, float b) {
   } else if constexpr (ACT == 3) {
     const float g = __builtin_amdgcn_exp2f(__fmul_rn(x, -1.442695041f));
     return __fmul_rn(x, __builtin_amdgcn_rcpf(__fadd_rn(1.f, g)));
+  } else if constexpr (ACT == kScaleEpilogue - 1) {
+    return __fmul_rn(z, b);
   } else {
     return x;
   }

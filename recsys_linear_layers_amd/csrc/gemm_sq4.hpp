@@ -97,7 +97,8 @@ __device__ __forceinline__ void sq4_bias(const GemmKArgs& p, const TileInfo& ti,
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const int col = ti.n0 + wn0 + 16 * j + (lane & 15);
-    b[j] = (EPI > 0 && col < p.N) ? bias_at(p, col) : 0.f;
+    if constexpr (EPI == kScaleEpilogue) b[j] = *p.bias;
+    else b[j] = (EPI > 0 && col < p.N) ? bias_at(p, col) : 0.f;
   }
 }
 
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(Sq4::THREADS) __attribute__((amdgpu_waves_per_
 #undef LL_SQ4_OPERANDS
 
     lds_barrier();  // every wave is done reading the ring before it is reused
-    if constexpr (EPI >= 5) {
+    if constexpr (EPI >= 5 && EPI <= 7) {
       sq4_softmax<F16, EPI>(p, ti, wm0, wn0, lane, smem + wave * Sq4::IMG);
       sq4_count_in(cnt, wave, lane);
       if (EPI != 5 && t + stride < p.total) lds_barrier();  // as below

@@ -125,4 +125,9 @@ hipError_t launch_gemm_sq4_xent(int f16, int epi, const GemmKArgs& a, int grid, 
   return hipErrorInvalidValue;
 }
 
+hipError_t launch_gemm_sq4_am_scaled_f16(const GemmKArgs& a, int grid, hipStream_t s) {
+  hipLaunchKernelGGL((gemm_sq4<true, kScaleEpilogue, false, true>), dim3(grid), dim3(Sq4::THREADS), 0, s, a);
+  return hipGetLastError();
+}
+
 }  // namespace ll

@@ -76,6 +76,8 @@ enum SoftmaxEpilogue {
 // Numerators are at most 1; times 2^15 those down to 2^-29 are normal fp16 numbers.
 constexpr float kNumeratorScale = 32768.f;
 hipError_t launch_gemm_sq4_xent(int f16, int epi, const GemmKArgs& args, int grid, hipStream_t stream);
+// C = A^T B * *bias for fp16 operands (A M-contiguous, B N-contiguous).
+hipError_t launch_gemm_sq4_am_scaled_f16(const GemmKArgs& args, int grid, hipStream_t stream);
 
 // Fused linear-compression kernel (lincomp_kernel.hpp).
 struct LincompKArgs;

@@ -390,6 +390,9 @@ ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t options, gemm_plan* o
   }
   const bool whole_tiles = options & kWholeTiles;
   if (whole_tiles) kind = KIND_SQ4_HO;
+  if ((options & kDeepK) && sq4_fits && M > 128 && N > 128 && d->K >= 8192 &&
+      ((M + 255) / 256) * ((N + 255) / 256) * 2 <= p.cus)
+    kind = KIND_SQ4_HO;
   // A fused epilogue runs in the kinds instantiated with it (the
   // producer/consumer tiles of the same orientation rule).
   if (d->epilogue && !kind_info(kind).epi) {
@@ -696,6 +699,10 @@ ll_status ll::gemm_run_plan(const gemm_plan* p, const void* A, const void* B, vo
     k.coef = softmax->coef;
     k.column = softmax->column;
     e = launch_gemm_sq4_xent(d.a_type == LL_F16, epi, k, p->grid, st);
+    return e == hipSuccess ? ok() : hip_fail(e, "gemm launch");
+  }
+  if (epi == kScaleEpilogue) {
+    e = launch_gemm_sq4_am_scaled_f16(k, p->grid, st);
     return e == hipSuccess ? ok() : hip_fail(e, "gemm launch");
   }
   e = p->epi ? launch_gemm_epi(p->layout, p->kind, d.a_type == LL_F16, p->epi, k, p->grid, st)

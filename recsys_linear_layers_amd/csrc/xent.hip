@@ -178,26 +178,32 @@ hipError_t launch_xent_stats(const XentRows& r, const float* z, int64_t ldz, int
   return hipGetLastError();
 }
 
-// Joins each row's parts: 64 rows per workgroup, 16 waves taking every 16th
-// part of each, joined in wave order.
+// Joins each row's parts: 16 rows per workgroup (a 128-byte line of each part),
+// 64 lanes taking every 64th part of a row, joined in a fixed order.  The
+// chain is a few loads long and the rows spread over the chip; 64 rows by 16
+// lanes took 38 us at 4096 rows of 1024 parts.
 __global__ void __launch_bounds__(1024) xent_lse_kernel(const XentRows r) {
-  __shared__ float red[16][2][64];
-  __shared__ float row_lse[64], row_coef[64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t i = (int64_t)blockIdx.x * 64 + lane;
+  __shared__ float red[16][2][16];
+  __shared__ float row_lse[16], row_coef[16];
+  const int y = threadIdx.x & 15, g = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+  const int64_t i = (int64_t)blockIdx.x * 16 + y;
   float m = kNegInf, s = 0.f;
   if (i < r.N) {
 #pragma unroll 4
-    for (int p = w; p < r.np; p += 16) {
+    for (int p = g; p < r.np; p += 64) {
       const float2 q = r.parts[(int64_t)p * r.part_ld + i];
       join(m, s, q.x, q.y);
     }
   }
-  red[w][0][lane] = m;
-  red[w][1][lane] = s;
+  join(m, s, __shfl_xor(m, 16, 64), __shfl_xor(s, 16, 64));
+  join(m, s, __shfl_xor(m, 32, 64), __shfl_xor(s, 32, 64));
+  if ((threadIdx.x & 63) < 16) {
+    red[wave][0][y] = m;
+    red[wave][1][y] = s;
+  }
   __syncthreads();
-  if (w == 0 && i < r.N) {
-    for (int k = 1; k < 16; ++k) join(m, s, red[k][0][lane], red[k][1][lane]);
+  if (threadIdx.x < 16 && i < r.N) {
+    for (int k = 1; k < 16; ++k) join(m, s, red[k][0][y], red[k][1][y]);
     const int64_t t = r.target[i];
     const bool live = has_target(r, t);
     const float lse = live ? m + logf(s) : 0.f;
@@ -207,20 +213,20 @@ __global__ void __launch_bounds__(1024) xent_lse_kernel(const XentRows r) {
     r.column[i] = live ? (int32_t)t : -1;
     r.loss[i] = live ? lse - r.zt[i] : 0.f;
     if (r.lse_out) r.lse_out[i] = lse;
-    row_lse[lane] = lse;
-    row_coef[lane] = coef * (1.f / kNumeratorScale);
+    row_lse[y] = lse;
+    row_coef[y] = coef * (1.f / kNumeratorScale);
   }
   if (r.factor0 >= r.np) return;  // uniform
   __syncthreads();
   if (i >= r.N) return;
-  for (int p = r.factor0 + w; p < r.np; p += 16) {
+  for (int p = r.factor0 + g; p < r.np; p += 64) {
     float2* const q = &r.parts[(int64_t)p * r.part_ld + i];
-    q->x = __expf(q->x - row_lse[lane]) * row_coef[lane];
+    q->x = __expf(q->x - row_lse[y]) * row_coef[y];
   }
 }
 
 hipError_t launch_xent_lse(const XentRows& r, hipStream_t s) {
-  hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((r.N + 63) / 64)), dim3(1024), 0, s, r);
+  hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((r.N + 15) / 16)), dim3(1024), 0, s, r);
   return hipGetLastError();
 }
 

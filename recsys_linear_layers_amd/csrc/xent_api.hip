@@ -29,6 +29,7 @@ struct xent_plan {
   int64_t rows;       // N, up to whole tiles where fused
   int64_t ldz, ldd;   // row strides of the fp32 logits and of the 16-bit dz of a piece
   bool dx_direct;     // dx leaves its product in its final form
+  bool dw_scaled;     // dw's product takes the scale of dz out
   gemm_plan logits[2], dxp[2], dwp[2];  // [1]: the last piece
   size_t off_xp, off_wp, off_zt, off_lse, off_coef, off_column, off_scale, off_parts, off_z, off_dz, off_dxa, off_dxb, off_dwt,
       off_gemm, gemm_bytes, ws_bytes;
@@ -119,7 +120,6 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   // 131072 x 4096 718 / 669.  LL_XENT_FUSED=0 / 1 overrides (measurement).
   const int64_t N = d->N, limit = d->piece_bytes ? d->piece_bytes : kDefaultPieceBytes;
   const uint32_t padded_w = p.pack_w ? kPaddedB : 0;
-  const bool dw_tmp = p.dw && f16 && d->dw_type != LL_F32;
   const int64_t tiles = (N + 255) / 256 * ((d->V + 255) / 256);
   // x, and 256 rows of w, below 2 GB; whole 64-deep slices of w
   const bool fits = N * p.ldp < (1 << 30) && p.ldw < (1 << 22) && (d->D % 64 == 0 || p.pack_w);
@@ -132,7 +132,8 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   // 2 GB, which the hand-ordered kind's descriptors need.  Where numerators are
   // kept but not all fit, a piece is a quarter of what fits, so that most of
   // the bound is used.
-  const int64_t per_col = (p.fused ? (grads ? p.rows * 2 : 0) : p.rows * (grads ? 6 : 4)) + (dw_tmp ? d->D * 4 : 0);
+  const bool f16_dw = p.dw && f16 && d->dw_type != LL_F32;
+  const int64_t per_col = (p.fused ? (grads ? p.rows * 2 : 0) : p.rows * (grads ? 6 : 4)) + (f16_dw ? d->D * 4 : 0);
   const int64_t two_gb = (1 << 30) / std::max(grads ? p.rows : 1, p.ldw) - 256;
   int64_t cols = std::min(per_col ? limit / per_col : two_gb, two_gb);
   if (p.fused && grads && cols < d->V) cols = std::min(limit / 4 / per_col, two_gb);
@@ -152,6 +153,11 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
                     : (int)std::max<int64_t>(1, std::min<int64_t>((first + 1023) / 1024, 8ll * p.cus / p.rows));
   p.np = (p.pieces - 1) * p.parts + (p.fused ? (int)(round_up(last, 256) / 128) : p.parts);
   p.dx_direct = p.dx && p.pieces == 1 && !f16;
+  // fp16: dw carries the scale of dz.  The hand-ordered kind takes it out in
+  // its epilogue; where its tiles would fill less than half of the CUs, dw goes
+  // through fp32 (in place for an fp32 dw).
+  p.dw_scaled = p.dw && f16 && p.fused && (first + 255) / 256 * ((d->D + 255) / 256) * 2 > p.cus;
+  const bool dw_tmp = f16_dw && !p.dw_scaled;
 
   size_t off = 0;
   auto take = [&](size_t n) {
@@ -183,14 +189,14 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
     if (p.dx) {
       g = product(N, d->D, n, p.ldd, 1, p.ldw, 1, p.dx_direct ? d->stride_dx : d->D, d->type,
                   p.dx_direct ? d->dx_type : LL_F32);
-      s = gemm_plan_build(&g, kPaddedA | padded_w, &p.dxp[i]);
+      s = gemm_plan_build(&g, kPaddedA | padded_w | kDeepK, &p.dxp[i]);
       if (s != LL_OK) return s;
       p.gemm_bytes = std::max(p.gemm_bytes, p.dxp[i].ws_bytes);
     }
     if (p.dw) {
       g = product(n, d->D, N, 1, p.ldd, p.ldp, 1, dw_tmp ? d->D : d->stride_dw, d->type,
                   dw_tmp ? (int)LL_F32 : d->dw_type);
-      s = gemm_plan_build(&g, kPaddedA | kPaddedB, &p.dwp[i]);
+      s = gemm_plan_build(&g, kPaddedA | kPaddedB | (p.dw_scaled ? kWholeTiles : 0), &p.dwp[i]);
       if (s != LL_OK) return s;
       p.gemm_bytes = std::max(p.gemm_bytes, p.dwp[i].ws_bytes);
     }
@@ -373,10 +379,11 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
     if (p->dw) {
       const int64_t esz = dtype_size(d.dw_type);
       char* const dst = (char*)dw + v0 * d.stride_dw * esz;
-      const bool tmp = f16 && d.dw_type != LL_F32;
-      s = gemm_run_plan(&p->dwp[li], dz, r.xp, tmp ? (void*)dwt : (void*)dst, nullptr, gws, p->gemm_bytes, st);
+      const bool tmp = f16 && !p->dw_scaled && d.dw_type != LL_F32;
+      s = gemm_run_plan(&p->dwp[li], dz, r.xp, tmp ? (void*)dwt : (void*)dst, p->dw_scaled ? unscale : nullptr, gws,
+                        p->gemm_bytes, st, p->dw_scaled ? kScaleEpilogue : 0);
       if (s != LL_OK) return s;
-      if (f16) {
+      if (f16 && !p->dw_scaled) {
         e = launch_xent_finish(tmp ? dwt : (const float*)dst, nullptr, N > 0 ? unscale : nullptr, cols, d.D,
                                tmp ? d.D : d.stride_dw, dst, d.stride_dw, d.dw_type, p->cus, st);
         if (e != hipSuccess) return hip_fail(e, "xent dw scale launch");
