@@ -133,6 +133,133 @@ hipError_t launch_xent_scale(const XentRows& r, hipStream_t s) {
   return hipGetLastError();
 }
 
+// ---------------------------------------------------------------------------
+// Few rows: the logits of up to 16 rows, w streamed once.
+//
+// HBM bound: 2 V D bytes of w against 2 N V D flops.  A wave takes 16 entries of
+// the vocabulary: the 16x16x32 matrix instruction with w's rows as its rows and
+// x's as its columns (columns past N repeat row 0 and are dropped).  w goes
+// straight from memory into the operand registers, 16 bytes per lane and
+// instruction (64 bytes of each of the 16 rows), the next 8 loads always in
+// flight while 8 are used: at 16 waves that is 128 KB per CU, what HBM latency
+// takes.  x sits in LDS, rows 16 bytes apart beyond their length so that the 16
+// rows of a read fall on different banks.  Each lane keeps (maximum, sum) of
+// its own entries over all its wave's tiles; lanes and waves are joined at the
+// end, so a workgroup leaves one pair per row.
+// ---------------------------------------------------------------------------
+
+template <int TY>
+__device__ __forceinline__ f32x4 mfma16(const Chunk<TY, 8>& a, const Chunk<TY, 8>& b, f32x4 c) {
+  if constexpr (TY == LL_F16) {
+    f16x8 u, v;
+    __builtin_memcpy(&u, &a, 16);
+    __builtin_memcpy(&v, &b, 16);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(u, v, c, 0, 0, 0);
+  } else {
+    bf16x8 u, v;
+    __builtin_memcpy(&u, &a, 16);
+    __builtin_memcpy(&v, &b, 16);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, v, c, 0, 0, 0);
+  }
+}
+
+template <int TY, bool TAIL>
+__global__ void __launch_bounds__(1024) xent_few_kernel(const XentRows r, float* z, int64_t ldz) {
+  constexpr int U = 8;
+  typedef Chunk<TY, 8> C;
+  extern __shared__ __attribute__((aligned(16))) uint16_t xs[];  // [N][Dp + 8], Dp: D up to whole 32s
+  __shared__ float red[16][2][16];
+  const int N = (int)r.N, D = r.D, steps = (D + 31) / 32, pitch = steps * 32 + 8;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int n = lane & 15, g = lane >> 4;
+  for (int i = 0; i < N; ++i)
+    for (int c = threadIdx.x; c < steps * 4; c += 1024) {
+      C v;
+      v.clear();
+      if (8 * c < D) v.template load<TAIL>((const uint16_t*)r.x + i * r.ldx + 8 * c, D - 8 * c);
+      __builtin_memcpy(xs + i * pitch + 8 * c, &v, 16);
+    }
+  const int64_t t = n < N ? r.target[n] : -1;
+  __syncthreads();
+  const uint16_t* const xrow = xs + (n < N ? n : 0) * pitch + 8 * g;
+  const int tiles = (int)((r.V + 15) / 16);
+  const int full = D / 32 / U * U;  // steps taken U at a time, whole
+  float m = kNegInf, s = 0.f;
+  for (int tile = blockIdx.x + gridDim.x * wave; tile < tiles; tile += gridDim.x * 16) {
+    const int64_t row = min((int64_t)tile * 16 + n, r.V - 1);
+    const uint16_t* const wrow = (const uint16_t*)r.w + row * r.ldw + 8 * g;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    C cur[U];
+    if (full > 0) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u].template load<false>(wrow + 32 * u, 8);
+    }
+    for (int k = 0; k < full; k += U) {
+      C next[U];
+      if (k + U < full) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) next[u].template load<false>(wrow + 32 * (k + U + u), 8);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        C b;
+        __builtin_memcpy(&b, xrow + 32 * (k + u), 16);
+        acc = mfma16(cur[u], b, acc);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) cur[u] = next[u];
+    }
+    for (int k = full; k < steps; ++k) {
+      const int left = D - 32 * k - 8 * g;
+      C a, b;
+      if (left > 0) a.template load<TAIL>(wrow + 32 * k, left);
+      else a.clear();
+      __builtin_memcpy(&b, xrow + 32 * k, 16);
+      acc = mfma16(a, b, acc);
+    }
+    // lane: row n of x, entries 16 tile + 4 g + 0 .. 3
+    const int64_t v0 = (int64_t)tile * 16 + 4 * g;
+    float m4 = kNegInf;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (v0 + i >= r.V) acc[i] = kNegInf;
+      else if (v0 + i == t) r.zt[n] = acc[i];
+      m4 = fmaxf(m4, acc[i]);
+    }
+    float s4 = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s4 += acc[i] == kNegInf ? 0.f : __expf(acc[i] - m4);
+    join(m, s, m4, s4);
+    if (z && n < N) *(f32x4*)(z + n * ldz + v0) = acc;  // ldz: whole groups of 16
+  }
+  join(m, s, __shfl_xor(m, 16, 64), __shfl_xor(s, 16, 64));
+  join(m, s, __shfl_xor(m, 32, 64), __shfl_xor(s, 32, 64));
+  if (lane < 16) {
+    red[wave][0][n] = m;
+    red[wave][1][n] = s;
+  }
+  __syncthreads();
+  if (threadIdx.x < N) {
+    for (int k = 1; k < 16; ++k) join(m, s, red[k][0][n], red[k][1][n]);
+    r.parts[(int64_t)blockIdx.x * r.part_ld + n] = float2{m, s};
+  }
+}
+
+hipError_t launch_xent_few(const XentRows& r, float* z, int64_t ldz, int type, hipStream_t s) {
+  const size_t lds = (size_t)r.N * ((r.D + 31) / 32 * 32 + 8) * 2;
+  if (r.N < 1 || r.N > kXentFewRows || lds > (size_t)kXentFewBytes) return hipErrorInvalidValue;
+#define LL_FEW(TY)                                                                                                  \
+  if (r.D % 8) hipLaunchKernelGGL((xent_few_kernel<TY, true>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);          \
+  else hipLaunchKernelGGL((xent_few_kernel<TY, false>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
+  if (type == LL_BF16) {
+    LL_FEW(LL_BF16)
+  } else {
+    LL_FEW(LL_F16)
+  }
+#undef LL_FEW
+  return hipGetLastError();
+}
+
 // Columns [lo, hi) of a split, in whole groups of four.
 __device__ __forceinline__ void split_range(int cols, int splits, int k, int& lo, int& hi) {
   const int quads = (cols + 3) / 4;

@@ -24,6 +24,7 @@ struct xent_plan {
   bool pack_w;
   int64_t cols;       // vocabulary entries per piece (the last may have fewer)
   bool fused;         // the softmax runs in the logits' product; else it reads fp32 logits
+  bool few;           // few rows: w is streamed once, with fp32 logits for the gradients
   int pieces, kept;   // kept: the last pieces, whose numerators stay for the gradients
   int parts, np;      // per row and piece, and over all pieces
   int64_t rows;       // N, up to whole tiles where fused
@@ -153,6 +154,15 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
                     : (int)std::max<int64_t>(1, std::min<int64_t>((first + 1023) / 1024, 8ll * p.cus / p.rows));
   p.np = (p.pieces - 1) * p.parts + (p.fused ? (int)(round_up(last, 256) / 128) : p.parts);
   p.dx_direct = p.dx && p.pieces == 1 && !f16;
+  // Few rows: w streamed once past x in LDS.
+  p.few = N >= 1 && N <= kXentFewRows && N * (round_up(d->D, 32) + 8) * 2 <= kXentFewBytes && !p.fused &&
+          (!grads || p.pieces == 1);
+  if (p.few) {
+    p.pieces = 1;
+    p.cols = round_up(d->V, 256);
+    p.ldz = round_up(d->V, 16);
+    p.parts = p.np = (int)std::min<int64_t>((d->V + 15) / 16, p.cus);
+  }
   // fp16: dw carries the scale of dz.  The hand-ordered kind takes it out in
   // its epilogue; where its tiles would fill less than half of the CUs, dw goes
   // through fp32 (in place for an fp32 dw).
@@ -166,14 +176,14 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
     return at;
   };
   p.off_xp = take((size_t)N * p.ldp * 2);
-  p.off_wp = take(p.pack_w ? (size_t)d->V * p.ldp * 2 : 0);
+  p.off_wp = take(p.pack_w && (grads || !p.few) ? (size_t)d->V * p.ldp * 2 : 0);
   p.off_zt = take((size_t)N * 4);
   p.off_lse = take((size_t)p.rows * 4);
   p.off_coef = take((size_t)p.rows * 4);
   p.off_column = take((size_t)p.rows * 4);
   p.off_scale = take(8);
   p.off_parts = take((size_t)p.rows * p.np * sizeof(float2));
-  if (!p.fused) p.off_z = take((size_t)N * p.ldz * 4);
+  if (!p.fused && (grads || !p.few)) p.off_z = take((size_t)N * p.ldz * 4);
   if (grads) p.off_dz = take((size_t)slot * p.kept);
   if (p.dx && !p.dx_direct) p.off_dxa = take((size_t)N * d->D * 4);
   if (p.dx && p.pieces > 1) p.off_dxb = take((size_t)N * d->D * 4);
@@ -217,7 +227,8 @@ ll_status xent_plan_workspace_size(const xent_plan* p, size_t* bytes) {
 ll_status xent_plan_describe(const xent_plan* p, char* buf, size_t len) {
   if (!p || !buf || len == 0) return fail(LL_ERR_INVALID_ARG, "null argument");
   snprintf(buf, len, "pieces=%d cols=%lld kept=%d fused=%d packW=%d logits=%s dx=%s dw=%s ws=%zu", p->pieces,
-           (long long)p->cols, p->kept, (int)p->fused, (int)p->pack_w, kind_info(p->logits[0].kind).name, p->dx ? kind_info(p->dxp[0].kind).name : "-",
+           (long long)p->cols, p->kept, (int)p->fused, (int)p->pack_w,
+           p->few ? "few_rows" : kind_info(p->logits[0].kind).name, p->dx ? kind_info(p->dxp[0].kind).name : "-",
            p->dw ? kind_info(p->dwp[0].kind).name : "-", p->ws_bytes);
   return ok();
 }
@@ -301,7 +312,7 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
     return base + p->off_dz + (is_kept(k) ? (size_t)(k - (p->pieces - p->kept)) * p->rows * p->ldd * 2 : 0);
   };
 
-  if (N > 0) {
+  if (N > 0 && (grads || !p->few)) {
     e = launch_xent_prep(r, d.type, st);
     if (e != hipSuccess) return hip_fail(e, "xent prep launch");
     if (r.scale) {
@@ -333,8 +344,12 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
                          &x);
   };
   ll_status s;
+  if (p->few) {
+    e = launch_xent_few(r, grads ? z : nullptr, p->ldz, d.type, st);
+    if (e != hipSuccess) return hip_fail(e, "xent few rows launch");
+  }
   if (N > 0) {
-    for (int k = 0; k < p->pieces; ++k) {
+    for (int k = 0; k < p->pieces && !p->few; ++k) {
       s = logits_of(k, grads && is_kept(k) ? kSoftmaxNumerators : kSoftmaxStats);
       if (s != LL_OK) return s;
       if (!p->fused) {

@@ -139,6 +139,26 @@ def test_loss_and_gradients(N, V, D, pad, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("N,V,D,pad", [(1, 15, 3, 0), (3, 17, 40, 0), (7, 1000, 33, 5), (16, 1001, 4096, 0),
+                                       (16, 70000, 264, 8), (2, 4099, 8192, 0), (17, 4099, 256, 0), (9, 300, 8200, 0)])
+def test_few_rows(N, V, D, pad, dtype):
+    """Up to 16 rows (as far as x fits) stream the vocabulary once; 17 do not."""
+    import torch
+    ll = _ll()
+    x, w, target, dloss = _case(N, V, D, dtype, pad, ignored=0.1)
+    few = N <= 16 and N * (-(-D // 32) * 32 + 8) * 2 <= 144 * 1024
+    assert ("few_rows" in ll.xent_plan_for(x, w).describe()) == few
+    what = f"{dtype} {N}x{V}x{D}+{pad}"
+    loss, lse = ll.vocab_xent(x, w, target)
+    _check(x, w, target, None, (loss, lse, None, None), -100, what)
+    _check(x, w, target, dloss, ll.vocab_xent_grad(x, w, target, dloss), -100, what)
+    bad, t = x.clone(), target.clone()
+    bad[-1], t[-1] = float("nan"), V
+    got = ll.vocab_xent(bad, w, t)
+    assert torch.equal(got[0][:-1], loss[:-1]) and float(got[0][-1]) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 @pytest.mark.parametrize("V,D", [(1, 8), (1000, 64), (40000, 520), (5001, 333)])
 def test_one_row_with_a_target(V, D, dtype):
     ll = _ll()
