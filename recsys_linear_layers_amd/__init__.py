@@ -490,7 +490,10 @@ _op_ws: dict = {}
 
 
 def _stream_of(t):
-    return _torch().cuda.current_stream(t.device).cuda_stream
+    if not t.is_cuda:
+        raise ValueError("tensors must be on a GPU")
+    # torch.cuda.current_stream() builds a Stream object for the same value (1.9 us, as long as some of the kernels)
+    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _op_workspace(device, stream: int, need: int):
@@ -536,7 +539,7 @@ def embedding(table, ids, scale: float = 1.0, out=None):
     _vector(ids, ids.numel(), "ids", (torch.int64,))
     (V, D), T = table.shape, ids.shape[0]
     if out is None:
-        out = torch.empty((T, D), dtype=table.dtype, device=table.device)
+        out = table.new_empty((T, D))
     if tuple(out.shape) != (T, D) or out.dtype != table.dtype:
         raise ValueError("out must be [T][D] of the table's type")
     _same_device(table, ids, out)
@@ -558,7 +561,7 @@ def embedding_grad(ids, dout, rows: int, scale: float = 1.0, padding_idx: int | 
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
-        out = torch.empty((rows, D), dtype=dout.dtype, device=dout.device)
+        out = dout.new_empty((rows, D))
     if tuple(out.shape) != (rows, D) or out.dtype != dout.dtype:
         raise ValueError("out must be [rows][D] of dout's type")
     if padding_idx is not None and padding_idx < 0:
@@ -589,7 +592,7 @@ def layernorm(x, gamma=None, beta=None, eps: float = 1e-5, out=None):
     torch = _torch()
     N, D = x.shape
     if out is None:
-        out = torch.empty((N, D), dtype=x.dtype, device=x.device)
+        out = x.new_empty((N, D))
     if tuple(out.shape) != (N, D) or out.dtype != x.dtype:
         raise ValueError("out must be [N][D] of x's type")
     ptype = _norm_params(x, gamma, beta)
@@ -610,7 +613,7 @@ def layernorm_grad(dy, x, mean, rstd, gamma=None, out=None, param_grads: bool = 
     if tuple(dy.shape) != (N, D) or dy.dtype != x.dtype:
         raise ValueError("dy must have x's shape and type")
     if out is None:
-        out = torch.empty((N, D), dtype=x.dtype, device=x.device)
+        out = x.new_empty((N, D))
     if tuple(out.shape) != (N, D) or out.dtype != x.dtype:
         raise ValueError("out must be [N][D] of x's type")
     for t in (mean, rstd):
@@ -698,9 +701,9 @@ def vocab_xent_grad(x, w, target, dloss, ignore_index: int = -100, piece_bytes: 
     torch = _torch()
     _vector(dloss, x.shape[0], "dloss", (torch.float32,))
     if want_dx and dx is None:
-        dx = torch.empty(tuple(x.shape), dtype=x.dtype, device=x.device)
+        dx = x.new_empty(x.shape)
     if want_dw and dw is None:
-        dw = torch.empty(tuple(w.shape), dtype=w.dtype, device=w.device)
+        dw = w.new_empty(w.shape)
     dx, dw = dx if want_dx else None, dw if want_dw else None
     for t, like, what in ((dx, x, "dx"), (dw, w, "dw")):
         if t is not None and (t.shape != like.shape or t.dtype not in (like.dtype, torch.float32)):

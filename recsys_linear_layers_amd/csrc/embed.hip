@@ -4,14 +4,15 @@
 // The lookup reads and writes each row once: HBM bound.
 //
 // The gradient sorts the tokens by id, stably (a counting sort by digits of
-// the (id, position) pairs, so a row's tokens stay in their order), and then
-// every row of dw is written once, by the lanes that own it, as the sum of its
-// tokens in that order: no floating-point atomics, so the result does not
-// depend on timing.  A few ids take a large share of the positions in real
-// data.  A row's tokens are consecutive after the sort, so sums over whole
-// chunks of kEmbedChunk sorted positions are formed ahead, in parallel over
-// the chunks, and the rows that hold one are shared out over workgroups of
-// their own.
+// the (id, position) pairs, so a row's tokens stay in their order), and sums
+// each row's tokens, now neighbours, in that order: no floating-point atomics,
+// so the result does not depend on timing.  Most rows of a large table have no
+// token.  The sort keeps few CUs busy, so its longer launches also write a
+// share of the zeros each, and the sums then overwrite the rows that have tokens.
+// A few ids take a large share of the positions in real data: sums over whole
+// chunks of kEmbedChunk sorted positions that belong to one row are formed in
+// parallel over the chunks, beside the rows that hold none, and a last launch
+// joins those of the rows that hold some.
 //
 // Rows start at any element and have any width: a 16-byte access needs no
 // alignment here, so the lanes always move 16 bytes and only a row's last
@@ -126,25 +127,48 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* tmp) {
   return base + s - v;
 }
 
-// Clears seg and the long-row count with the launch's workgroups from `first` on.
-__device__ __forceinline__ void clear_for_rows(const EmbedGradArgs& a, int first, int threads) {
-  const int64_t i0 = (int64_t)(blockIdx.x - first) * threads + threadIdx.x;
-  const int64_t step = (int64_t)(gridDim.x - first) * threads;
-  for (int64_t i = i0; i < a.V; i += step) a.seg[i] = int2{0, 0};
-  if (i0 == 0) *a.long_count = 0;
+// Share `part` of `parts` of the zeros of dw, by the launch's workgroups from
+// `first` on (none where the sums are added to dw).  Whole rows per share.
+struct FillShare {
+  int first, part, parts;
+};
+template <int THREADS>
+__device__ __forceinline__ void fill_share(const EmbedGradArgs& a, int esize, const FillShare f) {
+  const int64_t r0 = a.V * f.part / f.parts, r1 = a.V * (f.part + 1) / f.parts;
+  const int64_t id = (int64_t)(blockIdx.x - f.first) * THREADS + threadIdx.x;
+  const int64_t step = (int64_t)(gridDim.x - f.first) * THREADS;
+  typedef uint32_t words __attribute__((ext_vector_type(4)));
+  typedef words unaligned_words __attribute__((aligned(2)));
+  const words zero = {0, 0, 0, 0};
+  char* const base = (char*)a.dw;
+  if (a.ldw == a.D) {  // one run of bytes
+    const int64_t b0 = r0 * a.D * esize, n = (r1 - r0) * a.D * esize;
+    for (int64_t i = id; i < n / 16; i += step) __builtin_nontemporal_store(zero, (unaligned_words*)(base + b0) + i);
+    if (id < n % 16 / 2) ((uint16_t*)(base + b0 + n / 16 * 16))[id] = 0;
+  } else {
+    const int row_words = (int)(((int64_t)a.D * esize + 15) / 16);  // the last perhaps in part
+    for (int64_t i = id; i < (r1 - r0) * row_words; i += step) {
+      char* const row = base + (r0 + i / row_words) * a.ldw * esize;
+      const int64_t b = i % row_words * 16, n = (int64_t)a.D * esize - b;
+      if (n >= 16) __builtin_nontemporal_store(zero, (unaligned_words*)(row + b));
+      else
+        for (int k = 0; k < n / 2; ++k) ((uint16_t*)(row + b))[k] = 0;
+    }
+  }
 }
 
 // Up to kEmbedSmall tokens: all passes in the first workgroup, tokens in
 // registers between them.  Wave w holds tokens [512 w, 512 w + 512).
-__global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradArgs a) {
+__global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradArgs a, int esize, const FillShare f) {
   constexpr int I = kEmbedSmall / 1024;
   __shared__ uint32_t skey[kEmbedSmall], spos[kEmbedSmall];
   __shared__ uint32_t cnt[16][256];
   __shared__ uint32_t tmp[16];
-  if (blockIdx.x > 0) {
-    clear_for_rows(a, 1, 1024);
+  if ((int)blockIdx.x >= f.first) {
+    fill_share<1024>(a, esize, f);
     return;
   }
+  if (threadIdx.x == 0) *a.long_count = 0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const uint64_t below = (1ull << lane) - 1;
   const int t0 = wave * (I * 64) + lane;
@@ -211,13 +235,15 @@ __global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradA
 // digits with global atomics during the move is a launch less but slower: the
 // frequent ids meet on a few counters.  16 against 8.5 + 5 us at 32768 tokens.)
 template <bool FIRST>
-__global__ void __launch_bounds__(256) embed_hist_kernel(const EmbedGradArgs a, int pass, int nblk) {
+__global__ void __launch_bounds__(256) embed_hist_kernel(const EmbedGradArgs a, int pass, int esize,
+                                                         const FillShare f) {
   __shared__ uint32_t cnt[1 << kSortMaxBits];
   const int bins = 1 << a.bits, shift = pass * a.bits, src = pass & 1;
-  if (FIRST && (int)blockIdx.x >= nblk) {
-    clear_for_rows(a, nblk, 256);
+  if ((int)blockIdx.x >= f.first) {
+    fill_share<256>(a, esize, f);
     return;
   }
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.long_count = 0;
   for (int b = threadIdx.x; b < bins; b += 256) cnt[b] = 0;
   __syncthreads();
 #pragma unroll
@@ -230,12 +256,14 @@ __global__ void __launch_bounds__(256) embed_hist_kernel(const EmbedGradArgs a, 
 }
 
 // hist[k][b] becomes the tokens with digit b in workgroups before k; total[b]
-// all of them.  64 digits per workgroup, four waves with a quarter of the k each.
-__global__ void __launch_bounds__(256) embed_scan_kernel(uint32_t* hist, uint32_t* total, int nblk, int bins) {
-  __shared__ uint32_t part[4][64];
+// all of them.  64 digits per workgroup, 16 waves with a sixteenth of the k each.
+__global__ void __launch_bounds__(1024) embed_scan_kernel(const EmbedGradArgs a, int nblk) {
+  __shared__ uint32_t part[16][64];
+  uint32_t* const hist = a.hist;
+  const int bins = 1 << a.bits;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int b = blockIdx.x * 64 + lane;
-  const int lo = nblk * w / 4, hi = nblk * (w + 1) / 4;
+  const int lo = (int)((int64_t)nblk * w / 16), hi = (int)((int64_t)nblk * (w + 1) / 16);
   uint32_t sum = 0;
   if (b < bins) {
 #pragma unroll 8
@@ -246,7 +274,7 @@ __global__ void __launch_bounds__(256) embed_scan_kernel(uint32_t* hist, uint32_
   if (b >= bins) return;
   uint32_t at = 0;
   for (int q = 0; q < w; ++q) at += part[q][lane];
-  if (w == 3) total[b] = at + sum;
+  if (w == 15) a.total[b] = at + sum;
   for (int k0 = lo; k0 < hi; k0 += 8) {
     uint32_t v[8];
 #pragma unroll
@@ -263,10 +291,15 @@ __global__ void __launch_bounds__(256) embed_scan_kernel(uint32_t* hist, uint32_
 // Moves each token to its place by the pass's digit; a wave owns consecutive
 // tokens and takes them 64 at a time in order, so equal digits keep theirs.
 template <bool FIRST>
-__global__ void __launch_bounds__(256) embed_scatter_kernel(const EmbedGradArgs a, int pass) {
+__global__ void __launch_bounds__(256) embed_scatter_kernel(const EmbedGradArgs a, int pass, int esize,
+                                                            const FillShare f) {
   constexpr int I = kSortItems / 256;
   __shared__ uint32_t cnt[4][1 << kSortMaxBits];
   __shared__ uint32_t tmp[4];
+  if ((int)blockIdx.x >= f.first) {
+    fill_share<256>(a, esize, f);
+    return;
+  }
   const int bins = 1 << a.bits, shift = pass * a.bits, src = pass & 1;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int t0 = blockIdx.x * kSortItems + wave * (I * 64) + lane;
@@ -383,50 +416,6 @@ __device__ __forceinline__ void groups_sum(float* red, int lx_log2, int x, int g
   }
 }
 
-// Row bounds in the sorted order, the rows that hold a whole chunk of sorted
-// positions, and the sums of those chunks.
-template <int TY, bool TAIL>
-__global__ void __launch_bounds__(256) embed_chunk_kernel(const EmbedGradArgs a, int src, int lx_log2) {
-  constexpr int VEC = kWide<TY>;
-  __shared__ float red[256 * VEC];
-  const uint32_t* key = a.key[src];
-  const uint32_t* pos = a.pos[src];
-  const int p0 = blockIdx.x * kEmbedChunk;
-  if (blockIdx.y == 0 && threadIdx.x < kEmbedChunk) {
-    const int p = p0 + threadIdx.x;
-    if (p < a.T) {
-      const uint32_t k = key[p];
-      if ((int64_t)k < a.V) {
-        if (p == 0 || key[p - 1] != k) a.seg[k].x = p;
-        if (p == a.T - 1 || key[p + 1] != k) a.seg[k].y = p + 1;
-      }
-    }
-  }
-  if (p0 + kEmbedChunk > a.T) return;
-  const uint32_t k0 = key[p0];
-  if (key[p0 + kEmbedChunk - 1] != k0 || (int64_t)k0 >= a.V) return;  // uniform
-  // the first whole chunk of its row: sorted keys, so the one before is whole if it starts with the same key
-  if (blockIdx.y == 0 && threadIdx.x == 0 && (p0 == 0 || key[p0 - kEmbedChunk] != k0))
-    a.long_rows[atomicAdd(a.long_count, 1u)] = k0;
-  const int lx = 1 << lx_log2;
-  const int x = threadIdx.x & (lx - 1), g = threadIdx.x >> lx_log2;
-  const int groups = 256 >> lx_log2;
-  const int per = (kEmbedChunk + groups - 1) / groups;
-  const int lo = p0 + min(g * per, kEmbedChunk), hi = p0 + min((g + 1) * per, kEmbedChunk);
-  for (int d0 = blockIdx.y * lx * VEC; d0 < a.D; d0 += gridDim.y * lx * VEC) {
-    const int d = d0 + x * VEC;
-    float acc[VEC] = {};
-    if (d < a.D) add_tokens<TY, TAIL, 4>(a, [&](int p) { return pos[p]; }, lo, hi, d, acc);
-    groups_sum<VEC>(red, lx_log2, x, g, acc);
-    if (g == 0 && d < a.D) {
-      Chunk<LL_F32, VEC> o;
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) o.put(i, acc[i]);
-      o.template store<TAIL>((uint32_t*)a.partial + (int64_t)blockIdx.x * a.D + d, a.D - d);
-    }
-  }
-}
-
 template <int TY, bool TAIL>
 __device__ __forceinline__ void write_row(const EmbedGradArgs& a, int64_t v, int d, const float (&acc)[kWide<TY>]) {
   constexpr int VEC = kWide<TY>;
@@ -442,21 +431,102 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs& a, int64_t v, int
 #pragma unroll
     for (int i = 0; i < VEC; ++i) o.put(i, acc[i] * a.scale);
   }
-  // the gradient is not read again soon (items case 149 -> 109 us, vocabulary case 236 -> 222 us)
+  // the gradient is not read again soon (262144 tokens into 1000003 x 64 fp32: 149 -> 109 us)
   o.template store<TAIL, true>(dst, a.D - d);
 }
 
-// Rows a group handles one after the other.
-constexpr int kRowsPerGroup = 8;
-
-// The rows of dw after a sort.  The first `long_blocks` workgroups share out
-// the rows that hold a whole chunk, a block of columns at a time: loose tokens
-// in front, whole chunks, loose tokens behind, split over the groups and
-// joined in their order.  They come first because they take longest.  In the
-// other workgroups a group sums a row by itself.
+// The first `chunk_blocks` workgroups, in `chunk_cols` shares of the columns, go
+// through the chunks of sorted positions: the sum of a chunk that belongs to one row
+// whole, and that row's bounds.  The others: the rows without a whole chunk, a
+// group from the row's first sorted position, a block of columns at a time.
 template <int TY, bool TAIL>
-__global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedGradArgs a, int src, int lx_log2,
-                                                         int long_blocks, int col_blocks) {
+__global__ void __launch_bounds__(256) embed_sums_kernel(const EmbedGradArgs a, int src, int lx_log2, int chunk_blocks,
+                                                         int chunk_cols, int col_blocks) {
+  constexpr int VEC = kWide<TY>;
+  __shared__ float red[256 * VEC];
+  const uint32_t* key = a.key[src];
+  const uint32_t* order = a.pos[src];
+  auto pos = [&](int p) { return order[p]; };
+  const int lx = 1 << lx_log2;
+  const int x = threadIdx.x & (lx - 1), g = threadIdx.x >> lx_log2;
+  const int groups = 256 >> lx_log2;
+  if ((int)blockIdx.x < chunk_blocks) {
+    const int cb = blockIdx.x % chunk_cols, nch = a.T / kEmbedChunk;
+    for (int chunk = blockIdx.x / chunk_cols; chunk < nch; chunk += chunk_blocks / chunk_cols) {
+      const int p0 = chunk * kEmbedChunk;
+      const uint32_t k0 = key[p0];
+      if (key[p0 + kEmbedChunk - 1] != k0 || (int64_t)k0 >= a.V) continue;  // uniform
+      // the first whole chunk of its row: sorted keys, so the one before is whole if it starts with the same key
+      if (cb == 0 && threadIdx.x == 0 && (p0 == 0 || key[p0 - kEmbedChunk] != k0)) {
+        int lo = p0;
+        while (lo > 0 && key[lo - 1] == k0) --lo;
+        int in = p0 + kEmbedChunk - 1, out = a.T;  // last position known to be the row's, first known not to be
+        while (in + 1 < out) {
+          const int mid = in + (out - in) / 2;
+          if (key[mid] == k0) in = mid;
+          else out = mid;
+        }
+        a.long_rows[atomicAdd(a.long_count, 1u)] = int2{lo, out};
+      }
+      const int per = (kEmbedChunk + groups - 1) / groups;
+      const int lo = p0 + min(g * per, kEmbedChunk), hi = p0 + min((g + 1) * per, kEmbedChunk);
+      for (int d0 = cb * lx * VEC; d0 < a.D; d0 += chunk_cols * lx * VEC) {
+        const int d = d0 + x * VEC;
+        float acc[VEC] = {};
+        if (d < a.D) add_tokens<TY, TAIL, 4>(a, pos, lo, hi, d, acc);
+        groups_sum<VEC>(red, lx_log2, x, g, acc);
+        if (g == 0 && d < a.D) {
+          Chunk<LL_F32, VEC> o;
+  #pragma unroll
+          for (int i = 0; i < VEC; ++i) o.put(i, acc[i]);
+          o.template store<TAIL>((uint32_t*)a.partial + (int64_t)chunk * a.D + d, a.D - d);
+        }
+      }
+    }
+    return;
+  }
+  // Everything that depends on the position alone is loaded at once; a row of up
+  // to four tokens then needs their rows and nothing else.  (Two positions per
+  // group at once: more registers, fewer groups in flight, 206 against 195 us.)
+  constexpr uint32_t none = 0xFFFFFFFFu;  // no key
+  const int item = blockIdx.x - chunk_blocks, cb = item % col_blocks;
+  const int p = item / col_blocks * groups + g;
+  if (p >= a.T) return;
+  const int whole = (p + kEmbedChunk - 1) / kEmbedChunk * kEmbedChunk + kEmbedChunk - 1;
+  const uint32_t k = key[p], before = p > 0 ? key[p - 1] : none, in_whole = whole < a.T ? key[whole] : none;
+  uint32_t at[4];
+  at[0] = order[p];
+  int n = 1;  // tokens of the row that starts here, up to four
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    const uint32_t after = p + i < a.T ? key[p + i] : none;
+    at[i] = p + i < a.T ? order[p + i] : 0;
+    n += n == i && after == k;
+  }
+  if ((int64_t)k >= a.V || before == k || in_whole == k) return;  // not a row's first, or it holds a whole chunk
+  int end = p + n;
+  if (n == 4)
+    while (end < a.T && key[end] == k) ++end;
+  for (int d = (cb * lx + x) * VEC; d < a.D; d += col_blocks * lx * VEC) {
+    const typename Elem<TY>::raw* base = (const typename Elem<TY>::raw*)a.dout + d;
+    Chunk<TY, VEC> v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) v[i].template load<TAIL>(base + (int64_t)at[i] * a.ldg, a.D - d);
+      else v[i].clear();
+    float acc[VEC] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) add_chunk(acc, v[i]);
+    add_tokens<TY, TAIL, 4>(a, pos, p + n, end, d, acc);
+    write_row<TY, TAIL>(a, k, d, acc);
+  }
+}
+
+// The rows that hold whole chunks, a block of columns at a time: loose tokens
+// in front, whole chunks, loose tokens behind, split over the groups and joined
+// in their order.
+template <int TY, bool TAIL>
+__global__ void __launch_bounds__(256) embed_long_kernel(const EmbedGradArgs a, int src, int lx_log2) {
   constexpr int VEC = kWide<TY>;
   __shared__ float red[256 * VEC];
   const uint32_t* order = a.pos[src];
@@ -464,44 +534,30 @@ __global__ void __launch_bounds__(256) embed_rows_kernel(const EmbedGradArgs a, 
   const int lx = 1 << lx_log2;
   const int x = threadIdx.x & (lx - 1), g = threadIdx.x >> lx_log2;
   const int groups = 256 >> lx_log2;
-  if ((int)blockIdx.x < long_blocks) {
-    const int all_cols = (a.D + lx * VEC - 1) / (lx * VEC);
-    const int64_t items = (int64_t)*a.long_count * all_cols;
-    for (int64_t it = blockIdx.x; it < items; it += long_blocks) {
-      const int64_t v = a.long_rows[it / all_cols];
-      const int d = ((int)(it % all_cols) * lx + x) * VEC;
-      const int2 s = a.seg[v];
-      const int h0 = (s.x + kEmbedChunk - 1) / kEmbedChunk * kEmbedChunk, h1 = s.y / kEmbedChunk * kEmbedChunk;
-      const int nh = h0 - s.x, nc = (h1 - h0) / kEmbedChunk, n = nh + nc + (s.y - h1);
-      const int lo = (int)((int64_t)n * g / groups), hi = (int)((int64_t)n * (g + 1) / groups);
-      float acc[VEC] = {};
-      if (d < a.D) {
-        add_tokens<TY, TAIL, 4>(a, pos, s.x + lo, s.x + min(hi, nh), d, acc);
-        const int k0 = h0 / kEmbedChunk - nh;  // item i is chunk k0 + i
-        add_partials<VEC, TAIL>(a, k0 + max(lo, nh), k0 + min(hi, nh + nc), d, acc);
-        const int b0 = h1 - nh - nc;           // item i is sorted position b0 + i
-        add_tokens<TY, TAIL, 4>(a, pos, b0 + max(lo, nh + nc), b0 + hi, d, acc);
-      }
-      groups_sum<VEC>(red, lx_log2, x, g, acc);
-      if (g == 0 && d < a.D) write_row<TY, TAIL>(a, v, d, acc);
+  const int all_cols = (a.D + lx * VEC - 1) / (lx * VEC);
+  const int64_t items = (int64_t)*a.long_count * all_cols;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int2 s = a.long_rows[it / all_cols];
+    const int64_t v = a.key[src][s.x];
+    const int d = ((int)(it % all_cols) * lx + x) * VEC;
+    const int h0 = (s.x + kEmbedChunk - 1) / kEmbedChunk * kEmbedChunk, h1 = s.y / kEmbedChunk * kEmbedChunk;
+    const int nh = h0 - s.x, nc = (h1 - h0) / kEmbedChunk, n = nh + nc + (s.y - h1);
+    const int lo = (int)((int64_t)n * g / groups), hi = (int)((int64_t)n * (g + 1) / groups);
+    float acc[VEC] = {};
+    if (d < a.D) {
+      add_tokens<TY, TAIL, 4>(a, pos, s.x + lo, s.x + min(hi, nh), d, acc);
+      const int k0 = h0 / kEmbedChunk - nh;  // item i is chunk k0 + i
+      add_partials<VEC, TAIL>(a, k0 + max(lo, nh), k0 + min(hi, nh + nc), d, acc);
+      const int b0 = h1 - nh - nc;           // item i is sorted position b0 + i
+      add_tokens<TY, TAIL, 4>(a, pos, b0 + max(lo, nh + nc), b0 + hi, d, acc);
     }
-    return;
-  }
-  // rows far apart: neighbouring ids are often alike in frequency
-  const int item = blockIdx.x - long_blocks;
-  const int64_t step = (int64_t)((gridDim.x - long_blocks) / col_blocks) * groups;
-  const int cb = item % col_blocks;
-  for (int64_t v = (int64_t)(item / col_blocks) * groups + g; v < a.V; v += step) {
-    const int2 s = a.seg[v];
-    if ((s.x + kEmbedChunk - 1) / kEmbedChunk < s.y / kEmbedChunk) continue;  // holds a whole chunk
-    if (a.accumulate && s.x == s.y) continue;
-    for (int d = (cb * lx + x) * VEC; d < a.D; d += col_blocks * lx * VEC) {
-      float acc[VEC] = {};
-      add_tokens<TY, TAIL, 4>(a, pos, s.x, s.y, d, acc);
-      write_row<TY, TAIL>(a, v, d, acc);
-    }
+    groups_sum<VEC>(red, lx_log2, x, g, acc);
+    if (g == 0 && d < a.D) write_row<TY, TAIL>(a, v, d, acc);
   }
 }
+
+// Rows a group handles one after the other.
+constexpr int kRowsPerGroup = 8;
 
 // Few tokens: each workgroup picks its rows' tokens from ids itself, orders
 // them by (row, position) in LDS, and sums; rows of more than kEmbedChunk
@@ -574,49 +630,54 @@ __global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, i
 
 template <int TY, bool TAIL>
 static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream_t s) {
-  constexpr int VEC = kWide<TY>;
+  constexpr int VEC = kWide<TY>, ESIZE = (int)sizeof(typename Elem<TY>::raw);
   const int chunks = (a.D + VEC - 1) / VEC;
   const int lx = log2_up(chunks, 6);
-  const int nrows = (256 >> lx) * kRowsPerGroup;
-  const int64_t rb = (a.V + nrows - 1) / nrows;
-  // A block of columns per workgroup: a row of many tokens is then summed by
-  // several.  (The workgroups that pick their tokens from ids take all columns
-  // of a row unless the rows alone are few.)
-  const int all_cols = (chunks + (1 << lx) - 1) >> lx;
-  const int cb = a.T > kEmbedDirect
-                     ? all_cols
-                     : (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / rb));
-  if (rb * cb > 0x3FFFFFFF) return hipErrorInvalidValue;
+  const int groups = 256 >> lx;
+  const int all_cols = (chunks + (1 << lx) - 1) >> lx;  // blocks of columns
   if (a.T <= kEmbedDirect) {
+    const int nrows = groups * kRowsPerGroup;
+    const int64_t rb = (a.V + nrows - 1) / nrows;
+    // workgroups along the columns only where the rows alone are few
+    const int cb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / rb));
+    if (rb * cb > 0x7FFFFFFF) return hipErrorInvalidValue;
     hipLaunchKernelGGL((embed_few_kernel<TY, TAIL>), dim3((unsigned)(rb * cb)), dim3(256), 0, s, a, lx, cb);
     return hipGetLastError();
   }
+  // 8 KB of zeros per workgroup of 256: two stores per lane (64 KB took 28 us for
+  // a share of 134 MB instead of 22, 4 KB 29)
+  const int shares = a.T <= kEmbedSmall ? 1 : 2 * a.passes;
+  const int64_t share_bytes = a.V * (int64_t)a.D * ESIZE / shares + 1;
+  const int fill = a.accumulate ? 0 : (int)std::min<int64_t>((share_bytes + 8191) / 8192, 256 * cus);
   int src = 0;
-  const int clear = (int)std::min<int64_t>((a.V + 1023) / 1024, 4 * cus);
   if (a.T <= kEmbedSmall) {
-    hipLaunchKernelGGL(embed_small_sort_kernel, dim3(1 + clear), dim3(1024), 0, s, a);
+    hipLaunchKernelGGL(embed_small_sort_kernel, dim3(1 + (fill + 3) / 4), dim3(1024), 0, s, a, ESIZE,
+                       FillShare{1, 0, 1});
   } else {
     const int nblk = (a.T + kSortItems - 1) / kSortItems;
     for (int p = 0; p < a.passes; ++p) {
+      const FillShare h = {nblk, 2 * p, shares}, m = {nblk, 2 * p + 1, shares};
       if (p == 0)
-        hipLaunchKernelGGL((embed_hist_kernel<true>), dim3(nblk + clear), dim3(256), 0, s, a, p, nblk);
+        hipLaunchKernelGGL((embed_hist_kernel<true>), dim3(nblk + fill), dim3(256), 0, s, a, p, ESIZE, h);
       else
-        hipLaunchKernelGGL((embed_hist_kernel<false>), dim3(nblk), dim3(256), 0, s, a, p, nblk);
-      hipLaunchKernelGGL(embed_scan_kernel, dim3(((1 << a.bits) + 63) / 64), dim3(256), 0, s, a.hist, a.total, nblk,
-                         1 << a.bits);
+        hipLaunchKernelGGL((embed_hist_kernel<false>), dim3(nblk + fill), dim3(256), 0, s, a, p, ESIZE, h);
+      hipLaunchKernelGGL(embed_scan_kernel, dim3(((1 << a.bits) + 63) / 64), dim3(1024), 0, s, a, nblk);
       if (p == 0)
-        hipLaunchKernelGGL((embed_scatter_kernel<true>), dim3(nblk), dim3(256), 0, s, a, p);
+        hipLaunchKernelGGL((embed_scatter_kernel<true>), dim3(nblk + fill), dim3(256), 0, s, a, p, ESIZE, m);
       else
-        hipLaunchKernelGGL((embed_scatter_kernel<false>), dim3(nblk), dim3(256), 0, s, a, p);
+        hipLaunchKernelGGL((embed_scatter_kernel<false>), dim3(nblk + fill), dim3(256), 0, s, a, p, ESIZE, m);
       src ^= 1;
     }
   }
-  const int nch = (a.T + kEmbedChunk - 1) / kEmbedChunk;
+  const int nch = a.T / kEmbedChunk;  // whole chunks
   const int ccb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / nch));
-  const int lb = (int)std::min<int64_t>((int64_t)(a.T / kEmbedChunk) * all_cols, 4 * cus);
-  hipLaunchKernelGGL((embed_chunk_kernel<TY, TAIL>), dim3(nch, ccb), dim3(256), 0, s, a, src, lx);
-  hipLaunchKernelGGL((embed_rows_kernel<TY, TAIL>), dim3((unsigned)(lb + rb * cb)), dim3(256), 0, s, a, src, lx, lb,
-                     cb);
+  const int cwg = (int)std::min<int64_t>(nch, std::max<int64_t>(1, 8 * (int64_t)cus / ccb)) * ccb;
+  const int64_t pb = (a.T + groups - 1) / groups;
+  if (cwg + pb * all_cols > 0x7FFFFFFF) return hipErrorInvalidValue;
+  hipLaunchKernelGGL((embed_sums_kernel<TY, TAIL>), dim3((unsigned)(cwg + pb * all_cols)), dim3(256), 0, s, a, src, lx,
+                     cwg, ccb, all_cols);
+  const int lb = (int)std::min<int64_t>((int64_t)nch * all_cols, 4 * cus);
+  hipLaunchKernelGGL((embed_long_kernel<TY, TAIL>), dim3(lb), dim3(256), 0, s, a, src, lx);
   return hipGetLastError();
 }
 

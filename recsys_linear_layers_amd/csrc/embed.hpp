@@ -40,10 +40,9 @@ struct EmbedGradArgs {
   uint32_t* pos[2];
   uint32_t* hist;       // [sort workgroups][1 << bits]
   uint32_t* total;      // [1 << bits]
-  int2* seg;            // [V] sorted positions first, last + 1 of each row's tokens
   float* partial;       // [T / kEmbedChunk][D] sums of whole chunks
-  uint32_t* long_count; // rows that hold a whole chunk,
-  uint32_t* long_rows;  // in any order
+  uint32_t* long_count; // rows that hold a whole chunk, in any order:
+  int2* long_rows;      // their sorted positions first, last + 1
   int32_t bits, passes; // digits; 8 bits where one workgroup sorts
 };
 

@@ -110,10 +110,6 @@ struct RowCols {
       else v[k].clear();
     }
   }
-  __device__ __forceinline__ void keep_packed() {
-#pragma unroll
-    for (int k = 0; k < NCH; ++k) v[k].keep_packed();
-  }
 };
 
 // TPR lanes hold a row; THREADS / TPR rows per workgroup and step.  Loading the

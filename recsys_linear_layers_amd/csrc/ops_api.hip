@@ -49,7 +49,7 @@ ll_status embed_sizes(int64_t V, int64_t T, int64_t D, int64_t s0, int64_t s1, i
 
 struct EmbedGradLayout {
   int bits = 0, passes = 0;
-  size_t key[2] = {0, 0}, pos[2] = {0, 0}, hist = 0, total = 0, seg = 0, partial = 0, long_count = 0,
+  size_t key[2] = {0, 0}, pos[2] = {0, 0}, hist = 0, total = 0, partial = 0, long_count = 0,
          long_rows = 0, bytes = 0;
 };
 
@@ -80,10 +80,9 @@ EmbedGradLayout embed_grad_layout(const embed_grad_desc* d) {
     l.hist = take(((size_t)nblk << l.bits) * 4);
     l.total = take((size_t)4 << l.bits);
   }
-  l.seg = take((size_t)d->V * 8);
   l.partial = take((size_t)(d->T / kEmbedChunk) * (size_t)d->D * 4);
   l.long_count = take(4);
-  l.long_rows = take((size_t)(d->T / kEmbedChunk) * 4);
+  l.long_rows = take((size_t)(d->T / kEmbedChunk) * 8);
   l.bytes = off;
   return l;
 }
@@ -172,10 +171,9 @@ ll_status embed_grad_run(const embed_grad_desc* d, const int64_t* ids, const voi
     }
     a.hist = (uint32_t*)(w + l.hist);
     a.total = (uint32_t*)(w + l.total);
-    a.seg = (int2*)(w + l.seg);
     a.partial = (float*)(w + l.partial);
     a.long_count = (uint32_t*)(w + l.long_count);
-    a.long_rows = (uint32_t*)(w + l.long_rows);
+    a.long_rows = (int2*)(w + l.long_rows);
   }
   const hipError_t err = launch_embed_grad(a, d->type, info->cus, (hipStream_t)stream);
   return err == hipSuccess ? ok() : hip_fail(err, "embed gradient launch");

@@ -156,6 +156,7 @@ def test_python_checks():
     ids = torch.zeros(4, dtype=torch.int64)
     for call in (lambda: ll.embedding(x, ids.int()), lambda: ll.embedding(x.t(), ids), lambda: ll.embedding(x[0], ids),
                  lambda: ll.embedding(x, ids, out=torch.zeros(4, 9)), lambda: ll.embedding(x.double(), ids),
+                 lambda: ll.embedding(x, ids), lambda: ll.layernorm(x), lambda: ll.embedding_grad(ids, x, 5),  # on the host
                  lambda: ll.embedding_grad(ids, x[:3], 5), lambda: ll.embedding_grad(ids, x, 5, accumulate=True),
                  lambda: ll.embedding_grad(ids, x, 5, padding_idx=-1),
                  lambda: ll.embedding_grad(ids, x, 5, out=torch.zeros(5, 8, dtype=torch.float16)),
