@@ -556,14 +556,15 @@ __global__ void __launch_bounds__(256) embed_long_kernel(const EmbedGradArgs a, 
   }
 }
 
-// Rows a group handles one after the other.
+// Most rows a group handles one after the other.
 constexpr int kRowsPerGroup = 8;
 
 // Few tokens: each workgroup picks its rows' tokens from ids itself, orders
 // them by (row, position) in LDS, and sums; rows of more than kEmbedChunk
 // tokens with all groups together.
 template <int TY, bool TAIL>
-__global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, int lx_log2, int col_blocks) {
+__global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, int lx_log2, int group_rows,
+                                                        int col_blocks) {
   constexpr int VEC = kWide<TY>;
   __shared__ float red[256 * VEC];
   __shared__ uint32_t list[kEmbedDirect], order[kEmbedDirect];
@@ -572,7 +573,7 @@ __global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, i
   const int lx = 1 << lx_log2;
   const int x = threadIdx.x & (lx - 1), g = threadIdx.x >> lx_log2;
   const int groups = 256 >> lx_log2;
-  const int nrows = groups * kRowsPerGroup;
+  const int nrows = groups * group_rows;
   const int64_t v0 = (int64_t)(blockIdx.x / col_blocks) * nrows;
   const int cb = blockIdx.x % col_blocks;
   for (int r = threadIdx.x; r < nrows; r += 256) seg[r] = int2{0, 0};
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, i
   auto pos = [&](int p) { return order[p]; };
   for (int d0 = cb * lx * VEC; d0 < a.D; d0 += col_blocks * lx * VEC) {
     const int d = d0 + x * VEC;
-    for (int i = 0; i < kRowsPerGroup; ++i) {
+    for (int i = 0; i < group_rows; ++i) {
       const int r = i * groups + g;
       const int2 s = seg[r];
       if (v0 + r >= a.V || d >= a.D || s.y - s.x > kEmbedChunk || (a.accumulate && s.y == s.x)) continue;
@@ -636,12 +637,14 @@ static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream
   const int groups = 256 >> lx;
   const int all_cols = (chunks + (1 << lx) - 1) >> lx;  // blocks of columns
   if (a.T <= kEmbedDirect) {
-    const int nrows = groups * kRowsPerGroup;
-    const int64_t rb = (a.V + nrows - 1) / nrows;
-    // workgroups along the columns only where the rows alone are few
-    const int cb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / rb));
+    // Fewer rows per group, then workgroups along the columns, until there are
+    // 16 workgroups per CU (each scans all ids, so no more than that).
+    const int64_t want = 16 * (int64_t)cus;
+    const int rows = (int)std::max<int64_t>(1, std::min<int64_t>(kRowsPerGroup, a.V / (groups * want)));
+    const int64_t rb = (a.V + groups * rows - 1) / (groups * rows);
+    const int cb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, want / rb));
     if (rb * cb > 0x7FFFFFFF) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((embed_few_kernel<TY, TAIL>), dim3((unsigned)(rb * cb)), dim3(256), 0, s, a, lx, cb);
+    hipLaunchKernelGGL((embed_few_kernel<TY, TAIL>), dim3((unsigned)(rb * cb)), dim3(256), 0, s, a, lx, rows, cb);
     return hipGetLastError();
   }
   // 8 KB of zeros per workgroup of 256: two stores per lane (64 KB took 28 us for
