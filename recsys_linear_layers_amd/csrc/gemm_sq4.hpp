@@ -102,9 +102,8 @@ __device__ __forceinline__ void sq4_bias(const GemmKArgs& p, const TileInfo& ti,
   }
 }
 
-// Direct stores of block N: split-K partials (raw sums), or C of any type and
-// layout with bias and activation, element by element with bounds checks
-// (ragged tiles, fp32 C, C that the staged path does not take).
+// Direct stores of block N: C of any type and layout with bias and activation,
+// element by element with bounds checks (C that the paths below do not take).
 template <int EPI, int N>
 __device__ __forceinline__ void sq4_store_block(const GemmKArgs& p, const TileInfo& ti, int wm0, int wn0, int lane,
                                                 const float (&bias)[8]) {
@@ -112,13 +111,6 @@ __device__ __forceinline__ void sq4_store_block(const GemmKArgs& p, const TileIn
   f32x4 v = sq4_acc<N>();
   const int col = ti.n0 + wn0 + 16 * J + (lane & 15);
   const int row0 = ti.m0 + wm0 + 16 * I + 4 * (lane >> 4);
-  if (p.partial) {
-    float* P = p.partial + (int64_t)ti.ks * p.M * p.N;
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-      if (row0 + r < p.M && col < p.N) P[(int64_t)(row0 + r) * p.N + col] = v[r];
-    return;
-  }
   if constexpr (EPI > 0) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) v[r] = epi<EPI - 1>(v[r], bias[J]);
@@ -178,7 +170,7 @@ __device__ __forceinline__ void sq4_tail_all(const GemmKArgs& p, int slot, int w
 #undef LL_SQ4_TAIL
 }
 
-// Whole tiles of an fp32 C with unit column stride (any row stride): one
+// Tiles of an fp32 C with unit column stride (any row stride): one
 // base pointer per lane, the row offsets (16 I + r) * ldcm wave-uniform and
 // the column block an immediate offset, so each element costs one store
 // (the general path above spends ~10 operations per element on 64-bit
@@ -186,46 +178,53 @@ __device__ __forceinline__ void sq4_tail_all(const GemmKArgs& p, int slot, int w
 // a 64-byte row piece spans two cache lines, and L2 must merge the pieces of
 // neighbouring column blocks (non-temporal stores were slower on every shape
 // but one).
-template <int EPI, int N>
-__device__ __forceinline__ void sq4_store_f32_block(float* const (&rowp)[4], float bias) {
+// EDGE: a tile that reaches past M or N; each store is predicated (one compare
+// per element, the columns' against `cols`), which still costs a third of the
+// general path.
+template <int EPI, bool EDGE, int N>
+__device__ __forceinline__ void sq4_store_f32_block(float* const (&rowp)[4], float bias, int rows, int cols) {
   f32x4 v = sq4_acc<N>();
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     float x = v[r];
     if constexpr (EPI > 0) x = epi<EPI - 1>(x, bias);
-    rowp[r][16 * (N & 7)] = x;
+    if (!EDGE || (16 * (N >> 3) + r < rows && 16 * (N & 7) < cols)) rowp[r][16 * (N & 7)] = x;
   }
 }
 
-template <int EPI, int I>
-__device__ __forceinline__ void sq4_store_f32_rows(const GemmKArgs& p, float* base, const float (&bias)[8]) {
-  float* const rowp[4] = {base + (int64_t)(16 * I + 0) * p.ldcm, base + (int64_t)(16 * I + 1) * p.ldcm,
-                          base + (int64_t)(16 * I + 2) * p.ldcm, base + (int64_t)(16 * I + 3) * p.ldcm};
-  sq4_store_f32_block<EPI, 8 * I + 0>(rowp, bias[0]);
-  sq4_store_f32_block<EPI, 8 * I + 1>(rowp, bias[1]);
-  sq4_store_f32_block<EPI, 8 * I + 2>(rowp, bias[2]);
-  sq4_store_f32_block<EPI, 8 * I + 3>(rowp, bias[3]);
-  sq4_store_f32_block<EPI, 8 * I + 4>(rowp, bias[4]);
-  sq4_store_f32_block<EPI, 8 * I + 5>(rowp, bias[5]);
-  sq4_store_f32_block<EPI, 8 * I + 6>(rowp, bias[6]);
-  sq4_store_f32_block<EPI, 8 * I + 7>(rowp, bias[7]);
+// rows, cols: left of the matrix from this lane's first row and column on.
+template <int EPI, bool EDGE, int I>
+__device__ __forceinline__ void sq4_store_f32_rows(float* base, int64_t ld, const float (&bias)[8], int rows,
+                                                   int cols) {
+  float* const rowp[4] = {base + (int64_t)(16 * I + 0) * ld, base + (int64_t)(16 * I + 1) * ld,
+                          base + (int64_t)(16 * I + 2) * ld, base + (int64_t)(16 * I + 3) * ld};
+  sq4_store_f32_block<EPI, EDGE, 8 * I + 0>(rowp, bias[0], rows, cols);
+  sq4_store_f32_block<EPI, EDGE, 8 * I + 1>(rowp, bias[1], rows, cols);
+  sq4_store_f32_block<EPI, EDGE, 8 * I + 2>(rowp, bias[2], rows, cols);
+  sq4_store_f32_block<EPI, EDGE, 8 * I + 3>(rowp, bias[3], rows, cols);
+  sq4_store_f32_block<EPI, EDGE, 8 * I + 4>(rowp, bias[4], rows, cols);
+  sq4_store_f32_block<EPI, EDGE, 8 * I + 5>(rowp, bias[5], rows, cols);
+  sq4_store_f32_block<EPI, EDGE, 8 * I + 6>(rowp, bias[6], rows, cols);
+  sq4_store_f32_block<EPI, EDGE, 8 * I + 7>(rowp, bias[7], rows, cols);
 }
 
-template <int EPI>
-__device__ __forceinline__ void sq4_store_f32_full(const GemmKArgs& p, const TileInfo& ti, int wm0, int wn0,
-                                                   int lane) {
+// An fp32 C (or, EPI 0, one split's raw sums) with row stride ld and unit column stride.
+template <int EPI, bool EDGE>
+__device__ __forceinline__ void sq4_store_f32(const GemmKArgs& p, const TileInfo& ti, float* c, int64_t ld, int wm0,
+                                              int wn0, int lane) {
   float bias[8];
   sq4_bias<EPI>(p, ti, wn0, lane, bias);
-  float* const base =
-      (float*)p.c + (int64_t)(ti.m0 + wm0 + 4 * (lane >> 4)) * p.ldcm + ti.n0 + wn0 + (lane & 15);
-  sq4_store_f32_rows<EPI, 0>(p, base, bias);
-  sq4_store_f32_rows<EPI, 1>(p, base, bias);
-  sq4_store_f32_rows<EPI, 2>(p, base, bias);
-  sq4_store_f32_rows<EPI, 3>(p, base, bias);
-  sq4_store_f32_rows<EPI, 4>(p, base, bias);
-  sq4_store_f32_rows<EPI, 5>(p, base, bias);
-  sq4_store_f32_rows<EPI, 6>(p, base, bias);
-  sq4_store_f32_rows<EPI, 7>(p, base, bias);
+  const int row = ti.m0 + wm0 + 4 * (lane >> 4), col = ti.n0 + wn0 + (lane & 15);
+  float* const base = c + (int64_t)row * ld + col;
+  const int rows = p.M - row, cols = p.N - col;
+  sq4_store_f32_rows<EPI, EDGE, 0>(base, ld, bias, rows, cols);
+  sq4_store_f32_rows<EPI, EDGE, 1>(base, ld, bias, rows, cols);
+  sq4_store_f32_rows<EPI, EDGE, 2>(base, ld, bias, rows, cols);
+  sq4_store_f32_rows<EPI, EDGE, 3>(base, ld, bias, rows, cols);
+  sq4_store_f32_rows<EPI, EDGE, 4>(base, ld, bias, rows, cols);
+  sq4_store_f32_rows<EPI, EDGE, 5>(base, ld, bias, rows, cols);
+  sq4_store_f32_rows<EPI, EDGE, 6>(base, ld, bias, rows, cols);
+  sq4_store_f32_rows<EPI, EDGE, 7>(base, ld, bias, rows, cols);
 }
 
 template <int EPI>
@@ -296,6 +295,21 @@ __device__ __forceinline__ void sq4_flush(const GemmKArgs& p, const TileInfo& ti
     // 4096^3, +1.5% at 8192^3, FFN shapes within noise)
     __builtin_nontemporal_store(v, (i32x4*)(cb + (uint32_t)off));
     off += step;
+  }
+}
+
+// The same for a tile that reaches past M or N, N a multiple of 8.
+__device__ __forceinline__ void sq4_flush_edge(const GemmKArgs& p, const TileInfo& ti, int wm0, int wn0, int lane,
+                                               const char LL_LDS* img) {
+  const int pr = (lane >> 3) & 3, ch = ((lane >> 5) << 3) | (lane & 7);
+  const int row = ti.m0 + wm0 + pr, col = ti.n0 + wn0 + ch * 8;
+  if (col >= p.N) return;
+  const char LL_LDS* const src = img + pr * Sq4::IMG_PITCH + ch * 16;
+  uint16_t* const cb = (uint16_t*)p.c;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) {
+    const i32x4 v = *(const i32x4 LL_LDS*)(src + q * 4 * Sq4::IMG_PITCH);
+    if (row + 4 * q < p.M) __builtin_nontemporal_store(v, (i32x4*)(cb + (int64_t)(row + 4 * q) * p.ldcm + col));
   }
 }
 
@@ -537,27 +551,42 @@ __global__ void __launch_bounds__(Sq4::THREADS) __attribute__((amdgpu_waves_per_
       sq4_count_in(cnt, wave, lane);
       continue;
     }
-    // a whole tile inside a 16-bit row-major C with 16-byte aligned rows:
-    // staged through LDS (uniform over the workgroup)
-    const bool staged = p.c_fast && p.c_fmt != 0 && ti.m0 + Sq4::BM <= p.M && ti.n0 + Sq4::BN <= p.N &&
-                        ((uintptr_t)p.c & 15) == 0 && (p.ldcm & 7) == 0;
+    const bool whole = ti.m0 + Sq4::BM <= p.M && ti.n0 + Sq4::BN <= p.N;
+    // a tile of a 16-bit row-major C with 16-byte aligned rows, inside it or
+    // with whole 16-byte pieces to its edge: staged through LDS (uniform over
+    // the workgroup)
+    const bool staged = p.c_fast && p.c_fmt != 0 && (whole || (p.N & 7) == 0) && ((uintptr_t)p.c & 15) == 0 &&
+                        (p.ldcm & 7) == 0;
     if (staged) {
       char LL_LDS* img = smem + wave * Sq4::IMG;
       if (p.c_fmt == 1)
         sq4_stage_all<EPI, 1>(p, ti, wn0, lane, img);
       else
         sq4_stage_all<EPI, 2>(p, ti, wn0, lane, img);
-      sq4_flush(p, ti, wm0, wn0, lane, img);
+      if (whole)
+        sq4_flush(p, ti, wm0, wn0, lane, img);
+      else
+        sq4_flush_edge(p, ti, wm0, wn0, lane, img);
       sq4_count_in(cnt, wave, lane);
       // the next work item's loads land all over the LDS the other waves
       // may still be reading
       if (t + stride < p.total) lds_barrier();
       continue;
     }
-    if (p.c_fmt == 0 && p.ldcn == 1 && !p.partial && ti.m0 + Sq4::BM <= p.M && ti.n0 + Sq4::BN <= p.N)
-      sq4_store_f32_full<EPI>(p, ti, wm0, wn0, lane);
-    else
+    if (EPI == 0 && p.partial) {
+      float* const part = p.partial + (int64_t)ti.ks * p.M * p.N;
+      if (whole)
+        sq4_store_f32<0, false>(p, ti, part, p.N, wm0, wn0, lane);
+      else
+        sq4_store_f32<0, true>(p, ti, part, p.N, wm0, wn0, lane);
+    } else if (p.c_fmt == 0 && p.ldcn == 1) {
+      if (whole)
+        sq4_store_f32<EPI, false>(p, ti, (float*)p.c, p.ldcm, wm0, wn0, lane);
+      else
+        sq4_store_f32<EPI, true>(p, ti, (float*)p.c, p.ldcm, wm0, wn0, lane);
+    } else {
       sq4_store_all<EPI>(p, ti, wm0, wn0, lane);
+    }
     sq4_count_in(cnt, wave, lane);
     }
   }

@@ -46,6 +46,14 @@ constexpr int64_t kDefaultPieceBytes = 2ll << 30;
 // the hand-ordered kind.
 constexpr int64_t kPackRows = 512;
 
+// Vocabulary entries of a piece from which the logits' product prefetches the
+// next slice of w into L2, whatever D is (a plain product does from D = 8192
+// on).  Loss alone, us, with and without: 4096 x 131072 x 4096 2990 / 3270, x
+// 2048 1620 / 1750, x 1024 909 / 974; 300 x 131072 x 2048 204 / 225; 4096 x 32768
+// x 4096 760 / 828; below that it costs: 16384 x 16384 x 2048 804 / 778, 4096 x
+// 8192 x 4096 203 / 199.
+constexpr int64_t kPrefetchCols = 32768;
+
 ll_status xent_check(const xent_desc* d) {
   if (d->N < 0 || d->V < 0 || d->D < 0) return fail(LL_ERR_INVALID_ARG, "negative size");
   if (d->V == 0 || d->D == 0) return fail(LL_ERR_INVALID_ARG, "V and D must be positive");
@@ -195,6 +203,7 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
                           : product(N, n, d->D, p.ldp, 1, 1, p.ldw, p.ldz, d->type, LL_F32);
     s = gemm_plan_build(&g, kPaddedA | padded_w | (p.fused ? kWholeTiles : 0), &p.logits[i]);
     if (s != LL_OK) return s;
+    if (p.fused && n >= kPrefetchCols) p.logits[i].b_prefetch = 1;
     p.gemm_bytes = std::max(p.gemm_bytes, p.logits[i].ws_bytes);
     if (p.dx) {
       g = product(N, d->D, n, p.ldd, 1, p.ldw, 1, p.dx_direct ? d->stride_dx : d->D, d->type,
