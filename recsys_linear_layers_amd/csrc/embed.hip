@@ -158,7 +158,7 @@ __device__ __forceinline__ void fill_share(const EmbedGradArgs& a, int esize, co
 }
 
 // Up to kEmbedSmall tokens: all passes in the first workgroup, tokens in
-// registers between them.  Wave w holds tokens [512 w, 512 w + 512).
+// registers between them.  A wave holds `steps` times 64 consecutive tokens.
 __global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradArgs a, int esize, const FillShare f) {
   constexpr int I = kEmbedSmall / 1024;
   __shared__ uint32_t skey[kEmbedSmall], spos[kEmbedSmall];
@@ -171,12 +171,13 @@ __global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradA
   if (threadIdx.x == 0) *a.long_count = 0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const uint64_t below = (1ull << lane) - 1;
-  const int t0 = wave * (I * 64) + lane;
+  const int steps = (a.T + 1023) / 1024;
+  const int t0 = wave * (steps * 64) + lane;
   uint32_t key[I], pos[I];
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int t = t0 + i * 64;
-    key[i] = t < a.T ? token_key(a, t) : 0;
+    key[i] = i < steps && t < a.T ? token_key(a, t) : 0;
     pos[i] = t;
   }
   for (int p = 0; p < a.passes; ++p) {
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradA
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < I; ++i)
-      if (t0 + i * 64 < a.T) atomicAdd(&cnt[wave][(key[i] >> shift) & 255], 1u);  // whole numbers: any order
+      if (i < steps && t0 + i * 64 < a.T) atomicAdd(&cnt[wave][(key[i] >> shift) & 255], 1u);  // whole numbers: any order
     __syncthreads();
     uint32_t sum = 0;
     if (threadIdx.x < 256)
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradA
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < I; ++i) {
+      if (i >= steps) break;
       const bool live = t0 + i * 64 < a.T;
       const uint32_t q = wave_place(cnt[wave], (key[i] >> shift) & 255, 8, live, below);
       if (live) {
@@ -213,7 +215,7 @@ __global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradA
 #pragma unroll
     for (int i = 0; i < I; ++i) {
       const int t = t0 + i * 64;
-      if (t < a.T) {
+      if (i < steps && t < a.T) {
         key[i] = skey[t];
         pos[i] = spos[t];
       }
@@ -223,7 +225,7 @@ __global__ void __launch_bounds__(1024) embed_small_sort_kernel(const EmbedGradA
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int t = t0 + i * 64;
-    if (t < a.T) {
+    if (i < steps && t < a.T) {
       a.key[0][t] = key[i];
       a.pos[0][t] = pos[i];
     }
@@ -402,17 +404,18 @@ __device__ __forceinline__ void add_partials(const EmbedGradArgs& a, int lo, int
 }
 
 // Sum over the workgroup's groups in group order; the first group gets it.
-template <int VEC>
-__device__ __forceinline__ void groups_sum(float* red, int lx_log2, int x, int g, float (&acc)[VEC]) {
-  const int groups = 256 >> lx_log2;
+template <int THREADS, int VEC>
+__device__ __forceinline__ void groups_sum(float (&red)[THREADS * VEC], int lx_log2, int x, int g,
+                                           float (&acc)[VEC]) {
+  const int groups = THREADS >> lx_log2;
   __syncthreads();  // red may still be read for the sum before
 #pragma unroll
-  for (int i = 0; i < VEC; ++i) red[i * 256 + threadIdx.x] = acc[i];
+  for (int i = 0; i < VEC; ++i) red[i * THREADS + threadIdx.x] = acc[i];
   __syncthreads();
   if (g == 0) {
     for (int k = 1; k < groups; ++k)
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] += red[i * 256 + (k << lx_log2) + x];
+      for (int i = 0; i < VEC; ++i) acc[i] += red[i * THREADS + (k << lx_log2) + x];
   }
 }
 
@@ -474,7 +477,7 @@ __global__ void __launch_bounds__(256) embed_sums_kernel(const EmbedGradArgs a, 
         const int d = d0 + x * VEC;
         float acc[VEC] = {};
         if (d < a.D) add_tokens<TY, TAIL, 4>(a, pos, lo, hi, d, acc);
-        groups_sum<VEC>(red, lx_log2, x, g, acc);
+        groups_sum<256>(red, lx_log2, x, g, acc);
         if (g == 0 && d < a.D) {
           Chunk<LL_F32, VEC> o;
   #pragma unroll
@@ -505,8 +508,15 @@ __global__ void __launch_bounds__(256) embed_sums_kernel(const EmbedGradArgs a, 
   }
   if ((int64_t)k >= a.V || before == k || in_whole == k) return;  // not a row's first, or it holds a whole chunk
   int end = p + n;
-  if (n == 4)
-    while (end < a.T && key[end] == k) ++end;
+  if (n == 4) {  // without a whole chunk, fewer than two chunks: six halvings
+    int out = min(p + 2 * kEmbedChunk, a.T);
+    for (int in = p + 3; in + 1 < out;) {
+      const int mid = in + (out - in) / 2;
+      if (key[mid] == k) in = mid;
+      else out = mid;
+    }
+    end = out;
+  }
   for (int d = (cb * lx + x) * VEC; d < a.D; d += col_blocks * lx * VEC) {
     const typename Elem<TY>::raw* base = (const typename Elem<TY>::raw*)a.dout + d;
     Chunk<TY, VEC> v[4];
@@ -523,17 +533,17 @@ __global__ void __launch_bounds__(256) embed_sums_kernel(const EmbedGradArgs a, 
 }
 
 // The rows that hold whole chunks, a block of columns at a time: loose tokens
-// in front, whole chunks, loose tokens behind, split over the groups and joined
-// in their order.
+// in front, whole chunks, loose tokens behind, split over the groups of 16 waves
+// and joined in their order.
 template <int TY, bool TAIL>
-__global__ void __launch_bounds__(256) embed_long_kernel(const EmbedGradArgs a, int src, int lx_log2) {
+__global__ void __launch_bounds__(1024) embed_long_kernel(const EmbedGradArgs a, int src, int lx_log2) {
   constexpr int VEC = kWide<TY>;
-  __shared__ float red[256 * VEC];
+  __shared__ float red[1024 * VEC];
   const uint32_t* order = a.pos[src];
   auto pos = [&](int p) { return order[p]; };
   const int lx = 1 << lx_log2;
   const int x = threadIdx.x & (lx - 1), g = threadIdx.x >> lx_log2;
-  const int groups = 256 >> lx_log2;
+  const int groups = 1024 >> lx_log2;
   const int all_cols = (a.D + lx * VEC - 1) / (lx * VEC);
   const int64_t items = (int64_t)*a.long_count * all_cols;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
@@ -551,7 +561,7 @@ __global__ void __launch_bounds__(256) embed_long_kernel(const EmbedGradArgs a, 
       const int b0 = h1 - nh - nc;           // item i is sorted position b0 + i
       add_tokens<TY, TAIL, 4>(a, pos, b0 + max(lo, nh + nc), b0 + hi, d, acc);
     }
-    groups_sum<VEC>(red, lx_log2, x, g, acc);
+    groups_sum<1024>(red, lx_log2, x, g, acc);
     if (g == 0 && d < a.D) write_row<TY, TAIL>(a, v, d, acc);
   }
 }
@@ -623,7 +633,7 @@ __global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, i
       if (len <= kEmbedChunk) continue;
       float acc[VEC] = {};
       if (d < a.D) add_tokens<TY, TAIL, 4>(a, pos, s.x + len * g / groups, s.x + len * (g + 1) / groups, d, acc);
-      groups_sum<VEC>(red, lx_log2, x, g, acc);
+      groups_sum<256>(red, lx_log2, x, g, acc);
       if (g == 0 && d < a.D) write_row<TY, TAIL>(a, v0 + r, d, acc);
     }
   }
@@ -674,13 +684,13 @@ static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream
   }
   const int nch = a.T / kEmbedChunk;  // whole chunks
   const int ccb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / nch));
-  const int cwg = (int)std::min<int64_t>(nch, std::max<int64_t>(1, 8 * (int64_t)cus / ccb)) * ccb;
+  const int cwg = (int)std::min<int64_t>(nch, std::max<int64_t>(1, 16 * (int64_t)cus / ccb)) * ccb;
   const int64_t pb = (a.T + groups - 1) / groups;
   if (cwg + pb * all_cols > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((embed_sums_kernel<TY, TAIL>), dim3((unsigned)(cwg + pb * all_cols)), dim3(256), 0, s, a, src, lx,
                      cwg, ccb, all_cols);
-  const int lb = (int)std::min<int64_t>((int64_t)nch * all_cols, 4 * cus);
-  hipLaunchKernelGGL((embed_long_kernel<TY, TAIL>), dim3(lb), dim3(256), 0, s, a, src, lx);
+  const int lb = (int)std::min<int64_t>((int64_t)nch * all_cols, 2 * cus);
+  hipLaunchKernelGGL((embed_long_kernel<TY, TAIL>), dim3(lb), dim3(1024), 0, s, a, src, lx);
   return hipGetLastError();
 }
 

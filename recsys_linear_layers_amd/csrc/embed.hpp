@@ -17,7 +17,7 @@ struct EmbedArgs {
 
 // Sorted positions per chunk; a chunk that belongs to one row whole is summed
 // once, ahead of the rows.
-constexpr int kEmbedChunk = 32;
+constexpr int kEmbedChunk = 16;
 // Tokens up to which the rows find their tokens by themselves, without a sort,
 constexpr int kEmbedDirect = 512;
 // and up to which one workgroup sorts them in LDS.
