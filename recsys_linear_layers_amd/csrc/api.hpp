@@ -61,8 +61,9 @@ constexpr uint32_t kPaddedA = 1u, kPaddedB = 2u;
 // The hand-ordered kind in whole tiles, K not split: what a softmax epilogue
 // needs (LL_ERR_UNSUPPORTED where that kind cannot take the operands).
 constexpr uint32_t kWholeTiles = 4u;
-// The hand-ordered kind, K split over the idle CUs, where its tiles alone would
-// leave more than half of the chip idle.
+// A long K beside a small C: where tiles alone would leave more than half of the
+// chip idle, the hand-ordered kind with K split over the idle CUs; where C is
+// one or two small tiles, up to 256 splits (otherwise 64) and a reduce to match.
 constexpr uint32_t kDeepK = 8u;
 
 }  // namespace ll
@@ -76,6 +77,7 @@ struct gemm_plan {
   ll::OperandPlan a, b;
   int64_t Kp;       // K rounded up to a multiple of 8
   int splits;
+  int deep;         // kDeepK: many splits of a small C
   int epi;          // fused-epilogue instantiation (0: none, or the split-K reduce applies it)
   int kiters, kps;
   int tiles_m, tiles_n, total, grid, group_m;
@@ -97,7 +99,7 @@ ll_status gemm_plan_build(const gemm_desc* d, uint32_t options, gemm_plan* out);
 // gemm_run on it.  softmax, with a kWholeTiles plan: launches epilogue `epi`
 // (SoftmaxEpilogue) with the softmax fields of *softmax; C may be null, and has
 // rows and columns up to whole tiles.  epi kScaleEpilogue, with a kWholeTiles plan
-// of A^T B in fp16: C is multiplied by *bias.
+// of A^T B in fp16 or a plan with `deep` set: C is multiplied by *bias.
 ll_status gemm_run_plan(const gemm_plan* p, const void* A, const void* B, void* C, const float* bias, void* ws,
                         size_t ws_bytes, void* stream, int epi = 0, const GemmKArgs* softmax = nullptr);
 

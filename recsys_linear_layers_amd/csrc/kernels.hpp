@@ -98,6 +98,9 @@ hipError_t launch_pack_mnmajor(const uint16_t* src, int64_t s_r, int64_t s_k, in
 hipError_t launch_splitk_reduce(const float* partial, int splits, int64_t M, int64_t N, void* C,
                                 int64_t ldcm, int64_t ldcn, int c_fmt, const float* bias, int act,
                                 hipStream_t stream);
+// C = *scale (null: 1) times the sum; for few elements and many splits.
+hipError_t launch_splitk_reduce_deep(const float* partial, int splits, int64_t M, int64_t N, void* C, int64_t ldcm,
+                                     int64_t ldcn, int c_fmt, const float* scale, hipStream_t stream);
 hipError_t launch_fill_zero(void* C, int64_t M, int64_t N, int64_t ldcm, int64_t ldcn, int c_fmt, const float* bias,
                             int act,
                             hipStream_t stream);

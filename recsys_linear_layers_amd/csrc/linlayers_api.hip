@@ -94,6 +94,10 @@ int tail_splits_for(int64_t tiles, int64_t grid, int kiters) {
   return (kiters + kps - 1) / kps;  // every split gets >= 1 slice (>= kTailMinSlices but the last)
 }
 
+// Most elements of a C whose K may be split 256 ways (kDeepK): the partials are
+// then at most 64 MB, and the reduce has at most 1024 workgroups.
+constexpr int64_t kDeepElements = 1 << 16;
+
 // The hand-ordered kind's round counters: one per XCD, 128 bytes apart.
 constexpr int kRoundSyncWords = 8 * 32;
 // Fewest rounds (passes of the persistent grid over its tiles), and fewest
@@ -428,13 +432,16 @@ ll_status ll::gemm_plan_build(const gemm_desc* d, uint32_t options, gemm_plan* o
   int splits = 1;
   if (tiles > 0 && tiles * 2 <= slots && p.Kp >= 1024 && !whole_tiles) {
     int64_t want = slots / tiles;
-    int64_t by_k = p.Kp / 512;
+    const bool deep = (options & kDeepK) && M * N <= kDeepElements;
+    int64_t by_k = p.Kp / (deep ? 256 : 512);
     splits = (int)(want < by_k ? want : by_k);
     if (splits < 1) splits = 1;
-    if (splits > 64) splits = 64;
+    if (splits > (deep ? 256 : 64)) splits = deep ? 256 : 64;
+    p.deep = deep && splits > 1;
   }
   p.kps = (p.kiters + splits - 1) / splits;
   splits = p.kiters > 0 ? (p.kiters + p.kps - 1) / p.kps : 1;  // every split gets >= 1 k-step
+  p.deep = p.deep && splits > 1;
   // Split-K partials are raw sums; the reduce then applies the epilogue.
   p.epi = (d->epilogue && splits == 1) ? (int)((d->epilogue & LL_EPI_ACT_MASK) >> 4) + 1 : 0;
   p.splits = splits;
@@ -701,7 +708,7 @@ ll_status ll::gemm_run_plan(const gemm_plan* p, const void* A, const void* B, vo
     e = launch_gemm_sq4_xent(d.a_type == LL_F16, epi, k, p->grid, st);
     return e == hipSuccess ? ok() : hip_fail(e, "gemm launch");
   }
-  if (epi == kScaleEpilogue) {
+  if (epi == kScaleEpilogue && !p->deep) {
     e = launch_gemm_sq4_am_scaled_f16(k, p->grid, st);
     return e == hipSuccess ? ok() : hip_fail(e, "gemm launch");
   }
@@ -713,7 +720,11 @@ ll_status ll::gemm_run_plan(const gemm_plan* p, const void* A, const void* B, vo
                            p->group_m, d.M, d.N, C, d.stride_cm, d.stride_cn, cfmt, bias, act, st);
     if (e != hipSuccess) return hip_fail(e, "tail reduce launch");
   }
-  if (p->splits > 1) {
+  if (p->deep) {
+    e = launch_splitk_reduce_deep(k.partial, p->splits, d.M, d.N, C, d.stride_cm, d.stride_cn, cfmt,
+                                  epi == kScaleEpilogue ? bias : nullptr, st);
+    if (e != hipSuccess) return hip_fail(e, "split-K reduce launch");
+  } else if (p->splits > 1) {
     e = launch_splitk_reduce(k.partial, p->splits, d.M, d.N, C, d.stride_cm, d.stride_cn, cfmt, bias, act, st);
     if (e != hipSuccess) return hip_fail(e, "split-K reduce launch");
   }

@@ -42,61 +42,79 @@ __device__ __forceinline__ void block_join(float& m, float& s, float* red) {
 
 __device__ __forceinline__ bool has_target(const XentRows& r, int64_t t) { return t >= 0 && t < r.V && t != r.ignore; }
 
-// Eight elements from p, of which the first n exist.
-template <bool WIDE>
-__device__ __forceinline__ void load8(const uint16_t* p, int n, uint16_t (&v)[8]) {
-  if (WIDE && n >= 8) {
-    const uint4 q = *(const uint4*)p;
-    __builtin_memcpy(v, &q, 16);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? p[i] : (uint16_t)0;
-  }
-}
-
-// One workgroup per row: the aligned copy of x (a row without a target becomes
-// zeros, so that whatever it holds cannot reach dw through 0 * inf), and the
-// target's logit as a dot product of its own.
-template <int TY, bool WX, bool WW>
+// The aligned copy of x (a row without a target becomes zeros, so that whatever
+// it holds cannot reach dw through 0 * inf), and the target's logit as a dot
+// product of its own.  LANES lanes per row.
+template <int TY, int LANES>
 __global__ void __launch_bounds__(256) xent_prep_kernel(const XentRows r) {
   __shared__ float red[4];
-  for (int64_t i = blockIdx.x; i < r.N; i += gridDim.x) {
-    const int64_t t = r.target[i];
+  constexpr int ROWS = 256 / LANES;
+  typedef Chunk<TY, 8> C;
+  const int l = threadIdx.x % LANES, y = threadIdx.x / LANES;
+  for (int64_t i0 = (int64_t)blockIdx.x * ROWS; i0 < r.N; i0 += (int64_t)gridDim.x * ROWS) {
+    const int64_t i = i0 + y;
+    const int64_t t = i < r.N ? r.target[i] : -1;
     const bool live = has_target(r, t);
     const uint16_t* x = (const uint16_t*)r.x + i * r.ldx;
     const uint16_t* w = (const uint16_t*)r.w + (live ? t : 0) * r.ldw;
-    uint4* dst = (uint4*)((uint16_t*)r.xp + i * r.ldp);
+    uint16_t* dst = (uint16_t*)r.xp + i * r.ldp;
     float acc = 0.f;
-    for (int c = threadIdx.x; c < r.ldp / 8; c += 256) {
-      uint16_t v[8] = {};
-      if (live) {
-        uint16_t u[8];
-        const int n = r.D - 8 * c;
-        load8<WX>(x + 8 * c, n, v);
-        load8<WW>(w + 8 * c, n, u);
+    if (i < r.N) {
+      for (int c = 8 * l; c < r.ldp; c += 8 * LANES) {
+        C v, u;
+        v.clear();
+        u.clear();
+        if (live && c < r.D) {
+          v.template load<true>(x + c, r.D - c);
+          u.template load<true>(w + c, r.D - c);
+        }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc = fmaf(Elem<TY>::get(v[k]), Elem<TY>::get(u[k]), acc);
+        for (int k = 0; k < 8; ++k) acc = fmaf(v.get(k), u.get(k), acc);
+        v.template store<false>(dst + c, 8);
       }
-      uint4 q;
-      __builtin_memcpy(&q, v, 16);
-      dst[c] = q;
     }
-    acc = lanes_sum<64>(acc);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
-    __syncthreads();
-    if (threadIdx.x == 0) r.zt[i] = red[0] + red[1] + red[2] + red[3];
+    acc = lanes_sum<(LANES < 64 ? LANES : 64)>(acc);
+    if constexpr (LANES == 256) {
+      __syncthreads();
+      if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
+      __syncthreads();
+      acc = red[0] + red[1] + red[2] + red[3];
+    }
+    if (l == 0 && i < r.N) r.zt[i] = acc;
   }
 }
 
+// 16 bytes of a packed row per thread, rows of any alignment and width.
+__global__ void __launch_bounds__(256) xent_pack_kernel(const uint16_t* src, int64_t lds, int64_t rows, int cols,
+                                                        uint16_t* dst, int ldp) {
+  const int chunks = ldp / 8;
+  const int64_t n = rows * chunks;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t r = n >> 31 ? i / chunks : (int64_t)((uint32_t)i / (uint32_t)chunks);
+    const int c = (int)(i - r * chunks) * 8;
+    Chunk<LL_F16, 8> v;
+    if (c < cols) v.load<true>(src + r * lds + c, cols - c);
+    else v.clear();
+    v.store<false>(dst + i * 8, 8);
+  }
+}
+
+hipError_t launch_xent_pack(const void* src, int64_t lds, int64_t rows, int cols, void* dst, int ldp, int cus,
+                            hipStream_t s) {
+  const int64_t blocks = std::min<int64_t>((rows * (ldp / 8) + 1023) / 1024, 64ll * cus);
+  if (blocks == 0) return hipSuccess;
+  hipLaunchKernelGGL(xent_pack_kernel, dim3((unsigned)blocks), dim3(256), 0, s, (const uint16_t*)src, lds, rows, cols,
+                     (uint16_t*)dst, ldp);
+  return hipGetLastError();
+}
+
 hipError_t launch_xent_prep(const XentRows& r, int type, hipStream_t s) {
-  const bool wx = ((uintptr_t)r.x & 15) == 0 && r.ldx % 8 == 0, ww = ((uintptr_t)r.w & 15) == 0 && r.ldw % 8 == 0;
-  const dim3 grid((unsigned)std::min<int64_t>(r.N, 1 << 16));
-#define LL_PREP(TY)                                                                                            \
-  if (wx && ww) hipLaunchKernelGGL((xent_prep_kernel<TY, true, true>), grid, dim3(256), 0, s, r);             \
-  else if (wx) hipLaunchKernelGGL((xent_prep_kernel<TY, true, false>), grid, dim3(256), 0, s, r);             \
-  else if (ww) hipLaunchKernelGGL((xent_prep_kernel<TY, false, true>), grid, dim3(256), 0, s, r);             \
-  else hipLaunchKernelGGL((xent_prep_kernel<TY, false, false>), grid, dim3(256), 0, s, r);
+  const int lanes = r.ldp <= 128 ? 16 : r.ldp <= 512 ? 64 : 256, rows = 256 / lanes;
+  const dim3 grid((unsigned)std::min<int64_t>((r.N + rows - 1) / rows, 1 << 16));
+#define LL_PREP(TY)                                                                                  \
+  if (lanes == 16) hipLaunchKernelGGL((xent_prep_kernel<TY, 16>), grid, dim3(256), 0, s, r);         \
+  else if (lanes == 64) hipLaunchKernelGGL((xent_prep_kernel<TY, 64>), grid, dim3(256), 0, s, r);    \
+  else hipLaunchKernelGGL((xent_prep_kernel<TY, 256>), grid, dim3(256), 0, s, r);
   if (type == LL_BF16) {
     LL_PREP(LL_BF16)
   } else {
@@ -354,6 +372,76 @@ __global__ void __launch_bounds__(1024) xent_lse_kernel(const XentRows r) {
 
 hipError_t launch_xent_lse(const XentRows& r, hipStream_t s) {
   hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((r.N + 15) / 16)), dim3(1024), 0, s, r);
+  return hipGetLastError();
+}
+
+// The logits are read twice, the second time from L2 (a row is at most
+// kXentRowCols values); a launch for each step instead took 4 us more apiece.
+template <int TY>
+__global__ void __launch_bounds__(256) xent_rows_kernel(const XentRows r, const float* z, int64_t ldz, int cols,
+                                                        uint16_t* dz, int64_t ldd) {
+  __shared__ float red[8];
+  typedef Chunk<TY, 8> C;
+  for (int64_t i = blockIdx.x; i < r.N; i += gridDim.x) {
+    const int64_t t = r.target[i];
+    const bool live = has_target(r, t);
+    const float* row = z + i * ldz;
+    float m = kNegInf, s = 0.f;
+    if (live) {
+      for (int c = 4 * threadIdx.x; c < cols; c += 1024) {
+        const float4 q = *(const float4*)(row + c);  // ldz covers whole groups of four
+        const float v[4] = {q.x, c + 1 < cols ? q.y : kNegInf, c + 2 < cols ? q.z : kNegInf,
+                            c + 3 < cols ? q.w : kNegInf};
+        const float m4 = fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3]));
+        float s4 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s4 += v[e] == kNegInf ? 0.f : __expf(v[e] - m4);
+        join(m, s, m4, s4);
+      }
+    }
+    __syncthreads();  // red may still be read for the row before
+    block_join(m, s, red);
+    const float lse = live ? m + logf(s) : 0.f;
+    if (threadIdx.x == 0) {
+      r.loss[i] = live ? lse - row[t] : 0.f;
+      if (r.lse_out) r.lse_out[i] = lse;
+    }
+    if (!dz) continue;
+    const float coef = live ? r.dloss[i] * (r.scale ? r.scale[0] : 1.f) : 0.f;
+    for (int c = 8 * threadIdx.x; c < ldd; c += 2048) {
+      C o;
+      o.clear();
+      if (live) {
+#pragma unroll
+        for (int h = 0; h < 8; h += 4) {
+          if (c + h >= cols) continue;
+          const float4 q = *(const float4*)(row + c + h);
+          const float v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (c + h + e < cols) o.put(h + e, (__expf(v[e] - lse) - (c + h + e == t ? 1.f : 0.f)) * coef);
+        }
+      }
+      o.template store<false>(dz + i * ldd + c, 8);
+    }
+    if (!r.xp) continue;
+    const uint16_t* x = (const uint16_t*)r.x + i * r.ldx;
+    for (int c = 8 * threadIdx.x; c < r.ldp; c += 2048) {
+      C v;
+      v.clear();
+      if (live && c < r.D) v.template load<true>(x + c, r.D - c);
+      v.template store<false>((uint16_t*)r.xp + i * r.ldp + c, 8);
+    }
+  }
+}
+
+hipError_t launch_xent_rows(const XentRows& r, const float* z, int64_t ldz, int cols, void* dz, int64_t ldd, int type,
+                            hipStream_t s) {
+  const dim3 grid((unsigned)std::min<int64_t>(r.N, 1 << 16));
+  if (type == LL_BF16)
+    hipLaunchKernelGGL((xent_rows_kernel<LL_BF16>), grid, dim3(256), 0, s, r, z, ldz, cols, (uint16_t*)dz, ldd);
+  else
+    hipLaunchKernelGGL((xent_rows_kernel<LL_F16>), grid, dim3(256), 0, s, r, z, ldz, cols, (uint16_t*)dz, ldd);
   return hipGetLastError();
 }
 

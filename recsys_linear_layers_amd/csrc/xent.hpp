@@ -31,6 +31,9 @@ struct XentRows {
   float* lse_out;          // null: not wanted
 };
 
+// dst[i][0 .. ldp) = src[i][0 .. cols), zeros past cols; ldp a multiple of 64.
+hipError_t launch_xent_pack(const void* src, int64_t lds, int64_t rows, int cols, void* dst, int ldp, int cus,
+                            hipStream_t s);
 hipError_t launch_xent_prep(const XentRows& r, int type, hipStream_t s);
 // Power of two S that brings the largest |dloss| near 2^14 (fp16 gradients of the logits).
 hipError_t launch_xent_scale(const XentRows& r, hipStream_t s);
@@ -47,6 +50,12 @@ hipError_t launch_xent_lse(const XentRows& r, hipStream_t s);
 // dz[row][c] = (exp(z - lse) - (v0 + c == target)) * coef for c < cols, 0 up to ldd.
 hipError_t launch_xent_dz(const XentRows& r, const float* z, int64_t ldz, int64_t v0, int cols, void* dz,
                           int64_t ldd, int type, int cus, hipStream_t s);
+constexpr int kXentRowCols = 32768;
+// Everything between the logits of a whole row (fp32, cols wide) and the gradient
+// products, one workgroup per row: loss, lse and, with dz, dz [N][ldd] and the
+// copy of x in xp (if not null).  No parts, zt, lse or coef needed.
+hipError_t launch_xent_rows(const XentRows& r, const float* z, int64_t ldz, int cols, void* dz, int64_t ldd, int type,
+                            hipStream_t s);
 // In place on the fp16 numerators of one piece, 128 columns per part from part
 // p0 on: dz = numerator * factor as `type`, and the target's own from its logit.
 hipError_t launch_xent_numerators(const XentRows& r, void* dz, int64_t ldd, int64_t v0, int cols, int p0, int type,

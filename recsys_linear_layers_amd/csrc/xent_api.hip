@@ -25,13 +25,17 @@ struct xent_plan {
   int64_t cols;       // vocabulary entries per piece (the last may have fewer)
   bool fused;         // the softmax runs in the logits' product; else it reads fp32 logits
   bool few;           // few rows: w is streamed once, with fp32 logits for the gradients
+  bool by_row;        // one piece of at most kXentRowCols: one kernel from the logits to dz
+  bool x_direct;      // by_row: the logits' product reads x itself (where it is aligned)
   int pieces, kept;   // kept: the last pieces, whose numerators stay for the gradients
   int parts, np;      // per row and piece, and over all pieces
   int64_t rows;       // N, up to whole tiles where fused
   int64_t ldz, ldd;   // row strides of the fp32 logits and of the 16-bit dz of a piece
   bool dx_direct;     // dx leaves its product in its final form
+  bool dx_scaled;     // dx's product takes the scale of dz out
   bool dw_scaled;     // dw's product takes the scale of dz out
   gemm_plan logits[2], dxp[2], dwp[2];  // [1]: the last piece
+  gemm_plan logits_x; // x_direct
   size_t off_xp, off_wp, off_zt, off_lse, off_coef, off_column, off_scale, off_parts, off_z, off_dz, off_dxa, off_dxb, off_dwt,
       off_gemm, gemm_bytes, ws_bytes;
 };
@@ -171,6 +175,8 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
     p.ldz = round_up(d->V, 16);
     p.parts = p.np = (int)std::min<int64_t>((d->V + 15) / 16, p.cus);
   }
+  p.by_row = !p.fused && p.pieces == 1 && d->V <= kXentRowCols;
+  p.x_direct = p.by_row && !p.few && d->stride_x % 8 == 0 && d->D % 8 == 0;
   // fp16: dw carries the scale of dz.  The hand-ordered kind takes it out in
   // its epilogue; where its tiles would fill less than half of the CUs, dw goes
   // through fp32 (in place for an fp32 dw).
@@ -210,6 +216,14 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
                   p.dx_direct ? d->dx_type : LL_F32);
       s = gemm_plan_build(&g, kPaddedA | padded_w | kDeepK, &p.dxp[i]);
       if (s != LL_OK) return s;
+      if (i == 0 && p.pieces == 1 && p.dxp[0].deep) {
+        // the splits' sum also takes the scale out and rounds
+        p.dx_direct = p.dx_scaled = true;
+        g.stride_cm = d->stride_dx;
+        g.c_type = d->dx_type;
+        s = gemm_plan_build(&g, kPaddedA | padded_w | kDeepK, &p.dxp[0]);
+        if (s != LL_OK) return s;
+      }
       p.gemm_bytes = std::max(p.gemm_bytes, p.dxp[i].ws_bytes);
     }
     if (p.dw) {
@@ -219,6 +233,12 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
       if (s != LL_OK) return s;
       p.gemm_bytes = std::max(p.gemm_bytes, p.dwp[i].ws_bytes);
     }
+  }
+  if (p.x_direct) {
+    gemm_desc g = product(N, d->V, d->D, d->stride_x, 1, 1, p.ldw, p.ldz, d->type, LL_F32);
+    s = gemm_plan_build(&g, padded_w, &p.logits_x);
+    if (s != LL_OK) return s;
+    p.gemm_bytes = std::max(p.gemm_bytes, p.logits_x.ws_bytes);
   }
   p.ws_bytes = off + align256(p.gemm_bytes);
   xent_plan* h = new (std::nothrow) xent_plan(p);
@@ -321,15 +341,18 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
     return base + p->off_dz + (is_kept(k) ? (size_t)(k - (p->pieces - p->kept)) * p->rows * p->ldd * 2 : 0);
   };
 
-  if (N > 0 && (grads || !p->few)) {
-    e = launch_xent_prep(r, d.type, st);
-    if (e != hipSuccess) return hip_fail(e, "xent prep launch");
+  const bool x_direct = p->x_direct && !bad(x, 16);
+  if (N > 0) {
+    if (!(p->few && (!grads || p->by_row)) && !x_direct) {
+      e = launch_xent_prep(r, d.type, st);
+      if (e != hipSuccess) return hip_fail(e, "xent prep launch");
+    }
     if (r.scale) {
       e = launch_xent_scale(r, st);
       if (e != hipSuccess) return hip_fail(e, "xent scale launch");
     }
-    if (p->pack_w) {
-      e = launch_pack_kmajor((const uint16_t*)w, d.stride_w, 1, d.V, d.D, (uint16_t*)(base + p->off_wp), p->ldp, st);
+    if (p->pack_w && (grads || !p->few)) {
+      e = launch_xent_pack(w, d.stride_w, d.V, (int)d.D, base + p->off_wp, (int)p->ldp, p->cus, st);
       if (e != hipSuccess) return hip_fail(e, "pack w launch");
     }
   }
@@ -338,7 +361,8 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
   // The logits' product of piece k, fused with softmax epilogue `epi` or into z.
   auto logits_of = [&](int k, int epi) {
     const uint16_t* const wp = wk + (int64_t)k * p->cols * p->ldw;
-    const gemm_plan* const g = &p->logits[k + 1 == p->pieces];
+    const gemm_plan* const g = x_direct ? &p->logits_x : &p->logits[k + 1 == p->pieces];
+    if (x_direct) return gemm_run_plan(g, x, wp, z, nullptr, gws, p->gemm_bytes, st);
     if (!p->fused) return gemm_run_plan(g, r.xp, wp, z, nullptr, gws, p->gemm_bytes, st);
     GemmKArgs x;
     memset(&x, 0, sizeof x);
@@ -361,13 +385,21 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
     for (int k = 0; k < p->pieces && !p->few; ++k) {
       s = logits_of(k, grads && is_kept(k) ? kSoftmaxNumerators : kSoftmaxStats);
       if (s != LL_OK) return s;
-      if (!p->fused) {
+      if (!p->fused && !p->by_row) {
         e = launch_xent_stats(r, z, p->ldz, cols_of(k), k * p->parts, p->parts, st);
         if (e != hipSuccess) return hip_fail(e, "xent stats launch");
       }
     }
-    e = launch_xent_lse(r, st);
-    if (e != hipSuccess) return hip_fail(e, "xent lse launch");
+    if (p->by_row && (grads || !p->few)) {
+      XentRows q = r;
+      if (!x_direct && !p->few) q.xp = nullptr;  // copied already
+      if (!p->dw) q.xp = nullptr;
+      e = launch_xent_rows(q, z, p->ldz, (int)d.V, grads ? dz_of(0) : nullptr, p->ldd, d.type, st);
+      if (e != hipSuccess) return hip_fail(e, "xent rows launch");
+    } else {
+      e = launch_xent_lse(r, st);
+      if (e != hipSuccess) return hip_fail(e, "xent lse launch");
+    }
   }
   if (!grads) return ok();
   // The kept pieces first; the logits of the others are formed again.
@@ -381,14 +413,16 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
         s = logits_of(k, kSoftmaxGradient);
         if (s != LL_OK) return s;
       }
-      if (!p->fused)
+      if (!p->fused && !p->by_row)
         e = launch_xent_dz(r, z, p->ldz, v0, cols, dz, p->ldd, d.type, p->cus, st);
-      else if (is_kept(k))
+      else if (p->fused && is_kept(k))
         e = launch_xent_numerators(r, dz, p->ldd, v0, cols, k * p->parts, d.type, st);
       if (e != hipSuccess) return hip_fail(e, "xent dz launch");
       if (p->dx) {
-        s = gemm_run_plan(&p->dxp[li], dz, wk + v0 * p->ldw, p->dx_direct ? dx : n == 0 ? dxa : dxb, nullptr, gws,
-                          p->gemm_bytes, st);
+        const gemm_plan* const g = &p->dxp[p->pieces == 1 ? 0 : li];
+        const float* const f = p->dx_scaled ? unscale : nullptr;
+        s = gemm_run_plan(g, dz, wk + v0 * p->ldw, p->dx_direct ? dx : n == 0 ? dxa : dxb, f, gws, p->gemm_bytes, st,
+                          f ? kScaleEpilogue : 0);
         if (s != LL_OK) return s;
         if (!p->dx_direct) {
           if (k == 0)
