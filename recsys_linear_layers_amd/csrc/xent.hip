@@ -152,18 +152,22 @@ hipError_t launch_xent_scale(const XentRows& r, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: the logits of up to 16 rows, w streamed once.
+// Few rows: the logits of up to 64 rows (as far as x fits in LDS), w streamed
+// once.
 //
 // HBM bound: 2 V D bytes of w against 2 N V D flops.  A wave takes 16 entries of
 // the vocabulary: the 16x16x32 matrix instruction with w's rows as its rows and
-// x's as its columns (columns past N repeat row 0 and are dropped).  w goes
-// straight from memory into the operand registers, 16 bytes per lane and
-// instruction (64 bytes of each of the 16 rows), the next 8 loads always in
-// flight while 8 are used: at 16 waves that is 128 KB per CU, what HBM latency
-// takes.  x sits in LDS, rows 16 bytes apart beyond their length so that the 16
-// rows of a read fall on different banks.  Each lane keeps (maximum, sum) of
-// its own entries over all its wave's tiles; lanes and waves are joined at the
-// end, so a workgroup leaves one pair per row.
+// x's as its columns, NT times 16 of them (columns past N repeat row 0 and are
+// dropped).  w goes straight from memory into the operand registers, 16 bytes
+// per lane and instruction (64 bytes of each of the 16 rows), the next U loads
+// always in flight while U are used: with U = 8 and 16 waves that is 128 KB per
+// CU, what HBM latency takes.  x sits in LDS, rows 16 bytes apart beyond their
+// length so that the 16 rows of a read fall on different banks.  Each lane keeps
+// (maximum, sum) of its own entries over all its wave's tiles; lanes and waves
+// are joined at the end, so a workgroup leaves one pair per row.
+// 1 x 50021 x 2048: 35 us, 5.9 TB/s; the whole call at 64 x 131072 x 1024 58 us, 89
+// with the logits through a product of their own.  (128 rows: the state of 8
+// tiles does not fit in registers, 80 us against 58 at 128 x 131072 x 512.)
 // ---------------------------------------------------------------------------
 
 template <int TY>
@@ -181,32 +185,42 @@ __device__ __forceinline__ f32x4 mfma16(const Chunk<TY, 8>& a, const Chunk<TY, 8
   }
 }
 
-template <int TY, bool TAIL>
+template <int TY, bool TAIL, int NT>
 __global__ void __launch_bounds__(1024) xent_few_kernel(const XentRows r, float* z, int64_t ldz) {
-  constexpr int U = 8;
+  constexpr int U = NT <= 2 ? 8 : 4;
   typedef Chunk<TY, 8> C;
   extern __shared__ __attribute__((aligned(16))) uint16_t xs[];  // [N][Dp + 8], Dp: D up to whole 32s
   __shared__ float red[16][2][16];
   const int N = (int)r.N, D = r.D, steps = (D + 31) / 32, pitch = steps * 32 + 8;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int n = lane & 15, g = lane >> 4;
-  for (int i = 0; i < N; ++i)
-    for (int c = threadIdx.x; c < steps * 4; c += 1024) {
-      C v;
-      v.clear();
-      if (8 * c < D) v.template load<TAIL>((const uint16_t*)r.x + i * r.ldx + 8 * c, D - 8 * c);
-      __builtin_memcpy(xs + i * pitch + 8 * c, &v, 16);
-    }
-  const int64_t t = n < N ? r.target[n] : -1;
+  const int c16 = lane & 15, g = lane >> 4;
+  for (int q = threadIdx.x; q < N * steps * 4; q += 1024) {
+    const int i = q / (steps * 4), c = q % (steps * 4);
+    C v;
+    v.clear();
+    if (8 * c < D) v.template load<TAIL>((const uint16_t*)r.x + i * r.ldx + 8 * c, D - 8 * c);
+    __builtin_memcpy(xs + i * pitch + 8 * c, &v, 16);
+  }
+  int64_t t[NT];
+  const uint16_t* xrow[NT];
+  float m[NT], s[NT];
+#pragma unroll
+  for (int q = 0; q < NT; ++q) {
+    const int n = 16 * q + c16;
+    t[q] = n < N ? r.target[n] : -1;
+    xrow[q] = xs + (n < N ? n : 0) * pitch + 8 * g;
+    m[q] = kNegInf;
+    s[q] = 0.f;
+  }
   __syncthreads();
-  const uint16_t* const xrow = xs + (n < N ? n : 0) * pitch + 8 * g;
   const int tiles = (int)((r.V + 15) / 16);
   const int full = D / 32 / U * U;  // steps taken U at a time, whole
-  float m = kNegInf, s = 0.f;
   for (int tile = blockIdx.x + gridDim.x * wave; tile < tiles; tile += gridDim.x * 16) {
-    const int64_t row = min((int64_t)tile * 16 + n, r.V - 1);
+    const int64_t row = min((int64_t)tile * 16 + c16, r.V - 1);
     const uint16_t* const wrow = (const uint16_t*)r.w + row * r.ldw + 8 * g;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    f32x4 acc[NT];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
     C cur[U];
     if (full > 0) {
 #pragma unroll
@@ -219,62 +233,82 @@ __global__ void __launch_bounds__(1024) xent_few_kernel(const XentRows r, float*
         for (int u = 0; u < U; ++u) next[u].template load<false>(wrow + 32 * (k + U + u), 8);
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        C b;
-        __builtin_memcpy(&b, xrow + 32 * (k + u), 16);
-        acc = mfma16(cur[u], b, acc);
-      }
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < NT; ++q) {
+          C b;
+          __builtin_memcpy(&b, xrow[q] + 32 * (k + u), 16);
+          acc[q] = mfma16(cur[u], b, acc[q]);
+        }
 #pragma unroll
       for (int u = 0; u < U; ++u) cur[u] = next[u];
     }
     for (int k = full; k < steps; ++k) {
       const int left = D - 32 * k - 8 * g;
-      C a, b;
+      C a;
       if (left > 0) a.template load<TAIL>(wrow + 32 * k, left);
       else a.clear();
-      __builtin_memcpy(&b, xrow + 32 * k, 16);
-      acc = mfma16(a, b, acc);
+#pragma unroll
+      for (int q = 0; q < NT; ++q) {
+        C b;
+        __builtin_memcpy(&b, xrow[q] + 32 * k, 16);
+        acc[q] = mfma16(a, b, acc[q]);
+      }
     }
-    // lane: row n of x, entries 16 tile + 4 g + 0 .. 3
+    // lane: rows 16 q + c16 of x, entries 16 tile + 4 g + 0 .. 3
     const int64_t v0 = (int64_t)tile * 16 + 4 * g;
-    float m4 = kNegInf;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (v0 + i >= r.V) acc[i] = kNegInf;
-      else if (v0 + i == t) r.zt[n] = acc[i];
-      m4 = fmaxf(m4, acc[i]);
+    for (int q = 0; q < NT; ++q) {
+      const int n = 16 * q + c16;
+      float m4 = kNegInf;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (v0 + i >= r.V) acc[q][i] = kNegInf;
+        else if (v0 + i == t[q]) r.zt[n] = acc[q][i];
+        m4 = fmaxf(m4, acc[q][i]);
+      }
+      float s4 = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s4 += acc[q][i] == kNegInf ? 0.f : __expf(acc[q][i] - m4);
+      join(m[q], s[q], m4, s4);
+      if (z && n < N) *(f32x4*)(z + n * ldz + v0) = acc[q];  // ldz: whole groups of 16
     }
-    float s4 = 0.f;
+  }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s4 += acc[i] == kNegInf ? 0.f : __expf(acc[i] - m4);
-    join(m, s, m4, s4);
-    if (z && n < N) *(f32x4*)(z + n * ldz + v0) = acc;  // ldz: whole groups of 16
+  for (int q = 0; q < NT; ++q) {
+    const int n = 16 * q + (threadIdx.x & 15);
+    join(m[q], s[q], __shfl_xor(m[q], 16, 64), __shfl_xor(s[q], 16, 64));
+    join(m[q], s[q], __shfl_xor(m[q], 32, 64), __shfl_xor(s[q], 32, 64));
+    if (q > 0) __syncthreads();  // red is still read for the rows before
+    if (lane < 16) {
+      red[wave][0][lane] = m[q];
+      red[wave][1][lane] = s[q];
+    }
+    __syncthreads();
+    if (threadIdx.x < 16 && n < N) {
+      for (int k = 1; k < 16; ++k) join(m[q], s[q], red[k][0][lane], red[k][1][lane]);
+      r.parts[(int64_t)blockIdx.x * r.part_ld + n] = float2{m[q], s[q]};
+    }
   }
-  join(m, s, __shfl_xor(m, 16, 64), __shfl_xor(s, 16, 64));
-  join(m, s, __shfl_xor(m, 32, 64), __shfl_xor(s, 32, 64));
-  if (lane < 16) {
-    red[wave][0][n] = m;
-    red[wave][1][n] = s;
-  }
-  __syncthreads();
-  if (threadIdx.x < N) {
-    for (int k = 1; k < 16; ++k) join(m, s, red[k][0][n], red[k][1][n]);
-    r.parts[(int64_t)blockIdx.x * r.part_ld + n] = float2{m, s};
-  }
+}
+
+template <int TY, bool TAIL>
+static void few_go(const XentRows& r, float* z, int64_t ldz, size_t lds, hipStream_t s) {
+  if (r.N <= 16) hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 1>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
+  else if (r.N <= 32) hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 2>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
+  else hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 4>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
 }
 
 hipError_t launch_xent_few(const XentRows& r, float* z, int64_t ldz, int type, hipStream_t s) {
   const size_t lds = (size_t)r.N * ((r.D + 31) / 32 * 32 + 8) * 2;
   if (r.N < 1 || r.N > kXentFewRows || lds > (size_t)kXentFewBytes) return hipErrorInvalidValue;
-#define LL_FEW(TY)                                                                                                  \
-  if (r.D % 8) hipLaunchKernelGGL((xent_few_kernel<TY, true>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);          \
-  else hipLaunchKernelGGL((xent_few_kernel<TY, false>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
   if (type == LL_BF16) {
-    LL_FEW(LL_BF16)
+    if (r.D % 8) few_go<LL_BF16, true>(r, z, ldz, lds, s);
+    else few_go<LL_BF16, false>(r, z, ldz, lds, s);
   } else {
-    LL_FEW(LL_F16)
+    if (r.D % 8) few_go<LL_F16, true>(r, z, ldz, lds, s);
+    else few_go<LL_F16, false>(r, z, ldz, lds, s);
   }
-#undef LL_FEW
   return hipGetLastError();
 }
 

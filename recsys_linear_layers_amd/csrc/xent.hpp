@@ -40,7 +40,7 @@ hipError_t launch_xent_scale(const XentRows& r, hipStream_t s);
 // Few rows: up to kXentFewRows, x of at most kXentFewBytes (rows padded by 16
 // bytes).  Loss side in one pass over w: parts[workgroup][row], zt, and z if
 // not null.  x and w as given, any alignment; r.np workgroups.
-constexpr int kXentFewRows = 16;
+constexpr int kXentFewRows = 64;
 constexpr int64_t kXentFewBytes = 144 * 1024;
 hipError_t launch_xent_few(const XentRows& r, float* z, int64_t ldz, int type, hipStream_t s);
 // parts[p0 + split][row] of fp32 logits z [N][ldz], cols wide, in `splits` pieces per row.

@@ -166,9 +166,10 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
                     : (int)std::max<int64_t>(1, std::min<int64_t>((first + 1023) / 1024, 8ll * p.cus / p.rows));
   p.np = (p.pieces - 1) * p.parts + (p.fused ? (int)(round_up(last, 256) / 128) : p.parts);
   p.dx_direct = p.dx && p.pieces == 1 && !f16;
-  // Few rows: w streamed once past x in LDS.
+  // Few rows: w streamed once past x in LDS.  LL_XENT_FEW=0 overrides (measurement).
   p.few = N >= 1 && N <= kXentFewRows && N * (round_up(d->D, 32) + 8) * 2 <= kXentFewBytes && !p.fused &&
           (!grads || p.pieces == 1);
+  if (const char* env = getenv("LL_XENT_FEW")) p.few = p.few && env[0] != '0';
   if (p.few) {
     p.pieces = 1;
     p.cols = round_up(d->V, 256);
@@ -180,7 +181,8 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   // fp16: dw carries the scale of dz.  The hand-ordered kind takes it out in
   // its epilogue; where its tiles would fill less than half of the CUs, dw goes
   // through fp32 (in place for an fp32 dw).
-  p.dw_scaled = p.dw && f16 && p.fused && (first + 255) / 256 * ((d->D + 255) / 256) * 2 > p.cus;
+  p.dw_scaled = p.dw && f16 && N > 0 && N * p.ldp < (1 << 30) && p.ldd * p.rows < (1 << 30) &&
+                (first + 255) / 256 * ((d->D + 255) / 256) * 2 > p.cus;
   const bool dw_tmp = f16_dw && !p.dw_scaled;
 
   size_t off = 0;

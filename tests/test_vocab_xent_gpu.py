@@ -140,13 +140,15 @@ def test_loss_and_gradients(N, V, D, pad, dtype):
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 @pytest.mark.parametrize("N,V,D,pad", [(1, 15, 3, 0), (3, 17, 40, 0), (7, 1000, 33, 5), (16, 1001, 4096, 0),
-                                       (16, 70000, 264, 8), (2, 4099, 8192, 0), (17, 4099, 256, 0), (9, 300, 8200, 0)])
+                                       (16, 70000, 264, 8), (2, 4099, 8192, 0), (17, 4099, 256, 0), (9, 300, 8200, 0),
+                                       (32, 5000, 1001, 3), (33, 40000, 520, 0), (64, 2000, 64, 0), (65, 33000, 129, 0),
+                                       (128, 1111, 512, 0), (128, 3000, 640, 0), (129, 900, 64, 0)])
 def test_few_rows(N, V, D, pad, dtype):
-    """Up to 16 rows (as far as x fits) stream the vocabulary once; 17 do not."""
+    """Up to 64 rows (as far as x fits) stream the vocabulary once; 65 do not."""
     import torch
     ll = _ll()
     x, w, target, dloss = _case(N, V, D, dtype, pad, ignored=0.1)
-    few = N <= 16 and N * (-(-D // 32) * 32 + 8) * 2 <= 144 * 1024
+    few = N <= 64 and N * (-(-D // 32) * 32 + 8) * 2 <= 144 * 1024
     assert ("few_rows" in ll.xent_plan_for(x, w).describe()) == few
     what = f"{dtype} {N}x{V}x{D}+{pad}"
     loss, lse = ll.vocab_xent(x, w, target)
