@@ -45,7 +45,7 @@ def _run(cmd, verbose):
 # schedule, and iterative-ilp spilled their fused-epilogue instantiations
 # (bias + GELU 34 registers against 10).  The embedding, layer norm and
 # cross-entropy row kernels are bound by HBM too.
-DEFAULT_SCHED = {"lincomp.hip", "embed.hip", "layernorm.hip", "xent.hip"}
+DEFAULT_SCHED = {"lincomp.hip", "embed.hip", "layernorm.hip", "xent.hip", "xent_few.hip"}
 
 
 def _flags(src):

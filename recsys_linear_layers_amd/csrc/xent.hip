@@ -12,17 +12,9 @@
 
 #include "kernels.hpp"
 #include "ops_common.hpp"
+#include "xent_rows.hpp"
 
 namespace ll {
-
-constexpr float kNegInf = -__builtin_huge_valf();
-
-// (m, s) joined with (m2, s2).  An empty or all -inf piece is (-inf, 0).
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-  const float M = fmaxf(m, m2);
-  s = (m == M ? s : s * __expf(m - M)) + (m2 == M ? s2 : s2 * __expf(m2 - M));
-  m = M;
-}
 
 // Over the 256 threads of a workgroup; every thread gets it.
 __device__ __forceinline__ void block_join(float& m, float& s, float* red) {
@@ -39,8 +31,6 @@ __device__ __forceinline__ void block_join(float& m, float& s, float* red) {
 #pragma unroll
   for (int w = 1; w < 4; ++w) join(m, s, red[2 * w], red[2 * w + 1]);
 }
-
-__device__ __forceinline__ bool has_target(const XentRows& r, int64_t t) { return t >= 0 && t < r.V && t != r.ignore; }
 
 // The aligned copy of x (a row without a target becomes zeros, so that whatever
 // it holds cannot reach dw through 0 * inf), and the target's logit as a dot
@@ -148,167 +138,6 @@ __global__ void __launch_bounds__(1024) xent_scale_kernel(const XentRows r) {
 
 hipError_t launch_xent_scale(const XentRows& r, hipStream_t s) {
   hipLaunchKernelGGL(xent_scale_kernel, dim3(1), dim3(1024), 0, s, r);
-  return hipGetLastError();
-}
-
-// ---------------------------------------------------------------------------
-// Few rows: the logits of up to 64 rows (as far as x fits in LDS), w streamed
-// once.
-//
-// HBM bound: 2 V D bytes of w against 2 N V D flops.  A wave takes 16 entries of
-// the vocabulary: the 16x16x32 matrix instruction with w's rows as its rows and
-// x's as its columns, NT times 16 of them (columns past N repeat row 0 and are
-// dropped).  w goes straight from memory into the operand registers, 16 bytes
-// per lane and instruction (64 bytes of each of the 16 rows), the next U loads
-// always in flight while U are used: with U = 8 and 16 waves that is 128 KB per
-// CU, what HBM latency takes.  x sits in LDS, rows 16 bytes apart beyond their
-// length so that the 16 rows of a read fall on different banks.  Each lane keeps
-// (maximum, sum) of its own entries over all its wave's tiles; lanes and waves
-// are joined at the end, so a workgroup leaves one pair per row.
-// 1 x 50021 x 2048: 35 us, 5.9 TB/s; the whole call at 64 x 131072 x 1024 58 us, 89
-// with the logits through a product of their own.  (128 rows: the state of 8
-// tiles does not fit in registers, 80 us against 58 at 128 x 131072 x 512.)
-// ---------------------------------------------------------------------------
-
-template <int TY>
-__device__ __forceinline__ f32x4 mfma16(const Chunk<TY, 8>& a, const Chunk<TY, 8>& b, f32x4 c) {
-  if constexpr (TY == LL_F16) {
-    f16x8 u, v;
-    __builtin_memcpy(&u, &a, 16);
-    __builtin_memcpy(&v, &b, 16);
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(u, v, c, 0, 0, 0);
-  } else {
-    bf16x8 u, v;
-    __builtin_memcpy(&u, &a, 16);
-    __builtin_memcpy(&v, &b, 16);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, v, c, 0, 0, 0);
-  }
-}
-
-template <int TY, bool TAIL, int NT>
-__global__ void __launch_bounds__(1024) xent_few_kernel(const XentRows r, float* z, int64_t ldz) {
-  constexpr int U = NT <= 2 ? 8 : 4;
-  typedef Chunk<TY, 8> C;
-  extern __shared__ __attribute__((aligned(16))) uint16_t xs[];  // [N][Dp + 8], Dp: D up to whole 32s
-  __shared__ float red[16][2][16];
-  const int N = (int)r.N, D = r.D, steps = (D + 31) / 32, pitch = steps * 32 + 8;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int c16 = lane & 15, g = lane >> 4;
-  for (int q = threadIdx.x; q < N * steps * 4; q += 1024) {
-    const int i = q / (steps * 4), c = q % (steps * 4);
-    C v;
-    v.clear();
-    if (8 * c < D) v.template load<TAIL>((const uint16_t*)r.x + i * r.ldx + 8 * c, D - 8 * c);
-    __builtin_memcpy(xs + i * pitch + 8 * c, &v, 16);
-  }
-  int64_t t[NT];
-  const uint16_t* xrow[NT];
-  float m[NT], s[NT];
-#pragma unroll
-  for (int q = 0; q < NT; ++q) {
-    const int n = 16 * q + c16;
-    t[q] = n < N ? r.target[n] : -1;
-    xrow[q] = xs + (n < N ? n : 0) * pitch + 8 * g;
-    m[q] = kNegInf;
-    s[q] = 0.f;
-  }
-  __syncthreads();
-  const int tiles = (int)((r.V + 15) / 16);
-  const int full = D / 32 / U * U;  // steps taken U at a time, whole
-  for (int tile = blockIdx.x + gridDim.x * wave; tile < tiles; tile += gridDim.x * 16) {
-    const int64_t row = min((int64_t)tile * 16 + c16, r.V - 1);
-    const uint16_t* const wrow = (const uint16_t*)r.w + row * r.ldw + 8 * g;
-    f32x4 acc[NT];
-#pragma unroll
-    for (int q = 0; q < NT; ++q) acc[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-    C cur[U];
-    if (full > 0) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) cur[u].template load<false>(wrow + 32 * u, 8);
-    }
-    for (int k = 0; k < full; k += U) {
-      C next[U];
-      if (k + U < full) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) next[u].template load<false>(wrow + 32 * (k + U + u), 8);
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int q = 0; q < NT; ++q) {
-          C b;
-          __builtin_memcpy(&b, xrow[q] + 32 * (k + u), 16);
-          acc[q] = mfma16(cur[u], b, acc[q]);
-        }
-#pragma unroll
-      for (int u = 0; u < U; ++u) cur[u] = next[u];
-    }
-    for (int k = full; k < steps; ++k) {
-      const int left = D - 32 * k - 8 * g;
-      C a;
-      if (left > 0) a.template load<TAIL>(wrow + 32 * k, left);
-      else a.clear();
-#pragma unroll
-      for (int q = 0; q < NT; ++q) {
-        C b;
-        __builtin_memcpy(&b, xrow[q] + 32 * k, 16);
-        acc[q] = mfma16(a, b, acc[q]);
-      }
-    }
-    // lane: rows 16 q + c16 of x, entries 16 tile + 4 g + 0 .. 3
-    const int64_t v0 = (int64_t)tile * 16 + 4 * g;
-#pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      const int n = 16 * q + c16;
-      float m4 = kNegInf;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (v0 + i >= r.V) acc[q][i] = kNegInf;
-        else if (v0 + i == t[q]) r.zt[n] = acc[q][i];
-        m4 = fmaxf(m4, acc[q][i]);
-      }
-      float s4 = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s4 += acc[q][i] == kNegInf ? 0.f : __expf(acc[q][i] - m4);
-      join(m[q], s[q], m4, s4);
-      if (z && n < N) *(f32x4*)(z + n * ldz + v0) = acc[q];  // ldz: whole groups of 16
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < NT; ++q) {
-    const int n = 16 * q + (threadIdx.x & 15);
-    join(m[q], s[q], __shfl_xor(m[q], 16, 64), __shfl_xor(s[q], 16, 64));
-    join(m[q], s[q], __shfl_xor(m[q], 32, 64), __shfl_xor(s[q], 32, 64));
-    if (q > 0) __syncthreads();  // red is still read for the rows before
-    if (lane < 16) {
-      red[wave][0][lane] = m[q];
-      red[wave][1][lane] = s[q];
-    }
-    __syncthreads();
-    if (threadIdx.x < 16 && n < N) {
-      for (int k = 1; k < 16; ++k) join(m[q], s[q], red[k][0][lane], red[k][1][lane]);
-      r.parts[(int64_t)blockIdx.x * r.part_ld + n] = float2{m[q], s[q]};
-    }
-  }
-}
-
-template <int TY, bool TAIL>
-static void few_go(const XentRows& r, float* z, int64_t ldz, size_t lds, hipStream_t s) {
-  if (r.N <= 16) hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 1>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
-  else if (r.N <= 32) hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 2>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
-  else hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 4>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
-}
-
-hipError_t launch_xent_few(const XentRows& r, float* z, int64_t ldz, int type, hipStream_t s) {
-  const size_t lds = (size_t)r.N * ((r.D + 31) / 32 * 32 + 8) * 2;
-  if (r.N < 1 || r.N > kXentFewRows || lds > (size_t)kXentFewBytes) return hipErrorInvalidValue;
-  if (type == LL_BF16) {
-    if (r.D % 8) few_go<LL_BF16, true>(r, z, ldz, lds, s);
-    else few_go<LL_BF16, false>(r, z, ldz, lds, s);
-  } else {
-    if (r.D % 8) few_go<LL_F16, true>(r, z, ldz, lds, s);
-    else few_go<LL_F16, false>(r, z, ldz, lds, s);
-  }
   return hipGetLastError();
 }
 

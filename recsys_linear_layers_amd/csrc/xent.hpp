@@ -43,6 +43,14 @@ hipError_t launch_xent_scale(const XentRows& r, hipStream_t s);
 constexpr int kXentFewRows = 64;
 constexpr int64_t kXentFewBytes = 144 * 1024;
 hipError_t launch_xent_few(const XentRows& r, float* z, int64_t ldz, int type, hipStream_t s);
+// dw [V][ldo] of out_type from dz [N][ldd] and the copy xp, times *scale (null: 1).
+hipError_t launch_xent_dw_few(const XentRows& r, const void* dz, int64_t ldd, void* dw, int64_t ldo, int out_type,
+                              const float* scale, int type, int cus, hipStream_t s);
+// dx as partial[share][N][D] sums over shares of the vocabulary, from dz [N][ldd]
+// (zeros past V) and w as given.
+int xent_dx_few_shares(int64_t N, int64_t V, int D, int cus);
+hipError_t launch_xent_dx_few(const XentRows& r, const void* dz, int64_t ldd, float* partial, int type, int cus,
+                              hipStream_t s);
 // parts[p0 + split][row] of fp32 logits z [N][ldz], cols wide, in `splits` pieces per row.
 hipError_t launch_xent_stats(const XentRows& r, const float* z, int64_t ldz, int cols, int p0, int splits,
                              hipStream_t s);

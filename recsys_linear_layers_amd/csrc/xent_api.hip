@@ -25,6 +25,8 @@ struct xent_plan {
   int64_t cols;       // vocabulary entries per piece (the last may have fewer)
   bool fused;         // the softmax runs in the logits' product; else it reads fp32 logits
   bool few;           // few rows: w is streamed once, with fp32 logits for the gradients
+  bool any_w;         // w may start at any element (the contract; few rows need no alignment either way)
+  bool few_dx, few_dw;// few rows: gradients by kernels of their own, no copy of w
   bool by_row;        // one piece of at most kXentRowCols: one kernel from the logits to dz
   bool x_direct;      // by_row: the logits' product reads x itself (where it is aligned)
   int pieces, kept;   // kept: the last pieces, whose numerators stay for the gradients
@@ -36,7 +38,8 @@ struct xent_plan {
   bool dw_scaled;     // dw's product takes the scale of dz out
   gemm_plan logits[2], dxp[2], dwp[2];  // [1]: the last piece
   gemm_plan logits_x; // x_direct
-  size_t off_xp, off_wp, off_zt, off_lse, off_coef, off_column, off_scale, off_parts, off_z, off_dz, off_dxa, off_dxb, off_dwt,
+  int dx_shares;
+  size_t off_xp, off_wp, off_zt, off_lse, off_coef, off_column, off_scale, off_parts, off_z, off_dz, off_dxa, off_dxb, off_dxp, off_dwt,
       off_gemm, gemm_bytes, ws_bytes;
 };
 
@@ -132,7 +135,6 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   // rows the tiles' empty rows cost more: 64 x 131072 x 2048 451 / 421 and 1 x
   // 131072 x 4096 718 / 669.  LL_XENT_FUSED=0 / 1 overrides (measurement).
   const int64_t N = d->N, limit = d->piece_bytes ? d->piece_bytes : kDefaultPieceBytes;
-  const uint32_t padded_w = p.pack_w ? kPaddedB : 0;
   const int64_t tiles = (N + 255) / 256 * ((d->V + 255) / 256);
   // x, and 256 rows of w, below 2 GB; whole 64-deep slices of w
   const bool fits = N * p.ldp < (1 << 30) && p.ldw < (1 << 22) && (d->D % 64 == 0 || p.pack_w);
@@ -146,8 +148,12 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   // kept but not all fit, a piece is a quarter of what fits, so that most of
   // the bound is used.
   const bool f16_dw = p.dw && f16 && d->dw_type != LL_F32;
-  const int64_t per_col = (p.fused ? (grads ? p.rows * 2 : 0) : p.rows * (grads ? 6 : 4)) + (f16_dw ? d->D * 4 : 0);
+  const bool few_rows = N >= 1 && N <= kXentFewRows && !p.fused;
   const int64_t two_gb = (1 << 30) / std::max(grads ? p.rows : 1, p.ldw) - 256;
+  const int64_t per_row = p.fused ? (grads ? 2 : 0) : grads ? 6 : 4;
+  // few rows in one piece write dw in its own type
+  const bool few_dw = few_rows && d->V <= std::min(limit / (p.rows * per_row), two_gb);
+  const int64_t per_col = p.rows * per_row + (f16_dw && !few_dw ? d->D * 4 : 0);
   int64_t cols = std::min(per_col ? limit / per_col : two_gb, two_gb);
   if (p.fused && grads && cols < d->V) cols = std::min(limit / 4 / per_col, two_gb);
   cols = std::max<int64_t>(cols / 256 * 256, 256);
@@ -166,10 +172,29 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
                     : (int)std::max<int64_t>(1, std::min<int64_t>((first + 1023) / 1024, 8ll * p.cus / p.rows));
   p.np = (p.pieces - 1) * p.parts + (p.fused ? (int)(round_up(last, 256) / 128) : p.parts);
   p.dx_direct = p.dx && p.pieces == 1 && !f16;
-  // Few rows: w streamed once past x in LDS.  LL_XENT_FEW=0 overrides (measurement).
-  p.few = N >= 1 && N <= kXentFewRows && N * (round_up(d->D, 32) + 8) * 2 <= kXentFewBytes && !p.fused &&
-          (!grads || p.pieces == 1);
-  if (const char* env = getenv("LL_XENT_FEW")) p.few = p.few && env[0] != '0';
+  // Few rows: w streamed once past x in LDS; dw streamed out, by a kernel that
+  // also serves rows that do not fit there; dx by a kernel of its own where a
+  // general product would copy w first, go through fp32 (fp16) or fill one of
+  // its 16-row tiles.  Loss and gradients, us, all general / logits and dw / dx
+  // too: bf16 1 x 131072 x 4096 676 / 538 / 554, 4 x 233278 x 1417 1084 / 832 /
+  // 609, 8 x 32000 x 2048 126 / 119 / 110, 32 x 131072 x 2048 369 / 337 / 354, 64
+  // x 131072 x 1024 244 / 209 / 225; fp16 17 x 189756 x 896 307 / 274 / 229, 64 x
+  // 100000 x 512 164 / 127 / 117.  LL_XENT_FEW: sum of 1 (logits), 2 (dx), 4
+  // (dw) overrides (measurement).
+  const bool few = few_rows && (!grads || p.pieces == 1);
+  p.few = few && N * (round_up(d->D, 32) + 8) * 2 <= kXentFewBytes;
+  p.few_dx = p.few && p.dx && (N <= 16 || f16 || p.pack_w);
+  p.few_dw = few && p.dw;
+  if (const char* env = getenv("LL_XENT_FEW")) {
+    const int on = atoi(env);
+    p.few = p.few && (on & 1);
+    p.few_dx = few && p.dx && (on & 2);
+    p.few_dw = p.few_dw && (on & 4);
+  }
+  // no copy of w where no general product reads it
+  p.any_w = p.pack_w;
+  p.pack_w = p.pack_w && (!p.few || (p.dx && !p.few_dx));
+  p.ldw = p.pack_w ? p.ldp : d->stride_w;
   if (p.few) {
     p.pieces = 1;
     p.cols = round_up(d->V, 256);
@@ -181,9 +206,9 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   // fp16: dw carries the scale of dz.  The hand-ordered kind takes it out in
   // its epilogue; where its tiles would fill less than half of the CUs, dw goes
   // through fp32 (in place for an fp32 dw).
-  p.dw_scaled = p.dw && f16 && N > 0 && N * p.ldp < (1 << 30) && p.ldd * p.rows < (1 << 30) &&
+  p.dw_scaled = p.dw && !p.few_dw && f16 && N > 0 && N * p.ldp < (1 << 30) && p.ldd * p.rows < (1 << 30) &&
                 (first + 255) / 256 * ((d->D + 255) / 256) * 2 > p.cus;
-  const bool dw_tmp = f16_dw && !p.dw_scaled;
+  const bool dw_tmp = f16_dw && !p.dw_scaled && !p.few_dw;
 
   size_t off = 0;
   auto take = [&](size_t n) {
@@ -192,7 +217,7 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
     return at;
   };
   p.off_xp = take((size_t)N * p.ldp * 2);
-  p.off_wp = take(p.pack_w && (grads || !p.few) ? (size_t)d->V * p.ldp * 2 : 0);
+  p.off_wp = take(p.pack_w ? (size_t)d->V * p.ldp * 2 : 0);
   p.off_zt = take((size_t)N * 4);
   p.off_lse = take((size_t)p.rows * 4);
   p.off_coef = take((size_t)p.rows * 4);
@@ -204,16 +229,19 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   if (p.dx && !p.dx_direct) p.off_dxa = take((size_t)N * d->D * 4);
   if (p.dx && p.pieces > 1) p.off_dxb = take((size_t)N * d->D * 4);
   if (dw_tmp) p.off_dwt = take((size_t)first * d->D * 4);
+  p.dx_shares = p.few_dx ? xent_dx_few_shares(N, d->V, (int)d->D, p.cus) : 0;
+  if (p.few_dx) p.off_dxp = take((size_t)p.dx_shares * N * d->D * 4);
   p.off_gemm = off;
+  const uint32_t padded_w = p.pack_w ? kPaddedB : 0;
   for (int i = 0; i < 2; ++i) {
     const int64_t n = i ? last : first;
     gemm_desc g = p.fused ? product(N, n, d->D, p.ldp, 1, 1, p.ldw, p.ldd, d->type, d->type)
                           : product(N, n, d->D, p.ldp, 1, 1, p.ldw, p.ldz, d->type, LL_F32);
-    s = gemm_plan_build(&g, kPaddedA | padded_w | (p.fused ? kWholeTiles : 0), &p.logits[i]);
+    if (!p.few) s = gemm_plan_build(&g, kPaddedA | padded_w | (p.fused ? kWholeTiles : 0), &p.logits[i]);
     if (s != LL_OK) return s;
     if (p.fused && n >= kPrefetchCols) p.logits[i].b_prefetch = 1;
     p.gemm_bytes = std::max(p.gemm_bytes, p.logits[i].ws_bytes);
-    if (p.dx) {
+    if (p.dx && !p.few_dx) {
       g = product(N, d->D, n, p.ldd, 1, p.ldw, 1, p.dx_direct ? d->stride_dx : d->D, d->type,
                   p.dx_direct ? d->dx_type : LL_F32);
       s = gemm_plan_build(&g, kPaddedA | padded_w | kDeepK, &p.dxp[i]);
@@ -228,7 +256,7 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
       }
       p.gemm_bytes = std::max(p.gemm_bytes, p.dxp[i].ws_bytes);
     }
-    if (p.dw) {
+    if (p.dw && !p.few_dw) {
       g = product(n, d->D, N, 1, p.ldd, p.ldp, 1, dw_tmp ? d->D : d->stride_dw, d->type,
                   dw_tmp ? (int)LL_F32 : d->dw_type);
       s = gemm_plan_build(&g, kPaddedA | kPaddedB | (p.dw_scaled ? kWholeTiles : 0), &p.dwp[i]);
@@ -259,8 +287,9 @@ ll_status xent_plan_describe(const xent_plan* p, char* buf, size_t len) {
   if (!p || !buf || len == 0) return fail(LL_ERR_INVALID_ARG, "null argument");
   snprintf(buf, len, "pieces=%d cols=%lld kept=%d fused=%d packW=%d logits=%s dx=%s dw=%s ws=%zu", p->pieces,
            (long long)p->cols, p->kept, (int)p->fused, (int)p->pack_w,
-           p->few ? "few_rows" : kind_info(p->logits[0].kind).name, p->dx ? kind_info(p->dxp[0].kind).name : "-",
-           p->dw ? kind_info(p->dwp[0].kind).name : "-", p->ws_bytes);
+           p->few ? "few_rows" : kind_info(p->logits[0].kind).name,
+           !p->dx ? "-" : p->few_dx ? "few_rows" : kind_info(p->dxp[0].kind).name,
+           !p->dw ? "-" : p->few_dw ? "few_rows" : kind_info(p->dwp[0].kind).name, p->ws_bytes);
   return ok();
 }
 
@@ -281,7 +310,7 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
   if (bad(x, 2) || bad(w, 2) || bad(target, 8) || bad(dloss, 4) || bad(loss, 4) || bad(lse, 4) ||
       (p->dx && bad(dx, dtype_size(d.dx_type))) || (p->dw && bad(dw, dtype_size(d.dw_type))))
     return fail(LL_ERR_INVALID_ARG, "misaligned pointer");
-  if (!p->pack_w && bad(w, 16))
+  if (!p->any_w && bad(w, 16))
     return fail(LL_ERR_INVALID_ARG, "w must be 16-byte aligned unless packed (LL_XENT_PACK_W)");
   if (ws_bytes < p->ws_bytes || (p->ws_bytes > 0 && !ws))
     return fail(LL_ERR_WORKSPACE, "workspace %zu bytes, plan needs %zu", ws_bytes, p->ws_bytes);
@@ -353,7 +382,7 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
       e = launch_xent_scale(r, st);
       if (e != hipSuccess) return hip_fail(e, "xent scale launch");
     }
-    if (p->pack_w && (grads || !p->few)) {
+    if (p->pack_w) {
       e = launch_xent_pack(w, d.stride_w, d.V, (int)d.D, base + p->off_wp, (int)p->ldp, p->cus, st);
       if (e != hipSuccess) return hip_fail(e, "pack w launch");
     }
@@ -420,7 +449,14 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
       else if (p->fused && is_kept(k))
         e = launch_xent_numerators(r, dz, p->ldd, v0, cols, k * p->parts, d.type, st);
       if (e != hipSuccess) return hip_fail(e, "xent dz launch");
-      if (p->dx) {
+      if (p->few_dx) {
+        float* const part = (float*)(base + p->off_dxp);
+        e = launch_xent_dx_few(r, dz, p->ldd, part, d.type, p->cus, st);
+        if (e == hipSuccess)
+          e = launch_splitk_reduce_deep(part, p->dx_shares, N, d.D, dx, d.stride_dx, 1,
+                                        d.dx_type == LL_BF16 ? 1 : d.dx_type == LL_F16 ? 2 : 0, unscale, st);
+        if (e != hipSuccess) return hip_fail(e, "xent few rows dx launch");
+      } else if (p->dx) {
         const gemm_plan* const g = &p->dxp[p->pieces == 1 ? 0 : li];
         const float* const f = p->dx_scaled ? unscale : nullptr;
         s = gemm_run_plan(g, dz, wk + v0 * p->ldw, p->dx_direct ? dx : n == 0 ? dxa : dxb, f, gws, p->gemm_bytes, st,
@@ -436,7 +472,10 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
         }
       }
     }
-    if (p->dw) {
+    if (p->few_dw) {
+      e = launch_xent_dw_few(r, dz, p->ldd, dw, d.stride_dw, d.dw_type, unscale, d.type, p->cus, st);
+      if (e != hipSuccess) return hip_fail(e, "xent few rows dw launch");
+    } else if (p->dw) {
       const int64_t esz = dtype_size(d.dw_type);
       char* const dst = (char*)dw + v0 * d.stride_dw * esz;
       const bool tmp = f16 && !p->dw_scaled && d.dw_type != LL_F32;

@@ -208,14 +208,18 @@ def test_xent_null_arguments():
 
 @pytest.mark.gpu
 def test_xent_run_refusals():
-    """These need a plan, which needs a device; every call is refused on the host."""
+    """These need a plan, which needs a device; every call is refused on the host.
+    The buffers are real, and far larger than the call needs."""
     import torch
     ll = _ll()
     h = ll.xent_plan_create(_xent())
     try:
         need = ll.xent_plan_workspace_size(h)
         run = ll._lib.xent_run
-        X, W, T, G, L, E, DX, DW, WS = [(i + 1) << 32 for i in range(9)]
+        room = 1 << 20
+        assert need < room // 2
+        buf = torch.zeros(9 * room, dtype=torch.uint8, device="cuda")
+        X, W, T, G, L, E, DX, DW, WS = [buf.data_ptr() + i * room for i in range(9)]
         good = [X, W, T, G, L, E, DX, DW, WS]
 
         def status(args, ws_bytes=need):
@@ -232,6 +236,8 @@ def test_xent_run_refusals():
             a = list(good)
             a[i] = bad
             assert status(a) == "LL_ERR_" + want, (i, bad)
+        assert status(good) == "LL_OK"
+        torch.cuda.synchronize()
     finally:
         ll.xent_plan_destroy(h)
     with pytest.raises(ValueError):
