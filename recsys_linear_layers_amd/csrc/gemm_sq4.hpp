@@ -298,18 +298,36 @@ __device__ __forceinline__ void sq4_flush(const GemmKArgs& p, const TileInfo& ti
   }
 }
 
-// The same for a tile that reaches past M or N, N a multiple of 8.
+// The same for a tile that reaches past M or N, N a multiple of 8.  ANY: and for
+// rows of any alignment and length.  A 16-byte store may start at any element
+// (81655 x 2543 x 104, 415 MB of C: 256 us; 441 with 2-byte stores straight from
+// the accumulators, 276 with pieces aligned to C and 2-byte stores at their
+// ends); the lines it straddles are completed by its neighbours in L2, so it is
+// a plain store.
+template <bool ANY>
 __device__ __forceinline__ void sq4_flush_edge(const GemmKArgs& p, const TileInfo& ti, int wm0, int wn0, int lane,
                                                const char LL_LDS* img) {
+  typedef i32x4 unaligned __attribute__((aligned(2)));
   const int pr = (lane >> 3) & 3, ch = ((lane >> 5) << 3) | (lane & 7);
   const int row = ti.m0 + wm0 + pr, col = ti.n0 + wn0 + ch * 8;
   if (col >= p.N) return;
   const char LL_LDS* const src = img + pr * Sq4::IMG_PITCH + ch * 16;
   uint16_t* const cb = (uint16_t*)p.c;
+  const bool piece = ANY && col + 8 > p.N;  // the row ends inside these 16 bytes
 #pragma unroll
   for (int q = 0; q < 32; ++q) {
     const i32x4 v = *(const i32x4 LL_LDS*)(src + q * 4 * Sq4::IMG_PITCH);
-    if (row + 4 * q < p.M) __builtin_nontemporal_store(v, (i32x4*)(cb + (int64_t)(row + 4 * q) * p.ldcm + col));
+    uint16_t* const dst = cb + (int64_t)(row + 4 * q) * p.ldcm + col;
+    if (row + 4 * q >= p.M) continue;
+    if constexpr (!ANY) {
+      __builtin_nontemporal_store(v, (i32x4*)dst);
+    } else if (!piece) {
+      *(unaligned*)dst = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (col + i < p.N) dst[i] = (uint16_t)((uint32_t)v[i >> 1] >> (16 * (i & 1)));
+    }
   }
 }
 
@@ -552,21 +570,20 @@ __global__ void __launch_bounds__(Sq4::THREADS) __attribute__((amdgpu_waves_per_
       continue;
     }
     const bool whole = ti.m0 + Sq4::BM <= p.M && ti.n0 + Sq4::BN <= p.N;
-    // a tile of a 16-bit row-major C with 16-byte aligned rows, inside it or
-    // with whole 16-byte pieces to its edge: staged through LDS (uniform over
-    // the workgroup)
-    const bool staged = p.c_fast && p.c_fmt != 0 && (whole || (p.N & 7) == 0) && ((uintptr_t)p.c & 15) == 0 &&
-                        (p.ldcm & 7) == 0;
-    if (staged) {
+    // a 16-bit row-major C: staged through LDS (uniform over the workgroup)
+    if (p.c_fmt != 0 && p.ldcn == 1 && !p.partial) {
+      const bool aligned = ((uintptr_t)p.c & 15) == 0 && (p.ldcm & 7) == 0;
       char LL_LDS* img = smem + wave * Sq4::IMG;
       if (p.c_fmt == 1)
         sq4_stage_all<EPI, 1>(p, ti, wn0, lane, img);
       else
         sq4_stage_all<EPI, 2>(p, ti, wn0, lane, img);
-      if (whole)
+      if (whole && aligned && p.c_fast)
         sq4_flush(p, ti, wm0, wn0, lane, img);
+      else if (aligned && (p.N & 7) == 0)
+        sq4_flush_edge<false>(p, ti, wm0, wn0, lane, img);
       else
-        sq4_flush_edge(p, ti, wm0, wn0, lane, img);
+        sq4_flush_edge<true>(p, ti, wm0, wn0, lane, img);
       sq4_count_in(cnt, wave, lane);
       // the next work item's loads land all over the LDS the other waves
       // may still be reading

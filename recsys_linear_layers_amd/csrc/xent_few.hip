@@ -195,8 +195,10 @@ __device__ __forceinline__ Chunk<TY, 8> frag_tr(const uint16_t LL_LDS* tile, int
 // through LDS, 16 rows of 512 bytes together, 16 bytes per lane: stored straight
 // from the registers each instruction would write half of every 32 bytes, which
 // took 500 us instead of 185 for 131072 x 4096 of one row (1.07 GB, 5.8 TB/s; 64
-// rows of 131072 x 1024 65 us, 4.1 TB/s; 233278 rows of 1417, at odd addresses,
-// 265 us, 2.5 TB/s).
+// rows of 131072 x 1024 65 us, 4.1 TB/s).  Where rows are not 16-byte aligned, the
+// 16-byte pieces are taken where dw is, at any element of the row in LDS, and the
+// up to 7 elements left at its two ends by one 2-byte store per lane: 233278 x
+// 1417 160 us, against 265 with 16-byte stores at odd addresses.
 // ---------------------------------------------------------------------------
 
 constexpr int kDwCols = 256, kDwEntries = 64;
@@ -230,6 +232,7 @@ __global__ void __launch_bounds__(256) xent_dw_few_kernel(const XentRows r, cons
   const int blocks = (int)((r.V + kDwEntries - 1) / kDwEntries), step = gridDim.x / col_blocks;
   constexpr int OP = kDwCols + 32 / (int)sizeof(O);
   __shared__ __attribute__((aligned(16))) O out[16 * OP];
+  const bool aligned = (((uintptr_t)dw | (uint64_t)ldo * sizeof(O)) & 15) == 0;
   const int left = r.D - (blockIdx.x % col_blocks) * kDwCols;  // columns from this workgroup's first on
   auto stage = [&](int b, int slot) {  // rows n of dz, entries 64 b ..; ldd covers whole 256s
     for (int q = threadIdx.x; q < 32 * KS * (kDwEntries / 8); q += 256) {
@@ -267,14 +270,28 @@ __global__ void __launch_bounds__(256) xent_dw_few_kernel(const XentRows r, cons
         __builtin_memcpy(&out[c16 * OP + wave * 64 + 16 * g + h], &o, 16);
       }
       __syncthreads();
-      const int c = threadIdx.x % LANES * W;
+      const int l = threadIdx.x % LANES, cols = min(kDwCols, left);
 #pragma unroll
       for (int e = threadIdx.x / LANES; e < 16; e += 256 / LANES) {
         const int64_t v = (int64_t)b * kDwEntries + 16 * vt + e;
-        if (v >= r.V || c >= left) continue;
+        if (v >= r.V) break;
+        O* const dst = (O*)dw + v * ldo + d0 - wave * 64;
+        const O* const src = &out[e * OP];
         Chunk<OT, W> o;
-        __builtin_memcpy(&o, &out[e * OP + c], 16);
-        o.template store<true, true>((O*)dw + v * ldo + (d0 - wave * 64) + c, left - c);
+        if (aligned) {
+          if (W * l >= cols) continue;
+          __builtin_memcpy(&o, src + W * l, 16);
+          o.template store<true, true>(dst + W * l, cols - W * l);
+        } else {
+          const int at = (int)((uintptr_t)dst / sizeof(O)) & (W - 1), c = W * l - at;
+          if (c >= 0 && c + W <= cols) {
+            __builtin_memcpy(&o, src + c, 16);
+            o.template store<false>(dst + c, W);
+          }
+          const int head = min(-at & (W - 1), cols), tail = max(head, ((cols + at) & -W) - at);
+          const int q = l < W ? l : tail + l - W;
+          if (l < 2 * W && q < (l < W ? head : cols)) dst[q] = src[q];
+        }
       }
     }
   }
