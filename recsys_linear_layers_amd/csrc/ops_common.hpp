@@ -57,6 +57,17 @@ struct Chunk {
     else return (raw)(i & 1 ? w[i >> 1] >> 16 : w[i >> 1]);
   }
   __device__ __forceinline__ void put(int i, float v) { put_raw(i, Elem<TY>::put(v)); }
+  // Elements i and i + 1, i even, 16-bit types: one conversion and no merging of halves.
+  __device__ __forceinline__ void put2(int i, float a, float b) {
+    typedef float f2 __attribute__((ext_vector_type(2)));
+    if constexpr (TY == LL_BF16) {
+      typedef __bf16 h2 __attribute__((ext_vector_type(2)));
+      w[i >> 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, h2));
+    } else {
+      typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+      w[i >> 1] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, h2));
+    }
+  }
   __device__ __forceinline__ void clear() {
 #pragma unroll
     for (int i = 0; i < VEC / PER; ++i) w[i] = 0;

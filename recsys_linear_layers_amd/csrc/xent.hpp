@@ -51,6 +51,23 @@ hipError_t launch_xent_dw_few(const XentRows& r, const void* dz, int64_t ldd, vo
 int xent_dx_few_shares(int64_t N, int64_t V, int D, int cus);
 hipError_t launch_xent_dx_few(const XentRows& r, const void* dz, int64_t ldd, float* partial, int type, int cus,
                               hipStream_t s);
+// Narrow rows: D up to kXentNarrow (r.ldp 64 or 128), x and w as given, any
+// alignment.  parts[share][row] in r.np shares, and zt; then dx and dw, without
+// stored logits.
+constexpr int kXentNarrow = 128;
+enum { kNarrowStats = 0, kNarrowDx = 1, kNarrowDw = 2 };
+struct XentNarrowOut {
+  void* out;
+  int64_t ldo;
+  int type, shares;        // shares 0: not wanted
+  float* partial;          // [shares][rows][ldp] where there is more than one share
+  const float* scale;      // null: 1
+  int64_t rows;            // set by the launch
+  int row_blocks;
+};
+int xent_narrow_shares(int64_t own, int64_t streamed, int64_t slots);
+hipError_t launch_xent_narrow_stats(const XentRows& r, int type, hipStream_t s);
+hipError_t launch_xent_narrow_grad(const XentRows& r, XentNarrowOut dx, XentNarrowOut dw, int type, hipStream_t s);
 // parts[p0 + split][row] of fp32 logits z [N][ldz], cols wide, in `splits` pieces per row.
 hipError_t launch_xent_stats(const XentRows& r, const float* z, int64_t ldz, int cols, int p0, int splits,
                              hipStream_t s);

@@ -25,6 +25,8 @@ struct xent_plan {
   int64_t cols;       // vocabulary entries per piece (the last may have fewer)
   bool fused;         // the softmax runs in the logits' product; else it reads fp32 logits
   bool few;           // few rows: w is streamed once, with fp32 logits for the gradients
+  bool narrow;        // D <= kXentNarrow: logits formed in each step, never stored
+  int shares[3];      // narrow: of statistics, dx, dw
   bool any_w;         // w may start at any element (the contract; few rows need no alignment either way)
   bool few_dx, few_dw;// few rows: gradients by kernels of their own, no copy of w
   bool by_row;        // one piece of at most kXentRowCols: one kernel from the logits to dz
@@ -140,6 +142,16 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   const bool fits = N * p.ldp < (1 << 30) && p.ldw < (1 << 22) && (d->D % 64 == 0 || p.pack_w);
   p.fused = fits && N > 128 && tiles * 2 > p.cus;
   if (const char* env = getenv("LL_XENT_FUSED")) p.fused = fits && N > 0 && env[0] == '1';
+  // Narrow rows: forming a logit again costs less than storing it.  Loss and
+  // gradients, us, stored / formed again: bf16 16384 x 131072 x 64 5849 / 2015,
+  // 8192 x 32768 x 128 804 / 545, 1746 x 68132 x 93 441 / 318, 224 x 1406 x 128
+  // 44 / 34, fp16 14360 x 7374 x 64 377 / 169, 65 x 228624 x 64 173 / 86; loss
+  // alone 1042 / 598, 161 / 123, 97 / 78, 16 / 17, 72 / 50, 77 / 18.  Up to 64
+  // rows their own kernels win (3 x 47113 x 119 49 / 75).  LL_XENT_NARROW=0
+  // overrides (measurement).
+  p.narrow = d->D <= kXentNarrow && N > kXentFewRows;
+  if (const char* env = getenv("LL_XENT_NARROW")) p.narrow = p.narrow && env[0] == '1';
+  if (p.narrow) p.fused = false;
   p.rows = p.fused ? round_up(N, 256) : std::max<int64_t>(N, 1);
 
   // Pieces of the vocabulary: as many columns as the bound holds, in whole
@@ -148,7 +160,7 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   // kept but not all fit, a piece is a quarter of what fits, so that most of
   // the bound is used.
   const bool f16_dw = p.dw && f16 && d->dw_type != LL_F32;
-  const bool few_rows = N >= 1 && N <= kXentFewRows && !p.fused;
+  const bool few_rows = N >= 1 && N <= kXentFewRows && !p.fused && !p.narrow;
   const int64_t two_gb = (1 << 30) / std::max(grads ? p.rows : 1, p.ldw) - 256;
   const int64_t per_row = p.fused ? (grads ? 2 : 0) : grads ? 6 : 4;
   // few rows in one piece write dw in its own type
@@ -193,7 +205,16 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   }
   // no copy of w where no general product reads it
   p.any_w = p.pack_w;
-  p.pack_w = p.pack_w && (!p.few || (p.dx && !p.few_dx));
+  p.pack_w = p.pack_w && !p.narrow && (!p.few || (p.dx && !p.few_dx));
+  if (p.narrow) {
+    p.pieces = 1;
+    p.cols = round_up(d->V, 256);
+    const int64_t slots = (p.ldp == 64 ? 3 : 2) * p.cus, each = p.dx && p.dw ? slots / 2 : slots;
+    p.shares[0] = xent_narrow_shares(N, d->V, slots);
+    p.shares[1] = p.dx ? xent_narrow_shares(N, d->V, each) : 0;
+    p.shares[2] = p.dw ? xent_narrow_shares(d->V, N, each) : 0;
+    p.parts = p.np = p.shares[0];
+  }
   p.ldw = p.pack_w ? p.ldp : d->stride_w;
   if (p.few) {
     p.pieces = 1;
@@ -201,7 +222,7 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
     p.ldz = round_up(d->V, 16);
     p.parts = p.np = (int)std::min<int64_t>((d->V + 15) / 16, p.cus);
   }
-  p.by_row = !p.fused && p.pieces == 1 && d->V <= kXentRowCols;
+  p.by_row = !p.fused && !p.narrow && p.pieces == 1 && d->V <= kXentRowCols;
   p.x_direct = p.by_row && !p.few && d->stride_x % 8 == 0 && d->D % 8 == 0;
   // fp16: dw carries the scale of dz.  The hand-ordered kind takes it out in
   // its epilogue; where its tiles would fill less than half of the CUs, dw goes
@@ -216,7 +237,7 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
     off = align256(off + n);
     return at;
   };
-  p.off_xp = take((size_t)N * p.ldp * 2);
+  p.off_xp = take(p.narrow ? 0 : (size_t)N * p.ldp * 2);
   p.off_wp = take(p.pack_w ? (size_t)d->V * p.ldp * 2 : 0);
   p.off_zt = take((size_t)N * 4);
   p.off_lse = take((size_t)p.rows * 4);
@@ -224,16 +245,20 @@ ll_status xent_plan_create(xent_plan** out, const xent_desc* d) {
   p.off_column = take((size_t)p.rows * 4);
   p.off_scale = take(8);
   p.off_parts = take((size_t)p.rows * p.np * sizeof(float2));
-  if (!p.fused && (grads || !p.few)) p.off_z = take((size_t)N * p.ldz * 4);
-  if (grads) p.off_dz = take((size_t)slot * p.kept);
-  if (p.dx && !p.dx_direct) p.off_dxa = take((size_t)N * d->D * 4);
+  if (!p.fused && !p.narrow && (grads || !p.few)) p.off_z = take((size_t)N * p.ldz * 4);
+  if (grads && !p.narrow) p.off_dz = take((size_t)slot * p.kept);
+  if (p.dx && !p.dx_direct && !p.narrow) p.off_dxa = take((size_t)N * d->D * 4);
   if (p.dx && p.pieces > 1) p.off_dxb = take((size_t)N * d->D * 4);
-  if (dw_tmp) p.off_dwt = take((size_t)first * d->D * 4);
+  if (dw_tmp && !p.narrow) p.off_dwt = take((size_t)first * d->D * 4);
   p.dx_shares = p.few_dx ? xent_dx_few_shares(N, d->V, (int)d->D, p.cus) : 0;
   if (p.few_dx) p.off_dxp = take((size_t)p.dx_shares * N * d->D * 4);
+  if (p.narrow) {
+    if (p.shares[1] > 1) p.off_dxp = take((size_t)p.shares[1] * N * p.ldp * 4);
+    if (p.shares[2] > 1) p.off_dwt = take((size_t)p.shares[2] * d->V * p.ldp * 4);
+  }
   p.off_gemm = off;
   const uint32_t padded_w = p.pack_w ? kPaddedB : 0;
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 2 && !p.narrow; ++i) {
     const int64_t n = i ? last : first;
     gemm_desc g = p.fused ? product(N, n, d->D, p.ldp, 1, 1, p.ldw, p.ldd, d->type, d->type)
                           : product(N, n, d->D, p.ldp, 1, 1, p.ldw, p.ldz, d->type, LL_F32);
@@ -285,6 +310,10 @@ ll_status xent_plan_workspace_size(const xent_plan* p, size_t* bytes) {
 
 ll_status xent_plan_describe(const xent_plan* p, char* buf, size_t len) {
   if (!p || !buf || len == 0) return fail(LL_ERR_INVALID_ARG, "null argument");
+  if (p->narrow) {
+    snprintf(buf, len, "narrow shares=%d,%d,%d ws=%zu", p->shares[0], p->shares[1], p->shares[2], p->ws_bytes);
+    return ok();
+  }
   snprintf(buf, len, "pieces=%d cols=%lld kept=%d fused=%d packW=%d logits=%s dx=%s dw=%s ws=%zu", p->pieces,
            (long long)p->cols, p->kept, (int)p->fused, (int)p->pack_w,
            p->few ? "few_rows" : kind_info(p->logits[0].kind).name,
@@ -374,7 +403,7 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
 
   const bool x_direct = p->x_direct && !bad(x, 16);
   if (N > 0) {
-    if (!(p->few && (!grads || p->by_row)) && !x_direct) {
+    if (!(p->few && (!grads || p->by_row)) && !x_direct && !p->narrow) {
       e = launch_xent_prep(r, d.type, st);
       if (e != hipSuccess) return hip_fail(e, "xent prep launch");
     }
@@ -386,6 +415,19 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
       e = launch_xent_pack(w, d.stride_w, d.V, (int)d.D, base + p->off_wp, (int)p->ldp, p->cus, st);
       if (e != hipSuccess) return hip_fail(e, "pack w launch");
     }
+  }
+  if (p->narrow) {
+    e = launch_xent_narrow_stats(r, d.type, st);
+    if (e == hipSuccess) e = launch_xent_lse(r, st);
+    if (e == hipSuccess && grads) {
+      const XentNarrowOut ox = {dx, d.stride_dx, d.dx_type, p->shares[1],
+                                p->shares[1] > 1 ? (float*)(base + p->off_dxp) : nullptr, unscale, 0, 0};
+      const XentNarrowOut ow = {dw, d.stride_dw, d.dw_type, p->shares[2],
+                                p->shares[2] > 1 ? (float*)(base + p->off_dwt) : nullptr, unscale, 0, 0};
+      e = launch_xent_narrow_grad(r, ox, ow, d.type, st);
+    }
+    if (e != hipSuccess) return hip_fail(e, "xent narrow rows launch");
+    return ok();
   }
   const uint16_t* const wk = p->pack_w ? (const uint16_t*)(base + p->off_wp) : (const uint16_t*)w;
   auto cols_of = [&](int k) { return (int)std::min(p->cols, d.V - (int64_t)k * p->cols); };

@@ -26,21 +26,6 @@ namespace ll {
 // with the logits through a product of their own.  (128 rows: the state of 8
 // tiles does not fit in registers, 80 us against 58 at 128 x 131072 x 512.)
 
-template <int TY>
-__device__ __forceinline__ f32x4 mfma16(const Chunk<TY, 8>& a, const Chunk<TY, 8>& b, f32x4 c) {
-  if constexpr (TY == LL_F16) {
-    f16x8 u, v;
-    __builtin_memcpy(&u, &a, 16);
-    __builtin_memcpy(&v, &b, 16);
-    return __builtin_amdgcn_mfma_f32_16x16x32_f16(u, v, c, 0, 0, 0);
-  } else {
-    bf16x8 u, v;
-    __builtin_memcpy(&u, &a, 16);
-    __builtin_memcpy(&v, &b, 16);
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(u, v, c, 0, 0, 0);
-  }
-}
-
 template <int TY, bool TAIL, int NT>
 __global__ void __launch_bounds__(1024) xent_few_kernel(const XentRows r, float* z, int64_t ldz) {
   constexpr int U = NT <= 2 ? 8 : 4;
@@ -175,12 +160,7 @@ template <int TY>
 __device__ __forceinline__ Chunk<TY, 8> frag_tr(const uint16_t LL_LDS* tile, int pitch, int k0, int c0, int lane) {
   const int g = lane >> 4, sl = lane & 15;
   const uint16_t LL_LDS* const p = tile + (k0 + 8 * g + (sl >> 2)) * pitch + c0 + 4 * (sl & 3);
-  const i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((i16x4 LL_LDS*)p);
-  const i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((i16x4 LL_LDS*)(p + 4 * pitch));
-  const i16x8 v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-  Chunk<TY, 8> c;
-  __builtin_memcpy(&c, &v, 16);
-  return c;
+  return frag_pair<TY>(p, p + 4 * pitch);
 }
 
 // ---------------------------------------------------------------------------

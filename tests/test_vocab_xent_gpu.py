@@ -120,7 +120,7 @@ def _case(N, V, D, dtype, pad=0, seed=0, std=1.5, ignored=0.2):
 SIZES = [(1, 1, 8, 0), (1, 1000, 64, 0), (2, 300, 1, 0), (5, 257, 72, 8), (16, 4096, 128, 0), (65, 777, 100, 0),
          (130, 2001, 1000, 3), (300, 50, 33, 0), (257, 5003, 192, 0), (700, 1025, 96, 0), (1, 40000, 520, 0),
          (1030, 4100, 320, 0), (2048, 8192, 64, 0), (4, 3, 5000, 0), (4100, 2050, 72, 0), (300, 20000, 128, 8),
-         (1200, 9999, 200, 0), (513, 12801, 1088, 0)]
+         (1200, 9999, 200, 0), (513, 12801, 1088, 0), (2048, 8192, 192, 0), (4100, 2050, 136, 0), (70, 900, 150, 0)]
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
@@ -161,6 +161,40 @@ def test_few_rows(N, V, D, pad, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("N,V,D,pad", [(65, 1, 1, 0), (65, 63, 7, 0), (66, 65, 8, 0), (127, 2001, 9, 1), (128, 5000, 63, 0),
+                                       (129, 64, 65, 0), (300, 20001, 64, 3), (1000, 127, 127, 0), (777, 3001, 128, 8),
+                                       (5000, 129, 33, 0), (70, 60000, 100, 0), (40000, 300, 40, 0), (200, 70000, 16, 0)])
+def test_narrow_rows(N, V, D, pad, dtype):
+    """More than 64 rows of up to 128 columns: no logits are stored, whatever the bound on a piece."""
+    import torch
+    ll = _ll()
+    x, w, target, dloss = _case(N, V, D, dtype, pad, ignored=0.1)
+    plan = ll.xent_plan_for(x, w, x.clone(), w.clone())
+    assert plan.describe().startswith("narrow")
+    what = f"{dtype} {N}x{V}x{D}+{pad}"
+    loss, lse = ll.vocab_xent(x, w, target)
+    _check(x, w, target, None, (loss, lse, None, None), -100, what)
+    out = ll.vocab_xent_grad(x, w, target, dloss, piece_bytes=1)
+    _check(x, w, target, dloss, out, -100, what)
+    f = ll.vocab_xent_grad(x, w, target, dloss, dx=torch.empty((N, D + 3), device="cuda")[:, :D],
+                           dw=torch.empty((V, D), device="cuda"))
+    _check(x, w, target, dloss, f, -100, what + " fp32")
+    assert torch.equal(out[0], loss) and torch.equal(f[0], loss)
+    # what rows without a target hold stays out of dw, a NaN in its row's loss
+    bad = torch.where((target == -100)[:, None], float("nan"), x)
+    got = ll.vocab_xent_grad(bad, w, target, dloss)
+    assert torch.equal(got[3], out[3]) and torch.equal(got[0], loss)
+    # a whole vocabulary of -inf but for two entries
+    w2 = torch.full_like(w, float("-inf"))
+    w2[0] = w2[V // 2] = 0
+    ones = torch.ones_like(x)
+    t = torch.where(target >= 0, torch.where(target % 2 == 0, 0, V // 2), target)
+    loss, lse = ll.vocab_xent(ones, w2, t)
+    want = torch.where(t >= 0, math.log(2.0 if V > 1 else 1.0), 0.0).float()
+    assert torch.allclose(loss, want, rtol=1e-6) and torch.equal(loss, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 @pytest.mark.parametrize("V,D", [(1, 8), (1000, 64), (40000, 520), (5001, 333)])
 def test_one_row_with_a_target(V, D, dtype):
     ll = _ll()
@@ -169,7 +203,7 @@ def test_one_row_with_a_target(V, D, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
-@pytest.mark.parametrize("N,V,D,pieces", [(40, 1111, 64, 5), (300, 3000, 136, 3), (1, 700, 40, 3), (1024, 9000, 128, 4)])
+@pytest.mark.parametrize("N,V,D,pieces", [(40, 1111, 64, 5), (300, 3000, 136, 3), (1, 700, 40, 3), (1024, 9000, 136, 4)])
 def test_pieces_of_the_vocabulary(N, V, D, pieces, dtype):
     """A bound that holds a fraction of the vocabulary: the pieces join to the same."""
     ll = _ll()
@@ -190,7 +224,7 @@ def test_numerators_kept_for_some_pieces(dtype):
     """Large enough for the softmax in the product: some pieces keep their
     numerators, the logits of the others are formed again; the last is short."""
     ll = _ll()
-    N, V, D = 2000, 9000, 128
+    N, V, D = 2000, 9000, 192
     x, w, target, dloss = _case(N, V, D, dtype, seed=6)
     for cols, pieces, kept in ((1024, 9, 4), (1280, 8, 4), (256, 36, 4), (2048, 5, 4)):
         # a column takes 2 bytes per padded row, and with fp16 4 per column of the dw that is scaled afterwards
@@ -206,7 +240,8 @@ def test_numerators_kept_for_some_pieces(dtype):
 def test_one_gradient_alone_and_fp32_gradients(dtype):
     import torch
     ll = _ll()
-    for N, V, D, bound in ((70, 600, 96, 0), (70, 600, 96, 1), (600, 2100, 128, 0), (600, 2100, 128, 1)):
+    for N, V, D, bound in ((70, 600, 96, 0), (70, 600, 96, 1), (600, 2100, 128, 0), (600, 2100, 128, 1),
+                           (600, 2100, 192, 0), (600, 2100, 192, 1)):
         x, w, target, dloss = _case(N, V, D, dtype, seed=9)
         both = ll.vocab_xent_grad(x, w, target, dloss, piece_bytes=bound)
         a = ll.vocab_xent_grad(x, w, target, dloss, want_dw=False, piece_bytes=bound)
@@ -224,7 +259,7 @@ def test_one_gradient_alone_and_fp32_gradients(dtype):
 def test_rows_without_a_target_may_hold_anything():
     import torch
     ll = _ll()
-    for N, V, D in ((20, 300, 64), (600, 2304, 128)):
+    for N, V, D in ((20, 300, 64), (600, 2304, 128), (600, 2304, 192)):
         x, w, target, dloss = _case(N, V, D, "bfloat16", ignored=0.0)
         want = ll.vocab_xent_grad(x, w, torch.where(torch.arange(N, device="cuda") % 4 == 0, -100, target), dloss)
         bad = x.clone()
@@ -272,7 +307,7 @@ def test_large_and_lopsided_logits(dtype):
     (gradient near 0) and a hopeless one; entries of -inf (0 * exp)."""
     import torch
     ll = _ll()
-    for N, V, D in ((12, 900, 64), (520, 2304, 64)):
+    for N, V, D in ((12, 900, 64), (520, 2304, 64), (520, 2304, 192)):
         x, w, target, dloss = _case(N, V, D, dtype, std=30.0, ignored=0.1)
         _check(x, w, target, dloss, ll.vocab_xent_grad(x, w, target, dloss), -100, "large logits")
         best = (x.double() @ w.double().T).argmax(1)
@@ -291,7 +326,7 @@ def test_large_and_lopsided_logits(dtype):
 def test_nan_stays_in_its_row():
     import torch
     ll = _ll()
-    for N, V, D in ((9, 300, 64), (600, 2304, 128)):
+    for N, V, D in ((9, 300, 64), (600, 2304, 128), (600, 2304, 192)):
         x, w, target, dloss = _case(N, V, D, "bfloat16", ignored=0.0)
         want = ll.vocab_xent_grad(x, w, target, dloss)
         bad = x.clone()
