@@ -366,7 +366,8 @@ ll_status embed_run(const embed_desc* desc, const void* table, const int64_t* id
  * then not touched.  Tokens are sorted by id, stably; each row is summed in
  * fp32, in an order that depends on the ids alone, and rounded once to
  * `type`, so equal inputs give equal bits.
- * Workspace (256-byte aligned): embed_grad_workspace_size; 0 for few tokens.
+ * Workspace (256-byte aligned): embed_grad_workspace_size; 0 for few tokens
+ * into a small table.
  * Only kernels are launched, so the call may be captured into a HIP graph.
  * Errors as for embed_run (dtable must not overlap dout, ids or the
  * workspace), unknown flag bits (LL_ERR_INVALID_ARG), and LL_ERR_WORKSPACE.
@@ -452,11 +453,14 @@ ll_status layernorm_grad_run(const layernorm_grad_desc* desc, const void* dy, co
  * maximum; dz is rounded to `type` (with fp16 after multiplication by a power
  * of two, taken out again in fp32, so that small probabilities keep their
  * bits), dx and dw once each.
- * piece_bytes bounds the buffers that hold logits and dz (0: 2 GiB); when
- * the whole vocabulary does not fit, it is cut into pieces of a multiple of
- * 256 entries (at least one such), the logits of all but the last are formed
- * again for the gradients.  w must be 16-byte aligned unless it is copied into
- * the workspace: LL_XENT_PACK_W, or a D or stride_w not a multiple of 8, or
+ * piece_bytes bounds the buffers that hold logits, their softmax numerators and
+ * dz (0: 2 GiB); when the whole vocabulary does not fit, it is cut into pieces of
+ * a multiple of 256 entries (at least one such).  The numerators of as many
+ * pieces as fit stay for the gradients, the logits of the others are formed
+ * again.  With D up to 128 and more than 64 rows no logits are stored at all, and
+ * piece_bytes has no effect.  w must be 16-byte aligned unless LL_XENT_PACK_W is
+ * set (w may then be copied into the workspace), or D or stride_w is not a
+ * multiple of 8, or
  * D not a multiple of 64 with 512 rows or more.
  */
 #define LL_XENT_DX 0x1u

@@ -646,7 +646,7 @@ static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream
   const int lx = log2_up(chunks, 6);
   const int groups = 256 >> lx;
   const int all_cols = (chunks + (1 << lx) - 1) >> lx;  // blocks of columns
-  if (a.T <= kEmbedDirect) {
+  if (a.direct) {
     // Fewer rows per group, then workgroups along the columns, until there are
     // 16 workgroups per CU (each scans all ids, so no more than that).
     const int64_t want = 16 * (int64_t)cus;
@@ -683,12 +683,13 @@ static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream
     }
   }
   const int nch = a.T / kEmbedChunk;  // whole chunks
-  const int ccb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / nch));
+  const int ccb = nch ? (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / nch)) : 1;
   const int cwg = (int)std::min<int64_t>(nch, std::max<int64_t>(1, 16 * (int64_t)cus / ccb)) * ccb;
   const int64_t pb = (a.T + groups - 1) / groups;
   if (cwg + pb * all_cols > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL((embed_sums_kernel<TY, TAIL>), dim3((unsigned)(cwg + pb * all_cols)), dim3(256), 0, s, a, src, lx,
                      cwg, ccb, all_cols);
+  if (nch == 0) return hipGetLastError();
   const int lb = (int)std::min<int64_t>((int64_t)nch * all_cols, 2 * cus);
   hipLaunchKernelGGL((embed_long_kernel<TY, TAIL>), dim3(lb), dim3(1024), 0, s, a, src, lx);
   return hipGetLastError();

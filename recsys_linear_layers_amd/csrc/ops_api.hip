@@ -48,6 +48,7 @@ ll_status embed_sizes(int64_t V, int64_t T, int64_t D, int64_t s0, int64_t s1, i
 }
 
 struct EmbedGradLayout {
+  bool direct = true;
   int bits = 0, passes = 0;
   size_t key[2] = {0, 0}, pos[2] = {0, 0}, hist = 0, total = 0, partial = 0, long_count = 0,
          long_rows = 0, bytes = 0;
@@ -58,7 +59,10 @@ struct EmbedGradLayout {
 // that cover the keys 0 .. V.
 EmbedGradLayout embed_grad_layout(const embed_grad_desc* d) {
   EmbedGradLayout l;
-  if (d->T <= kEmbedDirect || d->V == 0 || d->D == 0) return l;
+  l.direct = d->T == 0 || d->V == 0 || d->D == 0 ||
+             (d->T <= kEmbedDirect && ((d->flags & LL_EMBED_ACCUMULATE) ||
+                                       d->V * d->D * (int64_t)dtype_size(d->type) <= kEmbedDirectBytes));
+  if (l.direct) return l;
   const bool small = d->T <= kEmbedSmall;
   int kb = 1;
   while (kb < 31 && (1ll << kb) <= d->V) ++kb;  // V itself is a key
@@ -161,6 +165,7 @@ ll_status embed_grad_run(const embed_grad_desc* d, const int64_t* ids, const voi
   a.D = (int32_t)d->D;
   a.accumulate = (d->flags & LL_EMBED_ACCUMULATE) != 0;
   a.scale = d->scale;
+  a.direct = l.direct;
   a.bits = l.bits;
   a.passes = l.passes;
   if (l.bytes > 0) {

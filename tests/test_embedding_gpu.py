@@ -152,6 +152,29 @@ def test_gradient_of_frequent_ids_padding_and_ids_outside(T, accumulate):
         _grad_case(dtype, T, V, D, 0, ids, 0.37, 7, accumulate, g)
 
 
+@pytest.mark.parametrize("dtype,V,D", [("bfloat16", 70000, 1001), ("float32", 9000, 4096)])
+@pytest.mark.parametrize("T", [0, 1, 15, 16, 40, 512])
+def test_gradient_of_few_tokens_into_a_large_table(T, dtype, V, D):
+    """More than 128 MB of zeros: the tokens are sorted however few they are."""
+    import torch
+    ll = _ll()
+    g = _gen(T + D)
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    ids[T // 2:] = ids[:1]  # one row with half of them
+    dt = getattr(torch, dtype)
+    dout = torch.randn((T, D), generator=g, device="cuda").to(dt)
+    got = ll.embedding_grad(ids, dout, V, scale=0.5)
+    rows = torch.unique(ids)
+    want = torch.zeros((V, D), dtype=torch.float64, device="cuda").index_add_(0, ids, dout.double()).mul_(0.5)
+    mag = torch.zeros((V, D), dtype=torch.float64, device="cuda").index_add_(0, ids, dout.double().abs()).mul_(0.5)
+    # T fp32 additions, the factor, and the rounding to the type
+    tol = mag * (T + 2) * 2.0 ** -24 * 1.01 + want.abs() * torch.finfo(dt).eps / 2 * 1.01
+    assert bool(((got.double() - want).abs() <= tol).all())
+    untouched = torch.ones(V, dtype=torch.bool, device="cuda")
+    untouched[rows] = False
+    assert int(got[untouched].count_nonzero()) == 0
+
+
 @pytest.mark.parametrize("T", [500, 700, 64 * 33, 5000])
 def test_gradient_of_one_id(T):
     import torch
