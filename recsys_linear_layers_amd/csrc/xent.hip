@@ -39,13 +39,19 @@ __device__ __forceinline__ void block_join(float& m, float& s, float* red) {
 // The aligned copy of x (a row without a target becomes zeros, so that whatever
 // it holds cannot reach dw through 0 * inf), and the target's logit as a dot
 // product of its own.  LANES lanes per row.
+// One workgroup more forms the scale (scaled): a launch of its own costs 4 us.
 template <int TY, int LANES>
-__global__ void __launch_bounds__(256) xent_prep_kernel(const XentRows r) {
+__global__ void __launch_bounds__(256) xent_prep_kernel(const XentRows r, int scaled) {
   __shared__ float red[4];
+  const int blocks = gridDim.x - scaled;
+  if ((int)blockIdx.x == blocks) {
+    scale_block<256>(r, red);
+    return;
+  }
   constexpr int ROWS = 256 / LANES;
   typedef Chunk<TY, 8> C;
   const int l = threadIdx.x % LANES, y = threadIdx.x / LANES;
-  for (int64_t i0 = (int64_t)blockIdx.x * ROWS; i0 < r.N; i0 += (int64_t)gridDim.x * ROWS) {
+  for (int64_t i0 = (int64_t)blockIdx.x * ROWS; i0 < r.N; i0 += (int64_t)blocks * ROWS) {
     const int64_t i = i0 + y;
     const int64_t t = i < r.N ? r.target[i] : -1;
     const bool live = has_target(r, t);
@@ -102,13 +108,13 @@ hipError_t launch_xent_pack(const void* src, int64_t lds, int64_t rows, int cols
   return hipGetLastError();
 }
 
-hipError_t launch_xent_prep(const XentRows& r, int type, hipStream_t s) {
+hipError_t launch_xent_prep(const XentRows& r, bool scaled, int type, hipStream_t s) {
   const int lanes = r.ldp <= 128 ? 16 : r.ldp <= 512 ? 64 : 256, rows = 256 / lanes;
-  const dim3 grid((unsigned)std::min<int64_t>((r.N + rows - 1) / rows, 1 << 16));
-#define LL_PREP(TY)                                                                                  \
-  if (lanes == 16) hipLaunchKernelGGL((xent_prep_kernel<TY, 16>), grid, dim3(256), 0, s, r);         \
-  else if (lanes == 64) hipLaunchKernelGGL((xent_prep_kernel<TY, 64>), grid, dim3(256), 0, s, r);    \
-  else hipLaunchKernelGGL((xent_prep_kernel<TY, 256>), grid, dim3(256), 0, s, r);
+  const dim3 grid((unsigned)std::min<int64_t>((r.N + rows - 1) / rows, 1 << 16) + scaled);
+#define LL_PREP(TY)                                                                                         \
+  if (lanes == 16) hipLaunchKernelGGL((xent_prep_kernel<TY, 16>), grid, dim3(256), 0, s, r, (int)scaled);   \
+  else if (lanes == 64) hipLaunchKernelGGL((xent_prep_kernel<TY, 64>), grid, dim3(256), 0, s, r, (int)scaled);\
+  else hipLaunchKernelGGL((xent_prep_kernel<TY, 256>), grid, dim3(256), 0, s, r, (int)scaled);
   if (type == LL_BF16) {
     LL_PREP(LL_BF16)
   } else {
@@ -120,24 +126,7 @@ hipError_t launch_xent_prep(const XentRows& r, int type, hipStream_t s) {
 
 __global__ void __launch_bounds__(1024) xent_scale_kernel(const XentRows r) {
   __shared__ float red[16];
-  float m = 0.f;
-  for (int64_t i = threadIdx.x; i < r.N; i += 1024) {
-    const float g = fabsf(r.dloss[i]);
-    if (has_target(r, r.target[i]) && g < __builtin_huge_valf()) m = fmaxf(m, g);
-  }
-#pragma unroll
-  for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 16; ++w) m = fmaxf(m, red[w]);
-    // largest |dloss| in [2^13, 2^14); the inverse stays a normal number
-    int e = 0;
-    if (m > 0.f) frexpf(m, &e);
-    e = max(-100, min(100, 14 - e));
-    r.scale[0] = ldexpf(1.f, e);
-    r.scale[1] = ldexpf(1.f, -e);
-  }
+  scale_block<1024>(r, red);
 }
 
 hipError_t launch_xent_scale(const XentRows& r, hipStream_t s) {

@@ -34,7 +34,8 @@ struct XentRows {
 // dst[i][0 .. ldp) = src[i][0 .. cols), zeros past cols; ldp a multiple of 64.
 hipError_t launch_xent_pack(const void* src, int64_t lds, int64_t rows, int cols, void* dst, int ldp, int cus,
                             hipStream_t s);
-hipError_t launch_xent_prep(const XentRows& r, int type, hipStream_t s);
+// scaled: also forms scale, as launch_xent_scale does (likewise below).
+hipError_t launch_xent_prep(const XentRows& r, bool scaled, int type, hipStream_t s);
 // Power of two S that brings the largest |dloss| near 2^14 (fp16 gradients of the logits).
 hipError_t launch_xent_scale(const XentRows& r, hipStream_t s);
 // Few rows: up to kXentFewRows, x of at most kXentFewBytes (rows padded by 16
@@ -42,7 +43,7 @@ hipError_t launch_xent_scale(const XentRows& r, hipStream_t s);
 // not null.  x and w as given, any alignment; r.np workgroups.
 constexpr int kXentFewRows = 64;
 constexpr int64_t kXentFewBytes = 144 * 1024;
-hipError_t launch_xent_few(const XentRows& r, float* z, int64_t ldz, int type, hipStream_t s);
+hipError_t launch_xent_few(const XentRows& r, bool scaled, float* z, int64_t ldz, int type, hipStream_t s);
 // dw [V][ldo] of out_type from dz [N][ldd] and the copy xp, times *scale (null: 1).
 hipError_t launch_xent_dw_few(const XentRows& r, const void* dz, int64_t ldd, void* dw, int64_t ldo, int out_type,
                               const float* scale, int type, int cus, hipStream_t s);
@@ -66,7 +67,7 @@ struct XentNarrowOut {
   int row_blocks;
 };
 int xent_narrow_shares(int64_t own, int64_t streamed, int64_t slots);
-hipError_t launch_xent_narrow_stats(const XentRows& r, int type, hipStream_t s);
+hipError_t launch_xent_narrow_stats(const XentRows& r, bool scaled, int type, hipStream_t s);
 hipError_t launch_xent_narrow_grad(const XentRows& r, XentNarrowOut dx, XentNarrowOut dw, int type, hipStream_t s);
 // parts[p0 + split][row] of fp32 logits z [N][ldz], cols wide, in `splits` pieces per row.
 hipError_t launch_xent_stats(const XentRows& r, const float* z, int64_t ldz, int cols, int p0, int splits,

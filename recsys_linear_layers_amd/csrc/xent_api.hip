@@ -402,13 +402,16 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
   };
 
   const bool x_direct = p->x_direct && !bad(x, 16);
+  bool scale_later = false;
   if (N > 0) {
-    if (!(p->few && (!grads || p->by_row)) && !x_direct && !p->narrow) {
-      e = launch_xent_prep(r, d.type, st);
+    // fp16: the scale of dz, by the first kernel that reads no part of it
+    const bool prep = !(p->few && (!grads || p->by_row)) && !x_direct && !p->narrow;
+    if (prep) {
+      e = launch_xent_prep(r, r.scale != nullptr, d.type, st);
       if (e != hipSuccess) return hip_fail(e, "xent prep launch");
-    }
-    if (r.scale) {
-      e = launch_xent_scale(r, st);
+    } else if (r.scale) {
+      scale_later = p->few || p->narrow;
+      if (!scale_later) e = launch_xent_scale(r, st);
       if (e != hipSuccess) return hip_fail(e, "xent scale launch");
     }
     if (p->pack_w) {
@@ -417,7 +420,7 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
     }
   }
   if (p->narrow) {
-    e = launch_xent_narrow_stats(r, d.type, st);
+    e = launch_xent_narrow_stats(r, scale_later, d.type, st);
     if (e == hipSuccess) e = launch_xent_lse(r, st);
     if (e == hipSuccess && grads) {
       const XentNarrowOut ox = {dx, d.stride_dx, d.dx_type, p->shares[1],
@@ -451,7 +454,7 @@ ll_status xent_run(const xent_plan* p, const void* x, const void* w, const int64
   };
   ll_status s;
   if (p->few) {
-    e = launch_xent_few(r, grads ? z : nullptr, p->ldz, d.type, st);
+    e = launch_xent_few(r, scale_later, grads ? z : nullptr, p->ldz, d.type, st);
     if (e != hipSuccess) return hip_fail(e, "xent few rows launch");
   }
   if (N > 0) {

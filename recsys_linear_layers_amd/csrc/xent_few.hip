@@ -32,6 +32,10 @@ __global__ void __launch_bounds__(1024) xent_few_kernel(const XentRows r, float*
   typedef Chunk<TY, 8> C;
   extern __shared__ __attribute__((aligned(16))) uint16_t xs[];  // [N][Dp + 8], Dp: D up to whole 32s
   __shared__ float red[16][2][16];
+  if ((int)blockIdx.x == r.np) {
+    scale_block<1024>(r, red[0][0]);
+    return;
+  }
   const int N = (int)r.N, D = r.D, steps = (D + 31) / 32, pitch = steps * 32 + 8;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   const int c16 = lane & 15, g = lane >> 4;
@@ -56,7 +60,7 @@ __global__ void __launch_bounds__(1024) xent_few_kernel(const XentRows r, float*
   __syncthreads();
   const int tiles = (int)((r.V + 15) / 16);
   const int full = D / 32 / U * U;  // steps taken U at a time, whole
-  for (int tile = blockIdx.x + gridDim.x * wave; tile < tiles; tile += gridDim.x * 16) {
+  for (int tile = blockIdx.x + r.np * wave; tile < tiles; tile += r.np * 16) {
     const int64_t row = min((int64_t)tile * 16 + c16, r.V - 1);
     const uint16_t* const wrow = (const uint16_t*)r.w + row * r.ldw + 8 * g;
     f32x4 acc[NT];
@@ -134,21 +138,21 @@ __global__ void __launch_bounds__(1024) xent_few_kernel(const XentRows r, float*
 }
 
 template <int TY, bool TAIL>
-static void few_go(const XentRows& r, float* z, int64_t ldz, size_t lds, hipStream_t s) {
-  if (r.N <= 16) hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 1>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
-  else if (r.N <= 32) hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 2>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
-  else hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 4>), dim3(r.np), dim3(1024), lds, s, r, z, ldz);
+static void few_go(const XentRows& r, bool scaled, float* z, int64_t ldz, size_t lds, hipStream_t s) {
+  if (r.N <= 16) hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 1>), dim3(r.np + scaled), dim3(1024), lds, s, r, z, ldz);
+  else if (r.N <= 32) hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 2>), dim3(r.np + scaled), dim3(1024), lds, s, r, z, ldz);
+  else hipLaunchKernelGGL((xent_few_kernel<TY, TAIL, 4>), dim3(r.np + scaled), dim3(1024), lds, s, r, z, ldz);
 }
 
-hipError_t launch_xent_few(const XentRows& r, float* z, int64_t ldz, int type, hipStream_t s) {
+hipError_t launch_xent_few(const XentRows& r, bool scaled, float* z, int64_t ldz, int type, hipStream_t s) {
   const size_t lds = (size_t)r.N * ((r.D + 31) / 32 * 32 + 8) * 2;
   if (r.N < 1 || r.N > kXentFewRows || lds > (size_t)kXentFewBytes) return hipErrorInvalidValue;
   if (type == LL_BF16) {
-    if (r.D % 8) few_go<LL_BF16, true>(r, z, ldz, lds, s);
-    else few_go<LL_BF16, false>(r, z, ldz, lds, s);
+    if (r.D % 8) few_go<LL_BF16, true>(r, scaled, z, ldz, lds, s);
+    else few_go<LL_BF16, false>(r, scaled, z, ldz, lds, s);
   } else {
-    if (r.D % 8) few_go<LL_F16, true>(r, z, ldz, lds, s);
-    else few_go<LL_F16, false>(r, z, ldz, lds, s);
+    if (r.D % 8) few_go<LL_F16, true>(r, scaled, z, ldz, lds, s);
+    else few_go<LL_F16, false>(r, scaled, z, ldz, lds, s);
   }
   return hipGetLastError();
 }

@@ -338,8 +338,11 @@ __device__ __forceinline__ void narrow_body(const XentRows& r, const XentNarrowO
 template <int TY, int DP>
 __global__ void __launch_bounds__(256, kNarrowWaves<DP>) xent_narrow_stats_kernel(const XentRows r, int row_blocks) {
   __shared__ NarrowLds<DP> lds;
-  narrow_body<TY, DP, kNarrowStats>(r, XentNarrowOut{}, lds, blockIdx.x % row_blocks, blockIdx.x / row_blocks,
-                                    gridDim.x / row_blocks);
+  if ((int)blockIdx.x == row_blocks * r.np) {
+    scale_block<256>(r, lds.lse[0]);
+    return;
+  }
+  narrow_body<TY, DP, kNarrowStats>(r, XentNarrowOut{}, lds, blockIdx.x % row_blocks, blockIdx.x / row_blocks, r.np);
 }
 
 // The first workgroups form dx, the others dw: each alone would leave CUs idle
@@ -393,10 +396,10 @@ int xent_narrow_shares(int64_t own, int64_t streamed, int64_t slots) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(slots / blocks, steps / 4));
 }
 
-hipError_t launch_xent_narrow_stats(const XentRows& r, int type, hipStream_t s) {
+hipError_t launch_xent_narrow_stats(const XentRows& r, bool scaled, int type, hipStream_t s) {
   if (r.N < 1 || r.ldp < r.D || (r.ldp != 64 && r.ldp != 128)) return hipErrorInvalidValue;
   const int row_blocks = (int)((r.N + kNarrowRows - 1) / kNarrowRows);
-  const dim3 grid((unsigned)(row_blocks * r.np));
+  const dim3 grid((unsigned)(row_blocks * r.np + scaled));
 #define LL_STATS(TY, DP) \
   hipLaunchKernelGGL((xent_narrow_stats_kernel<TY, DP>), grid, dim3(256), 0, s, r, row_blocks)
   if (type == LL_BF16) {

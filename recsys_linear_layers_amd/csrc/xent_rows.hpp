@@ -20,6 +20,30 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 
 __device__ __forceinline__ bool has_target(const XentRows& r, int64_t t) { return t >= 0 && t < r.V && t != r.ignore; }
 
+// scale = {S, 1 / S} by one workgroup of THREADS; red: THREADS / 64 floats.
+template <int THREADS>
+__device__ __forceinline__ void scale_block(const XentRows& r, float* red) {
+  float m = 0.f;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < r.N; i += THREADS) {
+    const float g = fabsf(r.dloss[i]);
+    if (has_target(r, r.target[i]) && g < __builtin_huge_valf()) m = fmaxf(m, g);
+  }
+#pragma unroll
+  for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = m;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < THREADS / 64; ++w) m = fmaxf(m, red[w]);
+    // largest |dloss| in [2^13, 2^14); the inverse stays a normal number
+    int e = 0;
+    if (m > 0.f) frexpf(m, &e);
+    e = max(-100, min(100, 14 - e));
+    r.scale[0] = ldexpf(1.f, e);
+    r.scale[1] = ldexpf(1.f, -e);
+  }
+}
+
 template <int TY>
 __device__ __forceinline__ f32x4 mfma16(const Chunk<TY, 8>& a, const Chunk<TY, 8>& b, f32x4 c) {
   if constexpr (TY == LL_F16) {
