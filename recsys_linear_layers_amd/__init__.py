@@ -288,6 +288,20 @@ def _torch():
     return torch
 
 
+def _workspace(device, need: int):
+    """Scratch of one call (None where it needs none), from torch's allocator on
+    the current stream.  Never kept for the next call: the library lets go of
+    the interpreter lock, so another thread's launches may fall between this
+    call's on the same stream; and what a call allocates under graph capture
+    stays with that graph's pool for as long as the graph can be replayed."""
+    torch = _torch()
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _dtype_code(dt) -> int:
     torch = _torch()
     if dt == torch.bfloat16:
@@ -416,9 +430,6 @@ def lincomp_desc_for(user, item, W, Y, flags: int = 0, epilogue: int = 0) -> Lin
                        sy[0], sy[1], sy[2], _dtype_code(Y.dtype), flags, epilogue)
 
 
-_lc_ws: dict = {}
-
-
 def lincomp(user, item, W, out=None, out_dtype=None, flags: int = 0, bias=None, act=None):
     """Y[r, c] = act(W^T . [user[r]; item[r, c]] + bias) for bf16 tensors user
     [R][Nu][D] (or [R][C][Nu][D], rows per candidate), item [R][C][Ni][D], W
@@ -433,14 +444,10 @@ def lincomp(user, item, W, out=None, out_dtype=None, flags: int = 0, bias=None, 
         out = torch.empty((R, C, Mo, D), dtype=out_dtype or torch.bfloat16, device=user.device)
     desc = lincomp_desc_for(user, item, W, out, flags, _lc_epilogue(bias, act, Mo))
     need = lincomp_workspace_size(desc)
-    key = user.device.index
-    ws = _lc_ws.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=user.device)
-        _lc_ws[key] = ws
+    ws = _workspace(user.device, need)
     stream = torch.cuda.current_stream(user.device).cuda_stream
     lincomp_run_ex(desc, user.data_ptr(), item.data_ptr(), W.data_ptr(),
-                   bias.data_ptr() if bias is not None else None, out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+                   bias.data_ptr() if bias is not None else None, out.data_ptr(), _ptr(ws), need, stream)
     return out
 
 
@@ -481,29 +488,14 @@ def lincomp_ragged(user, item, W, offsets, out=None, out_dtype=None, flags: int 
 
 
 # ---------------------------------------------------------------------------
-# Operators around the linear layers.  Workspaces: one buffer per device and
-# stream, grown to the largest call; calls on one stream run one after the
-# other, so they can share it.
+# Operators around the linear layers.
 # ---------------------------------------------------------------------------
-
-_op_ws: dict = {}
-
 
 def _stream_of(t):
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU")
     # torch.cuda.current_stream() builds a Stream object for the same value (1.9 us, as long as some of the kernels)
     return _torch()._C._cuda_getCurrentRawStream(t.get_device())
-
-
-def _op_workspace(device, stream: int, need: int):
-    torch = _torch()
-    key = (device.index, stream)
-    ws = _op_ws.get(key)
-    if ws is None or ws.numel() < need:
-        ws = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-        _op_ws[key] = ws
-    return ws
 
 
 def _rows(t, what: str):
@@ -526,10 +518,6 @@ def _same_device(*ts) -> None:
     for t in ts[1:]:
         if t is not None and t.device != dev:
             raise ValueError(f"tensors on different devices: {dev}, {t.device}")
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr()
 
 
 def embedding(table, ids, scale: float = 1.0, out=None):
@@ -570,8 +558,9 @@ def embedding_grad(ids, dout, rows: int, scale: float = 1.0, padding_idx: int | 
     desc = EmbedGradDesc(rows, T, D, _rows(dout, "dout"), _rows(out, "out"), -1 if padding_idx is None else padding_idx,
                          _dtype_code(dout.dtype), scale, LL_EMBED_ACCUMULATE if accumulate else 0)
     stream = _stream_of(dout)
-    ws = _op_workspace(dout.device, stream, embed_grad_workspace_size(desc))
-    embed_grad_run(desc, ids.data_ptr(), dout.data_ptr(), out.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+    need = embed_grad_workspace_size(desc)
+    ws = _workspace(dout.device, need)
+    embed_grad_run(desc, ids.data_ptr(), dout.data_ptr(), out.data_ptr(), _ptr(ws), need, stream)
     return out
 
 
@@ -624,9 +613,10 @@ def layernorm_grad(dy, x, mean, rstd, gamma=None, out=None, param_grads: bool = 
     desc = LayernormGradDesc(N, D, _rows(dy, "dy"), _rows(x, "x"), _rows(out, "out"), _dtype_code(x.dtype),
                              _dtype_code(ptype))
     stream = _stream_of(x)
-    ws = _op_workspace(x.device, stream, layernorm_grad_workspace_size(desc) if param_grads else 0)
+    need = layernorm_grad_workspace_size(desc) if param_grads else 0
+    ws = _workspace(x.device, need)
     layernorm_grad_run(desc, dy.data_ptr(), x.data_ptr(), _ptr(gamma), mean.data_ptr(), rstd.data_ptr(),
-                       out.data_ptr(), _ptr(dgamma), _ptr(dbeta), ws.data_ptr(), ws.numel(), stream)
+                       out.data_ptr(), _ptr(dgamma), _ptr(dbeta), _ptr(ws), need, stream)
     return out, dgamma, dbeta
 
 
@@ -678,9 +668,9 @@ def _xent(x, w, target, dloss, dx, dw, ignore_index, piece_bytes):
     _same_device(x, w, target, dloss, dx, dw)
     loss, lse = torch.empty((2, N), dtype=torch.float32, device=x.device).unbind(0)
     stream = _stream_of(x)
-    ws = _op_workspace(x.device, stream, plan.ws_bytes)
+    ws = _workspace(x.device, plan.ws_bytes)
     xent_run(plan.handle, x.data_ptr(), w.data_ptr(), target.data_ptr(), _ptr(dloss), loss.data_ptr(), lse.data_ptr(),
-             _ptr(dx), _ptr(dw), ws.data_ptr(), ws.numel(), stream)
+             _ptr(dx), _ptr(dw), _ptr(ws), plan.ws_bytes, stream)
     return loss, lse
 
 
