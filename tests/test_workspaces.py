@@ -54,6 +54,22 @@ def test_two_threads_have_workspaces_of_their_own(monkeypatch):
         assert n == m > 0 and (a + n <= b or b + m <= a), entry
 
 
+@pytest.mark.parametrize("stream", [None, 5])
+def test_two_threads_that_run_one_gemm_plan_have_workspaces_of_their_own(monkeypatch, stream):
+    torch = pytest.importorskip("torch")
+    ll = _ll()
+
+    class Stream:
+        cuda_stream = 5
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream)
+    plan = ll.GemmPlan.__new__(ll.GemmPlan)  # a plan needs a device
+    plan.desc, plan.handle, plan.ws_bytes, plan.device, plan._ws = ll.GemmDesc(), None, 4096, torch.device("cpu"), {}
+    a = torch.zeros(4, 4)
+    (p, n), (q, m) = _meet(monkeypatch, "gemm_run", 4, lambda: plan.run(a, a, a, stream))
+    assert n == m == 4096 and (p + n <= q or q + m <= p)
+
+
 def _calls(seed):
     """One call of each operator that takes a workspace, on inputs of its own."""
     import torch
@@ -100,6 +116,33 @@ def test_two_threads_on_one_stream_get_the_serial_results():
     for t in threads:
         t.join(100)
     assert not wrong and not any(t.is_alive() for t in threads)
+
+
+@pytest.mark.gpu
+def test_two_threads_run_one_gemm_plan_on_one_stream():
+    """Split K and packed operands: partials and copies in the workspace."""
+    import torch
+    ll = _ll()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(7)
+    pairs = [(torch.randn((64, 8193), generator=g, device="cuda").bfloat16(),
+              torch.randn((8193, 320), generator=g, device="cuda").bfloat16()) for _ in range(2)]
+    want = [ll.gemm(a, b, out_dtype=torch.float32) for a, b in pairs]
+    plan = ll.plan_for(*pairs[0], want[0])
+    assert plan.ws_bytes > 0
+    torch.cuda.synchronize()
+    start, got = threading.Barrier(2, timeout=30), [[], []]
+
+    def run(k):
+        start.wait()
+        got[k] = [ll.gemm(*pairs[k], out_dtype=torch.float32) for _ in range(100)]
+
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(100)
+    assert all(len(got[k]) == 100 and all(torch.equal(c, want[k]) for c in got[k]) for k in range(2))
 
 
 @pytest.mark.gpu
