@@ -304,6 +304,12 @@ __device__ __forceinline__ void narrow_body(const XentRows& r, const XentNarrowO
     for (int q = 0; q < RT; ++q) {
       const int i = own0 + 16 * q + c16;
       if (i >= own_n) continue;
+      if (MODE == kNarrowDx && column[q] < 0) {  // its sums of w itself may be infinite, and 0 times that a NaN
+#pragma unroll
+        for (int d = 0; d < KS / 2; ++d)
+#pragma unroll
+          for (int t = 0; t < 4; ++t) acc[d][t][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
       const float f = (MODE == kNarrowDx ? coef[q] * (1.f / (1 << kNarrowExp<TY>)) : 1.f) * unscale;
 #pragma unroll
       for (int d = 0; d < KS / 2; ++d) {
