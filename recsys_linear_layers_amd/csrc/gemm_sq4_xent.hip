@@ -21,6 +21,15 @@ namespace ll {
 
 constexpr float kLog2e = 1.442695041f;
 
+// z - base as exp2's argument is fma(z, log2 e, -base * log2 e), one instruction,
+// but with the rounding of its addend, half a step of |base| log2 e: at 256 that
+// is 2^-16, 1.1e-5 of the exponential.  Further out (an entry of the vocabulary
+// masked by a huge negative value, a logit of 1e9) it would grow past 1 and the
+// exponential become anything from 0 to infinity, so the difference is formed
+// first there, by a branch of the whole wave per 16 rows (statistics alone of
+// 16384 x 32768 x 192: 368 us with it, 363 without; a branch per row 388).
+constexpr float kFarBase = 256.f;
+
 // The value 8, 4, 2 or 1 lanes further in each group of 16 (rotated).
 template <int N>
 __device__ __forceinline__ float ror16(float v) {
@@ -51,9 +60,16 @@ __device__ __forceinline__ void softmax_rows(const GemmKArgs& p, const TileInfo&
     const int64_t r0 = ti.m0 + wm0 + row;  // a multiple of 4: the arrays are read 16 bytes at a time
     const f32x4 lse = *(const f32x4*)(p.lse + r0), coef = *(const f32x4*)(p.coef + r0);
     const i32x4 col = *(const i32x4*)(p.column + r0);
+    f32x4 base = lse;
+    const float top = fmaxf(fmaxf(fabsf(lse[0]), fabsf(lse[1])), fmaxf(fabsf(lse[2]), fabsf(lse[3])));
+    if (__any(top > kFarBase)) {
+#pragma unroll
+      for (int J = 0; J < 8; ++J) v[J] -= lse;
+      base = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const float l2 = lse[r] * kLog2e;
+      const float l2 = base[r] * kLog2e;
       const int at = col[r] - p.col0 - ti.n0 - wn0 - c;  // 16 J where this lane holds the target
 #pragma unroll
       for (int J = 0; J < 8; ++J) {
@@ -70,17 +86,30 @@ __device__ __forceinline__ void softmax_rows(const GemmKArgs& p, const TileInfo&
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[J][r] = -__builtin_huge_valf();
     }
-    float m[4], s[4];
+    float m[4], m2[4], s[4], top = 0.f;
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       m[r] = max16(fmaxf(fmaxf(fmaxf(v[0][r], v[1][r]), fmaxf(v[2][r], v[3][r])),
                          fmaxf(fmaxf(v[4][r], v[5][r]), fmaxf(v[6][r], v[7][r]))));
       // all -inf: exp2(-inf) = 0 for every column
-      const float m2 = m[r] == -__builtin_huge_valf() ? 0.f : m[r] * kLog2e;
+      m2[r] = m[r] == -__builtin_huge_valf() ? 0.f : m[r];
+      top = fmaxf(top, fabsf(m2[r]));
+    }
+    if (__any(top > kFarBase)) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+#pragma unroll
+        for (int J = 0; J < 8; ++J) v[J][r] -= m2[r];
+        m2[r] = 0.f;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      m2[r] *= kLog2e;
       float sum = 0.f;
 #pragma unroll
       for (int J = 0; J < 8; ++J) {
-        const float e = __builtin_amdgcn_exp2f(fmaf(v[J][r], kLog2e, -m2));
+        const float e = __builtin_amdgcn_exp2f(fmaf(v[J][r], kLog2e, -m2[r]));
         sum += e;
         if constexpr (EPI == kSoftmaxNumerators)
           *(uint16_t LL_LDS*)(img + sq4_stage_off(row + r, 32 * J + 2 * c)) =

@@ -1,7 +1,8 @@
-"""The cross entropy where values are at the ends of their types' ranges."""
+"""The cross entropy where values are at the ends of their types' ranges, with the
+tolerances of test_vocab_xent_gpu."""
 import pytest
 
-from test_vocab_xent_gpu import _case, _ll
+from test_vocab_xent_gpu import _case, _check, _ll
 
 pytestmark = pytest.mark.gpu
 
@@ -21,3 +22,51 @@ def test_a_row_without_a_target_has_no_gradient_beside_huge_entries(D):
         out = ll.vocab_xent_grad(x, w, target, dloss, dx=dx)
         assert 0 < int(dead.sum()) < N and bool((dx[dead] == 0).all())
         assert bool(torch.isfinite(out[0]).all()) and bool(torch.isfinite(dx[:, 2:]).all())
+
+
+# Entries of the vocabulary masked by huge negative logits, and logits far above
+# all others: x has a column of ones, and the same column of w holds the mask or
+# the far value, so the products are exact where they are large.
+# path, rows, entries, width, bound of a piece
+PATHS = [("fused=1", 600, 20000, 192, 0), ("fused=1", 600, 20000, 192, 4 * 1024 * 768 * 2), ("fused=1", 2000, 9001, 136, 1),
+         ("narrow", 300, 5003, 64, 0), ("few_rows", 20, 5003, 200, 0), ("fused=0", 100, 9000, 192, 0),
+         ("fused=0", 100, 40000, 136, 0)]
+
+
+def _run(path, N, V, D, bound, dtype, far, at):
+    import torch
+    ll = _ll()
+    x, w, target, dloss = _case(N, V, D, dtype, seed=11)
+    x[:, 0] = 1
+    w[:, 0] = 0
+    w[at, 0] = far
+    plan = ll.xent_plan_for(x, w, x.clone(), w.clone(), piece_bytes=bound).describe()
+    assert path in plan, plan
+    what = f"{dtype} {path} {N}x{V}x{D} {far:g}"
+    if far < 0:  # no row's target is a masked entry
+        live = torch.ones(V, dtype=torch.bool, device="cuda")
+        live[at] = False
+        keep = torch.nonzero(live).squeeze(1)
+        target = torch.where(target >= 0, keep[target.clamp_min(0) % len(keep)], target)
+    else:
+        target[::3] = torch.where(target[::3] >= 0, at.start, target[::3])
+    loss, lse = ll.vocab_xent(x, w, target, piece_bytes=bound)
+    _check(x, w, target, None, (loss, lse, None, None), -100, what)
+    out = ll.vocab_xent_grad(x, w, target, dloss, piece_bytes=bound)
+    _check(x, w, target, dloss, out, -100, what)
+    if far < 0:
+        assert float(out[3][at].float().abs().max()) == 0, "a masked entry has a gradient"
+
+
+@pytest.mark.parametrize("path,N,V,D,bound", PATHS)
+@pytest.mark.parametrize("dtype,mask", [("bfloat16", -3.3895e38), ("bfloat16", -1e30), ("bfloat16", -1e9), ("bfloat16", -1e5),
+                                        ("float16", -65504.0)])
+def test_masked_entries(path, N, V, D, bound, dtype, mask):
+    """A third of the vocabulary masked: whole blocks of 128 columns, and parts of two more."""
+    _run(path, N, V, D, bound, dtype, mask, slice(V // 3 + 5, 2 * V // 3))
+
+
+@pytest.mark.parametrize("path,N,V,D,bound", PATHS)
+@pytest.mark.parametrize("dtype,far", [("bfloat16", 1e30), ("bfloat16", 1e9), ("bfloat16", 3e4), ("float16", 3e4)])
+def test_one_entry_far_above_the_others(path, N, V, D, bound, dtype, far):
+    _run(path, N, V, D, bound, dtype, far, slice(V // 2, V // 2 + 1))
