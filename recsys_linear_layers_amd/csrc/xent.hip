@@ -212,7 +212,10 @@ __global__ void __launch_bounds__(1024) xent_lse_kernel(const XentRows r) {
     r.lse[i] = lse;
     r.coef[i] = coef;
     r.column[i] = live ? (int32_t)t : -1;
-    r.loss[i] = live ? lse - r.zt[i] : 0.f;
+    // zt is a sum of its own, in another order than the logits: where the target has
+    // almost all of the probability the difference of the roundings may be negative
+    const float loss = lse - r.zt[i];
+    r.loss[i] = live && !(loss < 0.f) ? loss : 0.f;
     if (r.lse_out) r.lse_out[i] = lse;
     row_lse[y] = lse;
     row_coef[y] = coef * (1.f / kNumeratorScale);
@@ -323,7 +326,8 @@ __global__ void __launch_bounds__(256) xent_numerators_kernel(const XentRows r, 
     for (int j = 0; j < 8; ++j) o.put(j, t < 0 ? 0.f : e.get(j) * g);
     const int64_t at = t - v0 - c;  // the numerator's rounding would be lost against the 1
     if (t >= 0 && at >= 0 && at < 8) {
-      const float own = (__expf(r.zt[i] - r.lse[i]) - 1.f) * r.coef[i];
+      const float d = r.zt[i] - r.lse[i];
+      const float own = (__expf(d > 0.f ? 0.f : d) - 1.f) * r.coef[i];
 #pragma unroll
       for (int j = 0; j < 8; ++j)
         if (at == j) o.put(j, own);

@@ -70,3 +70,21 @@ def test_masked_entries(path, N, V, D, bound, dtype, mask):
 @pytest.mark.parametrize("dtype,far", [("bfloat16", 1e30), ("bfloat16", 1e9), ("bfloat16", 3e4), ("float16", 3e4)])
 def test_one_entry_far_above_the_others(path, N, V, D, bound, dtype, far):
     _run(path, N, V, D, bound, dtype, far, slice(V // 2, V // 2 + 1))
+
+
+@pytest.mark.parametrize("path,N,V,D,bound", PATHS)
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_the_loss_of_a_certain_target_is_not_negative(path, N, V, D, bound, dtype):
+    """Targets that have all of the probability but what rounds away: the loss is
+    zero or more, as it is in exact arithmetic."""
+    import torch
+    ll = _ll()
+    x, w, target, dloss = _case(N, V, D, dtype, seed=12, std=40.0)
+    live = target >= 0
+    target = torch.where(live, (x.double() @ w.double().T).argmax(1), target)
+    assert path in ll.xent_plan_for(x, w, x.clone(), w.clone(), piece_bytes=bound).describe()
+    loss, lse = ll.vocab_xent(x, w, target, piece_bytes=bound)
+    assert bool((loss >= 0).all()), loss.min()
+    out = ll.vocab_xent_grad(x, w, target, dloss, piece_bytes=bound)
+    assert bool((out[0] >= 0).all()), out[0].min()
+    _check(x, w, target, dloss, out, -100, f"{dtype} {path}")
