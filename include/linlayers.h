@@ -344,7 +344,8 @@ ll_status lincomp_ragged_run_ex(const lincomp_ragged_desc* desc, const int64_t* 
  * One kernel on `stream`; no workspace; may be captured into a HIP graph.
  * Errors: LL_ERR_INVALID_ARG (null desc/pointer, negative size, stride below
  * D, a pointer not aligned to its element, out overlapping the table or ids),
- * LL_ERR_UNSUPPORTED (type, sizes of 2^31 and more, device),
+ * LL_ERR_UNSUPPORTED (type, V of 2^31 - 1 and more, T or D above 2^31 - 2^12,
+ * strides that put a row 2^58 elements or more from the first, device),
  * LL_ERR_NO_DEVICE, LL_ERR_HIP.
  */
 typedef struct {

@@ -479,8 +479,8 @@ __global__ void __launch_bounds__(256) embed_sums_kernel(const EmbedGradArgs a, 
       }
       const int per = (kEmbedChunk + groups - 1) / groups;
       const int lo = p0 + min(g * per, kEmbedChunk), hi = p0 + min((g + 1) * per, kEmbedChunk);
-      for (int d0 = cb * lx * VEC; d0 < a.D; d0 += chunk_cols * lx * VEC) {
-        const int d = d0 + x * VEC;
+      for (uint32_t d0 = cb * lx * VEC; d0 < (uint32_t)a.D; d0 += chunk_cols * lx * VEC) {
+        const int d = (int)d0 + x * VEC;
         float acc[VEC] = {};
         if (d < a.D) add_tokens<TY, TAIL, 4>(a, pos, lo, hi, d, acc);
         groups_sum<256>(red, lx_log2, x, g, acc);
@@ -523,7 +523,8 @@ __global__ void __launch_bounds__(256) embed_sums_kernel(const EmbedGradArgs a, 
     }
     end = out;
   }
-  for (int d = (cb * lx + x) * VEC; d < a.D; d += col_blocks * lx * VEC) {
+  for (uint32_t d0 = (cb * lx + x) * VEC; d0 < (uint32_t)a.D; d0 += col_blocks * lx * VEC) {
+    const int d = (int)d0;
     const typename Elem<TY>::raw* base = (const typename Elem<TY>::raw*)a.dout + d;
     Chunk<TY, VEC> v[4];
 #pragma unroll
@@ -622,8 +623,8 @@ __global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, i
   }
   __syncthreads();
   auto pos = [&](int p) { return order[p]; };
-  for (int d0 = cb * lx * VEC; d0 < a.D; d0 += col_blocks * lx * VEC) {
-    const int d = d0 + x * VEC;
+  for (uint32_t d0 = cb * lx * VEC; d0 < (uint32_t)a.D; d0 += col_blocks * lx * VEC) {
+    const int d = (int)d0 + x * VEC;
     for (int i = 0; i < group_rows; ++i) {
       const int r = i * groups + g;
       const int2 s = seg[r];

@@ -15,6 +15,9 @@ using namespace ll;
 namespace {
 
 constexpr int64_t kMaxSize = (1ll << 31) - 1;
+// Tokens and columns of the embedding: the kernels round their 32-bit indexes up
+// to whole workgroups, chunks and steps, by less than this room.
+constexpr int64_t kEmbedMaxSize = (1ll << 31) - (1ll << 12);
 
 bool known_type(int ty) { return ty == LL_BF16 || ty == LL_F16 || ty == LL_F32; }
 
@@ -39,8 +42,8 @@ ll_status check_workspace(const void* ws, size_t have, size_t need) {
 ll_status embed_sizes(int64_t V, int64_t T, int64_t D, int64_t s0, int64_t s1, int type, float scale) {
   if (V < 0 || T < 0 || D < 0) return fail(LL_ERR_INVALID_ARG, "negative size");
   if (!known_type(type)) return fail(LL_ERR_UNSUPPORTED, "type must be LL_BF16, LL_F16 or LL_F32");
-  if (V >= kMaxSize || T >= kMaxSize || D >= kMaxSize)
-    return fail(LL_ERR_UNSUPPORTED, "V, T and D must be below 2^31 - 1");
+  if (V >= kMaxSize || T > kEmbedMaxSize || D > kEmbedMaxSize)
+    return fail(LL_ERR_UNSUPPORTED, "V must be below 2^31 - 1, T and D at most 2^31 - 2^12");
   if (s0 < D || s1 < D) return fail(LL_ERR_INVALID_ARG, "row strides shorter than the rows");
   if (!extent_fits(std::max(V, T), std::max(s0, s1))) return fail(LL_ERR_UNSUPPORTED, "row strides too large");
   if (!isfinite(scale)) return fail(LL_ERR_INVALID_ARG, "scale must be finite");
