@@ -450,7 +450,7 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs& a, int64_t v, int
 // group from the row's first sorted position, a block of columns at a time.
 template <int TY, bool TAIL>
 __global__ void __launch_bounds__(256) embed_sums_kernel(const EmbedGradArgs a, int src, int lx_log2, int chunk_blocks,
-                                                         int chunk_cols, int col_blocks) {
+                                                         int chunk_cols, int col_blocks, int first_block) {
   constexpr int VEC = kWide<TY>;
   __shared__ float red[256 * VEC];
   const uint32_t* key = a.key[src];
@@ -459,9 +459,10 @@ __global__ void __launch_bounds__(256) embed_sums_kernel(const EmbedGradArgs a, 
   const int lx = 1 << lx_log2;
   const int x = threadIdx.x & (lx - 1), g = threadIdx.x >> lx_log2;
   const int groups = 256 >> lx_log2;
-  if ((int)blockIdx.x < chunk_blocks) {
-    const int cb = blockIdx.x % chunk_cols, nch = a.T / kEmbedChunk;
-    for (int chunk = blockIdx.x / chunk_cols; chunk < nch; chunk += chunk_blocks / chunk_cols) {
+  const int block = first_block + (int)blockIdx.x;
+  if (block < chunk_blocks) {
+    const int cb = block % chunk_cols, nch = a.T / kEmbedChunk;
+    for (int chunk = block / chunk_cols; chunk < nch; chunk += chunk_blocks / chunk_cols) {
       const int p0 = chunk * kEmbedChunk;
       const uint32_t k0 = key[p0];
       if (key[p0 + kEmbedChunk - 1] != k0 || (int64_t)k0 >= a.V) continue;  // uniform
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(256) embed_sums_kernel(const EmbedGradArgs a, 
   // to four tokens then needs their rows and nothing else.  (Two positions per
   // group at once: more registers, fewer groups in flight, 206 against 195 us.)
   constexpr uint32_t none = 0xFFFFFFFFu;  // no key
-  const int item = blockIdx.x - chunk_blocks, cb = item % col_blocks;
+  const int item = block - chunk_blocks, cb = item % col_blocks;
   const int p = item / col_blocks * groups + g;
   if (p >= a.T) return;
   const int whole = (p + kEmbedChunk - 1) / kEmbedChunk * kEmbedChunk + kEmbedChunk - 1;
@@ -646,6 +647,9 @@ __global__ void __launch_bounds__(256) embed_few_kernel(const EmbedGradArgs a, i
   }
 }
 
+// Most workgroups of 256 in a launch: a grid of 2^32 threads or more is not supported.
+constexpr int64_t kMaxBlocks = (1ll << 32) / 256 - 1;
+
 template <int TY, bool TAIL>
 static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream_t s) {
   constexpr int VEC = kWide<TY>, ESIZE = (int)sizeof(typename Elem<TY>::raw);
@@ -660,10 +664,15 @@ static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream
     const int rows = (int)std::max<int64_t>(1, std::min<int64_t>(kRowsPerGroup, a.V / (groups * want)));
     const int64_t rb = (a.V + groups * rows - 1) / (groups * rows);
     const int cb = (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, want / rb));
-    if (rb * cb > 0x7FFFFFFF) return hipErrorInvalidValue;
+    if (rb * cb > kMaxBlocks) return hipErrorInvalidValue;
     hipLaunchKernelGGL((embed_few_kernel<TY, TAIL>), dim3((unsigned)(rb * cb)), dim3(256), 0, s, a, lx, rows, cb);
     return hipGetLastError();
   }
+  const int nch = a.T / kEmbedChunk;  // whole chunks
+  const int ccb = nch ? (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / nch)) : 1;
+  const int cwg = (int)std::min<int64_t>(nch, std::max<int64_t>(1, 16 * (int64_t)cus / ccb)) * ccb;
+  const int64_t sums = cwg + (int64_t)(a.T + groups - 1) / groups * all_cols;
+  if (sums > 0x7FFFFFFF) return hipErrorInvalidValue;  // before anything is written
   // 8 KB of zeros per workgroup of 256: two stores per lane (64 KB took 28 us for
   // a share of 134 MB instead of 22, 4 KB 29)
   const int shares = a.T <= kEmbedSmall ? 1 : 2 * a.passes;
@@ -689,13 +698,9 @@ static hipError_t launch_embed_grad_t(const EmbedGradArgs& a, int cus, hipStream
       src ^= 1;
     }
   }
-  const int nch = a.T / kEmbedChunk;  // whole chunks
-  const int ccb = nch ? (int)std::min<int64_t>(all_cols, std::max<int64_t>(1, 16 * (int64_t)cus / nch)) : 1;
-  const int cwg = (int)std::min<int64_t>(nch, std::max<int64_t>(1, 16 * (int64_t)cus / ccb)) * ccb;
-  const int64_t pb = (a.T + groups - 1) / groups;
-  if (cwg + pb * all_cols > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((embed_sums_kernel<TY, TAIL>), dim3((unsigned)(cwg + pb * all_cols)), dim3(256), 0, s, a, src, lx,
-                     cwg, ccb, all_cols);
+  for (int64_t first = 0; first < sums; first += kMaxBlocks)
+    hipLaunchKernelGGL((embed_sums_kernel<TY, TAIL>), dim3((unsigned)std::min(sums - first, kMaxBlocks)), dim3(256), 0, s,
+                       a, src, lx, cwg, ccb, all_cols, (int)first);
   if (nch == 0) return hipGetLastError();
   const int lb = (int)std::min<int64_t>((int64_t)nch * all_cols, 2 * cus);
   hipLaunchKernelGGL((embed_long_kernel<TY, TAIL>), dim3(lb), dim3(1024), 0, s, a, src, lx);

@@ -392,22 +392,25 @@ __global__ void __launch_bounds__(1024) norm_reduce_kernel(const float* partial,
                                                            void* dbeta, int param_f32) {
   __shared__ float red[16][64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int64_t col = (int64_t)blockIdx.x * 64 + lane;  // over both sums
-  float s = 0.f;
   const int lo = nblk * w / 16, hi = nblk * (w + 1) / 16;
-  if (col < 2ll * D) {
+  for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < 2ll * D; c0 += (int64_t)gridDim.x * 64) {
+    const int64_t col = c0 + lane;  // over both sums
+    float s = 0.f;
+    if (col < 2ll * D) {
 #pragma unroll 8
-    for (int k = lo; k < hi; ++k) s += partial[(int64_t)k * 2 * D + col];
-  }
-  red[w][lane] = s;
-  __syncthreads();
-  if (w == 0 && col < 2ll * D) {
+      for (int k = lo; k < hi; ++k) s += partial[(int64_t)k * 2 * D + col];
+    }
+    red[w][lane] = s;
+    __syncthreads();
+    if (w == 0 && col < 2ll * D) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += red[i][lane];
-    void* out = col < D ? dgamma : dbeta;
-    const int64_t c = col < D ? col : col - D;
-    if (TY == LL_F32 || param_f32) ((float*)out)[c] = s;
-    else ((typename Elem<TY>::raw*)out)[c] = Elem<TY>::put(s);
+      for (int i = 1; i < 16; ++i) s += red[i][lane];
+      void* out = col < D ? dgamma : dbeta;
+      const int64_t c = col < D ? col : col - D;
+      if (TY == LL_F32 || param_f32) ((float*)out)[c] = s;
+      else ((typename Elem<TY>::raw*)out)[c] = Elem<TY>::put(s);
+    }
+    __syncthreads();  // red is free for the next columns
   }
 }
 
@@ -491,8 +494,10 @@ static hipError_t launch_norm_grad_t(const NormGradArgs& a, int cus, hipStream_t
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !a.partial) return e;
-  hipLaunchKernelGGL((norm_reduce_kernel<TY>), dim3((unsigned)((2ll * a.D + 63) / 64)), dim3(1024), 0, s, a.partial,
-                     blocks, a.D, a.dgamma, a.dbeta, a.param_f32);
+  // a grid of 2^32 threads or more is not supported
+  const int64_t reduce = std::min<int64_t>((2ll * a.D + 63) / 64, 1 << 20);
+  hipLaunchKernelGGL((norm_reduce_kernel<TY>), dim3((unsigned)reduce), dim3(1024), 0, s, a.partial, blocks, a.D,
+                     a.dgamma, a.dbeta, a.param_f32);
   return hipGetLastError();
 }
 

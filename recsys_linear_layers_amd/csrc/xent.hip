@@ -187,50 +187,53 @@ __global__ void __launch_bounds__(1024) xent_lse_kernel(const XentRows r) {
   __shared__ float red[16][2][16];
   __shared__ float row_lse[16], row_coef[16];
   const int y = threadIdx.x & 15, g = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-  const int64_t i = (int64_t)blockIdx.x * 16 + y;
-  float m = kNegInf, s = 0.f;
-  if (i < r.N) {
+  for (int64_t i0 = (int64_t)blockIdx.x * 16; i0 < r.N; i0 += (int64_t)gridDim.x * 16) {
+    const int64_t i = i0 + y;
+    float m = kNegInf, s = 0.f;
+    if (i < r.N) {
 #pragma unroll 4
-    for (int p = g; p < r.np; p += 64) {
-      const float2 q = r.parts[(int64_t)p * r.part_ld + i];
-      join(m, s, q.x, q.y);
+      for (int p = g; p < r.np; p += 64) {
+        const float2 q = r.parts[(int64_t)p * r.part_ld + i];
+        join(m, s, q.x, q.y);
+      }
     }
-  }
-  join(m, s, __shfl_xor(m, 16, 64), __shfl_xor(s, 16, 64));
-  join(m, s, __shfl_xor(m, 32, 64), __shfl_xor(s, 32, 64));
-  if ((threadIdx.x & 63) < 16) {
-    red[wave][0][y] = m;
-    red[wave][1][y] = s;
-  }
-  __syncthreads();
-  if (threadIdx.x < 16 && i < r.N) {
-    for (int k = 1; k < 16; ++k) join(m, s, red[k][0][y], red[k][1][y]);
-    const int64_t t = r.target[i];
-    const bool live = has_target(r, t);
-    const float lse = live ? m + logf(s) : 0.f;
-    const float coef = live && r.dloss ? r.dloss[i] * (r.scale ? r.scale[0] : 1.f) : 0.f;
-    r.lse[i] = lse;
-    r.coef[i] = coef;
-    r.column[i] = live ? (int32_t)t : -1;
-    // zt is a sum of its own, in another order than the logits: where the target has
-    // almost all of the probability the difference of the roundings may be negative
-    const float loss = lse - r.zt[i];
-    r.loss[i] = live && !(loss < 0.f) ? loss : 0.f;
-    if (r.lse_out) r.lse_out[i] = lse;
-    row_lse[y] = lse;
-    row_coef[y] = coef * (1.f / kNumeratorScale);
-  }
-  if (r.factor0 >= r.np) return;  // uniform
-  __syncthreads();
-  if (i >= r.N) return;
-  for (int p = r.factor0 + g; p < r.np; p += 64) {
-    float2* const q = &r.parts[(int64_t)p * r.part_ld + i];
-    q->x = __expf(q->x - row_lse[y]) * row_coef[y];
+    join(m, s, __shfl_xor(m, 16, 64), __shfl_xor(s, 16, 64));
+    join(m, s, __shfl_xor(m, 32, 64), __shfl_xor(s, 32, 64));
+    if ((threadIdx.x & 63) < 16) {
+      red[wave][0][y] = m;
+      red[wave][1][y] = s;
+    }
+    __syncthreads();
+    if (threadIdx.x < 16 && i < r.N) {
+      for (int k = 1; k < 16; ++k) join(m, s, red[k][0][y], red[k][1][y]);
+      const int64_t t = r.target[i];
+      const bool live = has_target(r, t);
+      const float lse = live ? m + logf(s) : 0.f;
+      const float coef = live && r.dloss ? r.dloss[i] * (r.scale ? r.scale[0] : 1.f) : 0.f;
+      r.lse[i] = lse;
+      r.coef[i] = coef;
+      r.column[i] = live ? (int32_t)t : -1;
+      // zt is a sum of its own, in another order than the logits: where the target has
+      // almost all of the probability the difference of the roundings may be negative
+      const float loss = lse - r.zt[i];
+      r.loss[i] = live && !(loss < 0.f) ? loss : 0.f;
+      if (r.lse_out) r.lse_out[i] = lse;
+      row_lse[y] = lse;
+      row_coef[y] = coef * (1.f / kNumeratorScale);
+    }
+    __syncthreads();  // the row's values are there, and red is free for the next rows
+    if (i < r.N) {
+      for (int p = r.factor0 + g; p < r.np; p += 64) {
+        float2* const q = &r.parts[(int64_t)p * r.part_ld + i];
+        q->x = __expf(q->x - row_lse[y]) * row_coef[y];
+      }
+    }
   }
 }
 
 hipError_t launch_xent_lse(const XentRows& r, hipStream_t s) {
-  hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)((r.N + 15) / 16)), dim3(1024), 0, s, r);
+  // a grid of 2^32 threads or more is not supported
+  hipLaunchKernelGGL(xent_lse_kernel, dim3((unsigned)std::min<int64_t>((r.N + 15) / 16, 1 << 20)), dim3(1024), 0, s, r);
   return hipGetLastError();
 }
 
@@ -312,33 +315,34 @@ __global__ void __launch_bounds__(256) xent_numerators_kernel(const XentRows r, 
   const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
   const int c = blockIdx.x * 256 + 8 * x;
   const float2* f = r.parts + (int64_t)(p0 + c / 128) * r.part_ld;
+  for (int64_t i0 = (int64_t)blockIdx.y * 64; i0 < r.N; i0 += (int64_t)gridDim.y * 64)
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int64_t i = (int64_t)blockIdx.y * 64 + 8 * k + y;
-    if (i >= r.N) return;
-    Chunk<LL_F16, 8> e;
-    Chunk<TY, 8> o;
-    uint16_t* const p = dz + i * ldd + c;
-    e.template load<false>(p, 8);
-    const float g = f[i].x;
-    const int32_t t = r.column[i];
+    for (int k = 0; k < 8; ++k) {
+      const int64_t i = i0 + 8 * k + y;
+      if (i >= r.N) break;
+      Chunk<LL_F16, 8> e;
+      Chunk<TY, 8> o;
+      uint16_t* const p = dz + i * ldd + c;
+      e.template load<false>(p, 8);
+      const float g = f[i].x;
+      const int32_t t = r.column[i];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o.put(j, t < 0 ? 0.f : e.get(j) * g);
-    const int64_t at = t - v0 - c;  // the numerator's rounding would be lost against the 1
-    if (t >= 0 && at >= 0 && at < 8) {
-      const float d = r.zt[i] - r.lse[i];
-      const float own = (__expf(d > 0.f ? 0.f : d) - 1.f) * r.coef[i];
+      for (int j = 0; j < 8; ++j) o.put(j, t < 0 ? 0.f : e.get(j) * g);
+      const int64_t at = t - v0 - c;  // the numerator's rounding would be lost against the 1
+      if (t >= 0 && at >= 0 && at < 8) {
+        const float d = r.zt[i] - r.lse[i];
+        const float own = (__expf(d > 0.f ? 0.f : d) - 1.f) * r.coef[i];
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (at == j) o.put(j, own);
+        for (int j = 0; j < 8; ++j)
+          if (at == j) o.put(j, own);
+      }
+      o.template store<false>(p, 8);
     }
-    o.template store<false>(p, 8);
-  }
 }
 
 hipError_t launch_xent_numerators(const XentRows& r, void* dz, int64_t ldd, int64_t v0, int cols, int p0, int type,
                                   hipStream_t s) {
-  const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)((r.N + 63) / 64));
+  const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)std::min<int64_t>((r.N + 63) / 64, 1 << 15));  // y ends at 2^16
   if (type == LL_BF16)
     hipLaunchKernelGGL((xent_numerators_kernel<LL_BF16>), grid, dim3(256), 0, s, r, (uint16_t*)dz, ldd, v0, p0);
   else

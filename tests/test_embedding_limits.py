@@ -57,3 +57,16 @@ def test_gradient_of_rows_wider_than_2_to_30(T, accumulate):
     ll.embedding_grad(ids, dout, 1, out=out, accumulate=accumulate)
     want = T * (T + 1) // 2 + accumulate
     assert bool((out[0, :-1] == want).all()) and float(out[0, -1]) == T + accumulate
+
+
+@pytest.mark.gpu
+def test_gradient_in_more_workgroups_than_one_launch_takes():
+    """2^25 tokens of two blocks of columns: more than 2^32 threads."""
+    import torch
+    ll = _ll()
+    T, V, D = 2 ** 25 + 1000, 2 ** 20, 513
+    ids = torch.arange(T, device="cuda") % V
+    dout = torch.ones((T, D), dtype=torch.bfloat16, device="cuda")
+    got = ll.embedding_grad(ids, dout, V)
+    counts = torch.bincount(ids, minlength=V).to(torch.bfloat16)
+    assert bool((got == counts[:, None]).all())
