@@ -12,6 +12,7 @@ Importing this module fails if the library has not been built
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import os
 import threading
@@ -644,11 +645,14 @@ class XentPlan:
             self.handle = None
 
 
-_xent_plans: dict = {}
+# The plans of the latest sizes: a program whose batches differ in rows asks for a
+# plan per row count, and a plan is needed for its own launches alone.
+_XENT_PLANS = 256
+_xent_plans: collections.OrderedDict = collections.OrderedDict()
 
 
 def xent_plan_for(x, w, dx=None, dw=None, ignore_index: int = -100, piece_bytes: int = 0) -> XentPlan:
-    """The (kept) plan for these tensors' sizes, strides and types."""
+    """The plan for these tensors' sizes, strides and types (the latest are kept)."""
     N, D = x.shape
     V = w.shape[0]
     if w.shape[1] != D or w.dtype != x.dtype:
@@ -660,9 +664,13 @@ def xent_plan_for(x, w, dx=None, dw=None, ignore_index: int = -100, piece_bytes:
     key = (x.device.index, N, V, D, _rows(x, "x"), _rows(w, "w"), _rows(dx, "dx") if dx is not None else 0,
            _rows(dw, "dw") if dw is not None else 0, ignore_index, piece_bytes, code,
            _dtype_code(dx.dtype) if dx is not None else code, _dtype_code(dw.dtype) if dw is not None else code, flags)
-    plan = _xent_plans.get(key)
-    if plan is None:
-        plan = _xent_plans[key] = XentPlan(XentDesc(*key[1:]))
+    plan = _xent_plans.pop(key, None) or XentPlan(XentDesc(*key[1:]))
+    _xent_plans[key] = plan  # the newest
+    while len(_xent_plans) > _XENT_PLANS:
+        try:
+            _xent_plans.popitem(last=False)
+        except KeyError:  # emptied by another thread
+            break
     return plan
 
 
