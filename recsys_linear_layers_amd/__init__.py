@@ -501,8 +501,11 @@ def lincomp_ragged(user, item, W, offsets, out=None, out_dtype=None, flags: int 
 def _stream_of(t):
     if not t.is_cuda:
         raise ValueError("tensors must be on a GPU")
+    C, device = _torch()._C, t.get_device()
+    if device != C._cuda_getDevice():  # the library launches on the current device, whatever the pointers
+        raise ValueError(f"tensors on cuda:{device}, but the current device is cuda:{C._cuda_getDevice()}")
     # torch.cuda.current_stream() builds a Stream object for the same value (1.9 us, as long as some of the kernels)
-    return _torch()._C._cuda_getCurrentRawStream(t.get_device())
+    return C._cuda_getCurrentRawStream(device)
 
 
 def _rows(t, what: str):
@@ -677,11 +680,11 @@ def xent_plan_for(x, w, dx=None, dw=None, ignore_index: int = -100, piece_bytes:
 def _xent(x, w, target, dloss, dx, dw, ignore_index, piece_bytes):
     torch = _torch()
     N = x.shape[0]
+    stream = _stream_of(x)
     plan = xent_plan_for(x, w, dx, dw, ignore_index, piece_bytes)
     _vector(target, N, "target", (torch.int64,))
     _same_device(x, w, target, dloss, dx, dw)
     loss, lse = torch.empty((2, N), dtype=torch.float32, device=x.device).unbind(0)
-    stream = _stream_of(x)
     ws = _workspace(x.device, plan.ws_bytes)
     xent_run(plan.handle, x.data_ptr(), w.data_ptr(), target.data_ptr(), _ptr(dloss), loss.data_ptr(), lse.data_ptr(),
              _ptr(dx), _ptr(dw), _ptr(ws), plan.ws_bytes, stream)
