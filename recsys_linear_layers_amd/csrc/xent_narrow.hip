@@ -110,9 +110,10 @@ __device__ __forceinline__ void narrow_body(const XentRows& r, const XentNarrowO
         const int64_t t = r.target[i];
         if (has_target(r, t)) column[q] = (int)t;
       } else if constexpr (MODE == kNarrowDx) {
-        lse[q] = r.lse[i];
         coef[q] = r.coef[i];
         column[q] = r.column[i];
+        // no target: exp(0 - infinity), so that the sums are 0; those of w itself may pass fp32's range
+        lse[q] = column[q] >= 0 ? r.lse[i] : __builtin_huge_valf();
       }
     }
 #pragma unroll
@@ -176,7 +177,7 @@ __device__ __forceinline__ void narrow_body(const XentRows& r, const XentNarrowO
 #pragma unroll
       for (int t = 0; t < 4; ++t) acc[d][t][q] = f32x4{0.f, 0.f, 0.f, 0.f};
   }
-  // SLOW: a row's target is among these logits, or w ends in this step
+  // SLOW: a row's target is among these logits, w ends in this step or holds infinities
   auto step = [&](auto slow, int slot, int b, int h) {
     constexpr bool SLOW = decltype(slow)::value;
     const uint16_t* const t0 = &lds.tile[slot][32 * h * PITCH];
@@ -240,7 +241,7 @@ __device__ __forceinline__ void narrow_body(const XentRows& r, const XentNarrowO
             if constexpr (SLOW) {
               const int v = v0 + 16 * t + e;
               if (MODE == kNarrowDw ? k4[e] == own0 + 16 * q + c16 : column[q] == v) y -= ONE;
-              if (MODE == kNarrowDx && v >= str_n) y = 0.f;
+              if (MODE == kNarrowDx ? v >= str_n : k4[e] < 0) y = 0.f;
             }
             z[t][q][e] = MODE == kNarrowDw ? y * c4[e] : y;
           }
@@ -270,6 +271,18 @@ __device__ __forceinline__ void narrow_body(const XentRows& r, const XentNarrowO
     load(b0);
     put(0);
   }
+  // an infinity in w (a masked entry): it meets the zeros of rows without a target as a NaN
+  bool endless = false;
+  if constexpr (MODE == kNarrowDw) {
+    constexpr uint32_t EXP = TY == LL_F16 ? 0x7C00u : 0x7F80u;
+#pragma unroll
+    for (int q = 0; q < RT; ++q)
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) endless |= (own[q][k].get_raw(i) & EXP) == EXP;
+    endless = __any(endless);
+  }
   for (int b = b0; b < b1; ++b, slot ^= 1) {
     __syncthreads();  // this block is there, and the other slot is free
     if (b + 1 < b1) load(b + 1);
@@ -280,7 +293,7 @@ __device__ __forceinline__ void narrow_body(const XentRows& r, const XentNarrowO
       for (int q = 0; q < RT; ++q) mine |= (unsigned)(column[q] - b * kNarrowBlock) < (unsigned)kNarrowBlock;
       slow |= __any(mine);
     } else {
-      slow = __any((unsigned)(lds.column[slot][lane] - own0) < (unsigned)(16 * RT));
+      slow = endless || __any((unsigned)(lds.column[slot][lane] - own0) < (unsigned)(16 * RT));
     }
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
@@ -304,12 +317,6 @@ __device__ __forceinline__ void narrow_body(const XentRows& r, const XentNarrowO
     for (int q = 0; q < RT; ++q) {
       const int i = own0 + 16 * q + c16;
       if (i >= own_n) continue;
-      if (MODE == kNarrowDx && column[q] < 0) {  // its sums of w itself may be infinite, and 0 times that a NaN
-#pragma unroll
-        for (int d = 0; d < KS / 2; ++d)
-#pragma unroll
-          for (int t = 0; t < 4; ++t) acc[d][t][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-      }
       const float f = (MODE == kNarrowDx ? coef[q] * (1.f / (1 << kNarrowExp<TY>)) : 1.f) * unscale;
 #pragma unroll
       for (int d = 0; d < KS / 2; ++d) {

@@ -88,3 +88,22 @@ def test_the_loss_of_a_certain_target_is_not_negative(path, N, V, D, bound, dtyp
     out = ll.vocab_xent_grad(x, w, target, dloss, piece_bytes=bound)
     assert bool((out[0] >= 0).all()), out[0].min()
     _check(x, w, target, dloss, out, -100, f"{dtype} {path}")
+
+
+@pytest.mark.parametrize("path,N,V,D,bound", PATHS)
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_entries_masked_by_minus_infinity(path, N, V, D, bound, dtype):
+    """Loss and dw (dx meets 0 times infinity by its formula) as with a mask of -6e4, rows without a target among them."""
+    import torch
+    ll = _ll()
+    x, w, target, dloss = _case(N, V, D, dtype, seed=13, ignored=0.3)
+    at = slice(V // 3 + 5, 2 * V // 3)
+    x[:, 0] = 1
+    w[:, 0] = 0
+    target = torch.where((target >= at.start) & (target < at.stop), 3, target)
+    finite, endless = w.clone(), w.clone()
+    finite[at, 0], endless[at, 0] = -6e4, float("-inf")
+    assert path in ll.xent_plan_for(x, w, None, w.clone(), piece_bytes=bound).describe()
+    loss, lse, _, dw = ll.vocab_xent_grad(x, endless, target, dloss, want_dx=False, piece_bytes=bound)
+    _check(x, finite, target, dloss, (loss, lse, None, dw), -100, f"{dtype} {path}")
+    assert float(dw[at].float().abs().max()) == 0
