@@ -26,7 +26,8 @@ constexpr float kLog2e = 1.442695041f;
 // is 2^-16, 1.1e-5 of the exponential.  Further out (an entry of the vocabulary
 // masked by a huge negative value, a logit of 1e9) it would grow past 1 and the
 // exponential become anything from 0 to infinity, so the difference is formed
-// first there, by a branch of the whole wave per 16 rows (statistics alone of
+// first there, for such rows alone (a row's bits depend on nothing but the row, and
+// rows past the last hold anything), by a branch per 16 rows (statistics alone of
 // 16384 x 32768 x 192: 368 us with it, 363 without; a branch per row 388).
 constexpr float kFarBase = 256.f;
 
@@ -64,8 +65,12 @@ __device__ __forceinline__ void softmax_rows(const GemmKArgs& p, const TileInfo&
     const float top = fmaxf(fmaxf(fabsf(lse[0]), fabsf(lse[1])), fmaxf(fabsf(lse[2]), fabsf(lse[3])));
     if (__any(top > kFarBase)) {
 #pragma unroll
-      for (int J = 0; J < 8; ++J) v[J] -= lse;
-      base = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int r = 0; r < 4; ++r) {
+        const bool far = fabsf(lse[r]) > kFarBase;
+#pragma unroll
+        for (int J = 0; J < 8; ++J) v[J][r] -= far ? lse[r] : 0.f;
+        base[r] = far ? 0.f : lse[r];
+      }
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
@@ -98,9 +103,10 @@ __device__ __forceinline__ void softmax_rows(const GemmKArgs& p, const TileInfo&
     if (__any(top > kFarBase)) {
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
+        const bool far = fabsf(m2[r]) > kFarBase;
 #pragma unroll
-        for (int J = 0; J < 8; ++J) v[J][r] -= m2[r];
-        m2[r] = 0.f;
+        for (int J = 0; J < 8; ++J) v[J][r] -= far ? m2[r] : 0.f;
+        m2[r] = far ? 0.f : m2[r];
       }
     }
 #pragma unroll

@@ -107,3 +107,41 @@ def test_entries_masked_by_minus_infinity(path, N, V, D, bound, dtype):
     loss, lse, _, dw = ll.vocab_xent_grad(x, endless, target, dloss, want_dx=False, piece_bytes=bound)
     _check(x, finite, target, dloss, (loss, lse, None, dw), -100, f"{dtype} {path}")
     assert float(dw[at].float().abs().max()) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_a_far_row_leaves_the_others_as_they_are(dtype):
+    """One row of every sixteen with logits of thousands: the other rows' bits, with and without it."""
+    import torch
+    ll = _ll()
+    for bound in (0, 1):
+        x, w, target, dloss = _case(600, 20000, 192, dtype, seed=14, ignored=0.1)
+        assert "fused=1" in ll.xent_plan_for(x, w, x, piece_bytes=bound).describe()
+        far = x.clone()
+        far[5::16] *= 1000
+        keep = torch.arange(600, device="cuda") % 16 != 5
+        a, b = (ll.vocab_xent_grad(p, w, target, dloss, want_dw=False, piece_bytes=bound) for p in (x, far))
+        assert all(torch.equal(p[keep], q[keep]) for p, q in zip(a[:3], b[:3]))
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_what_the_workspace_holds_does_not_matter(dtype):
+    """Rows up to whole tiles, columns up to whole parts: nothing is read there that the call has not written.
+    The workspace is filled with large numbers, NaN and zeros in turn."""
+    import torch
+    ll = _ll()
+    for N, V, D, bound in ((382, 20000, 304, 1 << 22), (2418, 3434, 192, 1), (777, 5003, 200, 0), (130, 40000, 136, 0),
+                           (20, 5003, 200, 0), (300, 5003, 64, 0), (100, 9000, 192, 1)):
+        x, w, target, dloss = _case(N, V, D, dtype, seed=15)
+        plan = ll.xent_plan_for(x, w, x, w, piece_bytes=bound)
+        outs = []
+        for fill in (1e30, float("nan"), 0.0, -1e9):
+            ws = torch.full((plan.ws_bytes // 4,), fill, device="cuda")
+            loss, lse = torch.empty(N, device="cuda"), torch.empty(N, device="cuda")
+            dx, dw = torch.empty_like(x), torch.empty_like(w)
+            ll.xent_run(plan.handle, x.data_ptr(), w.data_ptr(), target.data_ptr(), dloss.data_ptr(), loss.data_ptr(),
+                        lse.data_ptr(), dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), plan.ws_bytes,
+                        torch.cuda.current_stream().cuda_stream)
+            outs.append((loss, lse, dx, dw))
+        for out in outs[1:]:
+            assert all(torch.equal(p, q) for p, q in zip(out, outs[0])), (N, V, D, bound)
