@@ -400,7 +400,8 @@ ll_status embed_grad_run(const embed_grad_desc* desc, const int64_t* ids, const 
  * written.  One kernel on `stream`, no workspace, graph-capturable.
  * Errors: LL_ERR_INVALID_ARG (null desc, x or y; negative size, stride below
  * D, eps negative or not finite, misaligned pointer, y overlapping an input
- * otherwise), LL_ERR_UNSUPPORTED (types, D of 2^31 and more, device),
+ * otherwise), LL_ERR_UNSUPPORTED (types, D of 2^30 - 1 and more, N of 2^40 and
+ * more, strides that put a row 2^58 elements or more from the first, device),
  * LL_ERR_NO_DEVICE, LL_ERR_HIP.
  */
 typedef struct {
@@ -450,10 +451,22 @@ ll_status layernorm_grad_run(const layernorm_grad_desc* desc, const void* dy, co
  * which are wanted (neither: the loss alone).
  * A row whose target is ignore_index or outside [0, V) has no loss: loss, lse
  * and its row of dx are zeros, and it adds nothing to dw, whatever it holds.
+ * (dx = dz w meets 0 times infinity where w holds infinities.)  Entries of the
+ * vocabulary may be masked by logits of any size, -infinity included.
  * Products are accumulated in fp32, row sums carried in fp32 with their
- * maximum; dz is rounded to `type` (with fp16 after multiplication by a power
- * of two, taken out again in fp32, so that small probabilities keep their
- * bits), dx and dw once each.
+ * maximum; the loss is never negative.
+ * dz is formed from z - lse with lse rounded to fp32 (|lse| 2^-24 of each
+ * probability) and, as an operand of the matrix instruction, rounded to `type`
+ * before the products: half a step, 2^-8 (bf16) or 2^-11 (fp16) of each
+ * element, whatever dx_type and dw_type; dx and dw are rounded once more to
+ * theirs.  (Their mean error is then about 1.4 times that of rounding them
+ * alone.)  Before that, pieces whose softmax numerators are kept (below) hold
+ * those as fp16 times 2^15: another 2^-11 of each, and numerators below 2^-40
+ * of the largest of their 128 columns become 0; so the last bits of dx and dw
+ * depend on piece_bytes.  With fp16, dz is multiplied by one power of two for
+ * all rows, which brings the largest |dloss| to 2^13 or more and is taken out
+ * again in fp32: a row whose |dloss| is 2^k times smaller than the largest
+ * loses probabilities below 2^(k - 38).
  * piece_bytes bounds the buffers that hold logits, their softmax numerators and
  * dz (0: 2 GiB); when the whole vocabulary does not fit, it is cut into pieces of
  * a multiple of 256 entries (at least one such).  The numerators of as many

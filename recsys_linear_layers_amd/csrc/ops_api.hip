@@ -57,6 +57,8 @@ struct EmbedGradLayout {
          long_rows = 0, bytes = 0;
 };
 
+// Few tokens that are added to a table take the direct path whatever its size:
+// every row looks through the ids, 300 into 1000003 x 64 fp32 15 us.
 // Workspace of the sorted path.  One workgroup sorts in 8-bit digits; beyond
 // that, digits of at most kSortMaxBits bits, of equal width over the passes
 // that cover the keys 0 .. V.
