@@ -281,8 +281,8 @@ def xent_plan_destroy(plan: int) -> None:
 
 
 # ---------------------------------------------------------------------------
-# torch conveniences: build descriptors from tensor shapes/strides, keep plans
-# and workspaces, launch on torch's current stream.
+# torch conveniences: build descriptors from tensor shapes/strides, keep plans,
+# launch on torch's current stream.
 # ---------------------------------------------------------------------------
 
 def _torch():
