@@ -28,6 +28,10 @@
  *               activations, each with its gradients.
  *  - xent_*   : what stands behind them: the softmax cross entropy over a
  *               vocabulary, in pieces of the vocabulary, with its gradients.
+ *  - rmsnorm_*, quant8_*, gemm8_*: linear layers in 8 bits: the norm in front
+ *               (with the residual's addition, its output in 8 bits or not) and
+ *               its gradient, the quantisation in blocks of 128, and the product
+ *               of 8-bit operands with a scale per block.
  *
  * Conventions shared by every entry point:
  *
@@ -65,7 +69,13 @@ typedef enum {
   LL_ERR_NO_DEVICE = 5     /* no HIP device is visible */
 } ll_status;
 
-typedef enum { LL_BF16 = 0, LL_F32 = 1, LL_F16 = 2 /* IEEE binary16 */ } ll_dtype;
+typedef enum {
+  LL_BF16 = 0,
+  LL_F32 = 1,
+  LL_F16 = 2,  /* IEEE binary16 */
+  LL_E4M3 = 3, /* 8 bits, 4 of exponent: up to 448, no infinities (the operands of gemm8) */
+  LL_E5M2 = 4  /* 8 bits, 5 of exponent: up to 57344 */
+} ll_dtype;
 
 /* gemm_desc.flags */
 #define LL_FLAG_PACK_A 0x1u /* always copy A into an aligned workspace layout first */
@@ -517,6 +527,156 @@ ll_status xent_run(const xent_plan* plan, const void* x, const void* w, const in
                    float* loss, float* lse, void* dx, void* dw, void* workspace, size_t ws_bytes, void* stream);
 
 ll_status xent_plan_destroy(xent_plan* plan);
+
+/*
+ * Linear layers in 8 bits.
+ *
+ * A quantised matrix is one of 8-bit values (LL_E4M3 or LL_E5M2), K the
+ * dimension a product runs over, in rows of K consecutive values, and fp32
+ * scales, one for each block of 128 values along K:
+ *   block 1:   scale[row][k / 128], a block is 128 consecutive values of a row;
+ *   block 128: scale[row / 128][k / 128], a block is 128 x 128 values.
+ * Blocks at the ends are as short as the matrix.  The value that (i, k) stands
+ * for is q[i][k] * scale.  Scales may have any positive strides (scale strides
+ * are in fp32 elements); consecutive rows next to each other read fastest.
+ *
+ * How a block is quantised (here and in rmsnorm_run): with F the type's largest
+ * value (448, 57344),
+ *   scale = max(amax / F, 2^-126),  q = round(x * (1 / scale))
+ * amax the largest magnitude of the block, each operation rounded to fp32, the
+ * last to the 8-bit type, to nearest even: half a step, 2^-4 (e4m3) or 2^-3
+ * (e5m2) of each value of at least 2^-14 (2^-29) of amax.  A block that holds a
+ * NaN or an infinity has the scale NaN and NaNs in q.
+ */
+
+/*
+ * Root-mean-square norm of each of N rows of D columns, with the residual's
+ * addition in front:
+ *   h = x + residual (rounded to `type`; h = x where residual is NULL)
+ *   y = h * rstd * gamma,  rstd = 1 / sqrt(mean_D(h^2) + eps)
+ * of h as it is stored, in fp32 (squares are summed in fp32: h beyond 2^63
+ * overflows them), y rounded once to y_type: `type`, or LL_E4M3 / LL_E5M2
+ * quantised in blocks of 128 of a row (block 1 above), with scale[row][d / 128]
+ * at scale + row*stride_sn + (d / 128)*stride_sb.
+ * x, residual, h, y: row strides in elements, at least D, last dimension
+ * contiguous.  gamma: D values of param_type (`type` or LL_F32), NULL: ones.
+ * h: written if there is a residual (then required, else NULL); it may be x or
+ * residual (same pointer and stride).  y may be x where there is no residual and
+ * y_type is `type`.  rstd: N fp32 values for the gradient, may be NULL.
+ * N == 0 or D == 0: nothing is written.  One kernel on `stream`, no workspace,
+ * graph-capturable.
+ * Errors: LL_ERR_INVALID_ARG (null desc, x, y, or scale with an 8-bit y, negative
+ * size, stride below D, scale stride below 1, eps negative or not finite,
+ * misaligned pointer, an output overlapping an input otherwise or another output),
+ * LL_ERR_UNSUPPORTED (types, D of 2^30 - 1 and more, N of 2^40 and more, strides
+ * that put a row 2^58 elements or more from the first, device),
+ * LL_ERR_NO_DEVICE, LL_ERR_HIP.
+ */
+typedef struct {
+  int64_t N, D;
+  int64_t stride_x, stride_residual, stride_h, stride_y;
+  int64_t stride_sn, stride_sb;      /* of scale; ignored unless y_type is an 8-bit type */
+  int32_t type, param_type, y_type;  /* ll_dtype */
+  float eps;
+} rmsnorm_desc;
+
+ll_status rmsnorm_run(const rmsnorm_desc* desc, const void* x, const void* residual, const void* gamma, void* h,
+                      void* y, float* scale, float* rstd, void* stream);
+
+/*
+ * Gradients of the norm, from h as it saw it and the rstd it gave:
+ *   n = h * rstd,  g = dy * gamma,
+ *   dx = rstd * (g - n * mean_D(g * n)) + dh,  dgamma = sum over rows of dy * n
+ * in fp32, each result rounded once.  dx is the gradient of h, and so of x and of
+ * the residual; dh the gradient that reaches h by its other path, may be NULL,
+ * and dx may be dh (same pointer and stride).  dgamma: D values of param_type,
+ * may be NULL (not wanted).  Sums over rows are formed in an order that depends
+ * on the sizes alone.  N == 0: dgamma is written as zeros.  Workspace (256-byte
+ * aligned): rmsnorm_grad_workspace_size; none without dgamma.  Kernels only,
+ * graph-capturable.  Errors as for rmsnorm_run, and LL_ERR_WORKSPACE.
+ */
+typedef struct {
+  int64_t N, D;
+  int64_t stride_dy, stride_h, stride_dh, stride_dx;
+  int32_t type, param_type; /* ll_dtype */
+} rmsnorm_grad_desc;
+
+ll_status rmsnorm_grad_workspace_size(const rmsnorm_grad_desc* desc, size_t* bytes);
+ll_status rmsnorm_grad_run(const rmsnorm_grad_desc* desc, const void* dy, const void* h, const void* gamma,
+                           const float* rstd, const void* dh, void* dx, void* dgamma, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/*
+ * Quantises x [N][D] (`type` LL_BF16, LL_F16 or LL_F32, row stride stride_x) in
+ * blocks of 128, as it lies and/or transposed, reading x once:
+ *   q [N][D] of q_type, rows stride_q apart, blocks along D (block 1: 128
+ *     consecutive columns of a row; block 128: 128 x 128), with
+ *     scale[n or n / 128][d / 128] at n'*stride_sn + d'*stride_sb;
+ *   qt [D][N], rows stride_qt apart, blocks along N (block 1: 128 consecutive
+ *     rows of a column of x), with scale_t[d or d / 128][n / 128] at
+ *     d'*stride_tn + n'*stride_tb.
+ * q with scale, or qt with scale_t, may be NULL (not wanted), not both pairs.
+ * gemm8_run takes rows at multiples of 16 bytes: round stride_q (stride_qt) up.
+ * N == 0 or D == 0: nothing is written.  One kernel, no workspace,
+ * graph-capturable.  Errors: LL_ERR_INVALID_ARG (null desc, x or both forms, one
+ * of a pair, negative size, strides below the rows or, for scales, below 1, block
+ * other than 1 or 128, misaligned pointer, an output overlapping x or another
+ * output), LL_ERR_UNSUPPORTED (types, N or D of 2^30 and more, strides that put a
+ * row 2^58 elements or more from the first, device), LL_ERR_NO_DEVICE, LL_ERR_HIP.
+ */
+typedef struct {
+  int64_t N, D;
+  int64_t stride_x, stride_q, stride_qt;
+  int64_t stride_sn, stride_sb, stride_tn, stride_tb;
+  int32_t type, q_type; /* ll_dtype */
+  int32_t block;        /* 1 or 128 */
+} quant8_desc;
+
+ll_status quant8_run(const quant8_desc* desc, const void* x, void* q, float* scale, void* qt, float* scale_t,
+                     void* stream);
+
+/*
+ * The product of quantised matrices, both with K contiguous (a linear layer's
+ * input rows and its weight as stored):
+ *   C[i][j] = sum over b of a_scale[i][b] * b_scale[j or j / 128][b] *
+ *             sum over k in block b of A[i][k] * B[j][k]
+ * A [M][K] of a_type (LL_E4M3 or LL_E5M2), block 1; B [N][K], LL_E4M3, b_block 1
+ * or 128; C [M][N] of c_type (LL_BF16, LL_F16 or LL_F32), rows stride_c apart.
+ * A block's sum is formed by the matrix unit, the scaled sums are added in fp32 in
+ * ascending order of b (in several runs of blocks, then joined in order, where K
+ * is split), and C is rounded once, to nearest even.  With an fp32 C the blocks'
+ * sums have fp32's precision.  With a 16-bit C they come from the 8-bit matrix
+ * instruction, twice as fast, which drops from the products of a group of eight
+ * what lies below 2^-13 of the largest: about 1.4e-5 of the result's norm, where
+ * C's rounding is 1.6e-3 (bf16) or 2e-4 (fp16).  Equal inputs
+ * give equal bits.  A layer's gradients are the same product: dX = dY W takes W
+ * quantised transposed, dW = dY^T X takes dY and X quantised transposed, b_block 1.
+ * A and B must be 16-byte aligned, stride_a and stride_b multiples of 16 (what
+ * lies between K and the stride is read but not used).  Workspace (256-byte
+ * aligned): gemm8_workspace_size, often 0; only the call that it is given to uses
+ * it.  M == 0 or N == 0: nothing is written.  K == 0: C is zero.  Kernels only,
+ * graph-capturable.
+ * Errors: LL_ERR_INVALID_ARG (null desc or pointer, negative size, stride below
+ * the row, misaligned operand, scale stride below 1, b_block, C overlapping an
+ * input or the workspace), LL_ERR_UNSUPPORTED (types, M, N of 2^26 and more, C of
+ * more than 2^22 tiles of 256 x 256, K of 2^22 and more, stride_a or stride_b of 2^22 and more, scale strides along rows
+ * of 2^20 and more, strides that put a row or block 2^58 elements or more from
+ * the first, device), LL_ERR_WORKSPACE, LL_ERR_NO_DEVICE, LL_ERR_HIP.
+ */
+typedef struct {
+  int64_t M, N, K;
+  int64_t stride_a, stride_b, stride_c;
+  int64_t stride_am, stride_ab; /* of a_scale: from row to row, from block to block */
+  int64_t stride_bn, stride_bb; /* of b_scale */
+  int32_t a_type, b_type, c_type;
+  int32_t b_block; /* 1 or 128 */
+} gemm8_desc;
+
+ll_status gemm8_workspace_size(const gemm8_desc* desc, size_t* bytes);
+/* One line: the kernel, its tile, how K is split. */
+ll_status gemm8_describe(const gemm8_desc* desc, char* buf, size_t len);
+ll_status gemm8_run(const gemm8_desc* desc, const void* A, const float* a_scale, const void* B, const float* b_scale,
+                    void* C, void* workspace, size_t ws_bytes, void* stream);
 
 /* Static, human-readable name of a status code ("LL_OK", ...). */
 const char* ll_status_string(ll_status s);

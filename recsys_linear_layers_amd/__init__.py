@@ -27,7 +27,7 @@ if not os.path.exists(LIB_PATH):
 _lib = ctypes.CDLL(LIB_PATH)
 
 LL_OK, LL_ERR_INVALID_ARG, LL_ERR_UNSUPPORTED, LL_ERR_WORKSPACE, LL_ERR_HIP, LL_ERR_NO_DEVICE = range(6)
-LL_BF16, LL_F32, LL_F16 = 0, 1, 2
+LL_BF16, LL_F32, LL_F16, LL_E4M3, LL_E5M2 = 0, 1, 2, 3, 4
 LL_EPI_BIAS, LL_EPI_RELU, LL_EPI_GELU, LL_EPI_SILU = 0x1, 0x10, 0x20, 0x30
 ACTIVATIONS = {None: 0, "relu": LL_EPI_RELU, "gelu": LL_EPI_GELU, "silu": LL_EPI_SILU}
 LL_FLAG_PACK_A = 0x1
@@ -97,6 +97,34 @@ class XentDesc(ctypes.Structure):
                 ("flags", ctypes.c_uint32)]
 
 
+class RmsnormDesc(ctypes.Structure):
+    _fields_ = [("N", _i64), ("D", _i64),
+                ("stride_x", _i64), ("stride_residual", _i64), ("stride_h", _i64), ("stride_y", _i64),
+                ("stride_sn", _i64), ("stride_sb", _i64),
+                ("type", ctypes.c_int32), ("param_type", ctypes.c_int32), ("y_type", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class RmsnormGradDesc(ctypes.Structure):
+    _fields_ = [("N", _i64), ("D", _i64),
+                ("stride_dy", _i64), ("stride_h", _i64), ("stride_dh", _i64), ("stride_dx", _i64),
+                ("type", ctypes.c_int32), ("param_type", ctypes.c_int32)]
+
+
+class Quant8Desc(ctypes.Structure):
+    _fields_ = [("N", _i64), ("D", _i64), ("stride_x", _i64), ("stride_q", _i64), ("stride_qt", _i64),
+                ("stride_sn", _i64), ("stride_sb", _i64), ("stride_tn", _i64), ("stride_tb", _i64),
+                ("type", ctypes.c_int32), ("q_type", ctypes.c_int32), ("block", ctypes.c_int32)]
+
+
+class Gemm8Desc(ctypes.Structure):
+    _fields_ = [("M", _i64), ("N", _i64), ("K", _i64),
+                ("stride_a", _i64), ("stride_b", _i64), ("stride_c", _i64),
+                ("stride_am", _i64), ("stride_ab", _i64), ("stride_bn", _i64), ("stride_bb", _i64),
+                ("a_type", ctypes.c_int32), ("b_type", ctypes.c_int32), ("c_type", ctypes.c_int32),
+                ("b_block", ctypes.c_int32)]
+
+
 _lib.ll_status_string.restype = ctypes.c_char_p
 _lib.ll_status_string.argtypes = [ctypes.c_int]
 _lib.ll_last_error.restype = ctypes.c_char_p
@@ -124,11 +152,20 @@ _lib.xent_plan_workspace_size.argtypes = [_vp, ctypes.POINTER(ctypes.c_size_t)]
 _lib.xent_plan_describe.argtypes = [_vp, ctypes.c_char_p, ctypes.c_size_t]
 _lib.xent_run.argtypes = [*[_vp] * 10, ctypes.c_size_t, _vp]
 _lib.xent_plan_destroy.argtypes = [_vp]
+_lib.rmsnorm_run.argtypes = [ctypes.POINTER(RmsnormDesc), *[_vp] * 8]
+_lib.rmsnorm_grad_workspace_size.argtypes = [ctypes.POINTER(RmsnormGradDesc), ctypes.POINTER(ctypes.c_size_t)]
+_lib.rmsnorm_grad_run.argtypes = [ctypes.POINTER(RmsnormGradDesc), *[_vp] * 8, ctypes.c_size_t, _vp]
+_lib.quant8_run.argtypes = [ctypes.POINTER(Quant8Desc), *[_vp] * 6]
+_lib.gemm8_workspace_size.argtypes = [ctypes.POINTER(Gemm8Desc), ctypes.POINTER(ctypes.c_size_t)]
+_lib.gemm8_describe.argtypes = [ctypes.POINTER(Gemm8Desc), ctypes.c_char_p, ctypes.c_size_t]
+_lib.gemm8_run.argtypes = [ctypes.POINTER(Gemm8Desc), *[_vp] * 6, ctypes.c_size_t, _vp]
 for _f in ("gemm_plan_create", "gemm_plan_workspace_size", "gemm_plan_describe", "gemm_run", "gemm_run_ex",
            "gemm_run_noalloc", "gemm_plan_destroy", "lincomp_workspace_size", "lincomp_run", "lincomp_ragged_run",
            "lincomp_run_ex", "lincomp_ragged_run_ex", "embed_run", "embed_grad_workspace_size", "embed_grad_run",
            "layernorm_run", "layernorm_grad_workspace_size", "layernorm_grad_run", "xent_plan_create",
-           "xent_plan_workspace_size", "xent_plan_describe", "xent_run", "xent_plan_destroy"):
+           "xent_plan_workspace_size", "xent_plan_describe", "xent_run", "xent_plan_destroy", "rmsnorm_run",
+           "rmsnorm_grad_workspace_size", "rmsnorm_grad_run", "quant8_run", "gemm8_workspace_size", "gemm8_describe",
+           "gemm8_run"):
     getattr(_lib, _f).restype = ctypes.c_int
 
 
@@ -278,6 +315,45 @@ def xent_run(plan: int, x: int, w: int, target: int, dloss: int | None, loss: in
 
 def xent_plan_destroy(plan: int) -> None:
     _check(_lib.xent_plan_destroy(plan), "xent_plan_destroy")
+
+
+def rmsnorm_run(desc: RmsnormDesc, x: int, residual: int | None, gamma: int | None, h: int | None, y: int,
+                scale: int | None, rstd: int | None, stream: int = 0) -> None:
+    _check(_lib.rmsnorm_run(ctypes.byref(desc), x, residual, gamma, h, y, scale, rstd, stream), "rmsnorm_run")
+
+
+def rmsnorm_grad_workspace_size(desc: RmsnormGradDesc) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.rmsnorm_grad_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "rmsnorm_grad_workspace_size")
+    return n.value
+
+
+def rmsnorm_grad_run(desc: RmsnormGradDesc, dy: int, h: int, gamma: int | None, rstd: int, dh: int | None, dx: int,
+                     dgamma: int | None, workspace: int, ws_bytes: int, stream: int = 0) -> None:
+    _check(_lib.rmsnorm_grad_run(ctypes.byref(desc), dy, h, gamma, rstd, dh, dx, dgamma, workspace, ws_bytes, stream),
+           "rmsnorm_grad_run")
+
+
+def quant8_run(desc: Quant8Desc, x: int, q: int | None, scale: int | None, qt: int | None, scale_t: int | None,
+               stream: int = 0) -> None:
+    _check(_lib.quant8_run(ctypes.byref(desc), x, q, scale, qt, scale_t, stream), "quant8_run")
+
+
+def gemm8_workspace_size(desc: Gemm8Desc) -> int:
+    n = ctypes.c_size_t()
+    _check(_lib.gemm8_workspace_size(ctypes.byref(desc), ctypes.byref(n)), "gemm8_workspace_size")
+    return n.value
+
+
+def gemm8_describe(desc: Gemm8Desc) -> str:
+    buf = ctypes.create_string_buffer(512)
+    _check(_lib.gemm8_describe(ctypes.byref(desc), buf, 512), "gemm8_describe")
+    return buf.value.decode()
+
+
+def gemm8_run(desc: Gemm8Desc, A: int, a_scale: int, B: int, b_scale: int, C: int, workspace: int, ws_bytes: int,
+              stream: int = 0) -> None:
+    _check(_lib.gemm8_run(ctypes.byref(desc), A, a_scale, B, b_scale, C, workspace, ws_bytes, stream), "gemm8_run")
 
 
 # ---------------------------------------------------------------------------
@@ -717,3 +793,198 @@ def vocab_xent_grad(x, w, target, dloss, ignore_index: int = -100, piece_bytes: 
             raise ValueError(f"{what} must have its operand's shape, and its type or fp32")
     loss, lse = _xent(x, w, target, dloss, dx, dw, ignore_index, piece_bytes)
     return loss, lse, dx, dw
+
+
+# ---------------------------------------------------------------------------
+# Linear layers in 8 bits.
+# ---------------------------------------------------------------------------
+
+def _code8(dtype) -> int:
+    torch = _torch()
+    if dtype == torch.float8_e4m3fn:
+        return LL_E4M3
+    if dtype == torch.float8_e5m2:
+        return LL_E5M2
+    raise TypeError(f"unsupported 8-bit dtype {dtype} (float8_e4m3fn or float8_e5m2)")
+
+
+def _blocks8(n: int) -> int:
+    return -(-n // 128)
+
+
+def _new8(rows: int, cols: int, dtype, device):
+    """[rows][cols] in rows of a multiple of 16 bytes, as gemm8 takes them."""
+    return _torch().empty((rows, -(-cols // 16) * 16), dtype=dtype, device=device)[:, :cols]
+
+
+def _new_scale8(rows: int, cols: int, squares: bool, device):
+    """Scales [rows][blocks of cols]; row scales with the rows of one block next to each other."""
+    torch = _torch()
+    if squares:
+        return torch.empty((_blocks8(rows), _blocks8(cols)), dtype=torch.float32, device=device)
+    return torch.empty((_blocks8(cols), rows), dtype=torch.float32, device=device).t()
+
+
+def _scale_strides(t, what: str):
+    """Strides of 2-D fp32 scales; along a dimension of one they do not matter."""
+    if t.dim() != 2 or t.dtype != _torch().float32:
+        raise ValueError(f"{what} must be 2-D and fp32")
+    return tuple(s if n > 1 else 1 for n, s in zip(t.shape, t.stride()))
+
+
+def _rmsnorm(x, gamma, residual, eps, y, y_code, scale, residual_out):
+    torch = _torch()
+    N, D = x.shape
+    ptype = _norm_params(x, gamma)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        h = None
+    else:
+        if residual.shape != x.shape or residual.dtype != x.dtype:
+            raise ValueError("residual must have x's shape and type")
+        h = x.new_empty((N, D)) if residual_out is None else residual_out
+        if h.shape != x.shape or h.dtype != x.dtype:
+            raise ValueError("residual_out must have x's shape and type")
+    _same_device(x, gamma, residual, h, y)
+    stream = _stream_of(x)
+    rstd = torch.empty(N, dtype=torch.float32, device=x.device)
+    code = _dtype_code(x.dtype)
+    sn, sb = (1, 1) if scale is None else _scale_strides(scale, "scale")
+    desc = RmsnormDesc(N, D, _rows(x, "x"), 0 if h is None else _rows(residual, "residual"),
+                       0 if h is None else _rows(h, "residual_out"), _rows(y, "out"), sn, sb, code,
+                       _dtype_code(ptype), code if y_code is None else y_code, eps)
+    rmsnorm_run(desc, x.data_ptr(), _ptr(residual), _ptr(gamma), _ptr(h), y.data_ptr(), _ptr(scale), rstd.data_ptr(),
+                stream)
+    return x if h is None else h, rstd
+
+
+def rmsnorm(x, gamma=None, residual=None, eps: float = 1e-6, out=None, residual_out=None):
+    """(y, h, rstd): h = x + residual (x itself without a residual), rounded to x's
+    type, and y = h * rstd * gamma with rstd = 1 / sqrt(mean(h^2) + eps) over the
+    rows of x [N][D] (bf16, fp16 or fp32, any row stride).  gamma [D] of x's type
+    or fp32, or None.  residual_out: where h goes, may be residual or x.  h and
+    rstd (fp32 [N]) are what rmsnorm_grad takes."""
+    if out is None:
+        out = x.new_empty(x.shape)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and type")
+    h, rstd = _rmsnorm(x, gamma, residual, eps, out, None, None, residual_out)
+    return out, h, rstd
+
+
+def rmsnorm8(x, gamma=None, residual=None, eps: float = 1e-6, dtype=None, residual_out=None):
+    """(q, scale, h, rstd): ``rmsnorm`` with y quantised in blocks of 128 of a row,
+    as gemm8's first operand: q [N][D] of dtype (float8_e4m3fn by default, or
+    float8_e5m2), scale fp32 [N][blocks]."""
+    dtype = dtype or _torch().float8_e4m3fn
+    code = _code8(dtype)
+    N, D = x.shape
+    q, scale = _new8(N, D, dtype, x.device), _new_scale8(N, D, False, x.device)
+    h, rstd = _rmsnorm(x, gamma, residual, eps, q, code, scale, residual_out)
+    return q, scale, h, rstd
+
+
+def rmsnorm_grad(dy, h, rstd, gamma=None, dh=None, out=None, param_grads: bool = True):
+    """(dx, dgamma) of ``rmsnorm`` from the h and rstd it returned.  dx is the
+    gradient of h, and so of x and of the residual alike; dh: the gradient that
+    reaches h by its other path, added to dx (out may be dh).  dgamma has gamma's
+    type (h's without gamma); param_grads=False: dx alone, dgamma None."""
+    torch = _torch()
+    N, D = h.shape
+    if tuple(dy.shape) != (N, D) or dy.dtype != h.dtype:
+        raise ValueError("dy must have h's shape and type")
+    if dh is not None and (tuple(dh.shape) != (N, D) or dh.dtype != h.dtype):
+        raise ValueError("dh must have h's shape and type")
+    if out is None:
+        out = h.new_empty((N, D))
+    if tuple(out.shape) != (N, D) or out.dtype != h.dtype:
+        raise ValueError("out must be [N][D] of h's type")
+    _vector(rstd, N, "rstd", (torch.float32,))
+    ptype = _norm_params(h, gamma)
+    _same_device(h, dy, rstd, gamma, dh, out)
+    stream = _stream_of(h)
+    dgamma = torch.empty(D, dtype=ptype, device=h.device) if param_grads else None
+    desc = RmsnormGradDesc(N, D, _rows(dy, "dy"), _rows(h, "h"), 0 if dh is None else _rows(dh, "dh"),
+                           _rows(out, "out"), _dtype_code(h.dtype), _dtype_code(ptype))
+    need = rmsnorm_grad_workspace_size(desc) if param_grads else 0
+    ws = _workspace(h.device, need)
+    rmsnorm_grad_run(desc, dy.data_ptr(), h.data_ptr(), _ptr(gamma), rstd.data_ptr(), _ptr(dh), out.data_ptr(),
+                     _ptr(dgamma), _ptr(ws), need, stream)
+    return out, dgamma
+
+
+def _quant8(x, squares, dtype, plain, transposed):
+    dtype = dtype or _torch().float8_e4m3fn
+    code = _code8(dtype)
+    N, D = x.shape
+    stream = _stream_of(x)
+    q = s = qt = st = None
+    qs, qts, sn, sb, tn, tb = 0, 0, 1, 1, 1, 1
+    if plain:
+        q, s = _new8(N, D, dtype, x.device), _new_scale8(N, D, squares, x.device)
+        qs, (sn, sb) = _rows(q, "q"), _scale_strides(s, "scale")
+    if transposed:
+        qt, st = _new8(D, N, dtype, x.device), _new_scale8(D, N, squares, x.device)
+        qts, (tn, tb) = _rows(qt, "qt"), _scale_strides(st, "scale")
+    desc = Quant8Desc(N, D, _rows(x, "x"), qs, qts, sn, sb, tn, tb, _dtype_code(x.dtype), code, 128 if squares else 1)
+    quant8_run(desc, x.data_ptr(), _ptr(q), _ptr(s), _ptr(qt), _ptr(st), stream)
+    return q, s, qt, st
+
+
+def quant8(x, squares: bool = False, transpose: bool = False, dtype=None):
+    """(q, scale): x [N][D] (bf16, fp16 or fp32, any row stride) in 8 bits (dtype:
+    float8_e4m3fn by default, or float8_e5m2) with an fp32 scale for each block: 128
+    consecutive values of a row (scale [N][blocks of D]: what gemm8 takes as its
+    first operand), or squares of 128 x 128 (scale [blocks of N][blocks of D]: a
+    weight).  transpose: x^T [D][N] instead, the blocks along N.  A value stands
+    for q * its block's scale."""
+    q, s, qt, st = _quant8(x, squares, dtype, not transpose, transpose)
+    return (qt, st) if transpose else (q, s)
+
+
+def quant8_pair(x, squares: bool = False, dtype=None):
+    """(q, scale, qt, scale_t): both forms of ``quant8``, x read once: for a weight,
+    the operands of the forward product and of the inputs' gradient; for
+    activations and their gradients, of their product and of the weight's gradient."""
+    return _quant8(x, squares, dtype, True, True)
+
+
+def gemm8_desc_for(a, a_scale, b, b_scale, out) -> Gemm8Desc:
+    M, K = a.shape
+    N, K2 = b.shape
+    if K2 != K or tuple(out.shape) != (M, N):
+        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, out {tuple(out.shape)}")
+    kb = _blocks8(K)
+    sa, sb = _scale_strides(a_scale, "a_scale"), _scale_strides(b_scale, "b_scale")
+    if tuple(a_scale.shape) != (M, kb):
+        raise ValueError(f"a_scale must be [{M}][{kb}]")
+    if tuple(b_scale.shape) not in ((N, kb), (_blocks8(N), kb)):
+        raise ValueError(f"b_scale must be [{_blocks8(N)}][{kb}] or [{N}][{kb}]")
+    return Gemm8Desc(M, N, K, _rows16(a, "a"), _rows16(b, "b"), _rows(out, "out"), *sa, *sb, _code8(a.dtype),
+                     _code8(b.dtype), _dtype_code(out.dtype), 128 if b_scale.shape[0] == _blocks8(N) else 1)
+
+
+def _rows16(t, what: str):
+    """_rows of an operand of gemm8; the stride of a single row, or of empty ones, does not matter."""
+    s = _rows(t, what)
+    return s if t.shape[0] > 1 and t.shape[1] > 0 else -(-t.shape[1] // 16) * 16
+
+
+def gemm8(a, a_scale, b, b_scale, out=None, out_dtype=None):
+    """C = A B^T of two quantised matrices, a [M][K] (float8_e4m3fn or float8_e5m2)
+    with a_scale [M][blocks of K], and b [N][K] (float8_e4m3fn), a linear layer's
+    weight as stored, with b_scale [blocks of N][blocks of K] (squares) or
+    [N][blocks of K] (rows), as quant8 and rmsnorm8 give them; rows at multiples of
+    16 bytes.  C is bf16 (default), fp16 or fp32."""
+    torch = _torch()
+    if out is None:
+        out = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype or torch.bfloat16, device=a.device)
+    desc = gemm8_desc_for(a, a_scale, b, b_scale, out)
+    _same_device(a, a_scale, b, b_scale, out)
+    stream = _stream_of(a)
+    need = gemm8_workspace_size(desc)
+    ws = _workspace(a.device, need)
+    gemm8_run(desc, a.data_ptr(), a_scale.data_ptr(), b.data_ptr(), b_scale.data_ptr(), out.data_ptr(), _ptr(ws), need,
+              stream)
+    return out

@@ -43,10 +43,11 @@ def _run(cmd, verbose):
 # Units built with the compiler's default machine scheduler instead: the
 # linear-compression kernels are bound by HBM, not by their instruction
 # schedule, and iterative-ilp spilled their fused-epilogue instantiations
-# (bias + GELU 34 registers against 10).  The embedding, layer norm and
-# cross-entropy row kernels are bound by HBM too (xent_narrow.hip by the vector
+# (bias + GELU 34 registers against 10).  The embedding, norm,
+# quantisation and cross-entropy row kernels are bound by HBM too (xent_narrow.hip by the vector
 # ALU: the other schedule makes no difference there).
-DEFAULT_SCHED = {"lincomp.hip", "embed.hip", "layernorm.hip", "xent.hip", "xent_few.hip", "xent_narrow.hip"}
+DEFAULT_SCHED = {"lincomp.hip", "embed.hip", "layernorm.hip", "xent.hip", "xent_few.hip", "xent_narrow.hip",
+                 "rmsnorm.hip", "quant8.hip", "gemm8_few.hip"}
 
 
 def _flags(src):

@@ -1,0 +1,48 @@
+// The product of 8-bit matrices with a scale per block of 128 along K:
+// arguments, the choice of kernel, and launches (gemm8_tile.hpp, gemm8_few.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/linlayers.h"
+
+namespace ll {
+
+struct Gemm8Args {
+  const uint8_t* a;
+  const uint8_t* b;
+  const float* sa;
+  const float* sb;
+  void* c;          // c_type, or null where partial is set
+  float* partial;   // [splits][M][N] of a split K, or null
+  int64_t lda, ldb, ldc;
+  int64_t sam, sab, sbn, sbb;  // strides of the scales: from row to row, from block to block
+  int32_t M, N, K;
+  int32_t c_type;
+  int32_t blocks;   // of 128 along K
+  int32_t splits, per_split;  // K is split into runs of per_split blocks
+  int32_t tiles_m, tiles_n, total;
+  int32_t vec_c;    // rows of C (or the partials) take 16-byte stores
+};
+
+enum Gemm8Kind { kG8Few16, kG8Few32, kG8Few64, kG8Tile128, kG8Tile256, kG8Kinds };
+
+struct Gemm8Plan {
+  int kind;
+  int bm, bn;
+  int tiles_m, tiles_n, splits, per_split;
+  size_t partial_bytes;
+};
+
+// Sizes alone decide (no device is asked).
+Gemm8Plan gemm8_plan(const gemm8_desc& d);
+const char* gemm8_kind_name(int kind);
+// a_e5m2: A holds LL_E5M2; rows: B's scales are per row (b_block 1).
+hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s);
+
+hipError_t launch_gemm8_tile128(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile256(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_few(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s);
+
+}  // namespace ll

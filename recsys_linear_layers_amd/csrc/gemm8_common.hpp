@@ -1,0 +1,146 @@
+// What the kernels of the 8-bit product share: the matrix instruction, loads
+// into LDS, and stores of C.
+#pragma once
+
+#include "gemm8.hpp"
+#include "quant8.hpp"
+
+namespace ll {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ i32x8 frag8(i32x4 lo, i32x4 hi) {
+  return i32x8{lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+}
+
+// A block's sums: D[i][j] = sum over 128 k of W[i][k] X[j][k], from fragments of
+// which lane l holds row l % 16 and 32 of the 128 k (any, as long as both
+// operands take the same); lane l gets D[4 (l / 16) + r][l % 16].  W is LL_E4M3,
+// X LL_E5M2 if E5M2.
+//
+// The 8-bit matrix instructions align the eight products of a group to the
+// largest and drop what lies below 2^-13 of its power of two (measured: beside
+// 448 * 448 a product of 8 is kept, one of 4 lost): up to 7 * 2^-13 of the
+// group's largest product, and on normally distributed operands 1.4e-5 of the
+// result's norm.  A 16-bit C is rounded to 2^-8 or 2^-11 of itself and takes them.
+// A C in fp32 (EXACT) has its operands widened to bf16, which holds every 8-bit
+// value, and multiplied at half the rate, where the same sums are off by 8e-8.
+template <bool E5M2, bool EXACT>
+struct Block8;
+
+template <bool E5M2>
+struct Block8<E5M2, false> {
+  typedef i32x8 W;
+  typedef i32x8 X;
+  static __device__ __forceinline__ W w(i32x8 v) { return v; }
+  static __device__ __forceinline__ X x(i32x8 v) { return v; }
+  // with no scale operands the instruction's own (per-32) scales are 1
+  static __device__ __forceinline__ f32x4 product(const W& w, const X& x) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.f, 0.f, 0.f, 0.f}, 0, E5M2 ? 1 : 0, 0, 0, 0,
+                                                            0);
+  }
+};
+
+template <bool E5M2>
+struct Block8<E5M2, true> {
+  struct Wide {
+    bf16x8 v[4];
+  };
+  typedef Wide W;
+  typedef Wide X;
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  template <bool B5>
+  static __device__ __forceinline__ bf16x2 pair(int word, bool high) {
+    if constexpr (B5)
+      return high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)word, 1.f, true)
+                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_bf8((uint32_t)word, 1.f, false);
+    else
+      return high ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)word, 1.f, true)
+                  : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)word, 1.f, false);
+  }
+  template <bool B5>
+  static __device__ __forceinline__ Wide widen(i32x8 v) {
+    Wide o;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const bf16x2 lo = pair<B5>(v[i], false), hi = pair<B5>(v[i], true);
+      o.v[i >> 1][4 * (i & 1)] = lo[0];
+      o.v[i >> 1][4 * (i & 1) + 1] = lo[1];
+      o.v[i >> 1][4 * (i & 1) + 2] = hi[0];
+      o.v[i >> 1][4 * (i & 1) + 3] = hi[1];
+    }
+    return o;
+  }
+  static __device__ __forceinline__ W w(i32x8 v) { return widen<false>(v); }
+  static __device__ __forceinline__ X x(i32x8 v) { return widen<E5M2>(v); }
+  static __device__ __forceinline__ f32x4 product(const W& w, const X& x) {
+    f32x4 d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.v[h], x.v[h], d, 0, 0, 0);
+    return d;
+  }
+};
+
+// dma16 for one word per lane: lane l's 4 bytes land at LDS byte address m0 + 4 l.
+__device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
+  asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds"
+               :
+               : "v"(voff), "s"(rsrc), "{m0}"(lds_addr)
+               : "memory");
+}
+
+// num_records of an 8-bit operand from `origin` on: whole pieces of 16 bytes, so
+// that the last row's last piece is read whole (it never leaves the 16 bytes it
+// starts in, and rows start at multiples of 16).
+__device__ __forceinline__ uint32_t records8(int64_t bytes) {
+  if (bytes <= 0) return 0u;
+  const int64_t up = (bytes + 15) & ~15ll;
+  return up > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)up;
+}
+
+// CNT consecutive columns of row m of C from column n on, or of the partials.
+template <int CNT>
+__device__ __forceinline__ void store_c8(const Gemm8Args& p, int split, int m, int n, const float (&v)[CNT]) {
+  if (m >= p.M || n >= p.N) return;
+  const bool whole = n + CNT <= p.N && p.vec_c;
+  if (p.partial || p.c_type == LL_F32) {
+    float* dst = p.partial ? p.partial + ((int64_t)split * p.M + m) * p.N + n : (float*)p.c + (int64_t)m * p.ldc + n;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < CNT; i += 4) *(f32x4*)(dst + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < CNT; ++i)
+        if (n + i < p.N) dst[i] = v[i];
+    }
+    return;
+  }
+  uint16_t* dst = (uint16_t*)p.c + (int64_t)m * p.ldc + n;
+  uint32_t w[CNT / 2];
+  if (p.c_type == LL_BF16) {
+    Chunk<LL_BF16, CNT> c;
+#pragma unroll
+    for (int i = 0; i < CNT; i += 2) c.put2(i, v[i], v[i + 1]);
+    __builtin_memcpy(w, &c, sizeof w);
+  } else {
+    Chunk<LL_F16, CNT> c;
+#pragma unroll
+    for (int i = 0; i < CNT; i += 2) c.put2(i, v[i], v[i + 1]);
+    __builtin_memcpy(w, &c, sizeof w);
+  }
+  if (whole) {
+    if constexpr (CNT % 8 == 0) {
+#pragma unroll
+      for (int i = 0; i < CNT / 2; i += 4)
+        *(i32x4*)(dst + 2 * i) = i32x4{(int)w[i], (int)w[i + 1], (int)w[i + 2], (int)w[i + 3]};
+    } else {
+      __builtin_memcpy(__builtin_assume_aligned(dst, 8), w, sizeof w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CNT; ++i)
+      if (n + i < p.N) dst[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+
+}  // namespace ll
