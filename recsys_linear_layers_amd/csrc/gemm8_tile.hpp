@@ -123,58 +123,111 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   const int b_off = Cfg::A_BYTES + brow * 128 + ((g ^ swz8_b<FN>(brow)) << 4);         // + 512 f
   const int sb_row = (n0 + wn * Cfg::TN) / 128;                                         // block row of B, unless ROWS
 
+  const float __attribute__((address_space(4))) * sbs =
+      (const float __attribute__((address_space(4)))*)(p.sb + (int64_t)min(sb_row, (p.N - 1) / 128) * p.sbn);
+
   f32x4 acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int f = 0; f < FN; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  if (kb0 < kb1) issue(kb0, 0);
-  for (int kb = kb0; kb < kb1; ++kb) {
-    const int slot = (kb - kb0) & 1;
-    float sb = 0.f;
-    if constexpr (!ROWS) {
-      // columns past N have no block; their sums are not stored
-      if (sb_row * 128 < p.N) sb = p.sb[(int64_t)sb_row * p.sbn + (int64_t)kb * p.sbb];
+  // Clears the bytes past K of the piece that K ends in.
+  auto clear_tail = [&](int slot) {
+    const int c = (p.K & 127) >> 4;
+    for (int row = threadIdx.x; row < Cfg::BM + Cfg::BN; row += Cfg::THREADS) {
+      const bool of_a = row < Cfg::BM;
+      const int r = of_a ? row : row - Cfg::BM;
+      char* q = lds + slot * Cfg::SLOT + row * 128 + ((c ^ (of_a ? swz8_a(r) : swz8_b<FN>(r))) << 4);
+      for (int i = p.K & 15; i < 16; ++i) q[i] = 0;
     }
+    __syncthreads();
+  };
+  // The rows of the slot of step kb are there, for every wave.
+  auto arrive = [&](int kb, int slot) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier();
-    if (kb + 1 < kb1) issue(kb + 1, slot ^ 1);
-    const char* st = lds + slot * Cfg::SLOT;
-    if (kb * 128 + 128 > p.K && (p.K & 15)) {
-      // clear the bytes past K of the piece that K ends in
-      const int c = (p.K & 127) >> 4;
-      for (int row = threadIdx.x; row < Cfg::BM + Cfg::BN; row += Cfg::THREADS) {
-        const bool of_a = row < Cfg::BM;
-        const int r = of_a ? row : row - Cfg::BM;
-        char* q = (char*)st + row * 128 + ((c ^ (of_a ? swz8_a(r) : swz8_b<FN>(r))) << 4);
-        for (int i = p.K & 15; i < 16; ++i) q[i] = 0;
-      }
-      __syncthreads();
-    }
-    const float* sc = (const float*)(lds + SC + slot * (Cfg::BM + Cfg::BN) * 4);
-    typename Block::W w[FN];
+    if (kb * 128 + 128 > p.K && (p.K & 15)) clear_tail(slot);
+  };
+  auto read_x = [&](const char* st, int i) {
+    return frag8(*(const i32x4*)(st + a_off + 2048 * i), *(const i32x4*)(st + (a_off ^ 64) + 2048 * i));
+  };
+  auto read_w = [&](const char* st, int f) {
+    return frag8(*(const i32x4*)(st + b_off + 512 * f), *(const i32x4*)(st + (b_off ^ 64) + 512 * f));
+  };
+  const int sa_off = SC + (wm * Cfg::TM + row16) * 4;                              // + 64 i
+  const int sb_off = SC + (Cfg::BM + wn * Cfg::TN + 4 * FN * g) * 4;               // + 16 f
+  constexpr int SCALES = (Cfg::BM + Cfg::BN) * 4;
+
+  // A step is FM x FN products, in the order below.  A product's fmas follow LAG
+  // products later, when its result is there; the fragments of A are read one
+  // row of products ahead, those of the next step during the last row, after the
+  // barrier that says that its rows have landed and that nobody reads this step's.
+  constexpr int T = FM * FN, LAG = EXACT ? 1 : 2, ND = EXACT ? 2 : 4;
+  static_assert(T % ND == 0 && LAG < ND && LAG <= FN && FM % 2 == 0, "ring of results");
+  f32x4 d[ND];
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
-      w[f] = Block::w(frag8(*(const i32x4*)(st + b_off + 512 * f), *(const i32x4*)(st + (b_off ^ 64) + 512 * f)));
+  for (int i = 0; i < ND; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  if (kb0 < kb1) {
+    issue(kb0, 0);
+    arrive(kb0, 0);
+    if (kb0 + 1 < kb1) issue(kb0 + 1, 1);
+    i32x8 wr[FN], xr[2];
     f32x4 sbv[FN];
-    if constexpr (ROWS) {
+    typename Block::W w[FN];
+    float s_last = 0.f, sa_next, sb = 0.f;
+    if constexpr (!ROWS) sb = sbs[(int64_t)kb0 * p.sbb];
+    xr[0] = read_x(lds, 0);
+    sa_next = *(const float*)(lds + sa_off);
 #pragma unroll
-      for (int f = 0; f < FN; ++f) sbv[f] = *(const f32x4*)(sc + Cfg::BM + wn * Cfg::TN + 4 * FN * g + 4 * f);
-    }
+    for (int f = 0; f < FN; ++f) wr[f] = read_w(lds, f);
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const typename Block::X x =
-          Block::x(frag8(*(const i32x4*)(st + a_off + 2048 * i), *(const i32x4*)(st + (a_off ^ 64) + 2048 * i)));
-      const float sa = sc[wm * Cfg::TM + 16 * i + row16];
-      const float s = ROWS ? sa : sa * sb;
+    for (int f = 0; f < FN; ++f) sbv[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto add = [&](int t, float s) {
 #pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const f32x4 d = Block::product(w[f], x);
+      for (int r = 0; r < 4; ++r)
+        acc[t / FN][t % FN][r] = fmaf(d[t % ND][r], ROWS ? s * sbv[t % FN][r] : s, acc[t / FN][t % FN][r]);
+      asm volatile("" : "+v"(acc[t / FN][t % FN]));  // here, not where the compiler would sink them to
+    };
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const int slot = (kb - kb0) & 1;
+      const char* st = lds + slot * Cfg::SLOT;
+      const char* next = lds + (slot ^ 1) * Cfg::SLOT;
+      const char* sc = lds + slot * SCALES;
+      float sb_next = 0.f;
+      if constexpr (!ROWS) sb_next = sbs[(int64_t)min(kb + 1, kb1 - 1) * p.sbb];
+      float s = 0.f;
+      typename Block::X x;
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][f][r] = fmaf(d[r], ROWS ? s * sbv[f][r] : s, acc[i][f][r]);
+      for (int t = 0; t < T; ++t) {
+        const int i = t / FN, f = t % FN;
+        if (f == 0) {
+          if (i == FM - 1 && kb + 1 < kb1) {
+            arrive(kb + 1, slot ^ 1);
+            if (kb + 2 < kb1) issue(kb + 2, slot);
+          }
+          x = Block::x(xr[i & 1]);
+        }
+        if (i == 0) w[f] = Block::w(wr[f]);
+        d[t % ND] = Block::product(w[f], x);
+        if (t < LAG) add(T + t - LAG, s_last);
+        else add(t - LAG, s);
+        if (f == LAG - 1) s = ROWS ? sa_next : sa_next * sb;  // of this row of products from here on
+        if (t == LAG - 1 && ROWS) {
+#pragma unroll
+          for (int q = 0; q < FN; ++q) sbv[q] = *(const f32x4*)(sc + sb_off + 16 * q);
+        }
+        if (f == 0) xr[(i + 1) & 1] = i + 1 < FM ? read_x(st, i + 1) : read_x(next, 0);
+        if (f == LAG)
+          sa_next = *(const float*)(i + 1 < FM ? sc + sa_off + 64 * (i + 1) : lds + (slot ^ 1) * SCALES + sa_off);
+        if (i == FM - 1) wr[f] = read_w(next, f);
+        __builtin_amdgcn_sched_barrier(0);
       }
+      s_last = s;
+      sb = sb_next;
     }
+#pragma unroll
+    for (int t = T - LAG; t < T; ++t) add(t, s_last);
   }
 
 #pragma unroll
