@@ -27,7 +27,8 @@ struct G8Cfg {
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, SLOT = A_BYTES + B_BYTES;
   static constexpr int QA = BM / 8 / WAVES, QB = BN / 8 / WAVES;  // 1-KB loads of a wave
   static constexpr int SLOTS = 2;
-  static constexpr int LDS = SLOTS * (SLOT + (BM + BN) * 4);
+  static constexpr int SCALES = (BM + BN) * 4;  // of a step; three steps' worth, as those of one are read until its end
+  static constexpr int LDS = SLOTS * SLOT + 3 * SCALES;
   static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && TN <= 128 && 128 % TN == 0, "tile");
 };
 
@@ -86,7 +87,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
 
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32((const char LL_LDS*)lds));
   constexpr uint32_t SC = Cfg::SLOTS * Cfg::SLOT;  // scales: per slot, A's then B's
-  auto issue = [&](int kb, int slot) {
+  auto issue = [&](int kb, int slot, int sslot) {
     const uint32_t dst = lds0 + slot * Cfg::SLOT + wave * 1024;
     const int k0 = kb * 128;
     if (k0 + 128 <= p.K) {
@@ -110,7 +111,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
         dma16s(rb, dst + Cfg::A_BYTES + i * Cfg::WAVES * 1024, in ? vb[i] : kOOB, (uint32_t)k0);
       }
     }
-    const uint32_t sdst = lds0 + SC + slot * (Cfg::BM + Cfg::BN) * 4 + wave * 256;
+    const uint32_t sdst = lds0 + SC + sslot * Cfg::SCALES + wave * 256;
     if (wave < SA_WAVES) dma4(make_rsrc(sa_base + (int64_t)kb * p.sab, 0x7FFFFFF0u), sdst, vsa);
     if (ROWS && wave < SB_WAVES) dma4(make_rsrc(sb_base + (int64_t)kb * p.sbb, 0x7FFFFFF0u), sdst + Cfg::BM * 4, vsb);
   };
@@ -157,23 +158,23 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   };
   const int sa_off = SC + (wm * Cfg::TM + row16) * 4;                              // + 64 i
   const int sb_off = SC + (Cfg::BM + wn * Cfg::TN + 4 * FN * g) * 4;               // + 16 f
-  constexpr int SCALES = (Cfg::BM + Cfg::BN) * 4;
 
   // A step is FM x FN products, in the order below.  A product's fmas follow LAG
   // products later, when its result is there; the fragments of A are read one
   // row of products ahead, those of the next step during the last row, after the
   // barrier that says that its rows have landed and that nobody reads this step's.
+  constexpr bool FEW_SB = EXACT;
   constexpr int T = FM * FN, LAG = EXACT ? 1 : 2, ND = EXACT ? 2 : 4;
   static_assert(T % ND == 0 && LAG < ND && LAG <= FN && FM % 2 == 0, "ring of results");
   f32x4 d[ND];
 #pragma unroll
   for (int i = 0; i < ND; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (kb0 < kb1) {
-    issue(kb0, 0);
+    issue(kb0, 0, 0);
     arrive(kb0, 0);
-    if (kb0 + 1 < kb1) issue(kb0 + 1, 1);
+    if (kb0 + 1 < kb1) issue(kb0 + 1, 1, 1);
     i32x8 wr[FN], xr[2];
-    f32x4 sbv[FN];
+    f32x4 sbv[FEW_SB ? 1 : FN];  // ROWS: of all f, or (EXACT, whose operands take the registers) of the last product
     typename Block::W w[FN];
     float s_last = 0.f, sa_next, sb = 0.f;
     if constexpr (!ROWS) sb = sbs[(int64_t)kb0 * p.sbb];
@@ -182,18 +183,20 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
 #pragma unroll
     for (int f = 0; f < FN; ++f) wr[f] = read_w(lds, f);
 #pragma unroll
-    for (int f = 0; f < FN; ++f) sbv[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int f = 0; f < (FEW_SB ? 1 : FN); ++f) sbv[f] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto add = [&](int t, float s) {
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        acc[t / FN][t % FN][r] = fmaf(d[t % ND][r], ROWS ? s * sbv[t % FN][r] : s, acc[t / FN][t % FN][r]);
+        acc[t / FN][t % FN][r] =
+            fmaf(d[t % ND][r], ROWS ? s * sbv[FEW_SB ? 0 : t % FN][r] : s, acc[t / FN][t % FN][r]);
       asm volatile("" : "+v"(acc[t / FN][t % FN]));  // here, not where the compiler would sink them to
     };
+    int s0 = 0, s1 = 1, s2 = 2;  // scale slots of this step and of the next two
     for (int kb = kb0; kb < kb1; ++kb) {
       const int slot = (kb - kb0) & 1;
       const char* st = lds + slot * Cfg::SLOT;
       const char* next = lds + (slot ^ 1) * Cfg::SLOT;
-      const char* sc = lds + slot * SCALES;
+      const char* sc = lds + s0 * Cfg::SCALES;
       float sb_next = 0.f;
       if constexpr (!ROWS) sb_next = sbs[(int64_t)min(kb + 1, kb1 - 1) * p.sbb];
       float s = 0.f;
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
         if (f == 0) {
           if (i == FM - 1 && kb + 1 < kb1) {
             arrive(kb + 1, slot ^ 1);
-            if (kb + 2 < kb1) issue(kb + 2, slot);
+            if (kb + 2 < kb1) issue(kb + 2, slot, s2);
           }
           x = Block::x(xr[i & 1]);
         }
@@ -213,18 +216,21 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
         if (t < LAG) add(T + t - LAG, s_last);
         else add(t - LAG, s);
         if (f == LAG - 1) s = ROWS ? sa_next : sa_next * sb;  // of this row of products from here on
-        if (t == LAG - 1 && ROWS) {
+        if (ROWS && FEW_SB) sbv[0] = *(const f32x4*)(sc + sb_off + 16 * f);
+        if (ROWS && !FEW_SB && t == LAG - 1) {
 #pragma unroll
           for (int q = 0; q < FN; ++q) sbv[q] = *(const f32x4*)(sc + sb_off + 16 * q);
         }
         if (f == 0) xr[(i + 1) & 1] = i + 1 < FM ? read_x(st, i + 1) : read_x(next, 0);
         if (f == LAG)
-          sa_next = *(const float*)(i + 1 < FM ? sc + sa_off + 64 * (i + 1) : lds + (slot ^ 1) * SCALES + sa_off);
+          sa_next = *(const float*)(i + 1 < FM ? sc + sa_off + 64 * (i + 1) : lds + s1 * Cfg::SCALES + sa_off);
         if (i == FM - 1) wr[f] = read_w(next, f);
         __builtin_amdgcn_sched_barrier(0);
       }
       s_last = s;
       sb = sb_next;
+      const int first = s0;
+      s0 = s1, s1 = s2, s2 = first;
     }
 #pragma unroll
     for (int t = T - LAG; t < T; ++t) add(t, s_last);

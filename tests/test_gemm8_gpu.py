@@ -69,8 +69,9 @@ def test_against_64_bits(M, N, K, squares):
 
 
 @pytest.mark.parametrize("kind,M,N,K", [("TILE128", 3, 100, 300), ("TILE128", 300, 200, 700), ("TILE256", 5, 70, 90),
-                                        ("TILE256", 300, 520, 1000), ("TILE256", 513, 257, 4100), ("FEW64", 9, 333, 1000),
-                                        ("FEW32", 30, 100, 130), ("FEW64", 64, 64, 64)])
+                                        ("TILE256", 300, 520, 1000), ("TILE256", 513, 257, 4100), ("TILE192", 7, 65, 90),
+                                        ("TILE192", 400, 520, 1000), ("TILE192", 193, 257, 4100),
+                                        ("FEW64", 9, 333, 1000), ("FEW32", 30, 100, 130), ("FEW64", 64, 64, 64)])
 @pytest.mark.parametrize("splits", [1, 3])
 def test_every_kernel_and_split(monkeypatch, kind, M, N, K, splits):
     """Kernels and splits that the sizes alone would not pick."""
@@ -81,11 +82,11 @@ def test_every_kernel_and_split(monkeypatch, kind, M, N, K, splits):
     for squares in (True, False):
         a, sa = _operand(M, K, 1, t["e4m3"], False)
         b, sb = _operand(N, K, 3, t["e4m3"], squares)
-        out = a.new_empty((M, N), dtype=t["f32"])
-        assert f"kernel={kind} " in ll.gemm8_describe(ll.gemm8_desc_for(a, sa, b, sb, out))
         ref, S = _reference(a, sa, b, sb, squares)
-        _check(ll.gemm8(a, sa, b, sb, out=out), ref, S, K)
-        _check(ll.gemm8(a, sa, b, sb), ref, S, K)
+        for c in {"TILE256": ("bf16",), "TILE192": ("f32",)}.get(kind, ("bf16", "f32")):
+            out = a.new_empty((M, N), dtype=t[c])
+            assert f"kernel={kind} " in ll.gemm8_describe(ll.gemm8_desc_for(a, sa, b, sb, out))
+            _check(ll.gemm8(a, sa, b, sb, out=out), ref, S, K)
 
 
 def test_integers_are_exact():
