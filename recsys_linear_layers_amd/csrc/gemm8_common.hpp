@@ -89,15 +89,6 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t vof
                : "memory");
 }
 
-// num_records of an 8-bit operand from `origin` on: whole pieces of 16 bytes, so
-// that the last row's last piece is read whole (it never leaves the 16 bytes it
-// starts in, and rows start at multiples of 16).
-__device__ __forceinline__ uint32_t records8(int64_t bytes) {
-  if (bytes <= 0) return 0u;
-  const int64_t up = (bytes + 15) & ~15ll;
-  return up > 0x7FFFFFF0ll ? 0x7FFFFFF0u : (uint32_t)up;
-}
-
 // CNT consecutive columns of row m of C from column n on, or of the partials.
 template <int CNT>
 __device__ __forceinline__ void store_c8(const Gemm8Args& p, int split, int m, int n, const float (&v)[CNT]) {

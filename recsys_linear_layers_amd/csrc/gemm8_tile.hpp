@@ -27,21 +27,21 @@ struct G8Cfg {
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, SLOT = A_BYTES + B_BYTES;
   static constexpr int QA = BM / 8 / WAVES, QB = BN / 8 / WAVES;  // 1-KB loads of a wave
   static constexpr int SLOTS = 2;
-  static constexpr int SCALES = (BM + BN) * 4;  // of a step; three steps' worth, as those of one are read until its end
+  static constexpr int SCALES = WAVES * 256;  // of a step; three steps' worth, as those of one are read until its end
   static constexpr int LDS = SLOTS * SLOT + 3 * SCALES;
   static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && TN <= 128 && 128 % TN == 0, "tile");
+  static_assert(BM % 64 == 0 && BN % 64 == 0 && BM + BN <= WAVES * 64, "scales: 64 rows a wave");
 };
 
-// Chunk c of A's row r sits at c ^ swz8_a(r), of B's at c ^ swz8_b(r).  One pass
-// of a 16-byte LDS read serves lanes 8p..8p+7 and 32+8p..32+8p+7: 8 rows, each at
-// chunks x and x ^ 2, a row's 128 bytes being half of the banks (which half goes
-// by the row's parity).  The four rows of each parity need one value from each
-// of {0, 2}, {1, 3}, {4, 6}, {5, 7}.  A's eight rows follow one another; B's are
-// 4 and 4, 4 FN rows apart.
-__device__ __forceinline__ int swz8_a(int r) { return ((r >> 1) & 1) | (r & 4); }
+// Chunk c of A's row r sits at c ^ swz8_a(r), of B's at c ^ swz8_b(r).  A row's
+// 128 bytes are half of the banks (which half goes by the row's parity), and a
+// pass of a 16-byte LDS read serves 16 lanes, the 16 rows of a fragment at one
+// chunk: the eight rows of each parity need eight different values.  A's rows
+// follow one another; B's are four times four, 4 FN rows apart.
+__device__ __forceinline__ int swz8_a(int r) { return ((r >> 1) & 1) | (((r >> 3) & 1) << 1) | (r & 4); }
 template <int FN>
 __device__ __forceinline__ int swz8_b(int r) {
-  return ((r >> 1) & 1) | (((r / (4 * FN)) & 1) << 2);
+  return ((r >> 1) & 1) | (((r / (8 * FN)) & 1) << 1) | (((r / (4 * FN)) & 1) << 2);
 }
 
 template <class Cfg, bool E5M2, bool ROWS, bool EXACT>
@@ -63,57 +63,52 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
   const int kb0 = split * p.per_split, kb1 = min(p.blocks, kb0 + p.per_split);
 
-  // loads: instruction q takes rows 8q .. 8q+7 of the tile, lane l row l / 8, position l % 8
-  uint32_t va[Cfg::QA], vb[Cfg::QB];
-  const i32x4 ra = make_rsrc(p.a + (int64_t)m0 * p.lda, records8((int64_t)(p.M - m0 - 1) * p.lda + p.K));
-  const i32x4 rb = make_rsrc(p.b + (int64_t)n0 * p.ldb, records8((int64_t)(p.N - n0 - 1) * p.ldb + p.K));
-#pragma unroll
-  for (int i = 0; i < Cfg::QA; ++i) {
-    const int row = (wave + i * Cfg::WAVES) * 8 + (lane >> 3);
-    va[i] = m0 + row < p.M ? (uint32_t)(row * (int)p.lda + (((lane & 7) ^ swz8_a(row)) << 4)) : kOOB;
-  }
-#pragma unroll
-  for (int i = 0; i < Cfg::QB; ++i) {
-    const int row = (wave + i * Cfg::WAVES) * 8 + (lane >> 3);
-    vb[i] = n0 + row < p.N ? (uint32_t)(row * (int)p.ldb + (((lane & 7) ^ swz8_b<FN>(row)) << 4)) : kOOB;
-  }
-  // scales: a wave takes 64 rows of A's (and, with ROWS, B's)
-  constexpr int SA_WAVES = Cfg::BM / 64, SB_WAVES = ROWS ? Cfg::BN / 64 : 0;
-  static_assert(SA_WAVES <= Cfg::WAVES && SB_WAVES <= Cfg::WAVES, "scale loads");
-  const uint32_t vsa = m0 + wave * 64 + lane < p.M ? (uint32_t)((wave * 64 + lane) * (int)p.sam) * 4u : kOOB;
-  const uint32_t vsb = n0 + wave * 64 + lane < p.N ? (uint32_t)((wave * 64 + lane) * (int)p.sbn) * 4u : kOOB;
-  const float* sa_base = p.sa + (int64_t)m0 * p.sam;
-  const float* sb_base = ROWS ? p.sb + (int64_t)n0 * p.sbn : nullptr;
+  // loads: instruction q = wave + i WAVES takes rows 8q .. 8q+7 of the tile, lane
+  // l row l / 8 of them, position l % 8.  The offset of a lane outside the
+  // matrices is beyond every range, which reads zeros; the descriptors' own range
+  // is not used.
+  const int lrow = wave * 8 + (lane >> 3);
+  auto chunk_b = [&](int i) { return ((lane & 7) ^ swz8_b<FN>(lrow + i * Cfg::WAVES * 8)) << 4; };
+  const int la = ((lane & 7) ^ swz8_a(lrow)) << 4;
+  static_assert(Cfg::WAVES * 8 % 16 == 0, "A's rows of a lane have one permutation");
+  const uint32_t va = (uint32_t)((lane >> 3) * (int)p.lda + la);
+  const i32x4 rsrc_a = make_rsrc(p.a + ((int64_t)m0 + wave * 8) * p.lda, 0x7FFFFFF0u);
+  const i32x4 rsrc_b = make_rsrc(p.b + ((int64_t)n0 + wave * 8) * p.ldb, 0x7FFFFFF0u);
+  const int a_step = Cfg::WAVES * 8 * (int)p.lda, b_step = Cfg::WAVES * 8 * (int)p.ldb;
+  int k_next = kb0 * 128, k_end = kb0 < kb1 ? p.K : 0;  // of the next step to be loaded (k_end 0: there is none)
+  // scales: a wave takes 64 rows, of A's or (behind them) of B's; what nobody
+  // reads (B's without ROWS) is zeros
+  constexpr int SA_WAVES = Cfg::BM / 64;
+  const bool of_a = wave < SA_WAVES;
+  const int srow = (of_a ? wave : wave - SA_WAVES) * 64 + lane;
+  const bool s_live = of_a ? m0 + srow < p.M : ROWS && srow < Cfg::BN && n0 + srow < p.N;
+  const uint32_t vs = s_live ? (uint32_t)(srow * (int)(of_a ? p.sam : p.sbn)) * 4u : kOOB;
+  const int64_t s_step = of_a ? p.sab : p.sbb;
+  const float* ps = (of_a ? p.sa + (int64_t)m0 * p.sam : ROWS ? p.sb + (int64_t)n0 * p.sbn : p.sb) + kb0 * s_step;
 
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32((const char LL_LDS*)lds));
-  constexpr uint32_t SC = Cfg::SLOTS * Cfg::SLOT;  // scales: per slot, A's then B's
-  auto issue = [&](int kb, int slot, int sslot) {
-    const uint32_t dst = lds0 + slot * Cfg::SLOT + wave * 1024;
-    const int k0 = kb * 128;
-    if (k0 + 128 <= p.K) {
-#pragma unroll
-      for (int i = 0; i < Cfg::QA; ++i) dma16s(ra, dst + i * Cfg::WAVES * 1024, va[i], (uint32_t)k0);
-#pragma unroll
-      for (int i = 0; i < Cfg::QB; ++i)
-        dma16s(rb, dst + Cfg::A_BYTES + i * Cfg::WAVES * 1024, vb[i], (uint32_t)k0);
+  constexpr uint32_t SC = Cfg::SLOTS * Cfg::SLOT;  // scales: per step, A's then B's
+  // Load i (of QA + QB + 1) of the next step into its slot; past the last step it
+  // reads nothing and writes zeros that nobody reads.
+  constexpr int LOADS = Cfg::QA + Cfg::QB + 1;
+  auto issue = [&](int i, int slot, int sslot) {
+    const uint32_t at = lds0 + slot * Cfg::SLOT + wave * 1024;
+    if (i < Cfg::QA) {
+      const bool in = m0 + lrow + i * Cfg::WAVES * 8 < p.M && la < k_end - k_next;
+      dma16s(rsrc_a, at + i * Cfg::WAVES * 1024, in ? va : kOOB, (uint32_t)(k_next + i * a_step));
+    } else if (i < Cfg::QA + Cfg::QB) {
+      const int q = i - Cfg::QA, lb = chunk_b(q);
+      const bool in = n0 + lrow + q * Cfg::WAVES * 8 < p.N && lb < k_end - k_next;
+      dma16s(rsrc_b, at + Cfg::A_BYTES + q * Cfg::WAVES * 1024,
+             in ? (uint32_t)((lane >> 3) * (int)p.ldb + lb) : kOOB, (uint32_t)(k_next + q * b_step));
     } else {
-      // the last, short block: pieces that start at K or beyond are zeros
-#pragma unroll
-      for (int i = 0; i < Cfg::QA; ++i) {
-        const int row = (wave + i * Cfg::WAVES) * 8 + (lane >> 3);
-        const bool in = k0 + (((lane & 7) ^ swz8_a(row)) << 4) < p.K;
-        dma16s(ra, dst + i * Cfg::WAVES * 1024, in ? va[i] : kOOB, (uint32_t)k0);
-      }
-#pragma unroll
-      for (int i = 0; i < Cfg::QB; ++i) {
-        const int row = (wave + i * Cfg::WAVES) * 8 + (lane >> 3);
-        const bool in = k0 + (((lane & 7) ^ swz8_b<FN>(row)) << 4) < p.K;
-        dma16s(rb, dst + Cfg::A_BYTES + i * Cfg::WAVES * 1024, in ? vb[i] : kOOB, (uint32_t)k0);
-      }
+      dma4(make_rsrc(ps, k_end ? 0x7FFFFFF0u : 0u), lds0 + SC + sslot * Cfg::SCALES + wave * 256, vs);
     }
-    const uint32_t sdst = lds0 + SC + sslot * Cfg::SCALES + wave * 256;
-    if (wave < SA_WAVES) dma4(make_rsrc(sa_base + (int64_t)kb * p.sab, 0x7FFFFFF0u), sdst, vsa);
-    if (ROWS && wave < SB_WAVES) dma4(make_rsrc(sb_base + (int64_t)kb * p.sbb, 0x7FFFFFF0u), sdst + Cfg::BM * 4, vsb);
+  };
+  auto issued = [&]() {
+    k_next += 128;
+    ps += s_step;
+    if (k_next >= kb1 * 128) k_end = 0;
   };
 
   // fragments: lane l takes row l % 16 and chunks l / 16 and l / 16 + 4
@@ -148,7 +143,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   auto arrive = [&](int kb, int slot) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     lds_barrier();
-    if (kb * 128 + 128 > p.K && (p.K & 15)) clear_tail(slot);
+    if (kb * 128 < p.K && kb * 128 + 128 > p.K && (p.K & 15)) clear_tail(slot);
   };
   auto read_x = [&](const char* st, int i) {
     return frag8(*(const i32x4*)(st + a_off + 2048 * i), *(const i32x4*)(st + (a_off ^ 64) + 2048 * i));
@@ -170,9 +165,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
 #pragma unroll
   for (int i = 0; i < ND; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (kb0 < kb1) {
-    issue(kb0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) issue(i, 0, 0);
+    issued();
     arrive(kb0, 0);
-    if (kb0 + 1 < kb1) issue(kb0 + 1, 1, 1);
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) issue(i, 1, 1);
+    issued();
     i32x8 wr[FN], xr[2];
     f32x4 sbv[FEW_SB ? 1 : FN];  // ROWS: of all f, or (EXACT, whose operands take the registers) of the last product
     typename Block::W w[FN];
@@ -205,10 +204,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
       for (int t = 0; t < T; ++t) {
         const int i = t / FN, f = t % FN;
         if (f == 0) {
-          if (i == FM - 1 && kb + 1 < kb1) {
-            arrive(kb + 1, slot ^ 1);
-            if (kb + 2 < kb1) issue(kb + 2, slot, s2);
-          }
+          if (i == FM - 1) arrive(kb + 1, slot ^ 1);
           x = Block::x(xr[i & 1]);
         }
         if (i == 0) w[f] = Block::w(wr[f]);
@@ -224,7 +220,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
         if (f == 0) xr[(i + 1) & 1] = i + 1 < FM ? read_x(st, i + 1) : read_x(next, 0);
         if (f == LAG)
           sa_next = *(const float*)(i + 1 < FM ? sc + sa_off + 64 * (i + 1) : lds + s1 * Cfg::SCALES + sa_off);
-        if (i == FM - 1) wr[f] = read_w(next, f);
+        if (i == FM - 1) {
+          wr[f] = read_w(next, f);
+#pragma unroll
+          for (int q = f * LOADS / FN; q < (f + 1) * LOADS / FN; ++q) issue(q, slot, s2);
+          if (f == FN - 1) issued();
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       s_last = s;
@@ -234,6 +235,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
     }
 #pragma unroll
     for (int t = T - LAG; t < T; ++t) add(t, s_last);
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
   }
 
 #pragma unroll
