@@ -161,6 +161,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   constexpr bool FEW_SB = EXACT;
   constexpr int T = FM * FN, LAG = EXACT ? 1 : 2, ND = EXACT ? 2 : 4;
   static_assert(T % ND == 0 && LAG < ND && LAG <= FN && FM % 2 == 0, "ring of results");
+  // The loads of the step after the next begin behind that barrier and go on into
+  // the next step, one for every PACE products: in a burst they filled the address
+  // unit's queue, and the matrix unit stood still meanwhile.
+  constexpr int PACE = T >= 24 ? 2 : 1, EARLY = FN / PACE;
+  static_assert(FN % PACE == 0 && (LOADS - EARLY) * PACE <= T - FN, "loads of a step");
   f32x4 d[ND];
 #pragma unroll
   for (int i = 0; i < ND; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -170,8 +175,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
     issued();
     arrive(kb0, 0);
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) issue(i, 1, 1);
-    issued();
+    for (int i = 0; i < EARLY; ++i) issue(i, 1, 1);
     i32x8 wr[FN], xr[2];
     f32x4 sbv[FEW_SB ? 1 : FN];  // ROWS: of all f, or (EXACT, whose operands take the registers) of the last product
     typename Block::W w[FN];
@@ -220,11 +224,11 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
         if (f == 0) xr[(i + 1) & 1] = i + 1 < FM ? read_x(st, i + 1) : read_x(next, 0);
         if (f == LAG)
           sa_next = *(const float*)(i + 1 < FM ? sc + sa_off + 64 * (i + 1) : lds + s1 * Cfg::SCALES + sa_off);
-        if (i == FM - 1) {
-          wr[f] = read_w(next, f);
-#pragma unroll
-          for (int q = f * LOADS / FN; q < (f + 1) * LOADS / FN; ++q) issue(q, slot, s2);
-          if (f == FN - 1) issued();
+        if (i == FM - 1) wr[f] = read_w(next, f);
+        if (t % PACE == 0) {
+          if (t / PACE < LOADS - EARLY) issue(t / PACE + EARLY, slot ^ 1, s1);
+          if (t / PACE == LOADS - EARLY - 1) issued();
+          if (i == FM - 1) issue(f / PACE, slot, s2);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
