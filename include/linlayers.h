@@ -659,7 +659,7 @@ ll_status quant8_run(const quant8_desc* desc, const void* x, void* q, float* sca
  * Errors: LL_ERR_INVALID_ARG (null desc or pointer, negative size, stride below
  * the row, misaligned operand, scale stride below 1, b_block, C overlapping an
  * input or the workspace), LL_ERR_UNSUPPORTED (types, M, N of 2^26 and more, C of
- * more than 2^22 tiles of 192 x 256, K of 2^22 and more, stride_a or stride_b of 2^22 and more, scale strides along rows
+ * more than 2^22 tiles of 256 x 256, K of 2^22 and more, stride_a or stride_b of 2^22 and more, scale strides along rows
  * of 2^20 and more, strides that put a row or block 2^58 elements or more from
  * the first, device), LL_ERR_WORKSPACE, LL_ERR_NO_DEVICE, LL_ERR_HIP.
  */

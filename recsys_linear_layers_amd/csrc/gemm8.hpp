@@ -26,7 +26,7 @@ struct Gemm8Args {
   int32_t vec_c;    // rows of C (or the partials) take 16-byte stores
 };
 
-enum Gemm8Kind { kG8Few16, kG8Few32, kG8Few64, kG8Tile128, kG8Tile192, kG8Tile256, kG8Kinds };
+enum Gemm8Kind { kG8Few16, kG8Few32, kG8Few64, kG8Tile128, kG8Tile256, kG8Kinds };
 
 struct Gemm8Plan {
   int kind;
@@ -42,8 +42,8 @@ const char* gemm8_kind_name(int kind);
 hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s);
 
 hipError_t launch_gemm8_tile128(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
-hipError_t launch_gemm8_tile192(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
 hipError_t launch_gemm8_tile256(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile256_exact(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
 hipError_t launch_gemm8_few(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s);
 
 }  // namespace ll

@@ -159,12 +159,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   // row of products ahead, those of the next step during the last row, after the
   // barrier that says that its rows have landed and that nobody reads this step's.
   constexpr bool FEW_SB = EXACT;
-  constexpr int T = FM * FN, LAG = EXACT ? 1 : 2, ND = EXACT ? 2 : 4;
+  constexpr int T = FM * FN, LAG = EXACT ? 1 : 3, ND = EXACT ? 2 : 4;
   static_assert(T % ND == 0 && LAG < ND && LAG <= FN && FM % 2 == 0, "ring of results");
   // The loads of the step after the next begin behind that barrier and go on into
   // the next step, one for every PACE products: in a burst they filled the address
   // unit's queue, and the matrix unit stood still meanwhile.
-  constexpr int PACE = T >= 24 ? 2 : 1, EARLY = FN / PACE;
+  constexpr int PACE = EXACT && T >= 24 ? 2 : 1, EARLY = FN / PACE;
   static_assert(FN % PACE == 0 && (LOADS - EARLY) * PACE <= T - FN, "loads of a step");
   f32x4 d[ND];
 #pragma unroll
@@ -212,7 +212,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
           x = Block::x(xr[i & 1]);
         }
         if (i == 0) w[f] = Block::w(wr[f]);
+        if (EXACT) __builtin_amdgcn_s_setprio(1);  // 2212 -> 2169 us; without EXACT 1 or 2% slower
         d[t % ND] = Block::product(w[f], x);
+        if (EXACT) __builtin_amdgcn_s_setprio(0);
         if (t < LAG) add(T + t - LAG, s_last);
         else add(t - LAG, s);
         if (f == LAG - 1) s = ROWS ? sa_next : sa_next * sb;  // of this row of products from here on
@@ -230,7 +232,6 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
           if (t / PACE == LOADS - EARLY - 1) issued();
           if (i == FM - 1) issue(f / PACE, slot, s2);
         }
-        __builtin_amdgcn_sched_barrier(0);
       }
       s_last = s;
       sb = sb_next;

@@ -237,7 +237,7 @@ static ll_status gemm8_check(const gemm8_desc* d) {
   if (d->M >= (1ll << 26) || d->N >= (1ll << 26) || d->K >= (1ll << 22))
     return fail(LL_ERR_UNSUPPORTED, "M and N must be below 2^26, K below 2^22");
   // a launch of 2^32 threads or more is not supported
-  if (((d->M + 191) / 192) * ((d->N + 255) / 256) > kG8MostTiles) return fail(LL_ERR_UNSUPPORTED, "C is too large");
+  if (((d->M + 255) / 256) * ((d->N + 255) / 256) > kG8MostTiles) return fail(LL_ERR_UNSUPPORTED, "C is too large");
   if (d->stride_a < d->K || d->stride_b < d->K || d->stride_c < d->N)
     return fail(LL_ERR_INVALID_ARG, "row strides shorter than the rows");
   if (d->stride_a % 16 || d->stride_b % 16)
@@ -335,7 +335,7 @@ static const struct {
   const char* name;
   int bm, bn;
 } kKinds[kG8Kinds] = {{"FEW16", 16, 16}, {"FEW32", 32, 16}, {"FEW64", 64, 32}, {"TILE128", 128, 128},
-                      {"TILE192", 192, 256}, {"TILE256", 256, 256}};
+                      {"TILE256", 256, 256}};
 
 const char* gemm8_kind_name(int kind) { return kind >= 0 && kind < kG8Kinds ? kKinds[kind].name : "none"; }
 
@@ -346,14 +346,13 @@ Gemm8Plan gemm8_plan(const gemm8_desc& d) {
   const int64_t blocks = blocks8(d.K);
   auto tiles = [&](int kind) { return ((d.M + kKinds[kind].bm - 1) / kKinds[kind].bm) *
                                       ((d.N + kKinds[kind].bn - 1) / kKinds[kind].bn); };
-  const int large = d.c_type == LL_F32 ? kG8Tile192 : kG8Tile256;
   p.kind = d.M <= 16 ? kG8Few16 : d.M <= 32 ? kG8Few32 : d.M <= 64 ? kG8Few64
-           : tiles(large) >= 160 ? large : kG8Tile128;
+           : tiles(kG8Tile256) >= 160 ? kG8Tile256 : kG8Tile128;
   if (const char* env = getenv("LL_GEMM8_KIND")) {
     for (int k = 0; k < kG8Kinds; ++k) {
       bool same = true;
       for (int i = 0; same && (env[i] || kKinds[k].name[i]); ++i) same = env[i] == kKinds[k].name[i];
-      if (same) p.kind = (k < kG8Tile128 && d.M > kKinds[k].bm) || (k > kG8Tile128 && k != large) ? -1 : k;
+      if (same) p.kind = k < kG8Tile128 && d.M > kKinds[k].bm ? -1 : k;
     }
   }
   if (p.kind < 0) return p;
@@ -378,7 +377,6 @@ Gemm8Plan gemm8_plan(const gemm8_desc& d) {
 }
 
 hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s) {
-  if (kind == kG8Tile192) return launch_gemm8_tile192(a, a_e5m2, rows, s);
   if (kind == kG8Tile256) return launch_gemm8_tile256(a, a_e5m2, rows, s);
   if (kind == kG8Tile128) return launch_gemm8_tile128(a, a_e5m2, rows, s);
   return launch_gemm8_few(a, kind, a_e5m2, rows, s);
