@@ -26,10 +26,15 @@ struct Gemm8Args {
   int32_t vec_c;    // rows of C (or the partials) take 16-byte stores
 };
 
-enum Gemm8Kind { kG8Few16, kG8Few32, kG8Few64, kG8Tile128, kG8Tile256, kG8Kinds };
+// By rows and columns of C that a workgroup forms.
+enum Gemm8Kind {
+  kG8Few16x16, kG8Few16x32, kG8Few32x16, kG8Few32x32, kG8Few64x16, kG8Few64x32,
+  kG8Tile64x128, kG8Tile128x128, kG8Tile128x256, kG8Tile256x256,
+  kG8Kinds
+};
 
 struct Gemm8Plan {
-  int kind;
+  int kind;  // -1: a forced kernel that cannot take the sizes
   int bm, bn;
   int tiles_m, tiles_n, splits, per_split;
   size_t partial_bytes;
@@ -41,9 +46,14 @@ const char* gemm8_kind_name(int kind);
 // a_e5m2: A holds LL_E5M2; rows: B's scales are per row (b_block 1).
 hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s);
 
-hipError_t launch_gemm8_tile128(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
-hipError_t launch_gemm8_tile256(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
-hipError_t launch_gemm8_tile256_exact(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile64x128(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile64x128_exact(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile128x128(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile128x128_exact(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile128x256(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile128x256_exact(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile256x256(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_tile256x256_exact(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
 hipError_t launch_gemm8_few(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s);
 
 }  // namespace ll

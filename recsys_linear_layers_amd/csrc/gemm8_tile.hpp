@@ -20,17 +20,18 @@
 
 namespace ll {
 
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int SLOTS_>
 struct G8Cfg {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, WAVES = WM * WN, THREADS = WAVES * 64;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
   static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128, SLOT = A_BYTES + B_BYTES;
   static constexpr int QA = BM / 8 / WAVES, QB = BN / 8 / WAVES;  // 1-KB loads of a wave
-  static constexpr int SLOTS = 2;
-  static constexpr int SCALES = WAVES * 256;  // of a step; three steps' worth, as those of one are read until its end
-  static constexpr int LDS = SLOTS * SLOT + 3 * SCALES;
+  static constexpr int SLOTS = SLOTS_;  // steps whose rows are in LDS or on their way
+  static constexpr int SCALES = WAVES * 256;  // of a step; one more than SLOTS, as they are read until the step's end
+  static constexpr int LDS = SLOTS * SLOT + (SLOTS + 1) * SCALES;
+  static_assert(LDS <= 160 * 1024, "LDS");
   static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0 && TN <= 128 && 128 % TN == 0, "tile");
-  static_assert(BM % 64 == 0 && BN % 64 == 0 && BM + BN <= WAVES * 64, "scales: 64 rows a wave");
+  static_assert((BM + 63) / 64 + (BN + 63) / 64 <= WAVES, "scales: 64 rows a wave");
 };
 
 // Chunk c of A's row r sits at c ^ swz8_a(r), of B's at c ^ swz8_b(r).  A row's
@@ -78,10 +79,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   int k_next = kb0 * 128, k_end = kb0 < kb1 ? p.K : 0;  // of the next step to be loaded (k_end 0: there is none)
   // scales: a wave takes 64 rows, of A's or (behind them) of B's; what nobody
   // reads (B's without ROWS) is zeros
-  constexpr int SA_WAVES = Cfg::BM / 64;
+  constexpr int SA_WAVES = (Cfg::BM + 63) / 64;
   const bool of_a = wave < SA_WAVES;
   const int srow = (of_a ? wave : wave - SA_WAVES) * 64 + lane;
-  const bool s_live = of_a ? m0 + srow < p.M : ROWS && srow < Cfg::BN && n0 + srow < p.N;
+  const bool s_live = of_a ? srow < Cfg::BM && m0 + srow < p.M : ROWS && srow < Cfg::BN && n0 + srow < p.N;
   const uint32_t vs = s_live ? (uint32_t)(srow * (int)(of_a ? p.sam : p.sbn)) * 4u : kOOB;
   const int64_t s_step = of_a ? p.sab : p.sbb;
   const float* ps = (of_a ? p.sa + (int64_t)m0 * p.sam : ROWS ? p.sb + (int64_t)n0 * p.sbn : p.sb) + kb0 * s_step;
@@ -141,7 +142,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   };
   // The rows of the slot of step kb are there, for every wave.
   auto arrive = [&](int kb, int slot) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    static_assert((Cfg::SLOTS - 2) * LOADS < 64, "vmcnt");
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"((Cfg::SLOTS - 2) * LOADS) : "memory");  // those of later steps stay under way
     lds_barrier();
     if (kb * 128 < p.K && kb * 128 + 128 > p.K && (p.K & 15)) clear_tail(slot);
   };
@@ -152,30 +154,34 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
     return frag8(*(const i32x4*)(st + b_off + 512 * f), *(const i32x4*)(st + (b_off ^ 64) + 512 * f));
   };
   const int sa_off = SC + (wm * Cfg::TM + row16) * 4;                              // + 64 i
-  const int sb_off = SC + (Cfg::BM + wn * Cfg::TN + 4 * FN * g) * 4;               // + 16 f
+  const int sb_off = SC + (SA_WAVES * 64 + wn * Cfg::TN + 4 * FN * g) * 4;               // + 16 f
 
   // A step is FM x FN products, in the order below.  A product's fmas follow LAG
   // products later, when its result is there; the fragments of A are read one
   // row of products ahead, those of the next step during the last row, after the
   // barrier that says that its rows have landed and that nobody reads this step's.
   constexpr bool FEW_SB = EXACT;
-  constexpr int T = FM * FN, LAG = EXACT ? 1 : 3, ND = EXACT ? 2 : 4;
+  constexpr int T = FM * FN, LAG = EXACT ? 1 : FN < 3 ? FN : 3, ND = LAG < 2 ? 2 : 4;
   static_assert(T % ND == 0 && LAG < ND && LAG <= FN && FM % 2 == 0, "ring of results");
-  // The loads of the step after the next begin behind that barrier and go on into
-  // the next step, one for every PACE products: in a burst they filled the address
+  // The loads of a later step begin behind that barrier and go on into the next
+  // step, AT_ONCE for every PACE products: in a burst they filled the address
   // unit's queue, and the matrix unit stood still meanwhile.
-  constexpr int PACE = EXACT && T >= 24 ? 2 : 1, EARLY = FN / PACE;
-  static_assert(FN % PACE == 0 && (LOADS - EARLY) * PACE <= T - FN, "loads of a step");
+  constexpr int PACE = EXACT && T >= 24 ? 2 : 1, AT_ONCE = (LOADS * PACE + T - 1) / T;
+  constexpr int EARLY = FN / PACE * AT_ONCE < LOADS ? FN / PACE * AT_ONCE : LOADS;
+  static_assert(FN % PACE == 0 && T % PACE == 0, "loads of a step");
   f32x4 d[ND];
 #pragma unroll
   for (int i = 0; i < ND; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (kb0 < kb1) {
 #pragma unroll
-    for (int i = 0; i < LOADS; ++i) issue(i, 0, 0);
-    issued();
+    for (int n = 0; n < Cfg::SLOTS - 1; ++n) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) issue(i, n, n);
+      issued();
+    }
     arrive(kb0, 0);
 #pragma unroll
-    for (int i = 0; i < EARLY; ++i) issue(i, 1, 1);
+    for (int i = 0; i < EARLY; ++i) issue(i, Cfg::SLOTS - 1, Cfg::SLOTS - 1);
     i32x8 wr[FN], xr[2];
     f32x4 sbv[FEW_SB ? 1 : FN];  // ROWS: of all f, or (EXACT, whose operands take the registers) of the last product
     typename Block::W w[FN];
@@ -194,11 +200,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
             fmaf(d[t % ND][r], ROWS ? s * sbv[FEW_SB ? 0 : t % FN][r] : s, acc[t / FN][t % FN][r]);
       asm volatile("" : "+v"(acc[t / FN][t % FN]));  // here, not where the compiler would sink them to
     };
-    int s0 = 0, s1 = 1, s2 = 2;  // scale slots of this step and of the next two
+    int slot = 0, s0 = 0;  // slots of this step's rows and scales
     for (int kb = kb0; kb < kb1; ++kb) {
-      const int slot = (kb - kb0) & 1;
+      const int slot1 = slot + 1 < Cfg::SLOTS ? slot + 1 : 0, s1 = s0 < Cfg::SLOTS ? s0 + 1 : 0;  // of the next step
+      const int slot_before = slot > 0 ? slot - 1 : Cfg::SLOTS - 1;  // free since the last barrier
+      const int s_last2 = s0 >= 2 ? s0 - 2 : s0 + Cfg::SLOTS - 1, s_last1 = s0 >= 1 ? s0 - 1 : Cfg::SLOTS;
       const char* st = lds + slot * Cfg::SLOT;
-      const char* next = lds + (slot ^ 1) * Cfg::SLOT;
+      const char* next = lds + slot1 * Cfg::SLOT;
       const char* sc = lds + s0 * Cfg::SCALES;
       float sb_next = 0.f;
       if constexpr (!ROWS) sb_next = sbs[(int64_t)min(kb + 1, kb1 - 1) * p.sbb];
@@ -208,7 +216,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
       for (int t = 0; t < T; ++t) {
         const int i = t / FN, f = t % FN;
         if (f == 0) {
-          if (i == FM - 1) arrive(kb + 1, slot ^ 1);
+          if (i == FM - 1) arrive(kb + 1, slot1);
           x = Block::x(xr[i & 1]);
         }
         if (i == 0) w[f] = Block::w(wr[f]);
@@ -224,19 +232,30 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
           for (int q = 0; q < FN; ++q) sbv[q] = *(const f32x4*)(sc + sb_off + 16 * q);
         }
         if (f == 0) xr[(i + 1) & 1] = i + 1 < FM ? read_x(st, i + 1) : read_x(next, 0);
-        if (f == LAG)
+        // the scales of the next row of products, once those of this one have been taken
+        if (LAG == FN && f == 0) sa_next = *(const float*)(sc + sa_off + 64 * i);
+        if (LAG < FN && f == LAG)
           sa_next = *(const float*)(i + 1 < FM ? sc + sa_off + 64 * (i + 1) : lds + s1 * Cfg::SCALES + sa_off);
         if (i == FM - 1) wr[f] = read_w(next, f);
         if (t % PACE == 0) {
-          if (t / PACE < LOADS - EARLY) issue(t / PACE + EARLY, slot ^ 1, s1);
-          if (t / PACE == LOADS - EARLY - 1) issued();
-          if (i == FM - 1) issue(f / PACE, slot, s2);
+#pragma unroll
+          for (int n = 0; n < AT_ONCE; ++n) {
+            const int q = t / PACE * AT_ONCE + n + EARLY;
+            if (q < LOADS && i < FM - 1) issue(q, slot_before, s_last2);
+            if (q == LOADS - 1 && i < FM - 1) issued();
+          }
+#pragma unroll
+          for (int n = 0; n < AT_ONCE; ++n) {
+            const int q = f / PACE * AT_ONCE + n;
+            if (i == FM - 1 && q < EARLY) issue(q, slot, s_last1);
+            if (i == FM - 1 && q == LOADS - 1) issued();
+          }
         }
       }
       s_last = s;
       sb = sb_next;
-      const int first = s0;
-      s0 = s1, s1 = s2, s2 = first;
+      slot = slot1;
+      s0 = s1;
     }
 #pragma unroll
     for (int t = T - LAG; t < T; ++t) add(t, s_last);

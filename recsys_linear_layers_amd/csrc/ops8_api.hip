@@ -4,6 +4,7 @@
 #include <math.h>
 #include <stdio.h>
 #include <stdlib.h>
+#include <string.h>
 
 #include <algorithm>
 
@@ -331,55 +332,103 @@ ll_status gemm8_run(const gemm8_desc* d, const void* A, const float* a_scale, co
 
 namespace ll {
 
-static const struct {
+namespace {
+
+// step: microseconds of a step (128 of K) where all CUs hold a workgroup (tiles).
+const struct {
   const char* name;
   int bm, bn;
-} kKinds[kG8Kinds] = {{"FEW16", 16, 16}, {"FEW32", 32, 16}, {"FEW64", 64, 32}, {"TILE128", 128, 128},
-                      {"TILE256", 256, 256}};
+  float step;
+} kKinds[kG8Kinds] = {
+    {"FEW16x16", 16, 16, 0.f},          {"FEW16x32", 16, 32, 0.f},          {"FEW32x16", 32, 16, 0.f},
+    {"FEW32x32", 32, 32, 0.f},          {"FEW64x16", 64, 16, 0.f},          {"FEW64x32", 64, 32, 0.f},
+    {"TILE64x128", 64, 128, 0.44f},     {"TILE128x128", 128, 128, 0.63f},   {"TILE128x256", 128, 256, 1.03f},
+    {"TILE256x256", 256, 256, 1.75f}};
+
+constexpr int kCus = 256;  // that the choice is made for
+
+// What a kernel takes, in microseconds, as far as the choice needs it.
+//   Tiles: a round of workgroups over the CUs takes its steps, each at least as long
+//   as its rows of A and B come from memory (5.5 TB/s), and 2.5 for the first loads
+//   and the stores; a split K adds a launch and the partials' bytes, written
+//   and read.  Estimate and measured time (MI355X, bf16 C): 1024 x 4096 x 4096,
+//   128x128 24.7 / 24.6; 2048 x 4096 x 4096, 128x256 37.5 / 37.7; 4096^3, 256x256
+//   60.5 / 62, 128x256 73 / 76, 128x128 93 / 91; 128 x 8192 x 8192, 128x128 in four
+//   splits 23.2 / 23.1; 64 x 28672 x 8192, 64x128 47 / 49.
+//   Few rows: each CU's share of B comes at 10 bytes a clock (HBM), the rows of A,
+//   again for each workgroup, at 50 (L2), and the waits between them grow with the
+//   rows.  1 x 8192 x 8192, 16x16 14.8 / 12.3; 16 x 8192 x 8192, 16x32 15.7 / 13.6;
+//   64 x 8192 x 8192, 64x32 22.5 / 24.4 (64x128 in four splits 21 / 19.3); 64 x 4096 x
+//   4096, 64x16 10.6 / 11.8 (64x128 in four splits 14 / 13.5).
+float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, int64_t steps) {
+  const float rounds = (float)((tiles * splits + kCus - 1) / kCus);
+  const float mn = (float)d.M * (float)d.N;
+  const float join = splits > 1 ? 3.f + (float)splits * mn * 4.f / 3.0e6f : 0.f;
+  if (kind >= kG8Tile64x128) {
+    // an fp32 C is formed at about half the rate
+    const float work = kKinds[kind].step * (d.c_type == LL_F32 && kind > kG8Tile64x128 ? 1.8f : 1.f);
+    const float memory = (float)(d.M + d.N) * 128.f * (float)splits / rounds / 5.5e6f;
+    const float step = std::max(work, memory);
+    return 2.f + rounds * (2.5f + (float)steps * step) + join;
+  }
+  const float bytes = (float)steps * 128.f * ((float)kKinds[kind].bn / 10.f + (float)std::min<int64_t>(d.M, kKinds[kind].bm) / 50.f);
+  return 2.f + 0.05f * (float)kKinds[kind].bm + rounds * bytes / 2100.f + join;
+}
+
+}  // namespace
 
 const char* gemm8_kind_name(int kind) { return kind >= 0 && kind < kG8Kinds ? kKinds[kind].name : "none"; }
 
-// The environment variables LL_GEMM8_KIND (a name as gemm8_describe prints it)
-// and LL_GEMM8_SPLITS override the choice, for measurements.
+// The kernel and the split of K with the smallest estimate.  The environment
+// variables LL_GEMM8_KIND (a name as gemm8_describe prints it) and LL_GEMM8_SPLITS
+// override the choice, for measurements.
 Gemm8Plan gemm8_plan(const gemm8_desc& d) {
-  Gemm8Plan p = {};
+  const char* const forced = getenv("LL_GEMM8_KIND");
+  const char* const forced_splits = getenv("LL_GEMM8_SPLITS");
   const int64_t blocks = blocks8(d.K);
-  auto tiles = [&](int kind) { return ((d.M + kKinds[kind].bm - 1) / kKinds[kind].bm) *
-                                      ((d.N + kKinds[kind].bn - 1) / kKinds[kind].bn); };
-  p.kind = d.M <= 16 ? kG8Few16 : d.M <= 32 ? kG8Few32 : d.M <= 64 ? kG8Few64
-           : tiles(kG8Tile256) >= 160 ? kG8Tile256 : kG8Tile128;
-  if (const char* env = getenv("LL_GEMM8_KIND")) {
-    for (int k = 0; k < kG8Kinds; ++k) {
-      bool same = true;
-      for (int i = 0; same && (env[i] || kKinds[k].name[i]); ++i) same = env[i] == kKinds[k].name[i];
-      if (same) p.kind = k < kG8Tile128 && d.M > kKinds[k].bm ? -1 : k;
+  Gemm8Plan p = {};
+  p.kind = -1;
+  float best = 0.f;
+  for (int kind = 0; kind < kG8Kinds; ++kind) {
+    if (forced && strcmp(forced, kKinds[kind].name)) continue;
+    if (kind < kG8Tile64x128 && (d.M > kKinds[kind].bm || (!forced && 2 * d.M <= kKinds[kind].bm && kind >= kG8Few32x16)))
+      continue;  // the rows do not fit, or fit half of them
+    const int64_t tm = (d.M + kKinds[kind].bm - 1) / kKinds[kind].bm, tn = (d.N + kKinds[kind].bn - 1) / kKinds[kind].bn;
+    for (int64_t want = 1; want <= 16; want *= 2) {
+      int64_t splits = forced_splits ? std::max(1, atoi(forced_splits)) : want;
+      splits = std::max<int64_t>(1, std::min(splits, blocks));
+      const int64_t steps = std::max<int64_t>(1, (blocks + splits - 1) / splits);
+      splits = std::max<int64_t>(1, (blocks + steps - 1) / steps);
+      if (tm * tn * splits > kG8MostTiles) break;
+      const float t = gemm8_time(d, kind, tm * tn, splits, steps);
+      if (p.kind >= 0 && t >= best) continue;
+      best = t;
+      p.kind = kind;
+      p.bm = kKinds[kind].bm;
+      p.bn = kKinds[kind].bn;
+      p.tiles_m = (int)tm;
+      p.tiles_n = (int)tn;
+      p.per_split = (int)steps;
+      p.splits = (int)splits;
+      p.partial_bytes = splits > 1 ? align256((size_t)splits * (size_t)d.M * (size_t)d.N * 4) : 0;
     }
   }
-  if (p.kind < 0) return p;
-  p.bm = kKinds[p.kind].bm;
-  p.bn = kKinds[p.kind].bn;
-  p.tiles_m = (int)((d.M + p.bm - 1) / p.bm);
-  p.tiles_n = (int)((d.N + p.bn - 1) / p.bn);
-  const int64_t t = tiles(p.kind);
-  int64_t splits = 1;
-  if (p.kind == kG8Tile128) splits = std::min<int64_t>(512 / std::max<int64_t>(t, 1), blocks / 4);
-  else if (p.kind < kG8Tile128) splits = std::min<int64_t>(64 / std::max<int64_t>(t, 1), blocks / 32);
-  if (const char* env = getenv("LL_GEMM8_SPLITS")) splits = atoi(env);
-  splits = std::max<int64_t>(1, std::min<int64_t>(splits, blocks));
-  if (t * std::max<int64_t>(1, std::min<int64_t>(splits, blocks)) > kG8MostTiles) {
-    p.kind = -1;
-    return p;
-  }
-  p.per_split = (int)std::max<int64_t>(1, (blocks + splits - 1) / splits);
-  p.splits = (int)std::max<int64_t>(1, (blocks + p.per_split - 1) / p.per_split);
-  p.partial_bytes = p.splits > 1 ? align256((size_t)p.splits * d.M * d.N * 4) : 0;
   return p;
 }
 
 hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s) {
-  if (kind == kG8Tile256) return launch_gemm8_tile256(a, a_e5m2, rows, s);
-  if (kind == kG8Tile128) return launch_gemm8_tile128(a, a_e5m2, rows, s);
-  return launch_gemm8_few(a, kind, a_e5m2, rows, s);
+  const bool exact = a.c_type == LL_F32;
+  switch (kind) {
+    case kG8Tile64x128:
+      return exact ? launch_gemm8_tile64x128_exact(a, a_e5m2, rows, s) : launch_gemm8_tile64x128(a, a_e5m2, rows, s);
+    case kG8Tile128x128:
+      return exact ? launch_gemm8_tile128x128_exact(a, a_e5m2, rows, s) : launch_gemm8_tile128x128(a, a_e5m2, rows, s);
+    case kG8Tile128x256:
+      return exact ? launch_gemm8_tile128x256_exact(a, a_e5m2, rows, s) : launch_gemm8_tile128x256(a, a_e5m2, rows, s);
+    case kG8Tile256x256:
+      return exact ? launch_gemm8_tile256x256_exact(a, a_e5m2, rows, s) : launch_gemm8_tile256x256(a, a_e5m2, rows, s);
+    default: return launch_gemm8_few(a, kind, a_e5m2, rows, s);
+  }
 }
 
 }  // namespace ll

@@ -68,9 +68,14 @@ def test_against_64_bits(M, N, K, squares):
         _check(ll.gemm8(a, sa, b, sb, out_dtype=t[c]), ref, S, K)
 
 
-@pytest.mark.parametrize("kind,M,N,K", [("TILE128", 3, 100, 300), ("TILE128", 300, 200, 700), ("TILE256", 5, 70, 90),
-                                        ("TILE256", 300, 520, 1000), ("TILE256", 513, 257, 4100), ("TILE256", 7, 65, 4000),
-                                        ("FEW64", 9, 333, 1000), ("FEW32", 30, 100, 130), ("FEW64", 64, 64, 64)])
+@pytest.mark.parametrize("kind,M,N,K", [
+    ("FEW16x16", 3, 100, 300), ("FEW16x16", 16, 515, 5000), ("FEW16x32", 9, 333, 1000), ("FEW16x32", 1, 70, 9000),
+    ("FEW32x16", 30, 100, 130), ("FEW32x16", 17, 90, 7000), ("FEW32x32", 32, 64, 64), ("FEW32x32", 5, 200, 4100),
+    ("FEW64x16", 64, 64, 64), ("FEW64x16", 40, 333, 3000), ("FEW64x32", 9, 333, 1000), ("FEW64x32", 64, 95, 3000),
+    ("TILE64x128", 3, 100, 300), ("TILE64x128", 64, 257, 5000), ("TILE64x128", 130, 60, 1030),
+    ("TILE128x128", 3, 100, 300), ("TILE128x128", 300, 200, 700), ("TILE128x128", 129, 385, 4100),
+    ("TILE128x256", 5, 70, 90), ("TILE128x256", 200, 300, 3000), ("TILE128x256", 129, 513, 1111),
+    ("TILE256x256", 5, 70, 90), ("TILE256x256", 300, 520, 1000), ("TILE256x256", 513, 257, 4100)])
 @pytest.mark.parametrize("splits", [1, 3])
 def test_every_kernel_and_split(monkeypatch, kind, M, N, K, splits):
     """Kernels and splits that the sizes alone would not pick."""
