@@ -23,7 +23,6 @@ struct Gemm8Args {
   int32_t blocks;   // of 128 along K
   int32_t splits, per_split;  // K is split into runs of per_split blocks
   int32_t tiles_m, tiles_n, total;
-  int32_t vec_c;    // rows of C (or the partials) take 16-byte stores
 };
 
 // By rows and columns of C that a workgroup forms.

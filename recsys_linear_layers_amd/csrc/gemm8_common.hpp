@@ -89,16 +89,19 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t vof
                : "memory");
 }
 
-// CNT consecutive columns of row m of C from column n on, or of the partials.
+// CNT consecutive columns of row m of C from column n on, or of the partials, in
+// 16-byte stores at whatever alignment; at the row's end one by one.
 template <int CNT>
 __device__ __forceinline__ void store_c8(const Gemm8Args& p, int split, int m, int n, const float (&v)[CNT]) {
   if (m >= p.M || n >= p.N) return;
-  const bool whole = n + CNT <= p.N && p.vec_c;
   if (p.partial || p.c_type == LL_F32) {
     float* dst = p.partial ? p.partial + ((int64_t)split * p.M + m) * p.N + n : (float*)p.c + (int64_t)m * p.ldc + n;
-    if (whole) {
+    if (n + CNT <= p.N) {
 #pragma unroll
-      for (int i = 0; i < CNT; i += 4) *(f32x4*)(dst + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+      for (int i = 0; i < CNT; i += 4) {
+        const f32x4 q = {v[i], v[i + 1], v[i + 2], v[i + 3]};
+        __builtin_memcpy(dst + i, &q, sizeof q);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < CNT; ++i)
@@ -107,30 +110,20 @@ __device__ __forceinline__ void store_c8(const Gemm8Args& p, int split, int m, i
     return;
   }
   uint16_t* dst = (uint16_t*)p.c + (int64_t)m * p.ldc + n;
-  uint32_t w[CNT / 2];
-  if (p.c_type == LL_BF16) {
-    Chunk<LL_BF16, CNT> c;
+  constexpr int VEC = CNT < 8 ? CNT : 8;
 #pragma unroll
-    for (int i = 0; i < CNT; i += 2) c.put2(i, v[i], v[i + 1]);
-    __builtin_memcpy(w, &c, sizeof w);
-  } else {
-    Chunk<LL_F16, CNT> c;
+  for (int k = 0; k < CNT; k += VEC) {
+    if (p.c_type == LL_BF16) {
+      Chunk<LL_BF16, VEC> c;
 #pragma unroll
-    for (int i = 0; i < CNT; i += 2) c.put2(i, v[i], v[i + 1]);
-    __builtin_memcpy(w, &c, sizeof w);
-  }
-  if (whole) {
-    if constexpr (CNT % 8 == 0) {
-#pragma unroll
-      for (int i = 0; i < CNT / 2; i += 4)
-        *(i32x4*)(dst + 2 * i) = i32x4{(int)w[i], (int)w[i + 1], (int)w[i + 2], (int)w[i + 3]};
+      for (int i = 0; i < VEC; i += 2) c.put2(i, v[k + i], v[k + i + 1]);
+      c.template store<true>(dst + k, p.N - n - k);
     } else {
-      __builtin_memcpy(__builtin_assume_aligned(dst, 8), w, sizeof w);
-    }
-  } else {
+      Chunk<LL_F16, VEC> c;
 #pragma unroll
-    for (int i = 0; i < CNT; ++i)
-      if (n + i < p.N) dst[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+      for (int i = 0; i < VEC; i += 2) c.put2(i, v[k + i], v[k + i + 1]);
+      c.template store<true>(dst + k, p.N - n - k);
+    }
   }
 }
 

@@ -4,9 +4,10 @@
 // instruction per 16x16 of C, from zero; four vector fmas then add the scaled
 // sums to the fp32 accumulators, which therefore live in vector registers.  The
 // rows of B take the instruction's first operand: a lane then holds one row of C
-// (its scale of A is one register) and, with the rows of B dealt out as
-// 4 FN g + 4 f + r to instruction f, lane group g and register r, 4 FN
-// consecutive columns, which leave in 16-byte stores.
+// (its scale of A is one register) and, in four registers, four consecutive
+// columns; with a 16-bit C the rows of B are dealt out so that two instructions
+// make eight (8 g + 4 (f % 2) + r of 32 to instruction f, lane group g, register
+// r).  So a store is 16 bytes, and a row's 64 bytes leave together.
 //
 // A step is one block of 128 k: A's and B's rows of 128 bytes go straight from
 // memory to LDS (1 KB per instruction), two steps deep; one barrier per step.
@@ -40,9 +41,9 @@ struct G8Cfg {
 // chunk: the eight rows of each parity need eight different values.  A's rows
 // follow one another; B's are four times four, 4 FN rows apart.
 __device__ __forceinline__ int swz8_a(int r) { return ((r >> 1) & 1) | (((r >> 3) & 1) << 1) | (r & 4); }
-template <int FN>
+template <int GF>
 __device__ __forceinline__ int swz8_b(int r) {
-  return ((r >> 1) & 1) | (((r / (8 * FN)) & 1) << 1) | (((r / (4 * FN)) & 1) << 2);
+  return ((r >> 1) & 1) | (((r / (8 * GF)) & 1) << 1) | (((r / (4 * GF)) & 1) << 2);
 }
 
 template <class Cfg, bool E5M2, bool ROWS, bool EXACT>
@@ -50,6 +51,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   typedef Block8<E5M2, EXACT> Block;
   __shared__ __align__(1024) char lds[Cfg::LDS];
   constexpr int FM = Cfg::FM, FN = Cfg::FN;
+  constexpr int GF = EXACT || FN % 2 ? 1 : 2;  // instructions whose columns lie side by side
+  // row of B's tile (column of C's), from a wave's first on, that instruction f takes as its first
+  auto col_of = [](int f) { return 16 * GF * (f / GF) + 4 * (f % GF); };
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
@@ -69,7 +73,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   // matrices is beyond every range, which reads zeros; the descriptors' own range
   // is not used.
   const int lrow = wave * 8 + (lane >> 3);
-  auto chunk_b = [&](int i) { return ((lane & 7) ^ swz8_b<FN>(lrow + i * Cfg::WAVES * 8)) << 4; };
+  auto chunk_b = [&](int i) { return ((lane & 7) ^ swz8_b<GF>(lrow + i * Cfg::WAVES * 8)) << 4; };
   const int la = ((lane & 7) ^ swz8_a(lrow)) << 4;
   static_assert(Cfg::WAVES * 8 % 16 == 0, "A's rows of a lane have one permutation");
   const uint32_t va = (uint32_t)((lane >> 3) * (int)p.lda + la);
@@ -115,9 +119,9 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   // fragments: lane l takes row l % 16 and chunks l / 16 and l / 16 + 4
   const int row16 = lane & 15, g = lane >> 4;
   const int arow = wm * Cfg::TM + row16;
-  const int brow = wn * Cfg::TN + (row16 >> 2) * 4 * FN + (row16 & 3);
+  const int brow = wn * Cfg::TN + (row16 >> 2) * 4 * GF + (row16 & 3);
   const int a_off = arow * 128 + ((g ^ swz8_a(arow)) << 4);                            // + 2048 i
-  const int b_off = Cfg::A_BYTES + brow * 128 + ((g ^ swz8_b<FN>(brow)) << 4);         // + 512 f
+  const int b_off = Cfg::A_BYTES + brow * 128 + ((g ^ swz8_b<GF>(brow)) << 4);  // + 128 col_of(f)
   const int sb_row = (n0 + wn * Cfg::TN) / 128;                                         // block row of B, unless ROWS
 
   const float __attribute__((address_space(4))) * sbs =
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
     for (int row = threadIdx.x; row < Cfg::BM + Cfg::BN; row += Cfg::THREADS) {
       const bool of_a = row < Cfg::BM;
       const int r = of_a ? row : row - Cfg::BM;
-      char* q = lds + slot * Cfg::SLOT + row * 128 + ((c ^ (of_a ? swz8_a(r) : swz8_b<FN>(r))) << 4);
+      char* q = lds + slot * Cfg::SLOT + row * 128 + ((c ^ (of_a ? swz8_a(r) : swz8_b<GF>(r))) << 4);
       for (int i = p.K & 15; i < 16; ++i) q[i] = 0;
     }
     __syncthreads();
@@ -151,10 +155,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
     return frag8(*(const i32x4*)(st + a_off + 2048 * i), *(const i32x4*)(st + (a_off ^ 64) + 2048 * i));
   };
   auto read_w = [&](const char* st, int f) {
-    return frag8(*(const i32x4*)(st + b_off + 512 * f), *(const i32x4*)(st + (b_off ^ 64) + 512 * f));
+    return frag8(*(const i32x4*)(st + b_off + 128 * col_of(f)), *(const i32x4*)(st + (b_off ^ 64) + 128 * col_of(f)));
   };
   const int sa_off = SC + (wm * Cfg::TM + row16) * 4;                              // + 64 i
-  const int sb_off = SC + (SA_WAVES * 64 + wn * Cfg::TN + 4 * FN * g) * 4;               // + 16 f
+  const int sb_off = SC + (SA_WAVES * 64 + wn * Cfg::TN + 4 * GF * g) * 4;  // + 4 col_of(f)
 
   // A step is FM x FN products, in the order below.  A product's fmas follow LAG
   // products later, when its result is there; the fragments of A are read one
@@ -226,10 +230,10 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
         if (t < LAG) add(T + t - LAG, s_last);
         else add(t - LAG, s);
         if (f == LAG - 1) s = ROWS ? sa_next : sa_next * sb;  // of this row of products from here on
-        if (ROWS && FEW_SB) sbv[0] = *(const f32x4*)(sc + sb_off + 16 * f);
+        if (ROWS && FEW_SB) sbv[0] = *(const f32x4*)(sc + sb_off + 4 * col_of(f));
         if (ROWS && !FEW_SB && t == LAG - 1) {
 #pragma unroll
-          for (int q = 0; q < FN; ++q) sbv[q] = *(const f32x4*)(sc + sb_off + 16 * q);
+          for (int q = 0; q < FN; ++q) sbv[q] = *(const f32x4*)(sc + sb_off + 4 * col_of(q));
         }
         if (f == 0) xr[(i + 1) & 1] = i + 1 < FM ? read_x(st, i + 1) : read_x(next, 0);
         // the scales of the next row of products, once those of this one have been taken
@@ -263,14 +267,14 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   }
 
 #pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    float v[4 * FN];
+  for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int f = 0; f < FN; ++f)
+    for (int f = 0; f < FN; f += GF) {
+      float v[4 * GF];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) v[4 * f + r] = acc[i][f][r];
-    store_c8<4 * FN>(p, split, m0 + wm * Cfg::TM + 16 * i + row16, n0 + wn * Cfg::TN + 4 * FN * g, v);
-  }
+      for (int q = 0; q < 4 * GF; ++q) v[q] = acc[i][f + q / 4][q % 4];
+      store_c8<4 * GF>(p, split, m0 + wm * Cfg::TM + 16 * i + row16, n0 + wn * Cfg::TN + col_of(f) + 4 * GF * g, v);
+    }
 }
 
 template <class Cfg, bool EXACT>

@@ -320,7 +320,6 @@ ll_status gemm8_run(const gemm8_desc* d, const void* A, const float* a_scale, co
   a.tiles_m = plan.tiles_m;
   a.tiles_n = plan.tiles_n;
   a.total = plan.tiles_m * plan.tiles_n * plan.splits;
-  a.vec_c = a.partial ? d->N % 4 == 0 : d->stride_c * e % 16 == 0 && !misaligned(C, 16);
   hipError_t err = launch_gemm8(a, plan.kind, d->a_type == LL_E5M2, d->b_block == 1, (hipStream_t)stream);
   if (err == hipSuccess && a.partial)
     err = launch_splitk_reduce(a.partial, plan.splits, d->M, d->N, C, d->stride_c, 1,
@@ -355,8 +354,8 @@ constexpr int kCus = 256;  // that the choice is made for
 //   128x128 24.7 / 24.6; 2048 x 4096 x 4096, 128x256 37.5 / 37.7; 4096^3, 256x256
 //   60.5 / 62, 128x256 73 / 76, 128x128 93 / 91; 128 x 8192 x 8192, 128x128 in four
 //   splits 23.2 / 23.1; 64 x 28672 x 8192, 64x128 47 / 49.
-//   Few rows: each CU's share of B comes at 10 bytes a clock (HBM), the rows of A,
-//   again for each workgroup, at 50 (L2), and the waits between them grow with the
+//   Few rows: each CU's share of B comes at 10 bytes a clock (HBM; up to 25 where not
+//   all CUs ask), the rows of A, again for each workgroup, at 50 (L2), and the waits between them grow with the
 //   rows.  1 x 8192 x 8192, 16x16 14.8 / 12.3; 16 x 8192 x 8192, 16x32 15.7 / 13.6;
 //   64 x 8192 x 8192, 64x32 22.5 / 24.4 (64x128 in four splits 21 / 19.3); 64 x 4096 x
 //   4096, 64x16 10.6 / 11.8 (64x128 in four splits 14 / 13.5).
@@ -371,7 +370,9 @@ float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, i
     const float step = std::max(work, memory);
     return 2.f + rounds * (2.5f + (float)steps * step) + join;
   }
-  const float bytes = (float)steps * 128.f * ((float)kKinds[kind].bn / 10.f + (float)std::min<int64_t>(d.M, kKinds[kind].bm) / 50.f);
+  const float of_b = std::min(25.f, 10.f * kCus / (float)std::min<int64_t>(tiles * splits, kCus));
+  const float rows = (float)std::min<int64_t>(d.M, kKinds[kind].bm);
+  const float bytes = (float)steps * 128.f * ((float)kKinds[kind].bn / of_b + rows / 50.f);
   return 2.f + 0.05f * (float)kKinds[kind].bm + rounds * bytes / 2100.f + join;
 }
 
