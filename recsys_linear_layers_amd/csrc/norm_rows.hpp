@@ -85,6 +85,22 @@ __device__ __forceinline__ void row_sum2(float& a, float& b, float* red) {
   }
 }
 
+// The same for one sum.
+template <int TPR, int WAVES>
+__device__ __forceinline__ void row_sum(float& a, float* red) {
+  a = lanes_sum<64>(a);
+  if constexpr (TPR > 64) {
+    constexpr int W = TPR / 64;
+    const int wave = threadIdx.x >> 6;
+    if ((threadIdx.x & 63) == 0) red[wave] = a;
+    __syncthreads();
+    const int w0 = wave / W * W;
+    a = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) a += red[w0 + w];
+  }
+}
+
 // One row of a lane's columns: NCH chunks of VEC, TPR chunks apart.  Lanes past
 // the row's end and rows past the last hold zeros.
 template <int TY, int VEC, int TPR, int NCH, bool TAIL>

@@ -45,7 +45,7 @@ template <int TY, int OUT, int VEC, int TPR, int NCH, int THREADS, bool TAIL, bo
 __global__ void __launch_bounds__(THREADS) rms_kernel(const RmsArgs a) {
   typedef Chunk<TY, VEC> C;
   typedef typename Elem<TY>::raw raw;
-  __shared__ float red[2][THREADS / 64 * 2];
+  __shared__ float red[2][THREADS / 64];
   constexpr int ROWS = THREADS / TPR;
   const int x = threadIdx.x % TPR, y = threadIdx.x / TPR;
   const float cols = (float)a.D;
@@ -71,12 +71,12 @@ __global__ void __launch_bounds__(THREADS) rms_kernel(const RmsArgs a) {
         if (live && d < a.D) cur.v[k].template store<TAIL>(dst + d, a.D - d);
       }
     }
-    float s = 0.f, unused = 0.f;
+    float s = 0.f;
 #pragma unroll
     for (int k = 0; k < NCH; ++k)
 #pragma unroll
       for (int i = 0; i < VEC; ++i) s = fmaf(cur.v[k].get(i), cur.v[k].get(i), s);
-    row_sum2<TPR, THREADS / 64>(s, unused, red[flip]);
+    row_sum<TPR, THREADS / 64>(s, red[flip]);
     const float rstd = 1.f / sqrtf(s / cols + a.eps);
     if (live && x == 0 && a.rstd) a.rstd[r] = rstd;
     raw* dst = (raw*)a.y + r * a.ldy;
@@ -89,12 +89,12 @@ __global__ void __launch_bounds__(THREADS) rms_kernel(const RmsArgs a) {
         if (!live || d >= a.D) continue;
         C o;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) o.put(i, cur.v[k].get(i) * rstd * g[i]);
+        for (int i = 0; i < VEC; ++i) o.put(i, cur.v[k].get(i) * g[i] * rstd);
         o.template store<TAIL, true>(dst + d, a.D - d);
       } else {
         float v[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = d < a.D && (!TAIL || d + i < a.D) ? cur.v[k].get(i) * rstd * g[i] : 0.f;
+        for (int i = 0; i < VEC; ++i) v[i] = d < a.D && (!TAIL || d + i < a.D) ? cur.v[k].get(i) * g[i] * rstd : 0.f;
         put_block8<OUT, VEC, TAIL>(v, a, r, d);
       }
     }
@@ -108,11 +108,11 @@ __global__ void __launch_bounds__(1024) rms_long_kernel(const RmsArgs a) {
   constexpr int VEC = kWide<TY>, STEP = 1024 * VEC;
   typedef Chunk<TY, VEC> C;
   typedef typename Elem<TY>::raw raw;
-  __shared__ float red[2][32];
+  __shared__ float red[2][16];
   int flip = 0;
   for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, flip ^= 1) {
     const raw* src = (const raw*)a.x + r * a.ldx;
-    float s = 0.f, unused = 0.f;
+    float s = 0.f;
     for (int64_t d = threadIdx.x * VEC; d < a.D; d += STEP) {
       const int n = (int)min<int64_t>(VEC, a.D - d);
       C v;
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(1024) rms_long_kernel(const RmsArgs a) {
 #pragma unroll
       for (int i = 0; i < VEC; ++i) s = fmaf(v.get(i), v.get(i), s);
     }
-    row_sum2<1024, 16>(s, unused, red[flip]);
+    row_sum<1024, 16>(s, red[flip]);
     const float rstd = 1.f / sqrtf(s / (float)a.D + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[r] = rstd;
     const raw* again = a.residual ? (const raw*)a.h + r * a.ldh : src;  // what this lane has written itself
@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(1024) rms_long_kernel(const RmsArgs a) {
         load_param<TY, VEC, true>(a.gamma, a.param_f32, (int)d, n, 1.f, g);
       }
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) y[i] = i < n ? v.get(i) * rstd * g[i] : 0.f;
+      for (int i = 0; i < VEC; ++i) y[i] = i < n ? v.get(i) * g[i] * rstd : 0.f;
       if constexpr (OUT == 0) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v.put(i, y[i]);
@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(const RmsGradArgs a) 
   typedef Chunk<TY, VEC> C;
   typedef typename Elem<TY>::raw raw;
   constexpr int ROWS = THREADS / TPR;
-  __shared__ float red[2][THREADS / 64 * 2];
+  __shared__ float red[2][THREADS / 64];
   __shared__ float col[ROWS > 1 ? THREADS * VEC : 1];
   const int x = threadIdx.x % TPR, y = threadIdx.x / TPR;
   const float cols = (float)a.D;
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(const RmsGradArgs a) 
     vd.load(a.dy, a.lddy, r, live, x, a.D);
     if (a.dh) ve.load(a.dh, a.lddh, r, live, x, a.D);
     const float rstd = live ? a.rstd[r] : 0.f;
-    float s = 0.f, unused = 0.f;
+    float s = 0.f;
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {  // dy and h are 0 past the row's end, so nothing is added there
       const int d = (x + k * TPR) * VEC;
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(const RmsGradArgs a) 
         dg[k][i] = fmaf(v, n, dg[k][i]);
       }
     }
-    row_sum2<TPR, THREADS / 64>(s, unused, red[flip]);
+    row_sum<TPR, THREADS / 64>(s, red[flip]);
     if (live) {
       const float m = s / cols;
       raw* dst = (raw*)a.dx + r * a.lddx;
@@ -331,13 +331,13 @@ __global__ void __launch_bounds__(1024) rms_grad_long_kernel(const RmsGradArgs a
   constexpr int VEC = kWide<TY>, STEP = 1024 * VEC;
   typedef Chunk<TY, VEC> C;
   typedef typename Elem<TY>::raw raw;
-  __shared__ float red[2][32];
+  __shared__ float red[2][16];
   int flip = 0;
   for (int64_t r = blockIdx.x; r < a.N; r += gridDim.x, flip ^= 1) {
     const raw* sh = (const raw*)a.h + r * a.ldh;
     const raw* sd = (const raw*)a.dy + r * a.lddy;
     const float rstd = a.rstd[r];
-    float s = 0.f, unused = 0.f;
+    float s = 0.f;
     for (int64_t d = threadIdx.x * VEC; d < a.D; d += STEP) {
       const int n = (int)min<int64_t>(VEC, a.D - d);
       C vh, vd;
@@ -348,7 +348,7 @@ __global__ void __launch_bounds__(1024) rms_grad_long_kernel(const RmsGradArgs a
 #pragma unroll
       for (int i = 0; i < VEC; ++i) s = fmaf(vd.get(i) * g[i], vh.get(i) * rstd, s);
     }
-    row_sum2<1024, 16>(s, unused, red[flip]);
+    row_sum<1024, 16>(s, red[flip]);
     const float m = s / (float)a.D;
     for (int64_t d = threadIdx.x * VEC; d < a.D; d += STEP) {
       const int n = (int)min<int64_t>(VEC, a.D - d);
