@@ -103,7 +103,7 @@ __device__ __forceinline__ void row_sum(float& a, float* red) {
 
 // One row of a lane's columns: NCH chunks of VEC, TPR chunks apart.  Lanes past
 // the row's end and rows past the last hold zeros.
-template <int TY, int VEC, int TPR, int NCH, bool TAIL>
+template <int TY, int VEC, int TPR, int NCH, bool TAIL, bool NT = false>
 struct RowCols {
   Chunk<TY, VEC> v[NCH];
   __device__ __forceinline__ void load(const void* base, int64_t ld, int64_t r, bool live, int x, int D) {
@@ -111,7 +111,7 @@ struct RowCols {
 #pragma unroll
     for (int k = 0; k < NCH; ++k) {
       const int d = (x + k * TPR) * VEC;
-      if (live && d < D) v[k].template load<TAIL>(row + d, D - d);
+      if (live && d < D) v[k].template load<TAIL, NT>(row + d, D - d);
       else v[k].clear();
     }
   }

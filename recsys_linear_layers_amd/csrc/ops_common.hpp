@@ -82,11 +82,18 @@ struct Chunk {
     }
   }
   // The n elements of a row from p on, as many as there are (the others 0).
-  // TAIL false: all VEC are there.
-  template <bool TAIL>
+  // TAIL false: all VEC are there.  NT: read once (non-temporal).
+  template <bool TAIL, bool NT = false>
   __device__ __forceinline__ void load(const raw* p, int n) {
     if (!TAIL || n >= VEC) {
-      __builtin_memcpy(this, p, sizeof(*this));
+      if constexpr (NT) {
+        typedef uint32_t words __attribute__((ext_vector_type(VEC / PER)));
+        typedef words unaligned_words __attribute__((aligned(sizeof(raw))));
+        const words v = __builtin_nontemporal_load((const unaligned_words*)p);
+        __builtin_memcpy(this, &v, sizeof v);
+      } else {
+        __builtin_memcpy(this, p, sizeof(*this));
+      }
     } else {
       clear();
 #pragma unroll

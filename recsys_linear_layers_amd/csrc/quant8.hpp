@@ -86,6 +86,7 @@ struct Quant8Args {
   int64_t ldx, ldq, ldqt;
   int64_t sn, sb, tn, tb;
   int32_t N, D;
+  int32_t aligned;  // rows of x start at multiples of 16 bytes
 };
 
 hipError_t launch_quant8(const Quant8Args& a, int type, int q_type, int block, int cus, hipStream_t s);

@@ -57,10 +57,10 @@ __global__ void __launch_bounds__(THREADS) rms_kernel(const RmsArgs a) {
   // every row group takes part in each step's barriers
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += step, r += step, flip ^= 1) {
     const bool live = r < a.N;
-    RowCols<TY, VEC, TPR, NCH, TAIL> cur;
+    RowCols<TY, VEC, TPR, NCH, TAIL, true> cur;
     cur.load(a.x, a.ldx, r, live, x, a.D);
     if (a.residual) {
-      RowCols<TY, VEC, TPR, NCH, TAIL> res;
+      RowCols<TY, VEC, TPR, NCH, TAIL, true> res;
       res.load(a.residual, a.ldr, r, live, x, a.D);
       raw* dst = (raw*)a.h + r * a.ldh;
 #pragma unroll
@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(THREADS) rms_kernel(const RmsArgs a) {
         const int d = (x + k * TPR) * VEC;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) cur.v[k].put(i, cur.v[k].get(i) + res.v[k].get(i));
-        if (live && d < a.D) cur.v[k].template store<TAIL>(dst + d, a.D - d);
+        if (live && d < a.D) cur.v[k].template store<TAIL, true>(dst + d, a.D - d);
       }
     }
     float s = 0.f;
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(const RmsGradArgs a) 
   int flip = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += step, r += step, flip ^= 1) {
     const bool live = r < a.N;
-    RowCols<TY, VEC, TPR, NCH, TAIL> vh, vd, ve;
+    RowCols<TY, VEC, TPR, NCH, TAIL, true> vh, vd, ve;
     vh.load(a.h, a.ldh, r, live, x, a.D);
     vd.load(a.dy, a.lddy, r, live, x, a.D);
     if (a.dh) ve.load(a.dh, a.lddh, r, live, x, a.D);
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(const RmsGradArgs a) 
           const float v = (vd.v[k].get(i) * g[i] - n * m) * rstd;
           o.put(i, a.dh ? v + ve.v[k].get(i) : v);
         }
-        o.template store<TAIL>(dst + d, a.D - d);
+        o.template store<TAIL, true>(dst + d, a.D - d);
       }
     }
   }
