@@ -361,9 +361,15 @@ def gemm8_run(desc: Gemm8Desc, A: int, a_scale: int, B: int, b_scale: int, C: in
 # launch on torch's current stream.
 # ---------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:  # asked for several times a call: the import statement alone takes 0.3 us
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _workspace(device, need: int):
@@ -380,15 +386,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype_code(dt) -> int:
-    torch = _torch()
-    if dt == torch.bfloat16:
-        return LL_BF16
-    if dt == torch.float32:
-        return LL_F32
-    if dt == torch.float16:
-        return LL_F16
-    raise TypeError(f"unsupported dtype {dt}")
+    if not _dtype_codes:
+        torch = _torch()
+        _dtype_codes.update({torch.bfloat16: LL_BF16, torch.float32: LL_F32, torch.float16: LL_F16})
+    code = _dtype_codes.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    return code
 
 
 class GemmPlan:
@@ -600,10 +608,10 @@ def _vector(t, n: int, what: str, dtypes):
 
 
 def _same_device(*ts) -> None:
-    dev = ts[0].device
-    for t in ts[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors on different devices: {dev}, {t.device}")
+    dev = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {ts[0].device}, {t.device}")
 
 
 def embedding(table, ids, scale: float = 1.0, out=None):
@@ -799,13 +807,17 @@ def vocab_xent_grad(x, w, target, dloss, ignore_index: int = -100, piece_bytes: 
 # Linear layers in 8 bits.
 # ---------------------------------------------------------------------------
 
+_codes8: dict = {}
+
+
 def _code8(dtype) -> int:
-    torch = _torch()
-    if dtype == torch.float8_e4m3fn:
-        return LL_E4M3
-    if dtype == torch.float8_e5m2:
-        return LL_E5M2
-    raise TypeError(f"unsupported 8-bit dtype {dtype} (float8_e4m3fn or float8_e5m2)")
+    if not _codes8:
+        torch = _torch()
+        _codes8.update({torch.float8_e4m3fn: LL_E4M3, torch.float8_e5m2: LL_E5M2})
+    code = _codes8.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported 8-bit dtype {dtype} (float8_e4m3fn or float8_e5m2)")
+    return code
 
 
 def _blocks8(n: int) -> int:
@@ -814,7 +826,9 @@ def _blocks8(n: int) -> int:
 
 def _new8(rows: int, cols: int, dtype, device):
     """[rows][cols] in rows of a multiple of 16 bytes, as gemm8 takes them."""
-    return _torch().empty((rows, -(-cols // 16) * 16), dtype=dtype, device=device)[:, :cols]
+    ld = -(-cols // 16) * 16
+    t = _torch().empty((rows, ld), dtype=dtype, device=device)
+    return t if ld == cols else t[:, :cols]
 
 
 def _new_scale8(rows: int, cols: int, squares: bool, device):
@@ -822,6 +836,8 @@ def _new_scale8(rows: int, cols: int, squares: bool, device):
     torch = _torch()
     if squares:
         return torch.empty((_blocks8(rows), _blocks8(cols)), dtype=torch.float32, device=device)
+    if rows == 1:
+        return torch.empty((1, _blocks8(cols)), dtype=torch.float32, device=device)
     return torch.empty((_blocks8(cols), rows), dtype=torch.float32, device=device).t()
 
 
@@ -829,31 +845,32 @@ def _scale_strides(t, what: str):
     """Strides of 2-D fp32 scales; along a dimension of one they do not matter."""
     if t.dim() != 2 or t.dtype != _torch().float32:
         raise ValueError(f"{what} must be 2-D and fp32")
-    return tuple(s if n > 1 else 1 for n, s in zip(t.shape, t.stride()))
+    (n, m), (s, r) = t.shape, t.stride()
+    return s if n > 1 else 1, r if m > 1 else 1
 
 
 def _rmsnorm(x, gamma, residual, eps, y, y_code, scale, residual_out):
     torch = _torch()
     N, D = x.shape
-    ptype = _norm_params(x, gamma)
+    ptype = x.dtype if gamma is None else _norm_params(x, gamma)
+    h, ld_r, ld_h = None, 0, 0
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
-        h = None
     else:
         if residual.shape != x.shape or residual.dtype != x.dtype:
             raise ValueError("residual must have x's shape and type")
-        h = x.new_empty((N, D)) if residual_out is None else residual_out
+        h = torch.empty((N, D), dtype=x.dtype, device=x.device) if residual_out is None else residual_out
         if h.shape != x.shape or h.dtype != x.dtype:
             raise ValueError("residual_out must have x's shape and type")
+        ld_r, ld_h = _rows(residual, "residual"), _rows(h, "residual_out")
     _same_device(x, gamma, residual, h, y)
     stream = _stream_of(x)
     rstd = torch.empty(N, dtype=torch.float32, device=x.device)
     code = _dtype_code(x.dtype)
     sn, sb = (1, 1) if scale is None else _scale_strides(scale, "scale")
-    desc = RmsnormDesc(N, D, _rows(x, "x"), 0 if h is None else _rows(residual, "residual"),
-                       0 if h is None else _rows(h, "residual_out"), _rows(y, "out"), sn, sb, code,
-                       _dtype_code(ptype), code if y_code is None else y_code, eps)
+    desc = RmsnormDesc(N, D, _rows(x, "x"), ld_r, ld_h, _rows(y, "out"), sn, sb, code,
+                       code if gamma is None else _dtype_code(ptype), code if y_code is None else y_code, eps)
     rmsnorm_run(desc, x.data_ptr(), _ptr(residual), _ptr(gamma), _ptr(h), y.data_ptr(), _ptr(scale), rstd.data_ptr(),
                 stream)
     return x if h is None else h, rstd
