@@ -355,17 +355,18 @@ constexpr int kCus = 256;  // that the choice is made for
 //   60.5 / 62, 128x256 73 / 76, 128x128 93 / 91; 128 x 8192 x 8192, 128x128 in four
 //   splits 23.2 / 23.1; 64 x 28672 x 8192, 64x128 47 / 49.
 //   Few rows: each CU's share of B comes at 10 bytes a clock (HBM; up to 25 where not
-//   all CUs ask), the rows of A, again for each workgroup, at 50 (L2), and the waits between them grow with the
-//   rows.  1 x 8192 x 8192, 16x16 14.8 / 12.3; 16 x 8192 x 8192, 16x32 15.7 / 13.6;
-//   64 x 8192 x 8192, 64x32 22.5 / 24.4 (64x128 in four splits 21 / 19.3); 64 x 4096 x
-//   4096, 64x16 10.6 / 11.8 (64x128 in four splits 14 / 13.5).
+//   all CUs ask), the rows of A, again for each workgroup, at 50 (L2), a workgroup
+//   takes 1.5 at least, and the waits between loads grow with the rows.  1 x 8192 x
+//   8192, 16x16 15.5 / 12.3; 16 x 8192 x 8192, 16x32 16.5 / 13.6; 64 x 8192 x 8192,
+//   64x32 22.6 / 24.4 (64x128 in four splits 21 / 19.3); 64 x 4096 x 4096, 64x16 10.6 /
+//   11.8 (64x128 in four splits 14 / 13.5); 29 x 19904 x 512, 32x16 11 / 12 (64x128 6 / 6).
 float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, int64_t steps) {
   const float rounds = (float)((tiles * splits + kCus - 1) / kCus);
   const float mn = (float)d.M * (float)d.N;
   const float join = splits > 1 ? 3.f + (float)splits * mn * 4.f / 3.0e6f : 0.f;
   if (kind >= kG8Tile64x128) {
     // an fp32 C is formed at about half the rate
-    const float work = kKinds[kind].step * (d.c_type == LL_F32 && kind > kG8Tile64x128 ? 1.8f : 1.f);
+    const float work = kKinds[kind].step * (d.c_type == LL_F32 ? 1.8f : 1.f);
     const float memory = (float)(d.M + d.N) * 128.f * (float)splits / rounds / 5.5e6f;
     const float step = std::max(work, memory);
     return 2.f + rounds * (2.5f + (float)steps * step) + join;
@@ -373,7 +374,7 @@ float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, i
   const float of_b = std::min(25.f, 10.f * kCus / (float)std::min<int64_t>(tiles * splits, kCus));
   const float rows = (float)std::min<int64_t>(d.M, kKinds[kind].bm);
   const float bytes = (float)steps * 128.f * ((float)kKinds[kind].bn / of_b + rows / 50.f);
-  return 2.f + 0.05f * (float)kKinds[kind].bm + rounds * bytes / 2100.f + join;
+  return 2.f + 0.05f * (float)kKinds[kind].bm + rounds * std::max(1.5f, bytes / 2100.f) + join;
 }
 
 }  // namespace
