@@ -13,7 +13,12 @@ gradient with the operators' own gradient calls: ``vocab_xent_grad`` never holds
 the [positions][items] logits, and ``embedding_grad(accumulate=True)`` adds the
 lookup's gradient to the one the loss left in the same table.
 
-    python examples/next_item.py [--steps 60]
+With --eight-bit the two products of the middle, and their gradients', take
+operands in 8 bits: the weights quantised once per update in squares of 128, the
+activations and gradients row by row, each as it lies and transposed
+(``quant8_pair``), the products by ``gemm8``.
+
+    python examples/next_item.py [--steps 60] [--eight-bit]
 """
 from __future__ import annotations
 
@@ -34,7 +39,7 @@ PAD = 0  # pads short histories; never predicted, and no gradient through the lo
 class NextItem:
     """Weights in bf16 beside fp32 master copies; gradients as the operators give them."""
 
-    def __init__(self, items: int, width: int, hidden: int, seed: int = 0):
+    def __init__(self, items: int, width: int, hidden: int, seed: int = 0, eight_bit: bool = False):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
 
@@ -51,6 +56,7 @@ class NextItem:
             "g2": torch.ones(width, device="cuda"), "c2": torch.zeros(width, device="cuda"),
         }
         self.w = {}
+        self.eight_bit = eight_bit
         self.refresh()
         self.moments = {k: (torch.zeros_like(v), torch.zeros_like(v)) for k, v in self.master.items()}
         self.steps = 0
@@ -59,6 +65,36 @@ class NextItem:
         """bf16 matrices for the products; vectors stay fp32."""
         for k, v in self.master.items():
             self.w[k] = v.to(torch.bfloat16) if v.dim() == 2 else v
+        if self.eight_bit:
+            self.w8 = {k: ll.quant8_pair(self.w[k], squares=True) for k in ("W1", "W2")}
+
+    def middle(self, n1):
+        """relu(n1 W1^T + b1) W2^T, and what its gradients need."""
+        w = self.w
+        if not self.eight_bit:
+            h = ll.gemm(n1, w["W1"].t(), bias=w["b1"], act="relu")
+            return ll.gemm(h, w["W2"].t()), (n1, h)
+        n8 = ll.quant8_pair(n1)
+        h = torch.relu(ll.gemm8(*n8[:2], *self.w8["W1"][:2]) + w["b1"].to(torch.bfloat16))
+        h8 = ll.quant8_pair(h)
+        return ll.gemm8(*h8[:2], *self.w8["W2"][:2]), (n8, h, h8)
+
+    def middle_grads(self, do, kept):
+        """(dn1, dW1, db1, dW2) from the gradient of the middle's result."""
+        w = self.w
+        if not self.eight_bit:
+            n1, h = kept
+            dh = ll.gemm(do, w["W2"]) * (h > 0)
+            dW2 = ll.gemm(do.t(), h, out_dtype=torch.float32)
+            dW1 = ll.gemm(dh.t(), n1, out_dtype=torch.float32)
+            return ll.gemm(dh, w["W1"]), dW1, dh.float().sum(0), dW2
+        n8, h, h8 = kept
+        d8 = ll.quant8_pair(do)
+        dh = ll.gemm8(*d8[:2], *self.w8["W2"][2:]) * (h > 0)
+        dW2 = ll.gemm8(*d8[2:], *h8[2:], out_dtype=torch.float32)
+        d8 = ll.quant8_pair(dh)
+        dW1 = ll.gemm8(*d8[2:], *n8[2:], out_dtype=torch.float32)
+        return ll.gemm8(*d8[:2], *self.w8["W1"][2:]), dW1, dh.float().sum(0), dW2
 
     def loss_and_grads(self, ids, target):
         """ids, target: int64 [positions] (target PAD: none).  Returns the mean loss
@@ -66,22 +102,19 @@ class NextItem:
         w, items = self.w, self.w["E"].shape[0]
         e = ll.embedding(w["E"], ids, scale=self.scale)
         n1, m1, r1 = ll.layernorm(e, w["g1"], w["c1"])
-        h = ll.gemm(n1, w["W1"].t(), bias=w["b1"], act="relu")
-        o = e + ll.gemm(h, w["W2"].t())
+        m, kept = self.middle(n1)
+        o = e + m
         n2, m2, r2 = ll.layernorm(o, w["g2"], w["c2"])
         live = target != PAD
         dloss = live.float() / live.sum().clamp_min(1)
         loss, _, dn2, dE = ll.vocab_xent_grad(n2, w["E"], target, dloss, ignore_index=PAD)
 
         do, dg2, dc2 = ll.layernorm_grad(dn2, o, m2, r2, w["g2"])
-        dh = ll.gemm(do, w["W2"]) * (h > 0)
-        dW2 = ll.gemm(do.t(), h, out_dtype=torch.float32)
-        dW1 = ll.gemm(dh.t(), n1, out_dtype=torch.float32)
-        dn1 = ll.gemm(dh, w["W1"])
+        dn1, dW1, db1, dW2 = self.middle_grads(do, kept)
         de, dg1, dc1 = ll.layernorm_grad(dn1, e, m1, r1, w["g1"])
         de += do
         ll.embedding_grad(ids, de, items, scale=self.scale, padding_idx=PAD, out=dE, accumulate=True)
-        grads = {"E": dE, "W1": dW1, "W2": dW2, "b1": dh.float().sum(0), "g1": dg1, "c1": dc1, "g2": dg2, "c2": dc2}
+        grads = {"E": dE, "W1": dW1, "W2": dW2, "b1": db1, "g1": dg1, "c1": dc1, "g2": dg2, "c2": dc2}
         return (loss * dloss).sum(), grads
 
     def update(self, grads, lr: float = 2e-3, b1: float = 0.9, b2: float = 0.99):
@@ -120,8 +153,9 @@ def main():
     ap.add_argument("--hidden", type=int, default=1024)
     ap.add_argument("--users", type=int, default=256)
     ap.add_argument("--length", type=int, default=32)
+    ap.add_argument("--eight-bit", action="store_true")
     a = ap.parse_args()
-    model = NextItem(a.items, a.width, a.hidden)
+    model = NextItem(a.items, a.width, a.hidden, eight_bit=a.eight_bit)
     ids, target = histories(a.users, a.length, a.items)
     for step in range(a.steps):
         loss, grads = model.loss_and_grads(ids, target)
@@ -131,7 +165,7 @@ def main():
     # scoring: how likely the model finds each next item, from the loss alone
     e = ll.embedding(model.w["E"], ids[:1], scale=model.scale)
     n1, _, _ = ll.layernorm(e, model.w["g1"], model.w["c1"])
-    o = e + ll.gemm(ll.gemm(n1, model.w["W1"].t(), bias=model.w["b1"], act="relu"), model.w["W2"].t())
+    o = e + model.middle(n1)[0]
     n2, _, _ = ll.layernorm(o, model.w["g2"], model.w["c2"])
     loss, _ = ll.vocab_xent(n2, model.w["E"], target[:1], ignore_index=PAD)
     print(f"log-likelihood of the first next item: {-loss.item():.4f}")
