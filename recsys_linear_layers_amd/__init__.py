@@ -595,15 +595,17 @@ def _stream_of(t):
 def _rows(t, what: str):
     """Row stride of a 2-D tensor whose last dimension is contiguous (one of a
     single row or column may have any stride)."""
-    if t.dim() != 2:
+    strides = t.stride()
+    if len(strides) != 2:
         raise ValueError(f"{what} must be 2-D")
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    n, m = t.shape
+    if m > 1 and strides[1] != 1:
         raise ValueError(f"{what}: last dimension must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+    return strides[0] if n > 1 else max(strides[0], m)
 
 
 def _vector(t, n: int, what: str, dtypes):
-    if tuple(t.shape) != (n,) or t.dtype not in dtypes or (n > 1 and t.stride(0) != 1):
+    if t.shape != (n,) or t.dtype not in dtypes or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous tensor of {n} values ({', '.join(map(str, dtypes))})")
 
 
@@ -660,12 +662,15 @@ def embedding_grad(ids, dout, rows: int, scale: float = 1.0, padding_idx: int | 
 
 def _norm_params(x, *params):
     """param_type of gamma and beta (None: ones, zeros)."""
-    given = [p for p in params if p is not None]
-    for p in given:
-        _vector(p, x.shape[1], "gamma and beta", (x.dtype, _torch().float32))
-        if p.dtype != given[0].dtype:
-            raise ValueError("gamma and beta must have one type")
-    return given[0].dtype if given else x.dtype
+    first = None
+    for p in params:
+        if p is not None:
+            _vector(p, x.shape[1], "gamma and beta", (x.dtype, _torch().float32))
+            if first is None:
+                first = p.dtype
+            elif p.dtype != first:
+                raise ValueError("gamma and beta must have one type")
+    return x.dtype if first is None else first
 
 
 def layernorm(x, gamma=None, beta=None, eps: float = 1e-5, out=None):
@@ -824,53 +829,57 @@ def _blocks8(n: int) -> int:
     return -(-n // 128)
 
 
-def _new8(rows: int, cols: int, dtype, device):
-    """[rows][cols] in rows of a multiple of 16 bytes, as gemm8 takes them."""
+def _new8(like, rows: int, cols: int, dtype):
+    """([rows][cols], row stride) in rows of a multiple of 16 bytes, as gemm8 takes them."""
     ld = -(-cols // 16) * 16
-    t = _torch().empty((rows, ld), dtype=dtype, device=device)
-    return t if ld == cols else t[:, :cols]
+    t = like.new_empty((rows, ld), dtype=dtype)
+    return (t if ld == cols else t[:, :cols]), ld
 
 
-def _new_scale8(rows: int, cols: int, squares: bool, device):
-    """Scales [rows][blocks of cols]; row scales with the rows of one block next to each other."""
-    torch = _torch()
+def _new_scale8(like, rows: int, cols: int, squares: bool):
+    """(scales [rows][blocks of cols], their strides); row scales with the rows of one block next to each other."""
+    f32, blocks = _torch().float32, _blocks8(cols)
     if squares:
-        return torch.empty((_blocks8(rows), _blocks8(cols)), dtype=torch.float32, device=device)
+        return like.new_empty((_blocks8(rows), blocks), dtype=f32), max(blocks, 1), 1
     if rows == 1:
-        return torch.empty((1, _blocks8(cols)), dtype=torch.float32, device=device)
-    return torch.empty((_blocks8(cols), rows), dtype=torch.float32, device=device).t()
+        return like.new_empty((1, blocks), dtype=f32), 1, 1
+    return like.new_empty((blocks, rows), dtype=f32).t(), 1, max(rows, 1)
 
 
 def _scale_strides(t, what: str):
     """Strides of 2-D fp32 scales; along a dimension of one they do not matter."""
-    if t.dim() != 2 or t.dtype != _torch().float32:
+    shape = t.shape
+    if len(shape) != 2 or t.dtype != _torch().float32:
         raise ValueError(f"{what} must be 2-D and fp32")
-    (n, m), (s, r) = t.shape, t.stride()
+    (n, m), (s, r) = shape, t.stride()
     return s if n > 1 else 1, r if m > 1 else 1
 
 
-def _rmsnorm(x, gamma, residual, eps, y, y_code, scale, residual_out):
-    torch = _torch()
-    N, D = x.shape
-    ptype = x.dtype if gamma is None else _norm_params(x, gamma)
+def _rmsnorm(x, gamma, residual, eps, y, ld_y, y_code, scale, sn, sb, residual_out):
+    shape, dtype = x.shape, x.dtype
+    N, D = shape
+    code = _dtype_code(dtype)
+    pcode = code if gamma is None else _dtype_code(_norm_params(x, gamma))
     h, ld_r, ld_h = None, 0, 0
     if residual is None:
         if residual_out is not None:
             raise ValueError("residual_out needs a residual")
     else:
-        if residual.shape != x.shape or residual.dtype != x.dtype:
+        if residual.shape != shape or residual.dtype != dtype:
             raise ValueError("residual must have x's shape and type")
-        h = torch.empty((N, D), dtype=x.dtype, device=x.device) if residual_out is None else residual_out
-        if h.shape != x.shape or h.dtype != x.dtype:
-            raise ValueError("residual_out must have x's shape and type")
-        ld_r, ld_h = _rows(residual, "residual"), _rows(h, "residual_out")
+        ld_r = _rows(residual, "residual")
+        if residual_out is None:
+            h, ld_h = x.new_empty(shape), D
+        else:
+            h = residual_out
+            if h.shape != shape or h.dtype != dtype:
+                raise ValueError("residual_out must have x's shape and type")
+            ld_h = _rows(h, "residual_out")
     _same_device(x, gamma, residual, h, y)
     stream = _stream_of(x)
-    rstd = torch.empty(N, dtype=torch.float32, device=x.device)
-    code = _dtype_code(x.dtype)
-    sn, sb = (1, 1) if scale is None else _scale_strides(scale, "scale")
-    desc = RmsnormDesc(N, D, _rows(x, "x"), ld_r, ld_h, _rows(y, "out"), sn, sb, code,
-                       code if gamma is None else _dtype_code(ptype), code if y_code is None else y_code, eps)
+    rstd = x.new_empty(N, dtype=_torch().float32)
+    desc = RmsnormDesc(N, D, _rows(x, "x"), ld_r, ld_h, ld_y, sn, sb, code, pcode, code if y_code is None else y_code,
+                       eps)
     rmsnorm_run(desc, x.data_ptr(), _ptr(residual), _ptr(gamma), _ptr(h), y.data_ptr(), _ptr(scale), rstd.data_ptr(),
                 stream)
     return x if h is None else h, rstd
@@ -884,9 +893,9 @@ def rmsnorm(x, gamma=None, residual=None, eps: float = 1e-6, out=None, residual_
     rstd (fp32 [N]) are what rmsnorm_grad takes."""
     if out is None:
         out = x.new_empty(x.shape)
-    if out.shape != x.shape or out.dtype != x.dtype:
+    elif out.shape != x.shape or out.dtype != x.dtype:
         raise ValueError("out must have x's shape and type")
-    h, rstd = _rmsnorm(x, gamma, residual, eps, out, None, None, residual_out)
+    h, rstd = _rmsnorm(x, gamma, residual, eps, out, _rows(out, "out"), None, None, 1, 1, residual_out)
     return out, h, rstd
 
 
@@ -897,8 +906,9 @@ def rmsnorm8(x, gamma=None, residual=None, eps: float = 1e-6, dtype=None, residu
     dtype = dtype or _torch().float8_e4m3fn
     code = _code8(dtype)
     N, D = x.shape
-    q, scale = _new8(N, D, dtype, x.device), _new_scale8(N, D, False, x.device)
-    h, rstd = _rmsnorm(x, gamma, residual, eps, q, code, scale, residual_out)
+    q, ld = _new8(x, N, D, dtype)
+    scale, sn, sb = _new_scale8(x, N, D, False)
+    h, rstd = _rmsnorm(x, gamma, residual, eps, q, ld, code, scale, sn, sb, residual_out)
     return q, scale, h, rstd
 
 
@@ -939,11 +949,11 @@ def _quant8(x, squares, dtype, plain, transposed):
     q = s = qt = st = None
     qs, qts, sn, sb, tn, tb = 0, 0, 1, 1, 1, 1
     if plain:
-        q, s = _new8(N, D, dtype, x.device), _new_scale8(N, D, squares, x.device)
-        qs, (sn, sb) = _rows(q, "q"), _scale_strides(s, "scale")
+        q, qs = _new8(x, N, D, dtype)
+        s, sn, sb = _new_scale8(x, N, D, squares)
     if transposed:
-        qt, st = _new8(D, N, dtype, x.device), _new_scale8(D, N, squares, x.device)
-        qts, (tn, tb) = _rows(qt, "qt"), _scale_strides(st, "scale")
+        qt, qts = _new8(x, D, N, dtype)
+        st, tn, tb = _new_scale8(x, D, N, squares)
     desc = Quant8Desc(N, D, _rows(x, "x"), qs, qts, sn, sb, tn, tb, _dtype_code(x.dtype), code, 128 if squares else 1)
     quant8_run(desc, x.data_ptr(), _ptr(q), _ptr(s), _ptr(qt), _ptr(st), stream)
     return q, s, qt, st
@@ -970,22 +980,24 @@ def quant8_pair(x, squares: bool = False, dtype=None):
 def gemm8_desc_for(a, a_scale, b, b_scale, out) -> Gemm8Desc:
     M, K = a.shape
     N, K2 = b.shape
-    if K2 != K or tuple(out.shape) != (M, N):
+    if K2 != K or out.shape != (M, N):
         raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, out {tuple(out.shape)}")
     kb = _blocks8(K)
     sa, sb = _scale_strides(a_scale, "a_scale"), _scale_strides(b_scale, "b_scale")
-    if tuple(a_scale.shape) != (M, kb):
+    if a_scale.shape != (M, kb):
         raise ValueError(f"a_scale must be [{M}][{kb}]")
-    if tuple(b_scale.shape) not in ((N, kb), (_blocks8(N), kb)):
+    squares = b_scale.shape == (_blocks8(N), kb)
+    if not squares and b_scale.shape != (N, kb):
         raise ValueError(f"b_scale must be [{_blocks8(N)}][{kb}] or [{N}][{kb}]")
     return Gemm8Desc(M, N, K, _rows16(a, "a"), _rows16(b, "b"), _rows(out, "out"), *sa, *sb, _code8(a.dtype),
-                     _code8(b.dtype), _dtype_code(out.dtype), 128 if b_scale.shape[0] == _blocks8(N) else 1)
+                     _code8(b.dtype), _dtype_code(out.dtype), 128 if squares else 1)
 
 
 def _rows16(t, what: str):
     """_rows of an operand of gemm8; the stride of a single row, or of empty ones, does not matter."""
     s = _rows(t, what)
-    return s if t.shape[0] > 1 and t.shape[1] > 0 else -(-t.shape[1] // 16) * 16
+    n, k = t.shape
+    return s if n > 1 and k > 0 else -(-k // 16) * 16
 
 
 def gemm8(a, a_scale, b, b_scale, out=None, out_dtype=None):
@@ -996,7 +1008,7 @@ def gemm8(a, a_scale, b, b_scale, out=None, out_dtype=None):
     16 bytes.  C is bf16 (default), fp16 or fp32."""
     torch = _torch()
     if out is None:
-        out = torch.empty((a.shape[0], b.shape[0]), dtype=out_dtype or torch.bfloat16, device=a.device)
+        out = a.new_empty((a.shape[0], b.shape[0]), dtype=out_dtype or torch.bfloat16)
     desc = gemm8_desc_for(a, a_scale, b, b_scale, out)
     _same_device(a, a_scale, b, b_scale, out)
     stream = _stream_of(a)
