@@ -9,6 +9,19 @@
 
 namespace ll {
 
+// n / d as (n * magic) >> shift, for n < 2^22 and d < 2^26: with 2^s the power of two
+// from d on, shift = 22 + s and magic = 2^shift / d + e, 0 < e <= 1, the product
+// is too large by n * e < 2^22 <= 2^shift / d, less than what would reach the next quotient.
+struct Quotient8 {
+  uint32_t magic, shift;
+};
+
+inline Quotient8 quotient8(uint32_t d) {
+  uint32_t s = 0;
+  while ((1u << s) < d) ++s;
+  return {(uint32_t)(((uint64_t)1 << (22 + s)) / d + 1), 22 + s};
+}
+
 struct Gemm8Args {
   const uint8_t* a;
   const uint8_t* b;
@@ -23,6 +36,8 @@ struct Gemm8Args {
   int32_t blocks;   // of 128 along K
   int32_t splits, per_split;  // K is split into runs of per_split blocks
   int32_t tiles_m, tiles_n, total;
+  int32_t cus;      // of the device
+  Quotient8 by_group, by_last;  // a tile's group (8 rows of tiles), and its column in a last group of fewer rows
 };
 
 // By rows and columns of C that a workgroup forms.

@@ -89,14 +89,12 @@ __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t vof
                : "memory");
 }
 
-// CNT consecutive columns of row m of C from column n on, or of the partials, in
-// 16-byte stores at whatever alignment; at the row's end one by one.
-template <int CNT>
-__device__ __forceinline__ void store_c8(const Gemm8Args& p, int split, int m, int n, const float (&v)[CNT]) {
-  if (m >= p.M || n >= p.N) return;
-  if (p.partial || p.c_type == LL_F32) {
-    float* dst = p.partial ? p.partial + ((int64_t)split * p.M + m) * p.N + n : (float*)p.c + (int64_t)m * p.ldc + n;
-    if (n + CNT <= p.N) {
+// The first `left` (all, if as many) of CNT values to consecutive places, in
+// 16-byte stores at whatever alignment; fewer go one by one.
+template <int TYPE, int CNT, typename E>
+__device__ __forceinline__ void store_piece8(E* dst, const float (&v)[CNT], int left) {
+  if constexpr (TYPE == LL_F32) {
+    if (left >= CNT) {
 #pragma unroll
       for (int i = 0; i < CNT; i += 4) {
         const f32x4 q = {v[i], v[i + 1], v[i + 2], v[i + 3]};
@@ -105,26 +103,34 @@ __device__ __forceinline__ void store_c8(const Gemm8Args& p, int split, int m, i
     } else {
 #pragma unroll
       for (int i = 0; i < CNT; ++i)
-        if (n + i < p.N) dst[i] = v[i];
+        if (i < left) dst[i] = v[i];
     }
-    return;
-  }
-  uint16_t* dst = (uint16_t*)p.c + (int64_t)m * p.ldc + n;
-  constexpr int VEC = CNT < 8 ? CNT : 8;
+  } else {
+    constexpr int VEC = CNT < 8 ? CNT : 8;
 #pragma unroll
-  for (int k = 0; k < CNT; k += VEC) {
-    if (p.c_type == LL_BF16) {
-      Chunk<LL_BF16, VEC> c;
+    for (int k = 0; k < CNT; k += VEC) {
+      Chunk<TYPE, VEC> c;
 #pragma unroll
       for (int i = 0; i < VEC; i += 2) c.put2(i, v[k + i], v[k + i + 1]);
-      c.template store<true>(dst + k, p.N - n - k);
-    } else {
-      Chunk<LL_F16, VEC> c;
-#pragma unroll
-      for (int i = 0; i < VEC; i += 2) c.put2(i, v[k + i], v[k + i + 1]);
-      c.template store<true>(dst + k, p.N - n - k);
+      c.template store<true>(dst + k, left - k);
     }
   }
+}
+
+// CNT consecutive columns of row m of C from column n on, or of the partials.
+template <int CNT>
+__device__ __forceinline__ void store_c8(const Gemm8Args& p, int split, int m, int n, const float (&v)[CNT]) {
+  if (m >= p.M || n >= p.N) return;
+  const int left = p.N - n;
+  const int64_t at = (int64_t)m * p.ldc + n;
+  if (p.partial)
+    store_piece8<LL_F32, CNT>(p.partial + ((int64_t)split * p.M + m) * p.N + n, v, left);
+  else if (p.c_type == LL_F32)
+    store_piece8<LL_F32, CNT>((float*)p.c + at, v, left);
+  else if (p.c_type == LL_BF16)
+    store_piece8<LL_BF16, CNT>((uint16_t*)p.c + at, v, left);
+  else
+    store_piece8<LL_F16, CNT>((uint16_t*)p.c + at, v, left);
 }
 
 }  // namespace ll

@@ -9,6 +9,13 @@
 // make eight (8 g + 4 (f % 2) + r of 32 to instruction f, lane group g, register
 // r).  So a store is 16 bytes, and a row's 64 bytes leave together.
 //
+// A workgroup stays on its CU and takes tile after tile; the loads run ahead over a
+// tile's end, so that the next tile's rows arrive while C is stored.  With a workgroup
+// per tile each began with empty LDS: 16384 x 28672 x 512 took 426 us, now 394; 3000 x
+// 28672 x 1000 (128x256) 135 and 120; 500 x 28672 x 4096 (64x128) 135 and 117; one
+// tile per CU (4096^3) 59.8 and 60.5; where the card's power is the bound (16384 x
+// 28672 x 8192) 3140 and 3112.
+//
 // A step is one block of 128 k: A's and B's rows of 128 bytes go straight from
 // memory to LDS (1 KB per instruction), two steps deep; one barrier per step.
 // The chunks of 16 bytes of a row are permuted so that the fragment reads touch
@@ -16,6 +23,9 @@
 // the buffer's range, which reads zeros; the bytes of a last piece past K are
 // cleared in LDS.
 #pragma once
+
+#include <algorithm>
+#include <type_traits>
 
 #include "gemm8_common.hpp"
 
@@ -58,15 +68,44 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / Cfg::WN, wn = wave % Cfg::WN;
 
-  // work item -> (split, tile); the XCDs take runs of neighbouring tiles, in
-  // groups of 8 tile rows, so that those in flight share panels in L2
-  const int item = xcd_remap(blockIdx.x, gridDim.x);
-  const int split = item / (p.tiles_m * p.tiles_n), tile = item - split * (p.tiles_m * p.tiles_n);
-  const int group = tile / (8 * p.tiles_n), in_group = tile - group * 8 * p.tiles_n;
-  const int height = min(8, p.tiles_m - group * 8);
-  const int tm = group * 8 + in_group % height, tn = in_group / height;
-  const int m0 = tm * Cfg::BM, n0 = tn * Cfg::BN;
+  // The arguments that only a change of tiles needs are read again there: kept in
+  // scalar registers through the steps they pushed others out of them.
+  auto args = []() __attribute__((always_inline)) -> const Gemm8Args& {
+    auto q = __builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(q));
+    return *(const Gemm8Args*)q;
+  };
+
+  // Work item -> (split, tile): the XCDs, which take workgroups in turn, get runs of
+  // neighbouring tiles, in groups of 8 tile rows, so that those in flight share
+  // panels in L2.  A workgroup takes every gridDim-th item; with a split K there are
+  // as many workgroups as items, so that a workgroup has one split.
+  struct Place {
+    int m0, n0;
+  };
+  auto item_of = [](const Gemm8Args& a, uint32_t raw) __attribute__((always_inline)) {
+    const uint32_t xcd = raw & 7, more = (uint32_t)a.total & 7;
+    return xcd * ((uint32_t)a.total >> 3) + min(xcd, more) + (raw >> 3);
+  };
+  const int split = p.splits > 1 ? item_of(p, blockIdx.x) / (uint32_t)(p.tiles_m * p.tiles_n) : 0;
   const int kb0 = split * p.per_split, kb1 = min(p.blocks, kb0 + p.per_split);
+  auto place = [&](const Gemm8Args& a, int raw) __attribute__((always_inline)) {
+    const uint32_t tile = item_of(a, raw) - split * a.tiles_m * a.tiles_n;
+    const uint32_t group = (uint32_t)((uint64_t)tile * a.by_group.magic >> a.by_group.shift);
+    const uint32_t in_group = tile - group * 8 * a.tiles_n;
+    const bool full = group < (uint32_t)a.tiles_m >> 3;
+    const uint32_t n = full ? in_group >> 3 : (uint32_t)((uint64_t)in_group * a.by_last.magic >> a.by_last.shift);
+    const uint32_t height = full ? 8 : a.tiles_m & 7;
+    return Place{(int)(group * 8 + in_group - n * height) * Cfg::BM, (int)n * Cfg::BN};
+  };
+  if (p.blocks == 0) {  // sums of nothing
+    for (int raw = blockIdx.x; raw < p.total; raw += gridDim.x) {
+      const Place t = place(p, raw);
+      for (int e = threadIdx.x; e < Cfg::BM * Cfg::BN / 4; e += Cfg::THREADS)
+store_c8<4>(p, 0, t.m0 + e / (Cfg::BN / 4), t.n0 + e % (Cfg::BN / 4) * 4, {0.f, 0.f, 0.f, 0.f});
+    }
+    return;
+  }
 
   // loads: instruction q = wave + i WAVES takes rows 8q .. 8q+7 of the tile, lane
   // l row l / 8 of them, position l % 8.  The offset of a lane outside the
@@ -77,64 +116,101 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   const int la = ((lane & 7) ^ swz8_a(lrow)) << 4;
   static_assert(Cfg::WAVES * 8 % 16 == 0, "A's rows of a lane have one permutation");
   const uint32_t va = (uint32_t)((lane >> 3) * (int)p.lda + la);
-  const i32x4 rsrc_a = make_rsrc(p.a + ((int64_t)m0 + wave * 8) * p.lda, 0x7FFFFFF0u);
-  const i32x4 rsrc_b = make_rsrc(p.b + ((int64_t)n0 + wave * 8) * p.ldb, 0x7FFFFFF0u);
   const int a_step = Cfg::WAVES * 8 * (int)p.lda, b_step = Cfg::WAVES * 8 * (int)p.ldb;
-  int k_next = kb0 * 128, k_end = kb0 < kb1 ? p.K : 0;  // of the next step to be loaded (k_end 0: there is none)
   // scales: a wave takes 64 rows, of A's or (behind them) of B's; what nobody
   // reads (B's without ROWS) is zeros
   constexpr int SA_WAVES = (Cfg::BM + 63) / 64;
   const bool of_a = wave < SA_WAVES;
   const int srow = (of_a ? wave : wave - SA_WAVES) * 64 + lane;
-  const bool s_live = of_a ? srow < Cfg::BM && m0 + srow < p.M : ROWS && srow < Cfg::BN && n0 + srow < p.N;
-  const uint32_t vs = s_live ? (uint32_t)(srow * (int)(of_a ? p.sam : p.sbn)) * 4u : kOOB;
   const int64_t s_step = of_a ? p.sab : p.sbb;
-  const float* ps = (of_a ? p.sa + (int64_t)m0 * p.sam : ROWS ? p.sb + (int64_t)n0 * p.sbn : p.sb) + kb0 * s_step;
+  // The step that is loaded next, of a tile that may be ahead of the one being formed.
+  const int k_stop = kb1 * 128;
+  int l_raw = (int)blockIdx.x - (int)gridDim.x, m_left = 0, n_left = 0;  // rows of A and B from the tile's first on
+  int k_next = k_stop, k_end = 0;                                        // k_end 0: there is no such step
+  i32x4 rsrc_a = make_rsrc(p.a, 0x7FFFFFF0u), rsrc_b = make_rsrc(p.b, 0x7FFFFFF0u);
+  uint32_t vs = kOOB;
+  const float* ps = p.sa;
+  auto enter = [&]() __attribute__((always_inline)) {  // the next tile
+    const Gemm8Args& a = args();
+    l_raw = min(l_raw + (int)gridDim.x, a.total);
+    const Place t = place(a, min(l_raw, a.total - 1));
+    m_left = a.M - t.m0;
+    n_left = a.N - t.n0;
+    k_next = kb0 * 128;
+    k_end = l_raw < a.total ? a.K : 0;
+    rsrc_a = make_rsrc(a.a + (uint64_t)(uint32_t)(t.m0 + wave * 8) * (uint32_t)a.lda, 0x7FFFFFF0u);
+    rsrc_b = make_rsrc(a.b + (uint64_t)(uint32_t)(t.n0 + wave * 8) * (uint32_t)a.ldb, 0x7FFFFFF0u);
+    const uint32_t stride = of_a ? (uint32_t)a.sam : (uint32_t)a.sbn;
+    const bool live = of_a ? srow < Cfg::BM && srow < m_left : ROWS && srow < Cfg::BN && srow < n_left;
+    vs = live ? (uint32_t)srow * stride * 4u : kOOB;
+    ps = (of_a ? a.sa : a.sb) + (of_a || ROWS ? (uint64_t)(uint32_t)(of_a ? t.m0 : t.n0) * stride : 0) + kb0 * s_step;
+  };
 
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane(lds_u32((const char LL_LDS*)lds));
   constexpr uint32_t SC = Cfg::SLOTS * Cfg::SLOT;  // scales: per step, A's then B's
   // Load i (of QA + QB + 1) of the next step into its slot; past the last step it
   // reads nothing and writes zeros that nobody reads.
   constexpr int LOADS = Cfg::QA + Cfg::QB + 1;
-  auto issue = [&](int i, int slot, int sslot) {
+  auto issue = [&](int i, int slot, int sslot) __attribute__((always_inline)) {
     const uint32_t at = lds0 + slot * Cfg::SLOT + wave * 1024;
     if (i < Cfg::QA) {
-      const bool in = m0 + lrow + i * Cfg::WAVES * 8 < p.M && la < k_end - k_next;
+      const bool in = lrow + i * Cfg::WAVES * 8 < m_left && la < k_end - k_next;
       dma16s(rsrc_a, at + i * Cfg::WAVES * 1024, in ? va : kOOB, (uint32_t)(k_next + i * a_step));
     } else if (i < Cfg::QA + Cfg::QB) {
       const int q = i - Cfg::QA, lb = chunk_b(q);
-      const bool in = n0 + lrow + q * Cfg::WAVES * 8 < p.N && lb < k_end - k_next;
+      const bool in = lrow + q * Cfg::WAVES * 8 < n_left && lb < k_end - k_next;
       dma16s(rsrc_b, at + Cfg::A_BYTES + q * Cfg::WAVES * 1024,
              in ? (uint32_t)((lane >> 3) * (int)p.ldb + lb) : kOOB, (uint32_t)(k_next + q * b_step));
     } else {
       dma4(make_rsrc(ps, k_end ? 0x7FFFFFF0u : 0u), lds0 + SC + sslot * Cfg::SCALES + wave * 256, vs);
     }
   };
-  auto issued = [&]() {
-    k_next += 128;
-    ps += s_step;
-    if (k_next >= kb1 * 128) k_end = 0;
-  };
-
   // fragments: lane l takes row l % 16 and chunks l / 16 and l / 16 + 4
   const int row16 = lane & 15, g = lane >> 4;
   const int arow = wm * Cfg::TM + row16;
   const int brow = wn * Cfg::TN + (row16 >> 2) * 4 * GF + (row16 & 3);
   const int a_off = arow * 128 + ((g ^ swz8_a(arow)) << 4);                            // + 2048 i
   const int b_off = Cfg::A_BYTES + brow * 128 + ((g ^ swz8_b<GF>(brow)) << 4);  // + 128 col_of(f)
-  const int sb_row = (n0 + wn * Cfg::TN) / 128;                                         // block row of B, unless ROWS
-
-  const float __attribute__((address_space(4))) * sbs =
-      (const float __attribute__((address_space(4)))*)(p.sb + (int64_t)min(sb_row, (p.N - 1) / 128) * p.sbn);
+  // B's scales of squares: of the step's block row, unless ROWS
+  typedef const float __attribute__((address_space(4))) * ScalePtr;
+  auto squares_of = [&](const Gemm8Args& a, const Place& t) __attribute__((always_inline)) {
+    return (ScalePtr)(a.sb + (int64_t)min((t.n0 + wn * Cfg::TN) / 128, (a.N - 1) / 128) * a.sbn + kb0 * a.sbb);
+  };
 
   f32x4 acc[FM][FN];
+  // One type, and pieces known to be whole, at a time: with every choice made at every
+  // piece the stores' code was 40 KB, most of it jumped over.
+  auto store = [&](const Place& t) __attribute__((always_inline)) {
+    const Gemm8Args& a = args();
+    const int m = t.m0 + wm * Cfg::TM + row16, n = t.n0 + wn * Cfg::TN + 4 * GF * g;
+    auto pieces = [&](auto type, auto whole) __attribute__((always_inline)) {
+      constexpr int TYPE = decltype(type)::value;
+      typedef typename std::conditional<TYPE == LL_F32, float, uint16_t>::type E;
+      E* const base = a.partial ? (E*)(a.partial + ((int64_t)split * a.M + m) * a.N + n) : (E*)a.c + m * a.ldc + n;
+      const int64_t ld = 16 * (a.partial ? a.N : a.ldc);
 #pragma unroll
-  for (int i = 0; i < FM; ++i)
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int f = 0; f < FN; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
-
+        for (int f = 0; f < FN; f += GF) {
+          float v[4 * GF];
+#pragma unroll
+          for (int q = 0; q < 4 * GF; ++q) v[q] = acc[i][f + q / 4][q % 4];
+          const int left = a.N - n - col_of(f);
+          if (m + 16 * i < a.M && left > 0)
+            store_piece8<TYPE, 4 * GF>(base + i * ld + col_of(f), v, decltype(whole)::value ? 4 * GF : left);
+        }
+    };
+    auto typed = [&](auto whole) __attribute__((always_inline)) {
+      if (EXACT || a.partial) pieces(std::integral_constant<int, LL_F32>(), whole);
+      else if (a.c_type == LL_BF16) pieces(std::integral_constant<int, LL_BF16>(), whole);
+      else pieces(std::integral_constant<int, LL_F16>(), whole);
+    };
+    if (a.N % (4 * GF) == 0 || t.n0 + Cfg::BN <= a.N) typed(std::true_type());
+    else typed(std::false_type());
+  };
+  const int tail = p.K & 15 ? p.K / 128 : -1;  // the block whose last piece K ends in
   // Clears the bytes past K of the piece that K ends in.
-  auto clear_tail = [&](int slot) {
+  auto clear_tail = [&](int slot) __attribute__((always_inline)) {
     const int c = (p.K & 127) >> 4;
     for (int row = threadIdx.x; row < Cfg::BM + Cfg::BN; row += Cfg::THREADS) {
       const bool of_a = row < Cfg::BM;
@@ -144,12 +220,12 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
     }
     __syncthreads();
   };
-  // The rows of the slot of step kb are there, for every wave.
-  auto arrive = [&](int kb, int slot) {
+  // The rows of the next step are in their slot, for every wave, and nobody reads
+  // those of the step before: the loads of another may begin there.
+  auto landed = [&]() __attribute__((always_inline)) {
     static_assert((Cfg::SLOTS - 2) * LOADS < 64, "vmcnt");
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"((Cfg::SLOTS - 2) * LOADS) : "memory");  // those of later steps stay under way
     lds_barrier();
-    if (kb * 128 < p.K && kb * 128 + 128 > p.K && (p.K & 15)) clear_tail(slot);
   };
   auto read_x = [&](const char* st, int i) {
     return frag8(*(const i32x4*)(st + a_off + 2048 * i), *(const i32x4*)(st + (a_off ^ 64) + 2048 * i));
@@ -173,62 +249,75 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
   constexpr int PACE = EXACT && T >= 24 ? 2 : 1, AT_ONCE = (LOADS * PACE + T - 1) / T;
   constexpr int EARLY = FN / PACE * AT_ONCE < LOADS ? FN / PACE * AT_ONCE : LOADS;
   static_assert(FN % PACE == 0 && T % PACE == 0, "loads of a step");
-  f32x4 d[ND];
+  f32x4 d[ND], sbv[FEW_SB ? 1 : FN];  // sbv (ROWS): of all f, or (EXACT, whose operands take the registers) of the last product
+  i32x8 wr[FN], xr[2];
+  typename Block::W w[FN];
+  typename Block::X x;
+  float s = 0.f, sa_next = 0.f, sb = 0.f, sb_next = 0.f;  // s: scale of the last row of products
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-  for (int i = 0; i < ND; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (kb0 < kb1) {
+    for (int i = 0; i < FM; ++i)
 #pragma unroll
-    for (int n = 0; n < Cfg::SLOTS - 1; ++n) {
+      for (int f = 0; f < FN; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < LOADS; ++i) issue(i, n, n);
-      issued();
-    }
-    arrive(kb0, 0);
-#pragma unroll
-    for (int i = 0; i < EARLY; ++i) issue(i, Cfg::SLOTS - 1, Cfg::SLOTS - 1);
-    i32x8 wr[FN], xr[2];
-    f32x4 sbv[FEW_SB ? 1 : FN];  // ROWS: of all f, or (EXACT, whose operands take the registers) of the last product
-    typename Block::W w[FN];
-    float s_last = 0.f, sa_next, sb = 0.f;
-    if constexpr (!ROWS) sb = sbs[(int64_t)kb0 * p.sbb];
-    xr[0] = read_x(lds, 0);
-    sa_next = *(const float*)(lds + sa_off);
-#pragma unroll
-    for (int f = 0; f < FN; ++f) wr[f] = read_w(lds, f);
+    for (int i = 0; i < ND; ++i) d[i] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int f = 0; f < (FEW_SB ? 1 : FN); ++f) sbv[f] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto add = [&](int t, float s) {
+    s = 0.f;
+  };
+  auto add = [&](int t) __attribute__((always_inline)) {
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        acc[t / FN][t % FN][r] =
-            fmaf(d[t % ND][r], ROWS ? s * sbv[FEW_SB ? 0 : t % FN][r] : s, acc[t / FN][t % FN][r]);
-      asm volatile("" : "+v"(acc[t / FN][t % FN]));  // here, not where the compiler would sink them to
-    };
-    int slot = 0, s0 = 0;  // slots of this step's rows and scales
+    for (int r = 0; r < 4; ++r)
+      acc[t / FN][t % FN][r] =
+          fmaf(d[t % ND][r], ROWS ? s * sbv[FEW_SB ? 0 : t % FN][r] : s, acc[t / FN][t % FN][r]);
+    asm volatile("" : "+v"(acc[t / FN][t % FN]));  // here, not where the compiler would sink them to
+  };
+
+#pragma nounroll
+  for (int n = 0;; ++n) {
+    if (k_next >= k_stop) enter();
+    if (n == Cfg::SLOTS - 1) break;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) issue(i, n, n);
+    k_next += 128;
+    ps += s_step;
+  }
+  landed();
+  if (kb0 == tail) clear_tail(0);
+#pragma unroll
+  for (int i = 0; i < EARLY; ++i) issue(i, Cfg::SLOTS - 1, Cfg::SLOTS - 1);
+  xr[0] = read_x(lds, 0);
+  sa_next = *(const float*)(lds + sa_off);
+#pragma unroll
+  for (int f = 0; f < FN; ++f) wr[f] = read_w(lds, f);
+  int slot = 0, s0 = 0;  // of the step's rows and scales
+  Place at = place(p, blockIdx.x);
+  ScalePtr squares = squares_of(p, at);
+  if constexpr (!ROWS) sb = *squares;
+  for (int raw = blockIdx.x;;) {
+    clear();
+    raw += gridDim.x;
+    const bool more = raw < p.total;
+    ScalePtr squares_then = squares;
+    if (!ROWS && more) squares_then = squares_of(args(), place(args(), raw));
     for (int kb = kb0; kb < kb1; ++kb) {
+      const bool last = kb + 1 == kb1;
       const int slot1 = slot + 1 < Cfg::SLOTS ? slot + 1 : 0, s1 = s0 < Cfg::SLOTS ? s0 + 1 : 0;  // of the next step
       const int slot_before = slot > 0 ? slot - 1 : Cfg::SLOTS - 1;  // free since the last barrier
       const int s_last2 = s0 >= 2 ? s0 - 2 : s0 + Cfg::SLOTS - 1, s_last1 = s0 >= 1 ? s0 - 1 : Cfg::SLOTS;
       const char* st = lds + slot * Cfg::SLOT;
       const char* next = lds + slot1 * Cfg::SLOT;
       const char* sc = lds + s0 * Cfg::SCALES;
-      float sb_next = 0.f;
-      if constexpr (!ROWS) sb_next = sbs[(int64_t)min(kb + 1, kb1 - 1) * p.sbb];
-      float s = 0.f;
-      typename Block::X x;
-#pragma unroll
-      for (int t = 0; t < T; ++t) {
+      squares = last ? squares_then : squares + p.sbb;
+      if constexpr (!ROWS) sb_next = *squares;
+      auto product = [&](int t) __attribute__((always_inline)) {
         const int i = t / FN, f = t % FN;
-        if (f == 0) {
-          if (i == FM - 1) arrive(kb + 1, slot1);
-          x = Block::x(xr[i & 1]);
-        }
+        if (f == 0) x = Block::x(xr[i & 1]);
         if (i == 0) w[f] = Block::w(wr[f]);
         if (EXACT) __builtin_amdgcn_s_setprio(1);  // 2212 -> 2169 us; without EXACT 1 or 2% slower
         d[t % ND] = Block::product(w[f], x);
         if (EXACT) __builtin_amdgcn_s_setprio(0);
-        if (t < LAG) add(T + t - LAG, s_last);
-        else add(t - LAG, s);
+        add((t + T - LAG) % T);
         if (f == LAG - 1) s = ROWS ? sa_next : sa_next * sb;  // of this row of products from here on
         if (ROWS && FEW_SB) sbv[0] = *(const f32x4*)(sc + sb_off + 4 * col_of(f));
         if (ROWS && !FEW_SB && t == LAG - 1) {
@@ -246,43 +335,49 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
           for (int n = 0; n < AT_ONCE; ++n) {
             const int q = t / PACE * AT_ONCE + n + EARLY;
             if (q < LOADS && i < FM - 1) issue(q, slot_before, s_last2);
-            if (q == LOADS - 1 && i < FM - 1) issued();
           }
 #pragma unroll
           for (int n = 0; n < AT_ONCE; ++n) {
             const int q = f / PACE * AT_ONCE + n;
             if (i == FM - 1 && q < EARLY) issue(q, slot, s_last1);
-            if (i == FM - 1 && q == LOADS - 1) issued();
           }
         }
+      };
+#pragma unroll
+      for (int t = 0; t < T - FN; ++t) product(t);
+      k_next += 128;
+      ps += s_step;
+      landed();
+      const bool cut = (last ? kb0 : kb + 1) == tail, end = k_next >= k_stop;
+      if (cut || end) {
+        if (cut) clear_tail(slot1);
+        if (end) enter();
       }
-      s_last = s;
+#pragma unroll
+      for (int t = T - FN; t < T; ++t) product(t);
       sb = sb_next;
       slot = slot1;
       s0 = s1;
     }
 #pragma unroll
-    for (int t = T - LAG; t < T; ++t) add(t, s_last);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
+    for (int t = T - LAG; t < T; ++t) add(t);
+    store(at);
+    if (!more) break;
+    at = place(args(), raw);
   }
-
-#pragma unroll
-  for (int i = 0; i < FM; ++i)
-#pragma unroll
-    for (int f = 0; f < FN; f += GF) {
-      float v[4 * GF];
-#pragma unroll
-      for (int q = 0; q < 4 * GF; ++q) v[q] = acc[i][f + q / 4][q % 4];
-      store_c8<4 * GF>(p, split, m0 + wm * Cfg::TM + 16 * i + row16, n0 + wn * Cfg::TN + col_of(f) + 4 * GF * g, v);
-    }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // no load into LDS outlives the workgroup
 }
 
 template <class Cfg, bool EXACT>
-hipError_t launch_gemm8_tile(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s) {
+hipError_t launch_gemm8_tile(const Gemm8Args& args, bool a_e5m2, bool rows, hipStream_t s) {
   auto kernel = a_e5m2 ? (rows ? gemm8_tile_kernel<Cfg, true, true, EXACT> : gemm8_tile_kernel<Cfg, true, false, EXACT>)
                        : (rows ? gemm8_tile_kernel<Cfg, false, true, EXACT>
                                : gemm8_tile_kernel<Cfg, false, false, EXACT>);
-  hipLaunchKernelGGL(kernel, dim3((unsigned)a.total), dim3(Cfg::THREADS), 0, s, a);
+  Gemm8Args a = args;
+  a.by_group = quotient8(8u * (uint32_t)a.tiles_n);
+  a.by_last = quotient8(std::max(1u, (uint32_t)a.tiles_m & 7));
+  const int grid = a.splits > 1 ? a.total : std::min(a.total, a.cus);
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(Cfg::THREADS), 0, s, a);
   return hipGetLastError();
 }
 

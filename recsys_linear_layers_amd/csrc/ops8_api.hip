@@ -320,6 +320,7 @@ ll_status gemm8_run(const gemm8_desc* d, const void* A, const float* a_scale, co
   a.tiles_m = plan.tiles_m;
   a.tiles_n = plan.tiles_n;
   a.total = plan.tiles_m * plan.tiles_n * plan.splits;
+  a.cus = info->cus;
   hipError_t err = launch_gemm8(a, plan.kind, d->a_type == LL_E5M2, d->b_block == 1, (hipStream_t)stream);
   if (err == hipSuccess && a.partial)
     err = launch_splitk_reduce(a.partial, plan.splits, d->M, d->N, C, d->stride_c, 1,
