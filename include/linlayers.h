@@ -643,12 +643,11 @@ ll_status quant8_run(const quant8_desc* desc, const void* x, void* q, float* sca
  * A [M][K] of a_type (LL_E4M3 or LL_E5M2), block 1; B [N][K], LL_E4M3, b_block 1
  * or 128; C [M][N] of c_type (LL_BF16, LL_F16 or LL_F32), rows stride_c apart.
  * A block's sum is formed by the matrix unit, the scaled sums are added in fp32 in
- * ascending order of b (in several runs of blocks, then joined in order, where K
- * is split), and C is rounded once, to nearest even.  With an fp32 C the blocks'
- * sums have fp32's precision.  With a 16-bit C they come from the 8-bit matrix
- * instruction, twice as fast, which drops from the products of a group of eight
- * what lies below 2^-13 of the largest: about 1.4e-5 of the result's norm, where
- * C's rounding is 1.6e-3 (bf16) or 2e-4 (fp16).  Equal inputs
+ * an order that the sizes alone decide, and C is rounded once, to nearest even.
+ * With an fp32 C the blocks' sums have fp32's precision.  With a 16-bit C they come
+ * from the 8-bit matrix instruction, twice as fast, which drops from the products
+ * of a group of eight what lies below 2^-13 of the largest: about 1.4e-5 of the
+ * result's norm, where C's rounding is 1.6e-3 (bf16) or 2e-4 (fp16).  Equal inputs
  * give equal bits.  A layer's gradients are the same product: dX = dY W takes W
  * quantised transposed, dW = dY^T X takes dY and X quantised transposed, b_block 1.
  * A and B must be 16-byte aligned, stride_a and stride_b multiples of 16 (what
@@ -659,9 +658,10 @@ ll_status quant8_run(const quant8_desc* desc, const void* x, void* q, float* sca
  * Errors: LL_ERR_INVALID_ARG (null desc or pointer, negative size, stride below
  * the row, misaligned operand, scale stride below 1, b_block, C overlapping an
  * input or the workspace), LL_ERR_UNSUPPORTED (types, M, N of 2^26 and more, C of
- * more than 2^22 tiles of 256 x 256, K of 2^22 and more, stride_a or stride_b of 2^22 and more, scale strides along rows
- * of 2^20 and more, strides that put a row or block 2^58 elements or more from
- * the first, device), LL_ERR_WORKSPACE, LL_ERR_NO_DEVICE, LL_ERR_HIP.
+ * more than 2^22 tiles of 256 x 256, K of 2^22 and more, stride_a or stride_b of
+ * 2^22 and more, scale strides along rows of 2^20 and more, strides that put a row
+ * or block 2^58 elements or more from the first, device), LL_ERR_WORKSPACE,
+ * LL_ERR_NO_DEVICE, LL_ERR_HIP.
  */
 typedef struct {
   int64_t M, N, K;

@@ -890,7 +890,8 @@ def rmsnorm(x, gamma=None, residual=None, eps: float = 1e-6, out=None, residual_
     type, and y = h * rstd * gamma with rstd = 1 / sqrt(mean(h^2) + eps) over the
     rows of x [N][D] (bf16, fp16 or fp32, any row stride).  gamma [D] of x's type
     or fp32, or None.  residual_out: where h goes, may be residual or x.  h and
-    rstd (fp32 [N]) are what rmsnorm_grad takes."""
+    rstd (fp32 [N]) are what rmsnorm_grad takes; out may be x without a residual,
+    whose values (h) are then gone."""
     if out is None:
         out = x.new_empty(x.shape)
     elif out.shape != x.shape or out.dtype != x.dtype:

@@ -43,8 +43,12 @@ def _check(got, ref, S, K):
     import helpers8 as h
     aligned = 0.0 if got.dtype == torch.float32 else 7 * 2.0 ** -13
     tol = ((256 + h.blocks(K) + 3 + 64) * h.U + aligned) * S + ref.abs() * h.HALF_STEP[got.dtype] * (1 + 2 ** -10) + h.SMALL_STEP[got.dtype]
-    assert bool(torch.isfinite(got).all())
-    off = (got.double() - ref).abs() - tol
+    # a value that rounds beyond the type's largest is infinite: half a step above it
+    most = torch.finfo(got.dtype).max * (1 + h.HALF_STEP[got.dtype] / 2)
+    beyond = torch.isinf(got)
+    assert not bool(torch.isnan(got).any()) and bool((ref.abs() + tol >= most)[beyond].all())
+    assert bool((torch.sign(got) == torch.sign(ref))[beyond].all())
+    off = torch.where(beyond, 0.0, (got.double() - ref).abs()) - tol
     assert bool((off <= 0).all()), (off.max().item(), (off > 0).sum().item())
 
 
@@ -91,6 +95,25 @@ def test_every_kernel_and_split(monkeypatch, kind, M, N, K, splits):
             out = a.new_empty((M, N), dtype=t[c])
             assert f"kernel={kind} " in ll.gemm8_describe(ll.gemm8_desc_for(a, sa, b, sb, out))
             _check(ll.gemm8(a, sa, b, sb, out=out), ref, S, K)
+
+
+@pytest.mark.parametrize("kind,bm,bn", [("TILE64x128", 64, 128), ("TILE128x128", 128, 128), ("TILE128x256", 128, 256),
+                                        ("TILE256x256", 256, 256)])
+@pytest.mark.parametrize("K", [20, 128, 260, 1000])
+def test_more_tiles_than_compute_units(monkeypatch, kind, bm, bn, K):
+    """Workgroups that take several tiles, of one step each and of several, in 9 rows of
+    tiles (a group of 8 and a row alone), with short last pieces of K at each tile's end."""
+    import recsys_linear_layers_amd as ll
+    t = _types()
+    monkeypatch.setenv("LL_GEMM8_KIND", kind)
+    monkeypatch.setenv("LL_GEMM8_SPLITS", "1")
+    M, N = 9 * bm - 5, 61 * bn - 3
+    for squares in (True, False):
+        a, sa = _operand(M, K, 1, t["e5m2"] if squares else t["e4m3"], False, pad=1)
+        b, sb = _operand(N, K, 3, t["e4m3"], squares)
+        ref, S = _reference(a, sa, b, sb, squares)
+        for c in ("bf16", "f16", "f32"):
+            _check(ll.gemm8(a, sa, b, sb, out_dtype=t[c]), ref, S, K)
 
 
 def test_integers_are_exact():
