@@ -342,40 +342,44 @@ const struct {
 } kKinds[kG8Kinds] = {
     {"FEW16x16", 16, 16, 0.f},          {"FEW16x32", 16, 32, 0.f},          {"FEW32x16", 32, 16, 0.f},
     {"FEW32x32", 32, 32, 0.f},          {"FEW64x16", 64, 16, 0.f},          {"FEW64x32", 64, 32, 0.f},
-    {"TILE64x128", 64, 128, 0.44f},     {"TILE128x128", 128, 128, 0.63f},   {"TILE128x256", 128, 256, 1.03f},
-    {"TILE256x256", 256, 256, 1.75f}};
+    {"TILE64x128", 64, 128, 0.47f},     {"TILE128x128", 128, 128, 0.61f},   {"TILE128x256", 128, 256, 0.95f},
+    {"TILE256x256", 256, 256, 1.60f}};
 
 constexpr int kCus = 256;  // that the choice is made for
 
-// What a kernel takes, in microseconds, as far as the choice needs it.
-//   Tiles: a round of workgroups over the CUs takes its steps, each at least as long
-//   as its rows of A and B come from memory (5.5 TB/s), and 2.5 for the first loads
-//   and the stores; a split K adds a launch and the partials' bytes, written
-//   and read.  Estimate and measured time (MI355X, bf16 C): 1024 x 4096 x 4096,
-//   128x128 24.7 / 24.6; 2048 x 4096 x 4096, 128x256 37.5 / 37.7; 4096^3, 256x256
-//   60.5 / 62, 128x256 73 / 76, 128x128 93 / 91; 128 x 8192 x 8192, 128x128 in four
-//   splits 23.2 / 23.1; 64 x 28672 x 8192, 64x128 47 / 49.
+// What a kernel takes, in microseconds, as far as the choice needs it: 60 drawn
+// problems, of 1 to 16384 rows, took 2% longer on average than with the best
+// kernel and split of each.
+//   Tiles: 4.2 before the first step and after the last store; a round of tiles over
+//   the CUs takes its steps, each at least as long as its rows of A and B come
+//   from memory, and its stores (both 5.5 TB/s); a split K adds a launch and the
+//   partials' bytes, written and read.  Estimate and measured time (MI355X, bf16 C):
+//   1024 x 4096 x 4096, 128x128 26 / 26; 2048 x 4096 x 4096, 128x256 39 / 38; 4096^3,
+//   256x256 62.5 / 61.5, 128x256 73 / 71, 128x128 92 / 91; 64 x 8192 x 8192, 64x128 in
+//   four splits 25 / 19.5; 29 x 19904 x 512, 64x128 7.5 / 7.0; 9690 x 1600 x 192 to fp32,
+//   128x128 30 / 25 (256x256 34).
 //   Few rows: each CU's share of B comes at 10 bytes a clock (HBM; up to 25 where not
-//   all CUs ask), the rows of A, again for each workgroup, at 50 (L2), a workgroup
-//   takes 1.5 at least, and the waits between loads grow with the rows.  1 x 8192 x
-//   8192, 16x16 15.5 / 12.3; 16 x 8192 x 8192, 16x32 16.5 / 13.6; 64 x 8192 x 8192,
-//   64x32 22.6 / 24.4 (64x128 in four splits 21 / 19.3); 64 x 4096 x 4096, 64x16 10.6 /
-//   11.8 (64x128 in four splits 14 / 13.5); 29 x 19904 x 512, 32x16 11 / 12 (64x128 6 / 6).
+//   all CUs ask), the rows of A, again for each workgroup, at 25 (L2), and a workgroup
+//   takes 1.5 at least.  1 x 8192 x 8192, 16x32 15 / 12; 1 x 28672 x 8192, 16x16 47 / 39;
+//   16 x 8192 x 8192, 16x32 17 / 14; 64 x 8192 x 8192, 64x32 26 / 24; 64 x 4096 x 4096,
+//   64x16 11.4 / 11.7 (64x128 in four splits 14 / 13.5); 37 x 5003 x 4099, 64x32 10.2 / 9.6;
+//   30 x 1624 x 10045, 32x32 in four splits 10.5 / 10.8 (32x16 14.6).
 float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, int64_t steps) {
   const float rounds = (float)((tiles * splits + kCus - 1) / kCus);
   const float mn = (float)d.M * (float)d.N;
   const float join = splits > 1 ? 3.f + (float)splits * mn * 4.f / 3.0e6f : 0.f;
   if (kind >= kG8Tile64x128) {
     // an fp32 C is formed at about half the rate
-    const float work = kKinds[kind].step * (d.c_type == LL_F32 ? 1.8f : 1.f);
+    const float work = kKinds[kind].step * (d.c_type == LL_F32 ? 1.9f : 1.f);
     const float memory = (float)(d.M + d.N) * 128.f * (float)splits / rounds / 5.5e6f;
-    const float step = std::max(work, memory);
-    return 2.f + rounds * (2.5f + (float)steps * step) + join;
+    const float bytes = (float)(kKinds[kind].bm * kKinds[kind].bn * (splits > 1 ? 4 : dtype_size(d.c_type)));
+    const float stores = (float)std::min<int64_t>(tiles * splits, kCus) * bytes / 5.5e6f;
+    return 4.2f + rounds * (1.f + (float)steps * std::max(work, memory) + stores) + join;
   }
   const float of_b = std::min(25.f, 10.f * kCus / (float)std::min<int64_t>(tiles * splits, kCus));
   const float rows = (float)std::min<int64_t>(d.M, kKinds[kind].bm);
-  const float bytes = (float)steps * 128.f * ((float)kKinds[kind].bn / of_b + rows / 50.f);
-  return 2.f + 0.05f * (float)kKinds[kind].bm + rounds * std::max(1.5f, bytes / 2100.f) + join;
+  const float bytes = (float)steps * 128.f * ((float)kKinds[kind].bn / of_b + rows / 25.f);
+  return 2.f + 0.02f * (float)kKinds[kind].bm + rounds * std::max(1.5f, bytes / 2100.f) + join;
 }
 
 }  // namespace
