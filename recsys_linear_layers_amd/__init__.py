@@ -918,23 +918,25 @@ def rmsnorm_grad(dy, h, rstd, gamma=None, dh=None, out=None, param_grads: bool =
     gradient of h, and so of x and of the residual alike; dh: the gradient that
     reaches h by its other path, added to dx (out may be dh).  dgamma has gamma's
     type (h's without gamma); param_grads=False: dx alone, dgamma None."""
-    torch = _torch()
-    N, D = h.shape
-    if tuple(dy.shape) != (N, D) or dy.dtype != h.dtype:
+    shape, dtype = h.shape, h.dtype
+    N, D = shape
+    if dy.shape != shape or dy.dtype != dtype:
         raise ValueError("dy must have h's shape and type")
-    if dh is not None and (tuple(dh.shape) != (N, D) or dh.dtype != h.dtype):
+    if dh is not None and (dh.shape != shape or dh.dtype != dtype):
         raise ValueError("dh must have h's shape and type")
     if out is None:
-        out = h.new_empty((N, D))
-    if tuple(out.shape) != (N, D) or out.dtype != h.dtype:
-        raise ValueError("out must be [N][D] of h's type")
-    _vector(rstd, N, "rstd", (torch.float32,))
+        out, ld_out = h.new_empty(shape), D
+    else:
+        if out.shape != shape or out.dtype != dtype:
+            raise ValueError("out must be [N][D] of h's type")
+        ld_out = _rows(out, "out")
+    _vector(rstd, N, "rstd", (_torch().float32,))
     ptype = _norm_params(h, gamma)
     _same_device(h, dy, rstd, gamma, dh, out)
     stream = _stream_of(h)
-    dgamma = torch.empty(D, dtype=ptype, device=h.device) if param_grads else None
-    desc = RmsnormGradDesc(N, D, _rows(dy, "dy"), _rows(h, "h"), 0 if dh is None else _rows(dh, "dh"),
-                           _rows(out, "out"), _dtype_code(h.dtype), _dtype_code(ptype))
+    dgamma = h.new_empty(D, dtype=ptype) if param_grads else None
+    desc = RmsnormGradDesc(N, D, _rows(dy, "dy"), _rows(h, "h"), 0 if dh is None else _rows(dh, "dh"), ld_out,
+                           _dtype_code(dtype), _dtype_code(ptype))
     need = rmsnorm_grad_workspace_size(desc) if param_grads else 0
     ws = _workspace(h.device, need)
     rmsnorm_grad_run(desc, dy.data_ptr(), h.data_ptr(), _ptr(gamma), rstd.data_ptr(), _ptr(dh), out.data_ptr(),
