@@ -21,6 +21,14 @@
 
 namespace ll {
 
+// Whether a row's values are loaded as ones read once (non-temporal).  With an odd
+// number of 16-bit columns rows begin anywhere: pieces straddle lines, and the next
+// piece wants the line kept (8191 x 5003 in rows of 5006, non-temporal and not: norm
+// bf16 38 and 31 us, with residual fp16 65 and 63, its gradient 110 and 87; but in
+// fp32 102 and 105, and at whole pieces 16384 x 8192 bf16 171 and 187).
+template <int TY, bool TAIL>
+constexpr bool read_once = !TAIL || TY == LL_F32;
+
 // VEC columns of a row's 8-bit output and, once per block, its scale.  Lanes
 // past the row's end take part with zeros.
 template <int Q, int VEC, bool TAIL>
@@ -57,10 +65,10 @@ __global__ void __launch_bounds__(THREADS) rms_kernel(const RmsArgs a) {
   // every row group takes part in each step's barriers
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += step, r += step, flip ^= 1) {
     const bool live = r < a.N;
-    RowCols<TY, VEC, TPR, NCH, TAIL, true> cur;
+    RowCols<TY, VEC, TPR, NCH, TAIL, read_once<TY, TAIL>> cur;
     cur.load(a.x, a.ldx, r, live, x, a.D);
     if (a.residual) {
-      RowCols<TY, VEC, TPR, NCH, TAIL, true> res;
+      RowCols<TY, VEC, TPR, NCH, TAIL, read_once<TY, TAIL>> res;
       res.load(a.residual, a.ldr, r, live, x, a.D);
       raw* dst = (raw*)a.h + r * a.ldh;
 #pragma unroll
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(const RmsGradArgs a) 
   int flip = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < a.N; r0 += step, r += step, flip ^= 1) {
     const bool live = r < a.N;
-    RowCols<TY, VEC, TPR, NCH, TAIL, true> vh, vd, ve;
+    RowCols<TY, VEC, TPR, NCH, TAIL, read_once<TY, TAIL>> vh, vd, ve;
     vh.load(a.h, a.ldh, r, live, x, a.D);
     vd.load(a.dy, a.lddy, r, live, x, a.D);
     if (a.dh) ve.load(a.dh, a.lddh, r, live, x, a.D);
