@@ -53,7 +53,13 @@ __global__ void __launch_bounds__(kThreads) quant8_kernel(const Quant8Args a, in
   __shared__ uint32_t one_max[4];
   const int cg = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int tn = (int)(t / tiles_d), td = (int)(t - (int64_t)tn * tiles_d);
+    int tn = (int)(t / tiles_d), td = (int)(t - (int64_t)tn * tiles_d);
+    if constexpr (!ONCE) {  // eight rows of tiles, which the eight XCDs take in turn
+      const int first = tn & ~7, rows = min(8, (a.N + kBlock8 - 1) / kBlock8 - first);
+      const int64_t in = t - (int64_t)first * tiles_d;
+      td = (int)(in / rows);
+      tn = first + (int)(in - (int64_t)td * rows);
+    }
     const int n0 = tn * kBlock8 + rg * 8, d0 = td * kBlock8 + cg * 8;
     const int rows = min(8, a.N - n0), cols = a.D - d0;
     const raw* const src = (const raw*)a.x + (int64_t)n0 * a.ldx + d0;
@@ -175,7 +181,9 @@ hipError_t launch(const Quant8Args& a, int cus, hipStream_t s) {
   // Each value is read once (non-temporal); but pieces that straddle lines, and
   // fp32's two per lane, ask for a line twice and want it kept (non-temporal,
   // 16384 x 8192 bf16: 75 -> 70 us, 8191 x 5003 fp16 in rows of 5006: 30 -> 43,
-  // 8192 x 8192 fp32 80 -> 83).
+  // 8192 x 8192 fp32 80 -> 83).  Such tiles are also dealt out so that those beside
+  // each other, which share lines, run on one XCD and find them in its L2 (8191 x 5003
+  // fp16 in rows of 5006, both forms 40.7 -> 33.8, as it lies 30.3 -> 24.3; whole pieces 8192 x 4096 transposed 20.5 -> 21.4).
   auto kernel = pick<TY, Q, SQUARE, false>(a);
   if constexpr (TY != LL_F32) {
     if (a.aligned) kernel = pick<TY, Q, SQUARE, true>(a);
