@@ -245,8 +245,11 @@ store_c8<4>(p, 0, t.m0 + e / (Cfg::BN / 4), t.n0 + e % (Cfg::BN / 4) * 4, {0.f, 
   static_assert(T % ND == 0 && LAG < ND && LAG <= FN && FM % 2 == 0, "ring of results");
   // The loads of a later step begin behind that barrier and go on into the next
   // step, AT_ONCE for every PACE products: in a burst they filled the address
-  // unit's queue, and the matrix unit stood still meanwhile.
-  constexpr int PACE = EXACT && T >= 24 ? 2 : 1, AT_ONCE = (LOADS * PACE + T - 1) / T;
+  // unit's queue, and the matrix unit stood still meanwhile (8192^3, 256x256, one or
+  // two more at once: 3% and 12% more cycles; at every second product 7% fewer and,
+  // with the clock that the card's power then allows, 445 -> 436 us, but with B's
+  // scales by rows 504 -> 510, and 2048 x 4096 x 4096, 128x256, 37.5 -> 38.8).
+  constexpr int PACE = T >= 32 && (EXACT || !ROWS) ? 2 : 1, AT_ONCE = (LOADS * PACE + T - 1) / T;
   constexpr int EARLY = FN / PACE * AT_ONCE < LOADS ? FN / PACE * AT_ONCE : LOADS;
   static_assert(FN % PACE == 0 && T % PACE == 0, "loads of a step");
   f32x4 d[ND], sbv[FEW_SB ? 1 : FN];  // sbv (ROWS): of all f, or (EXACT, whose operands take the registers) of the last product
