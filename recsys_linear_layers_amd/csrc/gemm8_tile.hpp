@@ -16,8 +16,13 @@
 // tile per CU (4096^3) 59.8 and 60.5; where the card's power is the bound (16384 x
 // 28672 x 8192) 3140 and 3112.
 //
+// What bounds the large tiles: a step of a 256x256 tile takes 3000 to 3400 cycles, of
+// which the matrix unit works 2048 (without the loads into LDS 2830, without the fmas
+// 3100), at the clock that the card's power allows: on random bytes 1.9 to 2.0 GHz,
+// on zeros 2.4 (8192^3 436 and 358 us).  So fewer cycles pay a third of what they save.
+//
 // A step is one block of 128 k: A's and B's rows of 128 bytes go straight from
-// memory to LDS (1 KB per instruction), two steps deep; one barrier per step.
+// memory to LDS (1 KB per instruction), two to six steps deep; one barrier per step.
 // The chunks of 16 bytes of a row are permuted so that the fragment reads touch
 // every bank once.  Rows and k outside the matrices are given an offset out of
 // the buffer's range, which reads zeros; the bytes of a last piece past K are
@@ -248,8 +253,9 @@ store_c8<4>(p, 0, t.m0 + e / (Cfg::BN / 4), t.n0 + e % (Cfg::BN / 4) * 4, {0.f, 
   // unit's queue, and the matrix unit stood still meanwhile (8192^3, 256x256, one or
   // two more at once: 3% and 12% more cycles; at every second product 7% fewer and,
   // with the clock that the card's power then allows, 445 -> 436 us, but with B's
-  // scales by rows 504 -> 510, and 2048 x 4096 x 4096, 128x256, 37.5 -> 38.8).
-  constexpr int PACE = T >= 32 && (EXACT || !ROWS) ? 2 : 1, AT_ONCE = (LOADS * PACE + T - 1) / T;
+  // scales by rows 504 -> 510, to fp32 824 -> 832, and 2048 x 4096 x 4096, 128x256, 37.5
+  // -> 38.8).
+  constexpr int PACE = T >= 32 && !EXACT && !ROWS ? 2 : 1, AT_ONCE = (LOADS * PACE + T - 1) / T;
   constexpr int EARLY = FN / PACE * AT_ONCE < LOADS ? FN / PACE * AT_ONCE : LOADS;
   static_assert(FN % PACE == 0 && T % PACE == 0, "loads of a step");
   f32x4 d[ND], sbv[FEW_SB ? 1 : FN];  // sbv (ROWS): of all f, or (EXACT, whose operands take the registers) of the last product
@@ -317,9 +323,11 @@ store_c8<4>(p, 0, t.m0 + e / (Cfg::BN / 4), t.n0 + e % (Cfg::BN / 4) * 4, {0.f, 
         const int i = t / FN, f = t % FN;
         if (f == 0) x = Block::x(xr[i & 1]);
         if (i == 0) w[f] = Block::w(wr[f]);
-        if (EXACT) __builtin_amdgcn_s_setprio(1);  // 2212 -> 2169 us; without EXACT 1 or 2% slower
+        // (8192 x 8192 x 16384 to fp32 with B's scales by rows 1946 -> 1820 us; by squares
+        // 8192^3 824 -> 832, and without EXACT 3% more)
+        if (EXACT && ROWS) __builtin_amdgcn_s_setprio(1);
         d[t % ND] = Block::product(w[f], x);
-        if (EXACT) __builtin_amdgcn_s_setprio(0);
+        if (EXACT && ROWS) __builtin_amdgcn_s_setprio(0);
         add((t + T - LAG) % T);
         if (f == LAG - 1) s = ROWS ? sa_next : sa_next * sb;  // of this row of products from here on
         if (ROWS && FEW_SB) sbv[0] = *(const f32x4*)(sc + sb_off + 4 * col_of(f));
