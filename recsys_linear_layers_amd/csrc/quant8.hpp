@@ -68,7 +68,7 @@ __device__ __forceinline__ void store8(uint8_t* p, const uint32_t (&w)[W], int n
     typedef words unaligned_words __attribute__((aligned(1)));
     words v;
     __builtin_memcpy(&v, w, sizeof v);
-    if constexpr (W == 1) *(uint32_t __attribute__((aligned(1)))*)p = w[0];
+    if constexpr (W == 1) __builtin_memcpy(p, w, sizeof w);
     else __builtin_nontemporal_store(v, (unaligned_words*)p);
   } else {
 #pragma unroll
