@@ -846,13 +846,12 @@ def _new_scale8(like, rows: int, cols: int, squares: bool):
     return like.new_empty((blocks, rows), dtype=f32).t(), 1, max(rows, 1)
 
 
-def _scale_strides(t, what: str):
+def _scale_strides(t, shape, what: str):
     """Strides of 2-D fp32 scales; along a dimension of one they do not matter."""
-    shape = t.shape
-    if len(shape) != 2 or t.dtype != _torch().float32:
+    strides = t.stride()
+    if len(strides) != 2 or t.dtype != _torch().float32:
         raise ValueError(f"{what} must be 2-D and fp32")
-    (n, m), (s, r) = shape, t.stride()
-    return s if n > 1 else 1, r if m > 1 else 1
+    return strides[0] if shape[0] > 1 else 1, strides[1] if shape[1] > 1 else 1
 
 
 def _rmsnorm(x, gamma, residual, eps, y, ld_y, y_code, scale, sn, sb, residual_out):
@@ -869,7 +868,7 @@ def _rmsnorm(x, gamma, residual, eps, y, ld_y, y_code, scale, sn, sb, residual_o
             raise ValueError("residual must have x's shape and type")
         ld_r = _rows(residual, "residual")
         if residual_out is None:
-            h, ld_h = x.new_empty(shape), D
+            h, ld_h = _torch().empty_like(x), D
         else:
             h = residual_out
             if h.shape != shape or h.dtype != dtype:
@@ -981,26 +980,34 @@ def quant8_pair(x, squares: bool = False, dtype=None):
 
 
 def gemm8_desc_for(a, a_scale, b, b_scale, out) -> Gemm8Desc:
-    M, K = a.shape
-    N, K2 = b.shape
-    if K2 != K or out.shape != (M, N):
-        raise ValueError(f"shape mismatch: a {tuple(a.shape)}, b {tuple(b.shape)}, out {tuple(out.shape)}")
-    kb = _blocks8(K)
-    sa, sb = _scale_strides(a_scale, "a_scale"), _scale_strides(b_scale, "b_scale")
-    if a_scale.shape != (M, kb):
+    a_shape, b_shape = a.shape, b.shape
+    lda, ldb = _rows16(a, a_shape, "a"), _rows16(b, b_shape, "b")
+    M, K = a_shape
+    N = b_shape[0]
+    if b_shape[1] != K or out.shape != (M, N):
+        raise ValueError(f"shape mismatch: a {tuple(a_shape)}, b {tuple(b_shape)}, out {tuple(out.shape)}")
+    kb = -(-K // 128)
+    sa_shape, sb_shape = a_scale.shape, b_scale.shape
+    sam, sab = _scale_strides(a_scale, sa_shape, "a_scale")
+    sbn, sbb = _scale_strides(b_scale, sb_shape, "b_scale")
+    if sa_shape != (M, kb):
         raise ValueError(f"a_scale must be [{M}][{kb}]")
-    squares = b_scale.shape == (_blocks8(N), kb)
-    if not squares and b_scale.shape != (N, kb):
+    squares = sb_shape == (-(-N // 128), kb)
+    if not squares and sb_shape != (N, kb):
         raise ValueError(f"b_scale must be [{_blocks8(N)}][{kb}] or [{N}][{kb}]")
-    return Gemm8Desc(M, N, K, _rows16(a, "a"), _rows16(b, "b"), _rows(out, "out"), *sa, *sb, _code8(a.dtype),
-                     _code8(b.dtype), _dtype_code(out.dtype), 128 if squares else 1)
+    return Gemm8Desc(M, N, K, lda, ldb, _rows(out, "out"), sam, sab, sbn, sbb, _code8(a.dtype), _code8(b.dtype),
+                     _dtype_code(out.dtype), 128 if squares else 1)
 
 
-def _rows16(t, what: str):
+def _rows16(t, shape, what: str):
     """_rows of an operand of gemm8; the stride of a single row, or of empty ones, does not matter."""
-    s = _rows(t, what)
-    n, k = t.shape
-    return s if n > 1 and k > 0 else -(-k // 16) * 16
+    strides = t.stride()
+    if len(strides) != 2:
+        raise ValueError(f"{what} must be 2-D")
+    n, k = shape
+    if k > 1 and strides[1] != 1:
+        raise ValueError(f"{what}: last dimension must be contiguous")
+    return strides[0] if n > 1 and k > 0 else -(-k // 16) * 16
 
 
 def gemm8(a, a_scale, b, b_scale, out=None, out_dtype=None):
