@@ -81,6 +81,17 @@ struct Block8<E5M2, true> {
   }
 };
 
+// Chunk c of A's row r sits at c ^ swz8_a(r), of B's at c ^ swz8_b(r).  A row's
+// 128 bytes are half of the banks (which half goes by the row's parity), and a
+// pass of a 16-byte LDS read serves 16 lanes, the 16 rows of a fragment at one
+// chunk: the eight rows of each parity need eight different values.  A's rows
+// follow one another; B's are four times four, 4 FN rows apart.
+__device__ __forceinline__ int swz8_a(int r) { return ((r >> 1) & 1) | (((r >> 3) & 1) << 1) | (r & 4); }
+template <int GF>
+__device__ __forceinline__ int swz8_b(int r) {
+  return ((r >> 1) & 1) | (((r / (8 * GF)) & 1) << 1) | (((r / (4 * GF)) & 1) << 2);
+}
+
 // dma16 for one word per lane: lane l's 4 bytes land at LDS byte address m0 + 4 l.
 __device__ __forceinline__ void dma4(i32x4 rsrc, uint32_t lds_addr, uint32_t voff) {
   asm volatile("s_nop 4\n\tbuffer_load_dword %0, %1, 0 offen lds"

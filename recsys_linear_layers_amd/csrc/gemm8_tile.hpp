@@ -50,17 +50,6 @@ struct G8Cfg {
   static_assert((BM + 63) / 64 + (BN + 63) / 64 <= WAVES, "scales: 64 rows a wave");
 };
 
-// Chunk c of A's row r sits at c ^ swz8_a(r), of B's at c ^ swz8_b(r).  A row's
-// 128 bytes are half of the banks (which half goes by the row's parity), and a
-// pass of a 16-byte LDS read serves 16 lanes, the 16 rows of a fragment at one
-// chunk: the eight rows of each parity need eight different values.  A's rows
-// follow one another; B's are four times four, 4 FN rows apart.
-__device__ __forceinline__ int swz8_a(int r) { return ((r >> 1) & 1) | (((r >> 3) & 1) << 1) | (r & 4); }
-template <int GF>
-__device__ __forceinline__ int swz8_b(int r) {
-  return ((r >> 1) & 1) | (((r / (8 * GF)) & 1) << 1) | (((r / (4 * GF)) & 1) << 2);
-}
-
 template <class Cfg, bool E5M2, bool ROWS, bool EXACT>
 __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8Args p) {
   typedef Block8<E5M2, EXACT> Block;

@@ -347,8 +347,8 @@ const struct {
 
 constexpr int kCus = 256;  // that the choice is made for
 
-// What a kernel takes, in microseconds, as far as the choice needs it: 60 drawn
-// problems, of 1 to 16384 rows, took 2% longer on average than with the best
+// What a kernel takes, in microseconds, as far as the choice needs it: 96 drawn
+// problems, of 1 to 16384 rows, took 2 to 3% longer on average than with the best
 // kernel and split of each.
 //   Tiles: 4.2 before the first step and after the last store; a round of tiles over
 //   the CUs takes its steps, each at least as long as its rows of A and B come
@@ -359,11 +359,12 @@ constexpr int kCus = 256;  // that the choice is made for
 //   four splits 25 / 19.5; 29 x 19904 x 512, 64x128 7.5 / 7.0; 9690 x 1600 x 192 to fp32,
 //   128x128 30 / 25 (256x256 34).
 //   Few rows: each CU's share of B comes at 10 bytes a clock (HBM; up to 25 where not
-//   all CUs ask), the rows of A, again for each workgroup, at 25 (L2), and a workgroup
-//   takes 1.5 at least.  1 x 8192 x 8192, 16x32 15 / 12; 1 x 28672 x 8192, 16x16 47 / 39;
-//   16 x 8192 x 8192, 16x32 17 / 14; 64 x 8192 x 8192, 64x32 26 / 24; 64 x 4096 x 4096,
-//   64x16 11.4 / 11.7 (64x128 in four splits 14 / 13.5); 37 x 5003 x 4099, 64x32 10.2 / 9.6;
-//   30 x 1624 x 10045, 32x32 in four splits 10.5 / 10.8 (32x16 14.6).
+//   all CUs ask), the rows of A, again for each workgroup, at 60 (L2; 25 where rows are
+//   not whole lines), B's scales by rows take some more, and kernels of more than 128
+//   registers leave no room for a second workgroup on a CU.  1 x 8192 x 8192, 16x32 15 /
+//   12.4; 1 x 28672 x 8192, 16x16 47 / 39; 16 x 8192 x 8192, 16x32 16 / 11.6; 64 x 8192 x 8192,
+//   64x32 20 / 15.3; 64 x 4096 x 4096, 64x16 8.5 / 7.4; 37 x 5003 x 4099, 64x32 10.2 / 9.9; 30
+//   x 1624 x 10045 by rows, 32x32 in four splits 10.8 / 10.4.
 float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, int64_t steps) {
   const float rounds = (float)((tiles * splits + kCus - 1) / kCus);
   const float mn = (float)d.M * (float)d.N;
@@ -376,10 +377,14 @@ float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, i
     const float stores = (float)std::min<int64_t>(tiles * splits, kCus) * bytes / 5.5e6f;
     return 4.2f + rounds * (1.f + (float)steps * std::max(work, memory) + stores) + join;
   }
+  const bool by_rows = d.b_block == 1;
   const float of_b = std::min(25.f, 10.f * kCus / (float)std::min<int64_t>(tiles * splits, kCus));
+  const float of_a = d.stride_a % 128 == 0 && d.stride_b % 128 == 0 ? 60.f : 25.f;
   const float rows = (float)std::min<int64_t>(d.M, kKinds[kind].bm);
-  const float bytes = (float)steps * 128.f * ((float)kKinds[kind].bn / of_b + rows / 25.f);
-  return 2.f + 0.02f * (float)kKinds[kind].bm + rounds * std::max(1.5f, bytes / 2100.f) + join;
+  const float one = (float)steps * 128.f * ((float)kKinds[kind].bn / of_b + rows / of_a + (by_rows ? 0.3f : 0.f)) / 2100.f;
+  const bool alone = kKinds[kind].bm == 64 || (by_rows && kKinds[kind].bn == 32);  // no room for a second on a CU
+  const float turns = std::max(1.f, alone ? rounds : (float)(tiles * splits) / kCus);
+  return 2.f + 0.02f * (float)kKinds[kind].bm + turns * std::max(alone ? 1.5f : 0.6f, one) + join;
 }
 
 }  // namespace
