@@ -54,7 +54,7 @@ struct Gemm8Plan {
   size_t partial_bytes;
 };
 
-// Sizes alone decide (no device is asked).
+// Sizes and strides alone decide (no device is asked).
 Gemm8Plan gemm8_plan(const gemm8_desc& d);
 const char* gemm8_kind_name(int kind);
 // a_e5m2: A holds LL_E5M2; rows: B's scales are per row (b_block 1).

@@ -97,6 +97,34 @@ def test_every_kernel_and_split(monkeypatch, kind, M, N, K, splits):
             _check(ll.gemm8(a, sa, b, sb, out=out), ref, S, K)
 
 
+@pytest.mark.parametrize("kind,M", [("FEW16x16", 16), ("FEW16x32", 5), ("FEW32x16", 31), ("FEW32x32", 32), ("FEW64x16", 64),
+                                    ("FEW64x32", 37), ("FEW64x32", 64)])
+@pytest.mark.parametrize("K", [100, 128, 1000, 2100, 3456])
+def test_rows_of_whole_lines(monkeypatch, kind, M, K):
+    """Rows at multiples of 128 bytes, from a line's start and from behind it, K ending anywhere: the same bits."""
+    import torch
+    import recsys_linear_layers_amd as ll
+    t = _types()
+    monkeypatch.setenv("LL_GEMM8_KIND", kind)
+    ld = -(-K // 128) * 128 + 128
+    for N, squares in ((333, True), (65, False)):
+        a, sa = _operand(M, K, 1, t["e5m2"] if squares else t["e4m3"], False)
+        b, sb = _operand(N, K, 3, t["e4m3"], squares)
+        ref, S = _reference(a, sa, b, sb, squares)
+        for c in ("bf16", "f32"):
+            got = []
+            for start in (0, 16):
+                near = []
+                for x in (a, b):
+                    buf = torch.full((len(x) * ld + 128,), 0x7F, dtype=torch.uint8, device="cuda")
+                    buf = buf[start:start + len(x) * ld].view(len(x), ld)
+                    buf[:, :K] = x.view(torch.uint8)
+                    near.append(buf.view(x.dtype)[:, :K])
+                got.append(ll.gemm8(near[0], sa, near[1], sb, out_dtype=t[c]))
+                _check(got[-1], ref, S, K)
+            assert torch.equal(got[0], got[1])
+
+
 @pytest.mark.parametrize("kind,bm,bn", [("TILE64x128", 64, 128), ("TILE128x128", 128, 128), ("TILE128x256", 128, 256),
                                         ("TILE256x256", 256, 256)])
 @pytest.mark.parametrize("K", [20, 128, 260, 1000])
