@@ -352,17 +352,17 @@ constexpr int kCus = 256;  // that the choice is made for
 // kernel and split of each.
 //   Tiles: 4.2 before the first step and after the last store; a round of tiles over
 //   the CUs takes its steps, each at least as long as its rows of A and B come
-//   from memory, and its stores (both 5.5 TB/s); a split K adds a launch and the
+//   from memory (5 TB/s), and its stores (5.5); a split K adds a launch and the
 //   partials' bytes, written and read.  Estimate and measured time (MI355X, bf16 C):
 //   1024 x 4096 x 4096, 128x128 26 / 26; 2048 x 4096 x 4096, 128x256 39 / 38; 4096^3,
 //   256x256 62.5 / 61.5, 128x256 73 / 71, 128x128 92 / 91; 64 x 8192 x 8192, 64x128 in
 //   four splits 25 / 19.5; 29 x 19904 x 512, 64x128 7.5 / 7.0; 9690 x 1600 x 192 to fp32,
 //   128x128 30 / 25 (256x256 34).
-//   Few rows: each CU's share of B comes at 10 bytes a clock (HBM; up to 25 where not
-//   all CUs ask), the rows of A, again for each workgroup, at 60 (L2; 25 where rows are
+//   Few rows: each CU's share of B comes at 10 bytes a clock, or 11 for many small
+//   workgroups (HBM; up to 25 where not all CUs ask), the rows of A, again for each workgroup, at 60 (L2; 25 where rows are
 //   not whole lines), B's scales by rows take some more, and kernels of more than 128
 //   registers leave no room for a second workgroup on a CU.  1 x 8192 x 8192, 16x32 15 /
-//   12.4; 1 x 28672 x 8192, 16x16 47 / 39; 16 x 8192 x 8192, 16x32 16 / 11.6; 64 x 8192 x 8192,
+//   12.4; 1 x 28672 x 8192, 16x16 42.5 / 39 (16x32 46 / 44); 16 x 8192 x 8192, 16x32 16 / 11.6; 64 x 8192 x 8192,
 //   64x32 20 / 15.3; 64 x 4096 x 4096, 64x16 8.5 / 7.4; 37 x 5003 x 4099, 64x32 10.2 / 9.9; 30
 //   x 1624 x 10045 by rows, 32x32 in four splits 10.8 / 10.4.
 float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, int64_t steps) {
@@ -372,13 +372,13 @@ float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, i
   if (kind >= kG8Tile64x128) {
     // an fp32 C is formed at about half the rate
     const float work = kKinds[kind].step * (d.c_type == LL_F32 ? 1.9f : 1.f);
-    const float memory = (float)(d.M + d.N) * 128.f * (float)splits / rounds / 5.5e6f;
+    const float memory = (float)(d.M + d.N) * 128.f * (float)splits / rounds / 5.0e6f;
     const float bytes = (float)(kKinds[kind].bm * kKinds[kind].bn * (splits > 1 ? 4 : dtype_size(d.c_type)));
     const float stores = (float)std::min<int64_t>(tiles * splits, kCus) * bytes / 5.5e6f;
     return 4.2f + rounds * (1.f + (float)steps * std::max(work, memory) + stores) + join;
   }
   const bool by_rows = d.b_block == 1;
-  const float of_b = std::min(25.f, 10.f * kCus / (float)std::min<int64_t>(tiles * splits, kCus));
+  const float of_b = std::min(25.f, (kKinds[kind].bn == 16 ? 11.f : 10.f) * kCus / (float)std::min<int64_t>(tiles * splits, kCus));
   const float of_a = d.stride_a % 128 == 0 && d.stride_b % 128 == 0 ? 60.f : 25.f;
   const float rows = (float)std::min<int64_t>(d.M, kKinds[kind].bm);
   const float one = (float)steps * 128.f * ((float)kKinds[kind].bn / of_b + rows / of_a + (by_rows ? 0.3f : 0.f)) / 2100.f;
