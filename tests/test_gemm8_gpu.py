@@ -144,6 +144,26 @@ def test_more_tiles_than_compute_units(monkeypatch, kind, bm, bn, K):
             _check(ll.gemm8(a, sa, b, sb, out_dtype=t[c]), ref, S, K)
 
 
+@pytest.mark.parametrize("kind,M,N", [
+    ("FEW16x16", 3, 333), ("FEW16x32", 16, 333), ("FEW32x16", 31, 333), ("FEW32x32", 20, 333), ("FEW64x16", 64, 333),
+    ("FEW64x32", 50, 333), ("TILE64x128", 133, 259), ("TILE128x128", 261, 259), ("TILE128x256", 261, 515),
+    ("TILE256x256", 517, 515)])
+@pytest.mark.parametrize("qa", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("squares", [True, False])
+def test_every_variant(monkeypatch, kind, M, N, qa, squares):
+    """Each instantiation, with one to five blocks for each of eight waves, whole lines and not, a short block and none."""
+    import recsys_linear_layers_amd as ll
+    t = _types()
+    monkeypatch.setenv("LL_GEMM8_KIND", kind)
+    monkeypatch.setenv("LL_GEMM8_SPLITS", "1")
+    for K, pad in ((900, 7), (1900, 1), (3333, 2), (3333, 7), (4100, 0), (4100, 7), (4096, 0), (4096, 1)):
+        a, sa = _operand(M, K, 1, t[qa], False, pad=pad)
+        b, sb = _operand(N, K, 3, t["e4m3"], squares, pad=pad)
+        ref, S = _reference(a, sa, b, sb, squares)
+        for c in ("bf16", "f16", "f32"):
+            _check(ll.gemm8(a, sa, b, sb, out_dtype=t[c]), ref, S, K)
+
+
 def test_integers_are_exact():
     """Small whole numbers with scales of 2 and 1/2: every product is at least 2^-4 of
     any other, every sum exact in fp32, and C that sum rounded once."""
