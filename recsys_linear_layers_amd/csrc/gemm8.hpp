@@ -28,7 +28,7 @@ struct Gemm8Args {
   const float* sa;
   const float* sb;
   void* c;          // c_type, or null where partial is set
-  float* partial;   // [splits][M][N] of a split K, or null
+  float* partial;   // [splits][M][N], or null
   int64_t lda, ldb, ldc;
   int64_t sam, sab, sbn, sbb;  // strides of the scales: from row to row, from block to block
   int32_t M, N, K;
@@ -51,14 +51,18 @@ struct Gemm8Plan {
   int kind;  // -1: a forced kernel that cannot take the sizes
   int bm, bn;
   int tiles_m, tiles_n, splits, per_split;
-  size_t partial_bytes;
+  size_t partial_bytes;  // > 0: the kernel leaves its sums in the workspace, a second one joins and rounds them
 };
+
+// Whether blocks' sums have fp32's precision (Block8's EXACT).
+inline bool gemm8_exact(const gemm8_desc& d) { return d.c_type == LL_F32 || (d.flags & LL_GEMM8_FULL_SUMS); }
 
 // Sizes and strides alone decide (no device is asked).
 Gemm8Plan gemm8_plan(const gemm8_desc& d);
 const char* gemm8_kind_name(int kind);
-// a_e5m2: A holds LL_E5M2; rows: B's scales are per row (b_block 1).
-hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s);
+// a_e5m2: A holds LL_E5M2; rows: B's scales are per row (b_block 1); exact: gemm8_exact.
+// The tiles' exact kernels store fp32 alone: a 16-bit C goes by the partials.
+hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, bool exact, hipStream_t s);
 
 hipError_t launch_gemm8_tile64x128(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
 hipError_t launch_gemm8_tile64x128_exact(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
@@ -68,6 +72,6 @@ hipError_t launch_gemm8_tile128x256(const Gemm8Args& a, bool a_e5m2, bool rows, 
 hipError_t launch_gemm8_tile128x256_exact(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
 hipError_t launch_gemm8_tile256x256(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
 hipError_t launch_gemm8_tile256x256_exact(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s);
-hipError_t launch_gemm8_few(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s);
+hipError_t launch_gemm8_few(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, bool exact, hipStream_t s);
 
 }  // namespace ll

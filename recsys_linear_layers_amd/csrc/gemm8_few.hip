@@ -245,23 +245,23 @@ hipError_t launch(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s) {
 }
 
 template <int MF, int NF>
-hipError_t launch(const Gemm8Args& a, bool a_e5m2, bool rows, hipStream_t s) {
+hipError_t launch(const Gemm8Args& a, bool a_e5m2, bool rows, bool exact, hipStream_t s) {
   const bool lines = (((uintptr_t)a.a | (uintptr_t)a.b | (uint64_t)a.lda | (uint64_t)a.ldb) & 127) == 0;
-  if (a.c_type == LL_F32)
+  if (exact)
     return lines ? launch<MF, NF, true, true>(a, a_e5m2, rows, s) : launch<MF, NF, true, false>(a, a_e5m2, rows, s);
   return lines ? launch<MF, NF, false, true>(a, a_e5m2, rows, s) : launch<MF, NF, false, false>(a, a_e5m2, rows, s);
 }
 
 }  // namespace
 
-hipError_t launch_gemm8_few(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s) {
+hipError_t launch_gemm8_few(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, bool exact, hipStream_t s) {
   switch (kind) {
-    case kG8Few16x16: return launch<1, 1>(a, a_e5m2, rows, s);
-    case kG8Few16x32: return launch<1, 2>(a, a_e5m2, rows, s);
-    case kG8Few32x16: return launch<2, 1>(a, a_e5m2, rows, s);
-    case kG8Few32x32: return launch<2, 2>(a, a_e5m2, rows, s);
-    case kG8Few64x16: return launch<4, 1>(a, a_e5m2, rows, s);
-    default: return launch<4, 2>(a, a_e5m2, rows, s);
+    case kG8Few16x16: return launch<1, 1>(a, a_e5m2, rows, exact, s);
+    case kG8Few16x32: return launch<1, 2>(a, a_e5m2, rows, exact, s);
+    case kG8Few32x16: return launch<2, 1>(a, a_e5m2, rows, exact, s);
+    case kG8Few32x32: return launch<2, 2>(a, a_e5m2, rows, exact, s);
+    case kG8Few64x16: return launch<4, 1>(a, a_e5m2, rows, exact, s);
+    default: return launch<4, 2>(a, a_e5m2, rows, exact, s);
   }
 }
 

@@ -235,6 +235,7 @@ static ll_status gemm8_check(const gemm8_desc* d) {
   if (!known_type8(d->a_type) || d->b_type != LL_E4M3 || !known_type(d->c_type))
     return fail(LL_ERR_UNSUPPORTED, "A must be LL_E4M3 or LL_E5M2, B LL_E4M3, C LL_BF16, LL_F16 or LL_F32");
   if (d->b_block != 1 && d->b_block != kBlock8) return fail(LL_ERR_INVALID_ARG, "b_block must be 1 or 128");
+  if (d->flags & ~LL_GEMM8_FULL_SUMS) return fail(LL_ERR_INVALID_ARG, "unknown flags 0x%x", d->flags);
   if (d->M >= (1ll << 26) || d->N >= (1ll << 26) || d->K >= (1ll << 22))
     return fail(LL_ERR_UNSUPPORTED, "M and N must be below 2^26, K below 2^22");
   // a launch of 2^32 threads or more is not supported
@@ -302,7 +303,7 @@ ll_status gemm8_run(const gemm8_desc* d, const void* A, const float* a_scale, co
   a.sa = a_scale;
   a.sb = b_scale;
   a.c = C;
-  a.partial = plan.splits > 1 ? (float*)ws : nullptr;
+  a.partial = plan.partial_bytes ? (float*)ws : nullptr;
   a.lda = d->stride_a;
   a.ldb = d->stride_b;
   a.ldc = d->stride_c;
@@ -321,7 +322,8 @@ ll_status gemm8_run(const gemm8_desc* d, const void* A, const float* a_scale, co
   a.tiles_n = plan.tiles_n;
   a.total = plan.tiles_m * plan.tiles_n * plan.splits;
   a.cus = info->cus;
-  hipError_t err = launch_gemm8(a, plan.kind, d->a_type == LL_E5M2, d->b_block == 1, (hipStream_t)stream);
+  hipError_t err =
+      launch_gemm8(a, plan.kind, d->a_type == LL_E5M2, d->b_block == 1, gemm8_exact(*d), (hipStream_t)stream);
   if (err == hipSuccess && a.partial)
     err = launch_splitk_reduce(a.partial, plan.splits, d->M, d->N, C, d->stride_c, 1,
                                d->c_type == LL_F32 ? 0 : d->c_type == LL_BF16 ? 1 : 2, nullptr, 0, (hipStream_t)stream);
@@ -365,15 +367,21 @@ constexpr int kCus = 256;  // that the choice is made for
 //   12.4; 1 x 28672 x 8192, 16x16 42.5 / 39 (16x32 46 / 44); 16 x 8192 x 8192, 16x32 16 / 11.6; 64 x 8192 x 8192,
 //   64x32 20 / 15.3; 64 x 4096 x 4096, 64x16 8.5 / 7.4; 37 x 5003 x 4099, 64x32 10.2 / 9.9; 30
 //   x 1624 x 10045 by rows, 32x32 in four splits 10.8 / 10.4.
+// Whether the sums go by the partials: a split K, and tiles that leave a 16-bit C in fp32.
+bool gemm8_joins(const gemm8_desc& d, int kind, int64_t splits) {
+  return splits > 1 || (kind >= kG8Tile64x128 && d.c_type != LL_F32 && gemm8_exact(d));
+}
+
 float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, int64_t steps) {
   const float rounds = (float)((tiles * splits + kCus - 1) / kCus);
   const float mn = (float)d.M * (float)d.N;
-  const float join = splits > 1 ? 3.f + (float)splits * mn * 4.f / 3.0e6f : 0.f;
+  const bool joins = gemm8_joins(d, kind, splits);
+  const float join = joins ? 3.f + (float)splits * mn * 4.f / 3.0e6f : 0.f;
   if (kind >= kG8Tile64x128) {
-    // an fp32 C is formed at about half the rate
-    const float work = kKinds[kind].step * (d.c_type == LL_F32 ? 1.9f : 1.f);
+    // sums of fp32's precision are formed at about half the rate
+    const float work = kKinds[kind].step * (gemm8_exact(d) ? 1.9f : 1.f);
     const float memory = (float)(d.M + d.N) * 128.f * (float)splits / rounds / 5.0e6f;
-    const float bytes = (float)(kKinds[kind].bm * kKinds[kind].bn * (splits > 1 ? 4 : dtype_size(d.c_type)));
+    const float bytes = (float)(kKinds[kind].bm * kKinds[kind].bn * (joins ? 4 : dtype_size(d.c_type)));
     const float stores = (float)std::min<int64_t>(tiles * splits, kCus) * bytes / 5.5e6f;
     return 4.2f + rounds * (1.f + (float)steps * std::max(work, memory) + stores) + join;
   }
@@ -422,14 +430,13 @@ Gemm8Plan gemm8_plan(const gemm8_desc& d) {
       p.tiles_n = (int)tn;
       p.per_split = (int)steps;
       p.splits = (int)splits;
-      p.partial_bytes = splits > 1 ? align256((size_t)splits * (size_t)d.M * (size_t)d.N * 4) : 0;
+      p.partial_bytes = gemm8_joins(d, kind, splits) ? align256((size_t)splits * (size_t)d.M * (size_t)d.N * 4) : 0;
     }
   }
   return p;
 }
 
-hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hipStream_t s) {
-  const bool exact = a.c_type == LL_F32;
+hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, bool exact, hipStream_t s) {
   switch (kind) {
     case kG8Tile64x128:
       return exact ? launch_gemm8_tile64x128_exact(a, a_e5m2, rows, s) : launch_gemm8_tile64x128(a, a_e5m2, rows, s);
@@ -439,7 +446,7 @@ hipError_t launch_gemm8(const Gemm8Args& a, int kind, bool a_e5m2, bool rows, hi
       return exact ? launch_gemm8_tile128x256_exact(a, a_e5m2, rows, s) : launch_gemm8_tile128x256(a, a_e5m2, rows, s);
     case kG8Tile256x256:
       return exact ? launch_gemm8_tile256x256_exact(a, a_e5m2, rows, s) : launch_gemm8_tile256x256(a, a_e5m2, rows, s);
-    default: return launch_gemm8_few(a, kind, a_e5m2, rows, s);
+    default: return launch_gemm8_few(a, kind, a_e5m2, rows, exact, s);
   }
 }
 
