@@ -555,7 +555,8 @@ ll_status xent_plan_destroy(xent_plan* plan);
  *   h = x + residual (rounded to `type`; h = x where residual is NULL)
  *   y = h * rstd * gamma,  rstd = 1 / sqrt(mean_D(h^2) + eps)
  * of h as it is stored, in fp32 (squares are summed in fp32: h beyond 2^63
- * overflows them), y rounded once to y_type: `type`, or LL_E4M3 / LL_E5M2
+ * overflows them, and beside an eps of 0 h below 2^-63 loses them), y formed in
+ * this order and rounded once to y_type: `type`, or LL_E4M3 / LL_E5M2
  * quantised in blocks of 128 of a row (block 1 above), with scale[row][d / 128]
  * at scale + row*stride_sn + (d / 128)*stride_sb.
  * x, residual, h, y: row strides in elements, at least D, last dimension

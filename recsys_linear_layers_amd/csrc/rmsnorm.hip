@@ -12,6 +12,8 @@
 // keeps the column sums of dgamma in fp32 registers over all rows a workgroup
 // visits; one partial row per workgroup goes to the workspace and a second
 // kernel adds them in a fixed order, so the result does not depend on timing.
+// h is multiplied by rstd before gamma: their product is of the size of 1, where
+// h * gamma can overflow or lose its bits though y is an ordinary number.
 #include "rmsnorm.hpp"
 
 #include <algorithm>
@@ -109,12 +111,12 @@ __global__ void __launch_bounds__(THREADS) rms_kernel(const RmsArgs a) {
         if (!live || d >= a.D) continue;
         C o;
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) o.put(i, cur.v[k].get(i) * g[i] * rstd);
+        for (int i = 0; i < VEC; ++i) o.put(i, cur.v[k].get(i) * rstd * g[i]);
         o.template store<TAIL, true>(dst + d, a.D - d);
       } else {
         float v[VEC];
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) v[i] = d < a.D && (!TAIL || d + i < a.D) ? cur.v[k].get(i) * g[i] * rstd : 0.f;
+        for (int i = 0; i < VEC; ++i) v[i] = d < a.D && (!TAIL || d + i < a.D) ? cur.v[k].get(i) * rstd * g[i] : 0.f;
         put_block8<OUT, VEC, TAIL>(v, a, r, d);
       }
     }
@@ -161,7 +163,7 @@ __global__ void __launch_bounds__(1024) rms_long_kernel(const RmsArgs a) {
         load_param<TY, VEC, true>(a.gamma, a.param_f32, (int)d, n, 1.f, g);
       }
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) y[i] = i < n ? v.get(i) * g[i] * rstd : 0.f;
+      for (int i = 0; i < VEC; ++i) y[i] = i < n ? v.get(i) * rstd * g[i] : 0.f;
       if constexpr (OUT == 0) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) v.put(i, y[i]);
