@@ -120,9 +120,8 @@ ll_status rmsnorm_run(const rmsnorm_desc* d, const void* x, const void* residual
   return err == hipSuccess ? ok() : hip_fail(err, "rmsnorm launch");
 }
 
-// The partial rows of as many workgroups as any device of this architecture runs.
 static size_t rms_grad_bytes(const rmsnorm_grad_desc* d) {
-  return align256((size_t)rms_grad_blocks(d->N, kRmsGradMaxCus) * (size_t)d->D * 4);
+  return align256((size_t)rms_grad_blocks(d->N) * (size_t)d->D * 4);
 }
 
 static ll_status rms_grad_check(const rmsnorm_grad_desc* d) {
@@ -175,7 +174,7 @@ ll_status rmsnorm_grad_run(const rmsnorm_grad_desc* d, const void* dy, const voi
   const RmsGradArgs a = {dy,          h,           gamma,        rstd,         dh,           dx,
                          dgamma,      dgamma ? (float*)ws : nullptr, d->N, d->stride_dy, d->stride_h, d->stride_dh,
                          d->stride_dx, (int32_t)d->D, d->param_type == LL_F32};
-  const hipError_t err = launch_rmsnorm_grad(a, d->type, std::min(info->cus, kRmsGradMaxCus), (hipStream_t)stream);
+  const hipError_t err = launch_rmsnorm_grad(a, d->type, info->cus, (hipStream_t)stream);
   return err == hipSuccess ? ok() : hip_fail(err, "rmsnorm gradient launch");
 }
 

@@ -437,15 +437,15 @@ __global__ void __launch_bounds__(256) rms_grad_columns_kernel(const RmsGradArgs
   sum.template store<true>((uint32_t*)a.partial + (int64_t)blockIdx.y * a.D + d, n);
 }
 
-int rms_grad_blocks(int64_t N, int cus) { return (int)std::max<int64_t>(1, std::min<int64_t>(N, 2ll * cus)); }
+int rms_grad_blocks(int64_t N) { return (int)std::max<int64_t>(1, std::min<int64_t>(N, 512)); }
 
 template <int TY, int VEC, int TPR, int NCH, int THREADS, bool TAIL>
-static int rms_grad_go(const RmsGradArgs& a, int cus, hipStream_t s) {
+static int rms_grad_go(const RmsGradArgs& a, hipStream_t s) {
   // Up to two rows per row group are one workgroup's, which saves the launch that
   // adds up (a call of 4 x 2048: 16.5 -> 12.4 us).
   constexpr int ROWS = THREADS / TPR;
   const int64_t steps = (a.N + ROWS - 1) / ROWS;
-  const int blocks = steps <= 2 ? 1 : rms_grad_blocks(steps, cus);
+  const int blocks = steps <= 2 ? 1 : rms_grad_blocks(steps);
   auto kernel = rms_grad_kernel<TY, VEC, TPR, NCH, THREADS, TAIL, true>;
   if constexpr (TY != LL_F32) {
     if (a.param_f32) kernel = rms_grad_kernel<TY, VEC, TPR, NCH, THREADS, TAIL, false>;
@@ -459,18 +459,18 @@ static hipError_t launch_rms_grad_t(const RmsGradArgs& a, int cus, hipStream_t s
   constexpr int VEC = kWide<TY>, K = 32 / VEC;
   const int chunks = (int)(((int64_t)a.D + VEC - 1) / VEC);
   int blocks;
-  if (chunks <= 64) blocks = rms_grad_go<TY, VEC, 64, 1, 256, TAIL>(a, cus, s);
-  else if (chunks <= 64 * (K / 2)) blocks = rms_grad_go<TY, VEC, 64, K / 2, 256, TAIL>(a, cus, s);
-  else if (chunks <= 64 * K) blocks = rms_grad_go<TY, VEC, 64, K, 256, TAIL>(a, cus, s);
-  else if (chunks <= 256 * (K / 2)) blocks = rms_grad_go<TY, VEC, 256, K / 2, 256, TAIL>(a, cus, s);
-  else if (chunks <= 512 * (K / 2)) blocks = rms_grad_go<TY, VEC, 512, K / 2, 512, TAIL>(a, cus, s);
-  else if (a.D <= 16384) blocks = rms_grad_go<TY, VEC, 1024, K / 2, 1024, TAIL>(a, cus, s);
+  if (chunks <= 64) blocks = rms_grad_go<TY, VEC, 64, 1, 256, TAIL>(a, s);
+  else if (chunks <= 64 * (K / 2)) blocks = rms_grad_go<TY, VEC, 64, K / 2, 256, TAIL>(a, s);
+  else if (chunks <= 64 * K) blocks = rms_grad_go<TY, VEC, 64, K, 256, TAIL>(a, s);
+  else if (chunks <= 256 * (K / 2)) blocks = rms_grad_go<TY, VEC, 256, K / 2, 256, TAIL>(a, s);
+  else if (chunks <= 512 * (K / 2)) blocks = rms_grad_go<TY, VEC, 512, K / 2, 512, TAIL>(a, s);
+  else if (a.D <= 16384) blocks = rms_grad_go<TY, VEC, 1024, K / 2, 1024, TAIL>(a, s);
   else {
     const int64_t rows = std::min<int64_t>(a.N, (int64_t)cus * 64);
     if (rows > 0)
       hipLaunchKernelGGL((rms_grad_long_kernel<TY>), dim3((unsigned)rows), dim3(1024), 0, s, a);
     const int across = (chunks + 255) / 256;  // a grid of 2^32 threads or more is not supported
-    blocks = std::min(rms_grad_blocks(a.N, cus), std::max(1, (1 << 23) / across));
+    blocks = std::min(rms_grad_blocks(a.N), std::max(1, (1 << 23) / across));
     if (a.partial)
       hipLaunchKernelGGL((rms_grad_columns_kernel<TY>), dim3(across, blocks), dim3(256), 0, s, a);
   }

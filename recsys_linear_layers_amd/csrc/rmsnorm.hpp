@@ -35,10 +35,9 @@ struct RmsGradArgs {
 };
 
 hipError_t launch_rmsnorm(const RmsArgs& a, int type, int y_type, int cus, hipStream_t s);
-// CUs the workspace is sized for (the size is asked for without a device).
-constexpr int kRmsGradMaxCus = 256;
-// Most workgroups (partial rows) of the gradient's first kernel.
-int rms_grad_blocks(int64_t N, int cus);
+// Workgroups (partial rows) of the gradient's first kernel: two for each of 256 CUs,
+// whatever the device has, so that sizes alone decide which rows are added up together.
+int rms_grad_blocks(int64_t N);
 hipError_t launch_rmsnorm_grad(const RmsGradArgs& a, int type, int cus, hipStream_t s);
 
 }  // namespace ll
