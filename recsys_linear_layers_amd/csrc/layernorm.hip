@@ -340,12 +340,12 @@ __global__ void __launch_bounds__(256) norm_grad_columns_kernel(const NormGradAr
   out[a.D + c] = db;
 }
 
-int norm_grad_blocks(int64_t N, int cus) { return (int)std::max<int64_t>(1, std::min<int64_t>(N, 2ll * cus)); }
+int norm_grad_blocks(int64_t N) { return (int)std::max<int64_t>(1, std::min<int64_t>(N, 512)); }
 
 template <int TY, int VEC, int TPR, int NCH, int THREADS, bool TAIL>
-static int norm_grad_go(const NormGradArgs& a, int cus, hipStream_t s) {
+static int norm_grad_go(const NormGradArgs& a, hipStream_t s) {
   constexpr int ROWS = THREADS / TPR;
-  const int blocks = norm_grad_blocks((a.N + ROWS - 1) / ROWS, cus);
+  const int blocks = norm_grad_blocks((a.N + ROWS - 1) / ROWS);
   auto kernel = norm_grad_kernel<TY, VEC, TPR, NCH, THREADS, TAIL, true>;
   if constexpr (TY != LL_F32) {
     if (a.param_f32) kernel = norm_grad_kernel<TY, VEC, TPR, NCH, THREADS, TAIL, false>;
@@ -359,17 +359,17 @@ static hipError_t launch_norm_grad_t(const NormGradArgs& a, int cus, hipStream_t
   constexpr int VEC = kWide<TY>, K = 32 / VEC;
   const int chunks = (a.D + VEC - 1) / VEC;
   int blocks;
-  if (chunks <= 64) blocks = norm_grad_go<TY, VEC, 64, 1, 256, TAIL>(a, cus, s);
-  else if (chunks <= 64 * (K / 2)) blocks = norm_grad_go<TY, VEC, 64, K / 2, 256, TAIL>(a, cus, s);
-  else if (chunks <= 64 * K) blocks = norm_grad_go<TY, VEC, 64, K, 256, TAIL>(a, cus, s);
-  else if (chunks <= 256 * (K / 2)) blocks = norm_grad_go<TY, VEC, 256, K / 2, 256, TAIL>(a, cus, s);
-  else if (chunks <= 512 * (K / 2)) blocks = norm_grad_go<TY, VEC, 512, K / 2, 512, TAIL>(a, cus, s);
-  else if (a.D <= 16384) blocks = norm_grad_go<TY, VEC, 1024, K / 2, 1024, TAIL>(a, cus, s);
+  if (chunks <= 64) blocks = norm_grad_go<TY, VEC, 64, 1, 256, TAIL>(a, s);
+  else if (chunks <= 64 * (K / 2)) blocks = norm_grad_go<TY, VEC, 64, K / 2, 256, TAIL>(a, s);
+  else if (chunks <= 64 * K) blocks = norm_grad_go<TY, VEC, 64, K, 256, TAIL>(a, s);
+  else if (chunks <= 256 * (K / 2)) blocks = norm_grad_go<TY, VEC, 256, K / 2, 256, TAIL>(a, s);
+  else if (chunks <= 512 * (K / 2)) blocks = norm_grad_go<TY, VEC, 512, K / 2, 512, TAIL>(a, s);
+  else if (a.D <= 16384) blocks = norm_grad_go<TY, VEC, 1024, K / 2, 1024, TAIL>(a, s);
   else {
     const int64_t rows = std::min<int64_t>(a.N, (int64_t)cus * 64);
     if (rows > 0)
       hipLaunchKernelGGL((norm_grad_long_kernel<TY>), dim3((unsigned)rows), dim3(1024), 0, s, a);
-    blocks = norm_grad_blocks(a.N, cus);
+    blocks = norm_grad_blocks(a.N);
     if (a.partial)
       hipLaunchKernelGGL((norm_grad_columns_kernel<TY>), dim3((a.D + 255) / 256, blocks), dim3(256), 0, s, a);
   }

@@ -35,10 +35,9 @@ struct NormGradArgs {
 };
 
 hipError_t launch_norm(const NormArgs& a, int type, int cus, hipStream_t s);
-// CUs the workspace is sized for (the size is asked for without a device).
-constexpr int kNormGradMaxCus = 256;
-// Most workgroups (partial rows) of the gradient's first kernel.
-int norm_grad_blocks(int64_t N, int cus);
+// Workgroups (partial rows) of the gradient's first kernel: two for each of 256 CUs,
+// whatever the device has, so that sizes alone decide which rows are added up together.
+int norm_grad_blocks(int64_t N);
 hipError_t launch_norm_grad(const NormGradArgs& a, int type, int cus, hipStream_t s);
 
 }  // namespace ll

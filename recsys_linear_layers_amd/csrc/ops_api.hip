@@ -244,9 +244,8 @@ ll_status layernorm_run(const layernorm_desc* d, const void* x, const void* gamm
   return err == hipSuccess ? ok() : hip_fail(err, "layernorm launch");
 }
 
-// The partial rows of as many workgroups as any device of this architecture runs.
 static size_t norm_grad_bytes(const layernorm_grad_desc* d) {
-  return align256((size_t)norm_grad_blocks(d->N, kNormGradMaxCus) * 2 * (size_t)d->D * 4);
+  return align256((size_t)norm_grad_blocks(d->N) * 2 * (size_t)d->D * 4);
 }
 
 static ll_status norm_grad_check(const layernorm_grad_desc* d) {
@@ -298,7 +297,7 @@ ll_status layernorm_grad_run(const layernorm_grad_desc* d, const void* dy, const
   if (s != LL_OK) return s;
   const NormGradArgs a = {dy, x, gamma, mean, rstd, dx, dgamma, dbeta, dgamma ? (float*)ws : nullptr, d->N,
                           d->stride_dy, d->stride_x, d->stride_dx, (int32_t)d->D, d->param_type == LL_F32};
-  const hipError_t err = launch_norm_grad(a, d->type, std::min(info->cus, kNormGradMaxCus), (hipStream_t)stream);
+  const hipError_t err = launch_norm_grad(a, d->type, info->cus, (hipStream_t)stream);
   return err == hipSuccess ? ok() : hip_fail(err, "layernorm gradient launch");
 }
 

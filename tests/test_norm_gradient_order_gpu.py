@@ -61,3 +61,15 @@ def test_rmsnorm(D, N, per_step):
     _, got = ll.rmsnorm_grad(dy.cuda(), h.cuda(), rstd.cuda(), gamma)
     term = dy.double() * (h.double() * rstd.double()[:, None])
     assert torch.equal(got.cpu(), _joined(_partials(term, per_step, True)))
+
+
+@pytest.mark.parametrize("D,N,per_step", SIZES)
+def test_layernorm(D, N, per_step):
+    import torch
+    import recsys_linear_layers_amd as ll
+    dy, x, rstd = _inputs(N, D)
+    mean, gamma = torch.zeros(N, device="cuda"), torch.ones(D, device="cuda")  # with a mean of 0 x * rstd is exact
+    _, dgamma, dbeta = ll.layernorm_grad(dy.cuda(), x.cuda(), mean, rstd.cuda(), gamma)
+    term = dy.double() * (x.double() * rstd.double()[:, None])
+    assert torch.equal(dgamma.cpu(), _joined(_partials(term, per_step, True)))
+    assert torch.equal(dbeta.cpu(), _joined(_partials(dy.double(), per_step, False)))
