@@ -75,7 +75,8 @@ class NextItem:
             h = ll.gemm(n1, w["W1"].t(), bias=w["b1"], act="relu")
             return ll.gemm(h, w["W2"].t()), (n1, h)
         n8 = ll.quant8_pair(n1)
-        h = torch.relu(ll.gemm8(*n8[:2], *self.w8["W1"][:2]) + w["b1"].to(torch.bfloat16))
+        # in fp32 until bias and relu are done: rounded once, as gemm's epilogue does
+        h = torch.relu(ll.gemm8(*n8[:2], *self.w8["W1"][:2], out_dtype=torch.float32) + w["b1"]).to(torch.bfloat16)
         h8 = ll.quant8_pair(h)
         return ll.gemm8(*h8[:2], *self.w8["W2"][:2]), (n8, h, h8)
 
