@@ -1,5 +1,5 @@
 """Compile the HIP sources under csrc/ for gfx950 into liblinlayers.so (in-tree),
-and the measurement probes under probes/ into libllprobes.so.
+and the measurement probes and checks under probes/ into libllprobes.so.
 
 Each .hip file is compiled to an object in parallel, then linked into its
 shared library next to this file.
