@@ -30,16 +30,16 @@ struct Piece8 {
   i32x4 lo, hi;
 };
 
-// The 16 bytes at p, of which n are there; the others are zeros.
-__device__ __forceinline__ i32x4 load_masked(const uint8_t* p, int n) {
-  i32x4 v = {0, 0, 0, 0};
-  if (n <= 0) return v;
-  v = *(const i32x4*)p;
+// The 16 bytes of piece `piece` at p + at, of a row's block that has `left` more bytes;
+// what lies past them is zeros.  Without branches (a piece past the end is read as
+// piece 0, which is there), so that the words are no merge of two branches' values.
+__device__ __forceinline__ i32x4 load_masked(const uint8_t* p, uint32_t at, int piece, int left) {
+  const int n = left - (piece << 4);
+  i32x4 v = *(const i32x4*)(p + (n > 0 ? at : at - (piece << 4)));
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int have = n - 4 * i;
-    if (have <= 0) v[i] = 0;
-    else if (have < 4) v[i] &= (int)((1u << (8 * have)) - 1u);
+    const int have = min(max(n - 4 * i, 0), 4);
+    v[i] &= have == 4 ? -1 : (1 << (8 * have)) - 1;
   }
   return v;
 }
@@ -200,17 +200,20 @@ __global__ void __launch_bounds__(kFewWaves * 64, 2) gemm8_few_kernel(const Gemm
     }
     kb += steps * kFewWaves;
   }
-  if (kb < kb1) {  // the short block
+  // The short block, behind the loop.  Loaded inside it, by a branch in load(), an
+  // earlier form of this kernel (16x16, 16-bit C, two blocks ahead; clang 22 of ROCm
+  // 7.2.0) gave wrong sums: half of a matrix operand that the branch had made a merge
+  // of two values held an address when the instruction read it.  The kernel as it is
+  // now passes its tests that way too; test_every_variant with K = 3333 and 4100 finds it.
+  if (kb < kb1) {
     const int k = kb * kBlock8, left = p.K - k;
     Set s;
 #pragma unroll
     for (int f = 0; f < NF; ++f)
-      s.w[f] = {load_masked(b0 + k + brow[f][0], left - (piece[0] << 4)),
-                load_masked(b0 + k + brow[f][1], left - (piece[1] << 4))};
+      s.w[f] = {load_masked(b0 + k, brow[f][0], piece[0], left), load_masked(b0 + k, brow[f][1], piece[1], left)};
 #pragma unroll
     for (int i = 0; i < MF; ++i)
-      s.x[i] = {load_masked(p.a + k + arow[i][0], left - (piece[0] << 4)),
-                load_masked(p.a + k + arow[i][1], left - (piece[1] << 4))};
+      s.x[i] = {load_masked(p.a + k, arow[i][0], piece[0], left), load_masked(p.a + k, arow[i][1], piece[1], left)};
     scales(s, kb);
     add(s);
   }
