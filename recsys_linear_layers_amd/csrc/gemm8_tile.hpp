@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 2) gemm8_tile_kernel(const Gemm8
     for (int raw = blockIdx.x; raw < p.total; raw += gridDim.x) {
       const Place t = place(p, raw);
       for (int e = threadIdx.x; e < Cfg::BM * Cfg::BN / 4; e += Cfg::THREADS)
-store_c8<4>(p, 0, t.m0 + e / (Cfg::BN / 4), t.n0 + e % (Cfg::BN / 4) * 4, {0.f, 0.f, 0.f, 0.f});
+        store_c8<4>(p, 0, t.m0 + e / (Cfg::BN / 4), t.n0 + e % (Cfg::BN / 4) * 4, {0.f, 0.f, 0.f, 0.f});
     }
     return;
   }

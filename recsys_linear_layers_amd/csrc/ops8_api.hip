@@ -220,7 +220,7 @@ ll_status quant8_run(const quant8_desc* d, const void* x, void* q, float* scale,
   const Quant8Args a = {x,           (uint8_t*)q,  scale,        (uint8_t*)qt, scale_t,      d->stride_x,
                         d->stride_q, d->stride_qt, d->stride_sn, d->stride_sb, d->stride_tn, d->stride_tb,
                         (int32_t)d->N, (int32_t)d->D,  !misaligned(x, 16) && d->stride_x * e % 16 == 0};
-  const hipError_t err = launch_quant8(a, d->type, d->q_type, d->block, info->cus, (hipStream_t)stream);
+  const hipError_t err = launch_quant8(a, d->type, d->q_type, d->block, (hipStream_t)stream);
   return err == hipSuccess ? ok() : hip_fail(err, "quant8 launch");
 }
 

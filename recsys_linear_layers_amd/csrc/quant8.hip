@@ -175,7 +175,7 @@ auto pick(const Quant8Args& a) {
 }
 
 template <int TY, int Q, bool SQUARE>
-hipError_t launch(const Quant8Args& a, int cus, hipStream_t s) {
+hipError_t launch(const Quant8Args& a, hipStream_t s) {
   const int tiles_d = (a.D + kBlock8 - 1) / kBlock8;
   const int64_t tiles = (int64_t)((a.N + kBlock8 - 1) / kBlock8) * tiles_d;
   // Each value is read once (non-temporal); but pieces that straddle lines, and
@@ -194,19 +194,19 @@ hipError_t launch(const Quant8Args& a, int cus, hipStream_t s) {
 }
 
 template <int TY>
-hipError_t launch_t(const Quant8Args& a, int q_type, int block, int cus, hipStream_t s) {
+hipError_t launch_t(const Quant8Args& a, int q_type, int block, hipStream_t s) {
   if (q_type == LL_E4M3)
-    return block == 1 ? launch<TY, LL_E4M3, false>(a, cus, s) : launch<TY, LL_E4M3, true>(a, cus, s);
-  return block == 1 ? launch<TY, LL_E5M2, false>(a, cus, s) : launch<TY, LL_E5M2, true>(a, cus, s);
+    return block == 1 ? launch<TY, LL_E4M3, false>(a, s) : launch<TY, LL_E4M3, true>(a, s);
+  return block == 1 ? launch<TY, LL_E5M2, false>(a, s) : launch<TY, LL_E5M2, true>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_quant8(const Quant8Args& a, int type, int q_type, int block, int cus, hipStream_t s) {
+hipError_t launch_quant8(const Quant8Args& a, int type, int q_type, int block, hipStream_t s) {
   switch (type) {
-    case LL_BF16: return launch_t<LL_BF16>(a, q_type, block, cus, s);
-    case LL_F16: return launch_t<LL_F16>(a, q_type, block, cus, s);
-    case LL_F32: return launch_t<LL_F32>(a, q_type, block, cus, s);
+    case LL_BF16: return launch_t<LL_BF16>(a, q_type, block, s);
+    case LL_F16: return launch_t<LL_F16>(a, q_type, block, s);
+    case LL_F32: return launch_t<LL_F32>(a, q_type, block, s);
     default: return hipErrorInvalidValue;
   }
 }

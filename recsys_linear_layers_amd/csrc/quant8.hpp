@@ -89,6 +89,6 @@ struct Quant8Args {
   int32_t aligned;  // rows of x start at multiples of 16 bytes
 };
 
-hipError_t launch_quant8(const Quant8Args& a, int type, int q_type, int block, int cus, hipStream_t s);
+hipError_t launch_quant8(const Quant8Args& a, int type, int q_type, int block, hipStream_t s);
 
 }  // namespace ll
