@@ -652,18 +652,21 @@ ll_status quant8_run(const quant8_desc* desc, const void* x, void* q, float* sca
  * smaller than its products.  Measured, of the result's norm: 1.4e-5 on normally
  * distributed operands, 3e-5 to 7e-5 where a hundredth of A's columns stands out by
  * 20 to 1000; C's rounding is 1.6e-3 (bf16) or 2e-4 (fp16).  LL_GEMM8_FULL_SUMS: fp32's
- * precision for a 16-bit C too, at an fp32 C's speed (for more than a few rows M * N
+ * precision for a 16-bit C too, at about an fp32 C's speed (beyond few rows M * N
  * fp32 values of the workspace hold the sums until they are rounded).  Equal inputs
  * give equal bits.  A layer's gradients are the same product: dX = dY W takes W
  * quantised transposed, dW = dY^T X takes dY and X quantised transposed, b_block 1.
- * A and B must be 16-byte aligned, stride_a and stride_b multiples of 16 (what
- * lies between K and the stride is read but not used).  Workspace (256-byte
+ * The two scales of a block are multiplied first, in fp32: where that overflows, C is
+ * an infinity or a NaN (also of sums that are 0), and below 2^-126 it loses bits.
+ * A and B must be 16-byte aligned, stride_a and stride_b multiples of 16; the bytes
+ * from K to the next multiple of 16 are read, behind the last row too, and not used
+ * (device allocations end at multiples of more than that).  Workspace (256-byte
  * aligned): gemm8_workspace_size, often 0; only the call that it is given to uses
  * it.  M == 0 or N == 0: nothing is written.  K == 0: C is zero.  Kernels only,
  * graph-capturable.
  * Errors: LL_ERR_INVALID_ARG (null desc or pointer, negative size, stride below
- * the row, misaligned operand, scale stride below 1, b_block, unknown flag bits, C overlapping an
- * input or the workspace), LL_ERR_UNSUPPORTED (types, M, N of 2^26 and more, C of
+ * the row, misaligned operand, scale stride below 1, b_block, unknown flag bits, C
+ * overlapping an input or the workspace), LL_ERR_UNSUPPORTED (types, M, N of 2^26 and more, C of
  * more than 2^22 tiles of 256 x 256, K of 2^22 and more, stride_a or stride_b of
  * 2^22 and more, scale strides along rows of 2^20 and more, strides that put a row
  * or block 2^58 elements or more from the first, device), LL_ERR_WORKSPACE,

@@ -1023,7 +1023,7 @@ def gemm8(a, a_scale, b, b_scale, out=None, out_dtype=None, full_sums: bool = Fa
     below 2^-13 of the largest: at most 7 * 2^-13 of the sum of the products'
     magnitudes; of the result's norm 1.4e-5 on normally distributed operands and up to
     7e-5 where single columns of a stand far out.  full_sums=True: fp32's precision for
-    a 16-bit C too, rounded once, at an fp32 C's speed."""
+    a 16-bit C too, rounded once, at about an fp32 C's speed."""
     torch = _torch()
     if out is None:
         out = a.new_empty((a.shape[0], b.shape[0]), dtype=out_dtype or torch.bfloat16)

@@ -23,9 +23,10 @@ constexpr int kFewWaves = 8;
 // itself needs, pieces l / 16 and l / 16 + 4 of row l % 16: sixteen lanes then ask for
 // sixteen rows, in the same banks of the cache where rows are whole lines.  Where
 // they are not LINES would fetch most lines twice.  (LINES and not, whole lines: 64 x
-// 4096 x 4096 7.5 and 11.7 us, 64 x 8192 x 8192 16 and 24, 16 x 8192 x 8192 12.2 and 13.8, 1 x
-// 28672 x 8192 38.5 and 39.0, 1 x 8192 x 8192 12.6 and 11.9; rows of 4112 or 8208 bytes: 64 x
-// 4096 10.0 and 8.8, 1 x 28672 46 and 41.)
+// 4096 x 4096 7.5 and 11.8 us, 64 x 8192 x 8192 15.8 and 24.6, 16 x 8192 x 8192 11.6 and 16.6, 2 x
+// 8704 x 7168 12.2 and 14.8, 1 x 5120 x 5120 7.1 and 8.2, 1 x 8192 x 8192 12.5 and 12.4, 1 x 28672 x
+// 8192 39.2 and 39.4, 1 x 8192 x 28672 41.4 and 41.0; rows of 4112 or 8208 bytes: 64 x 4096 10.0
+// and 8.8, 1 x 28672 46 and 41.)
 struct Piece8 {
   i32x4 lo, hi;
 };

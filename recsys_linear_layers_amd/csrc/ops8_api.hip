@@ -348,29 +348,33 @@ const struct {
 
 constexpr int kCus = 256;  // that the choice is made for
 
+// Whether the sums go by the partials: a split K, and tiles that leave a 16-bit C in fp32.
+bool gemm8_joins(const gemm8_desc& d, int kind, int64_t splits) {
+  return splits > 1 || (kind >= kG8Tile64x128 && d.c_type != LL_F32 && gemm8_exact(d));
+}
+
 // What a kernel takes, in microseconds, as far as the choice needs it: 96 drawn
 // problems, of 1 to 16384 rows, took 2 to 3% longer on average than with the best
 // kernel and split of each.
 //   Tiles: 4.2 before the first step and after the last store; a round of tiles over
 //   the CUs takes its steps, each at least as long as its rows of A and B come
 //   from memory (5 TB/s), and its stores (5.5); a split K adds a launch and the
-//   partials' bytes, written and read.  Estimate and measured time (MI355X, bf16 C):
-//   1024 x 4096 x 4096, 128x128 26 / 26; 2048 x 4096 x 4096, 128x256 39 / 38; 4096^3,
-//   256x256 62.5 / 61.5, 128x256 73 / 71, 128x128 92 / 91; 64 x 8192 x 8192, 64x128 in
-//   four splits 25 / 19.5; 29 x 19904 x 512, 64x128 7.5 / 7.0; 9690 x 1600 x 192 to fp32,
-//   128x128 30 / 25 (256x256 34).
+//   partials' bytes, written and read.  Estimate and measured time (MI355X, bf16 C) of
+//   kernels that are taken: 1024 x 4096 x 4096, 128x128 26 / 25; 2048 x 4096 x 4096,
+//   128x256 39 / 36; 4096^3, 256x256 62.5 / 59; 128 x 8192 x 8192, 64x128 in two splits
+//   28 / 25.5; 64 x 28672 x 8192, 64x128 53 / 54; 9690 x 1600 x 192 to fp32, 128x128 30 / 25;
+//   of others: 4096^3, 128x256 73 / 71, 128x128 92 / 91; 64 x 8192 x 8192, 64x128 in four
+//   splits 26 / 19.5; 29 x 19904 x 512, 64x128 7.7 / 7.0.
 //   Few rows: each CU's share of B comes at 10 bytes a clock, or 11 for many small
-//   workgroups (HBM; up to 25 where not all CUs ask), the rows of A, again for each workgroup, at 60 (L2; 25 where rows are
-//   not whole lines), B's scales by rows take some more, and kernels of more than 128
-//   registers leave no room for a second workgroup on a CU.  1 x 8192 x 8192, 16x32 15 /
-//   12.4; 1 x 28672 x 8192, 16x16 42.5 / 39 (16x32 46 / 44); 16 x 8192 x 8192, 16x32 16 / 11.6; 64 x 8192 x 8192,
-//   64x32 20 / 15.3; 64 x 4096 x 4096, 64x16 8.5 / 7.4; 37 x 5003 x 4099, 64x32 10.2 / 9.9; 30
-//   x 1624 x 10045 by rows, 32x32 in four splits 10.8 / 10.4.
-// Whether the sums go by the partials: a split K, and tiles that leave a 16-bit C in fp32.
-bool gemm8_joins(const gemm8_desc& d, int kind, int64_t splits) {
-  return splits > 1 || (kind >= kG8Tile64x128 && d.c_type != LL_F32 && gemm8_exact(d));
-}
-
+//   workgroups (HBM; up to 25 where not all CUs ask), the rows of A, again for each
+//   workgroup, at 60 (L2; 25 where rows are not whole lines), B's scales by rows take
+//   some more, and kernels of more than 128 registers leave no room for a second
+//   workgroup on a CU.  Taken: 1 x 8192 x 8192, 16x16 14 / 12.5; 16 x 8192 x 8192, 16x16 16 /
+//   11.7; 32 x 8192 x 8192, 32x32 17 / 12.2; 64 x 8192 x 8192, 64x32 20 / 15.3; 1 x 28672 x
+//   8192, 16x16 42.5 / 39; 64 x 4096 x 4096, 64x16 8.2 / 7.4; 37 x 5003 x 4099, 64x32 10.2 /
+//   9.5; 29 x 19904 x 512, 32x32 4.8 / 5.2; 30 x 1624 x 10045 by rows, 32x32 in four splits
+//   10.8 / 9.9.  Others: 1 x 8192 x 8192, 16x32 15 / 12.4; 16 x 8192 x 8192, 16x32 16 / 11.5; 1 x
+//   28672 x 8192, 16x32 46 / 44.
 float gemm8_time(const gemm8_desc& d, int kind, int64_t tiles, int64_t splits, int64_t steps) {
   const float rounds = (float)((tiles * splits + kCus - 1) / kCus);
   const float mn = (float)d.M * (float)d.N;

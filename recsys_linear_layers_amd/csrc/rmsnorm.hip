@@ -252,9 +252,12 @@ __global__ void __launch_bounds__(THREADS) rms_grad_kernel(const RmsGradArgs a) 
   const int64_t step = (int64_t)gridDim.x * ROWS;
   int64_t r = (int64_t)blockIdx.x * ROWS + y;
   int flip = 0;
-  // The next row's loads go out before this row's sums (16384 x 8192 bf16 187 -> 190,
-  // where they are left out; 4096 x 16384 104.5 -> 103, 65536 x 512 53 -> 48; 8191 x 5003 in
-  // rows of 5006, fp16 86 -> 80, fp32 102 -> 93).
+  // The next row's loads go out before this row's sums (4096 x 16384 104.5 -> 103, 65536 x
+  // 512 53 -> 48; 8191 x 5003 in rows of 5006, fp16 86 -> 80, fp32 102 -> 93), but not in
+  // whole pieces by 512 lanes, where many rows are in flight as it is and the registers
+  // cost more (bf16, not ahead and ahead, 65536 x 4352 397 and 440, 16384 x 5120 116 and 126,
+  // 16384 x 8192 188 and 193, without dh 137 and 146, in fp32 361 and 378; few rows gain 1 to
+  // 3%: 4096 x 8192 54.6 and 52.9, 1024 x 8192 24.2 and 23.6, 8192 x 5120 fp32 119 and 116).
   constexpr bool AHEAD = TAIL || TPR != 512;
   typedef RowCols<TY, VEC, TPR, NCH, TAIL, read_once<TY, TAIL>> Cols;
   Cols nh, nd, ne;
