@@ -305,7 +305,9 @@ hipError_t launch_splitk_reduce(const float* partial, int splits, int64_t M, int
   if (N % 4 == 0 && ((uintptr_t)partial & 15) == 0) {
     const int64_t bx = (N / 4 + 255) / 256;
     if (bx <= 0x7FFFFFFF) {
-      const dim3 grid((unsigned)bx, (unsigned)(M < 65535 ? M : 65535));
+      // a grid of 2^32 threads or more is not supported
+      const int64_t most = bx < (1 << 24) ? ((1 << 24) - 1) / bx : 1, rows = most < 65535 ? most : 65535;
+      const dim3 grid((unsigned)bx, (unsigned)(M < rows ? M : rows));
       hipLaunchKernelGGL(splitk_reduce4_kernel, grid, dim3(256), 0, stream, partial, splits, M, N, C, ldcm, ldcn,
                          c_fmt, bias, act);
       return hipGetLastError();

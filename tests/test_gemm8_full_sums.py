@@ -140,6 +140,28 @@ def test_captured():
             torch.cuda.synchronize()
 
 
+@pytest.mark.gpu
+def test_c_of_more_elements_than_a_launch_takes():
+    """The kernel that rounds the sums takes 1024 of a row per workgroup: 2^24 workgroups
+    and more would be 2^32 threads, which a launch cannot have."""
+    import torch
+    import recsys_linear_layers_amd as ll
+    M, N, K = 65600, 262144, 16
+    if torch.cuda.mem_get_info()[0] < 8 * M * N:
+        pytest.skip("C and its sums take 103 GB")
+    g = torch.Generator().manual_seed(1)
+    A, B = (torch.randint(-4, 5, (r, K), generator=g).float().cuda() for r in (M, N))
+    a, b = A.to(torch.float8_e4m3fn), B.to(torch.float8_e4m3fn)
+    out = torch.full((M, N), 77.5, dtype=torch.bfloat16, device="cuda")
+    ll.gemm8(a, torch.ones(M, 1, device="cuda"), b, torch.ones(N // 128, 1, device="cuda"), out=out, full_sums=True)
+    for m in range(0, M, 4096):
+        want = A[m:m + 4096] @ B.T  # whole numbers up to 256: exact
+        assert torch.equal(out[m:m + 4096], want.to(torch.bfloat16)), m
+        del want
+    del out
+    torch.cuda.empty_cache()
+
+
 def _desc(**kw):
     import recsys_linear_layers_amd as ll
     base = dict(M=200, N=300, K=256, stride_a=256, stride_b=256, stride_c=300, stride_am=1, stride_ab=200, stride_bn=2,
